@@ -93,6 +93,14 @@ typedef enum pkv_dtype {
                                             output rows unspecified */
 #define PKV_FLAG_QUERY_OVER_HINT 0x100   /* prefill: a sequence has more queries than max_q_len;
                                             rows past max_q_len are not computed */
+#define PKV_FLAG_STEP_INVALID 0x200      /* pkv_build_step: a length, block count or total the step
+                                            cannot have; the step is empty, nothing changed */
+#define PKV_FLAG_OUT_OF_BLOCKS 0x400     /* pkv_build_step: more blocks needed than are free; the
+                                            step is empty, nothing changed */
+#define PKV_FLAG_TOKENS_OVER 0x1000      /* pkv_build_step: more than max_tokens new tokens; the
+                                            lists hold the first max_tokens, all else is done */
+#define PKV_FLAG_POSITION 0x800          /* pkv_rope_write: a kept token's position is outside
+                                            [0, max_position); the token is skipped */
 #define PKV_FLAG_APPEND_MISMATCH 0x40    /* pkv_write_decode_attention: a kept slot is not the
                                             slot of position context_lens[b] - 1 through
                                             block_tables (or context_lens[b] == 0); the token
@@ -355,6 +363,192 @@ PKV_API pkv_status pkv_prefill_attention(void *out, const void *q, const void *k
                                          int head_dim, int block_size, int max_blocks,
                                          int64_t num_blocks, float scale, pkv_dtype dt,
                                          int max_q_len, int *err_flags, pkv_stream_t stream);
+
+/*
+ * pkv_build_step -- one serving step's block tables, slots, positions and
+ * query offsets, built on the GPU from the requests' lengths, with the blocks
+ * taken from and returned to a free list in device memory: what the host
+ * block manager (pkv_block_manager.h) hands out, without the host in the
+ * loop, so that a captured graph can replay whole steps whose lengths change
+ * on the device (drafted tokens accepted or turned down, requests that end).
+ *
+ *   block_tables  [B, max_blocks] int32, updated in place: request b's first
+ *                 held[b] entries are its blocks
+ *   held, held_out  [B] int32: blocks request b holds before / after
+ *   free_blocks   [free_capacity] int32, updated in place: a stack whose first
+ *                 *free_count entries are the free blocks
+ *   free_count, free_count_out  one int32: free blocks before / after
+ *   cached_lens   [B] int32: tokens of request b that are in the cache already
+ *   new_lens      [B] int32: tokens it adds in this step (0 = none)
+ *   context_lens  [B] int32 out: cached_lens[b] + new_lens[b]
+ *   cu_seqlens_q  [B + 1] int32 out: exclusive sums of new_lens
+ *   slot_mapping  [max_tokens] int64 out: slots of the new tokens, requests in
+ *                 order, -1 behind the last one
+ *   positions     [max_tokens] int32 out: their positions, 0 behind the last
+ *   num_blocks    blocks in the pool (every table and free entry read is
+ *                 checked against it)
+ * Request b ends with want = ceil((cached_lens[b] + new_lens[b]) / block_size)
+ * blocks.  Requests that hold more give theirs back first -- entries
+ * [want, held) of their rows are pushed on the stack, requests and entries in
+ * ascending order (the entries stay in the table row as they were) -- then
+ * requests that hold fewer take theirs from its top, requests and entries in
+ * ascending order.  A request that ended has both lengths 0; one whose drafted
+ * tokens were turned down comes with the smaller cached length.
+ * held_out may be held, free_count_out may be free_count, and context_lens
+ * may be cached_lens; no other two arguments may overlap.
+ * All or nothing: with a negative length, a held outside [0, max_blocks], a
+ * request that holds fewer than ceil(cached_lens[b] / block_size) blocks or
+ * needs more than max_blocks, 2^30 new tokens or more in all, or a free list
+ * that is (or would become) larger than free_capacity, the call raises
+ * PKV_FLAG_STEP_INVALID; with too few free blocks PKV_FLAG_OUT_OF_BLOCKS.  In both cases tables, free list and counts stay
+ * as they were (held_out and free_count_out get the old values) and the step
+ * is empty: context_lens 0, cu_seqlens_q 0, every slot -1.  More than
+ * max_tokens new tokens raise PKV_FLAG_TOKENS_OVER: slot_mapping and positions
+ * hold the first max_tokens, everything else is as without the bound (what
+ * attends over max_tokens query rows skips and flags the requests past it).
+ * An entry outside
+ * [0, num_blocks) raises PKV_FLAG_BLOCK_OUT_OF_RANGE where a token or a
+ * request would get it; that token's slot is -1.
+ * Supported: B <= 16384, max_tokens <= 2^30.  Errors: PKV_ERR_INVALID_ARG
+ * (NULL or misaligned pointers, sizes), PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * B == 0 with max_tokens == 0 enqueues nothing.
+ */
+PKV_API pkv_status pkv_build_step(int32_t *block_tables, const int32_t *held, int32_t *held_out,
+                                  int32_t *free_blocks, const int32_t *free_count,
+                                  int32_t *free_count_out, const int32_t *cached_lens,
+                                  const int32_t *new_lens, int32_t *context_lens,
+                                  int32_t *cu_seqlens_q, int64_t *slot_mapping, int32_t *positions,
+                                  int B, int max_blocks, int64_t num_blocks, int block_size,
+                                  int64_t free_capacity, int64_t max_tokens, int *err_flags,
+                                  pkv_stream_t stream);
+
+/*
+ * pkv_rope_write -- rotary positions and pkv_write in one pass: every kept
+ * token's query heads are rotated into q_out, its key heads are rotated into
+ * the cache and its value heads copied there.
+ *
+ *   q             [num_tokens, H, head_dim], token i at element i * q_token_stride
+ *   k, v          [num_tokens, num_kv_heads, head_dim], strides as in pkv_write
+ *   q_out         [num_tokens, H, head_dim] contiguous; may be q itself (with
+ *                 q_token_stride = H * head_dim), else no overlap
+ *   k_cache, v_cache, slot_mapping  as in pkv_write
+ *   cos_sin       [max_position, rot_dim] float32: row p holds the cosines of
+ *                 the rot_dim / 2 pairs' angles at position p, then the sines
+ *   positions     [num_axes, num_tokens] int32, axis a at element
+ *                 a * positions_stride: a token's position on each axis (for
+ *                 images and video: time, height, width)
+ *   pair_axis     HOST array of rot_dim / 2 bytes: the axis in [0, num_axes)
+ *                 whose position turns pair j (sections, or any interleaving
+ *                 of the axes); NULL = axis 0 for all; read during the call
+ *   rot_dim       even, 0 .. head_dim: the leading elements of a head that
+ *                 turn; the rest is copied
+ *   interleaved   0: pair j is elements (j, j + rot_dim / 2); else (2j, 2j + 1)
+ * With (x, y) a pair and c, s its table entries: (x c - y s, y c + x s), in
+ * fp32, rounded once to dtype.  A negative slot is a padding token: nothing
+ * is read or written for it (its q_out row stays as it was).  A kept token
+ * with a used axis' position outside [0, max_position) raises
+ * PKV_FLAG_POSITION and is skipped the same way; a slot past the pool raises
+ * PKV_FLAG_SLOT_OUT_OF_RANGE, its q_out row is written and the cache is not.
+ * Two kept tokens with the same slot race, as in pkv_write.
+ * Supported: head_dim <= 512, num_axes 1 .. 4, any alignment of elements
+ * (16-byte aligned rows are fastest).  Errors: PKV_ERR_INVALID_ARG,
+ * PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.  num_tokens == 0 enqueues nothing.
+ */
+PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, const void *q,
+                                  const void *k, const void *v, const float *cos_sin,
+                                  const int32_t *positions, const uint8_t *pair_axis,
+                                  const int64_t *slot_mapping, int64_t num_tokens,
+                                  int64_t q_token_stride, int64_t k_token_stride,
+                                  int64_t v_token_stride, int64_t positions_stride, int num_axes,
+                                  int H, int num_kv_heads, int head_dim, int rot_dim,
+                                  int interleaved, int64_t max_position, int64_t num_blocks,
+                                  int block_size, pkv_dtype dt, int *err_flags,
+                                  pkv_stream_t stream);
+
+/*
+ * pkv_chunk_attention -- attention of each sequence's newest tokens over its
+ * paged context, with the score forms models use beside plain causal
+ * attention.  As in pkv_prefill_attention the qlen = cu_seqlens_q[b+1] -
+ * cu_seqlens_q[b] queries of sequence b are the last qlen of its
+ * n = context_lens[b] tokens, query i at position p = n - qlen + i; qlen = 1
+ * is decode.  For key j and query head h:
+ *   x = scale * q . k_j
+ *   x = softcap * tanh(x / softcap)           if softcap > 0
+ *   x = x - slopes[h] * |p - j|               if slopes
+ *   visible:  (j <= p  or  j < prefix_lens[b])
+ *             and (window == 0 or p - j < window)  and  j >= kv_starts[row]
+ * then an fp32 softmax over the visible keys and the weighted sum of V.  A
+ * query that sees no key gives a row of zeros.
+ *
+ *   out, q, cu_seqlens_q, k_cache, v_cache, block_tables, context_lens
+ *                 as in pkv_prefill_attention; out rows behind
+ *                 cu_seqlens_q[B] are left as they were
+ *   softcap       0 = none, else > 0
+ *   window        0 = none, else a query sees at most the last `window` keys
+ *                 up to itself (and the prefix positions above p)
+ *   slopes        [H] float32 or NULL: linear distance bias per query head
+ *   prefix_lens   [B] int32 or NULL: keys below it are visible to every query
+ *                 of the sequence, also to earlier positions (prefix mask);
+ *                 values past n act as n, negative ones as 0
+ *   kv_starts     [total_q] int32 or NULL: the first key a query may see, for
+ *                 example its document's first position in a packed sequence
+ *   max_q_len     host bound on qlen (0 = total_q); a longer sequence raises
+ *                 PKV_FLAG_QUERY_OVER_HINT, its output rows are unspecified
+ *   max_context_len  host bound on context_lens (0 = max_blocks *
+ *                 block_size); a longer one raises PKV_FLAG_CONTEXT_OVER_HINT,
+ *                 its output rows are unspecified
+ *   partition_size  0 = automatic, else a positive multiple of 128: keys per
+ *                 part of the split over the context
+ *   workspace     pkv_chunk_workspace_size(...) bytes, 256-byte aligned,
+ *                 zero-filled before its first use; every call that completes
+ *                 without PKV_FLAG_TIMEOUT leaves it ready for the next on the
+ *                 same stream.  Calls that may overlap need workspaces of
+ *                 their own (two captured graphs that share one must not
+ *                 replay at the same time).
+ * A sequence with qlen < 0, qlen > n or a context longer than its table
+ * raises PKV_FLAG_QUERY_LEN and is skipped, its rows unspecified.  Cache rows
+ * that no query of a sequence sees (behind its context, before its window)
+ * may hold anything, NaN included, and an invisible key or value never
+ * changes a row, whatever it holds.  Table entries of blocks that no query
+ * sees are not read.
+ * Supported: fp32, bf16, fp16; head_dim <= 512; any block size; element-
+ * aligned pointers.  bf16 / fp16 with 16-byte aligned tensors, block_size a
+ * multiple of 16 and head_dim 64, 128, 192 or 256 run tensor-core kernels:
+ * chunks of up to 16 (query, head) rows per KV head, and every chunk at
+ * head_dim 192 and 256, an mma.sync kernel; longer chunks at head_dim 64 and
+ * 128 a tcgen05 kernel.  Everything else runs on the CUDA cores.
+ * Errors: PKV_ERR_INVALID_ARG (also a negative or NaN softcap, a negative
+ * window), PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA.  B == 0 or
+ * total_q == 0 enqueues nothing.
+ */
+PKV_API pkv_status pkv_chunk_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, const int32_t *cu_seqlens_q, const int32_t *context_lens,
+    const float *slopes, const int32_t *prefix_lens, const int32_t *kv_starts, int B,
+    int64_t total_q, int H, int num_kv_heads, int head_dim, int block_size, int max_blocks,
+    int64_t num_blocks, float scale, float softcap, int window, pkv_dtype dt, int max_q_len,
+    int max_context_len, int partition_size, void *workspace, size_t workspace_bytes,
+    int *err_flags, pkv_stream_t stream);
+
+/*
+ * pkv_chunk_workspace_size -- bytes of workspace pkv_chunk_attention needs for
+ * these sizes, for every dtype, window and score form (host only).  Returns 0
+ * for invalid sizes.
+ */
+PKV_API size_t pkv_chunk_workspace_size(int B, int64_t total_q, int H, int num_kv_heads,
+                                        int head_dim, int block_size, int max_blocks,
+                                        int max_q_len, int max_context_len, int partition_size);
+
+/*
+ * pkv_chunk_plan -- the kernel (2 tcgen05, 1 mma.sync, 0 CUDA cores) and the
+ * split that pkv_chunk_attention would use for these arguments with 16-byte
+ * aligned tensors (host only; for tests and tuning).  has_prefix: prefix_lens
+ * is given.  Returns the keys per part, or 0 for invalid sizes.
+ */
+PKV_API int pkv_chunk_plan(int B, int64_t total_q, int H, int num_kv_heads, int head_dim,
+                           int block_size, int max_blocks, int max_q_len, int max_context_len,
+                           int window, int has_prefix, int partition_size, pkv_dtype dt,
+                           int *max_parts, int *kernel);
 
 /*
  * The layout experiment: vLLM's packed cache layout, which the interview

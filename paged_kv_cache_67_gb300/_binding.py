@@ -32,6 +32,10 @@ FLAG_TIMEOUT = 0x20
 FLAG_APPEND_MISMATCH = 0x40
 FLAG_QUERY_LEN = 0x80
 FLAG_QUERY_OVER_HINT = 0x100
+FLAG_STEP_INVALID = 0x200
+FLAG_OUT_OF_BLOCKS = 0x400
+FLAG_POSITION = 0x800
+FLAG_TOKENS_OVER = 0x1000
 
 _lock = threading.Lock()
 _lib = None
@@ -89,6 +93,18 @@ def load_library():
                                               c_int, c_int, c_int, i64, ctypes.c_float, c_int, c_int,
                                               vp, vp]
         lib.pkv_prefill_attention.restype = c_int
+        c_float = ctypes.c_float
+        lib.pkv_build_step.argtypes = [vp] * 12 + [c_int, c_int, i64, c_int, i64, i64, vp, vp]
+        lib.pkv_build_step.restype = c_int
+        lib.pkv_rope_write.argtypes = [vp] * 10 + [i64] * 5 + [c_int] * 6 + [i64, i64, c_int, c_int, vp, vp]
+        lib.pkv_rope_write.restype = c_int
+        lib.pkv_chunk_attention.argtypes = [vp] * 10 + [c_int, i64] + [c_int] * 5 + [
+            i64, c_float, c_float, c_int, c_int, c_int, c_int, c_int, vp, c_size, vp, vp]
+        lib.pkv_chunk_attention.restype = c_int
+        lib.pkv_chunk_workspace_size.argtypes = [c_int, i64] + [c_int] * 8
+        lib.pkv_chunk_workspace_size.restype = c_size
+        lib.pkv_chunk_plan.argtypes = [c_int, i64] + [c_int] * 11 + [ctypes.POINTER(c_int)] * 2
+        lib.pkv_chunk_plan.restype = c_int
         P = ctypes.POINTER
         lib.pkv_bm_create.argtypes = [i64, c_int, c_int, P(vp)]
         lib.pkv_bm_create.restype = c_int
@@ -287,13 +303,18 @@ class PreparedCall:
     list built at preparation, so each call costs one ctypes call and no
     Python-side checks.  Raises PkvError on a status other than PKV_OK."""
 
-    __slots__ = ("_fn", "_args", "_what", "_keep")
+    __slots__ = ("_fn", "_args", "_what", "_keep", "_device")
 
-    def __init__(self, fn, args, what, keep):
+    def __init__(self, fn, args, what, keep, device=None):
         self._fn, self._args, self._what, self._keep = fn, tuple(args), what, keep
+        self._device = None if device is None else device.index  # made current for the call
 
     def __call__(self):
-        status = self._fn(*self._args)
+        if self._device is None or self._device == torch.cuda.current_device():
+            status = self._fn(*self._args)
+        else:
+            with torch.cuda.device(self._device):
+                status = self._fn(*self._args)
         if status != 0:
             raise PkvError(status, self._what)
 
@@ -524,6 +545,233 @@ def pkv_fp32_fma_peak(out, iters: int, a: float = 1.0, b: float = 1.0, never: fl
     _check(lib.pkv_fp32_fma_peak(_ptr(out), out.numel(), int(iters), float(a), float(b), float(never),
                                  int(bool(paired)), _stream_handle(stream, out.device)),
            "pkv_fp32_fma_peak")
+
+
+# ------------------------------------------------------- a step on the GPU
+
+def _flags_ok(err_flags, dev):
+    _require(err_flags is None or (err_flags.dtype == torch.int32 and err_flags.numel() >= 1
+                                   and err_flags.device == dev),
+             "err_flags must be int32 on the same CUDA device")
+
+
+def _build_step_args(block_tables, held, held_out, free_blocks, free_count, free_count_out,
+                     cached_lens, new_lens, context_lens, cu_seqlens_q, slot_mapping, positions,
+                     num_blocks, block_size, err_flags, stream):
+    i32 = torch.int32
+    _require(block_tables.dim() == 2 and block_tables.dtype == i32, "block_tables must be int32 [B, max_blocks]")
+    B, max_blocks = block_tables.shape
+    for t, name in ((held, "held"), (held_out, "held_out"), (cached_lens, "cached_lens"),
+                    (new_lens, "new_lens"), (context_lens, "context_lens")):
+        _require(t.dtype == i32 and t.shape == (B,), f"{name} must be int32 [B]")
+    _require(cu_seqlens_q.dtype == i32 and cu_seqlens_q.shape == (B + 1,), "cu_seqlens_q must be int32 [B + 1]")
+    _require(free_blocks.dtype == i32 and free_blocks.dim() == 1, "free_blocks must be int32 [capacity]")
+    for t, name in ((free_count, "free_count"), (free_count_out, "free_count_out")):
+        _require(t.dtype == i32 and t.numel() == 1, f"{name} must be one int32")
+    _require(slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1, "slot_mapping must be int64 [max_tokens]")
+    _require(positions.dtype == i32 and positions.shape == slot_mapping.shape, "positions must be int32 [max_tokens]")
+    tensors = (block_tables, held, held_out, free_blocks, free_count, free_count_out, cached_lens,
+               new_lens, context_lens, cu_seqlens_q, slot_mapping, positions)
+    for t in tensors:
+        _require(t.is_contiguous(), "tensors must be contiguous")
+    dev = block_tables.device
+    _require(dev.type == "cuda" and all(t.device == dev for t in tensors),
+             "all tensors must be on the same CUDA device")
+    _flags_ok(err_flags, dev)
+    args = tuple(_ptr(t) for t in tensors) + (
+        B, max_blocks, int(num_blocks), int(block_size), free_blocks.numel(), slot_mapping.numel(),
+        _ptr(err_flags), _stream_handle(stream, dev))
+    return args, tensors + (err_flags,), dev
+
+
+def pkv_build_step(block_tables, held, held_out, free_blocks, free_count, free_count_out, cached_lens,
+                   new_lens, context_lens, cu_seqlens_q, slot_mapping, positions, num_blocks: int,
+                   block_size: int, err_flags=None, stream=None) -> None:
+    """One step's block tables (in place), slots, positions and query offsets
+    from the requests' cached and new lengths, with the blocks taken from and
+    returned to the stack ``free_blocks[:free_count]``.  ``held_out`` may be
+    ``held``, ``free_count_out`` ``free_count`` and ``context_lens``
+    ``cached_lens`` (a loop then carries its state in place)."""
+    lib = load_library()
+    args, _, dev = _build_step_args(block_tables, held, held_out, free_blocks, free_count, free_count_out,
+                                    cached_lens, new_lens, context_lens, cu_seqlens_q, slot_mapping,
+                                    positions, num_blocks, block_size, err_flags, stream)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_build_step(*args), "pkv_build_step")
+
+
+def prepare_build_step(block_tables, held, held_out, free_blocks, free_count, free_count_out, cached_lens,
+                       new_lens, context_lens, cu_seqlens_q, slot_mapping, positions, num_blocks: int,
+                       block_size: int, err_flags=None, stream=None) -> PreparedCall:
+    """pkv_build_step, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _build_step_args(block_tables, held, held_out, free_blocks, free_count, free_count_out,
+                                     cached_lens, new_lens, context_lens, cu_seqlens_q, slot_mapping,
+                                     positions, num_blocks, block_size, err_flags, stream)
+    return PreparedCall(lib.pkv_build_step, args, "pkv_build_step", keep, dev)
+
+
+def _rope_write_args(q_out, k_cache, v_cache, q, k, v, cos_sin, positions, slot_mapping, pair_axis,
+                     interleaved, err_flags, stream):
+    _require(k_cache.dim() == 4 and v_cache.shape == k_cache.shape, "caches must be [nb, bs, KVH, D]")
+    nb, bs, kvh, d = k_cache.shape
+    _require(k_cache.is_contiguous() and v_cache.is_contiguous(), "caches must be contiguous")
+    _require(q.dim() == 3 and q.shape[2] == d, "q must be [T, H, D]")
+    T, H, _ = q.shape
+    _require(k.shape == (T, kvh, d) and v.shape == k.shape, "k, v must be [T, KVH, D]")
+    _require(q_out.shape == q.shape and q_out.is_contiguous(), "q_out must be contiguous [T, H, D]")
+    for t in (q, k, v):
+        _require(t.stride(2) == 1 and t.stride(1) == d, "each token's heads must be contiguous")
+    _require(q.dtype == k.dtype == v.dtype == q_out.dtype == k_cache.dtype == v_cache.dtype and q.dtype in _DT,
+             "dtype mismatch")
+    _require(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous(),
+             "cos_sin must be contiguous float32 [max_position, rot_dim]")
+    max_pos, rot = cos_sin.shape
+    _require(rot % 2 == 0 and rot <= d, "rot_dim must be even and at most head_dim")
+    _require(positions.dtype == torch.int32 and positions.dim() in (1, 2) and positions.shape[-1] == T
+             and (T == 0 or positions.stride(-1) == 1 or T == 1), "positions must be int32 [T] or [axes, T]")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    pos_stride = positions.stride(0) if positions.dim() == 2 and axes > 1 else T
+    _require(slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.shape == (T,),
+             "slot_mapping must be contiguous int64 [T]")
+    host = None
+    if pair_axis is not None:
+        pa = [int(x) for x in pair_axis]
+        _require(len(pa) == rot // 2 and all(0 <= x < axes for x in pa),
+                 "pair_axis must name an axis for each of the rot_dim / 2 pairs")
+        host = (ctypes.c_uint8 * max(1, len(pa)))(*pa)
+    tensors = (q_out, k_cache, v_cache, q, k, v, cos_sin, positions, slot_mapping)
+    dev = q.device
+    _require(dev.type == "cuda" and all(t.device == dev for t in tensors),
+             "all tensors must be on the same CUDA device")
+    _flags_ok(err_flags, dev)
+    row, qrow = kvh * d, H * d
+    args = (_ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(q), _ptr(k), _ptr(v), _ptr(cos_sin),
+            _ptr(positions), None if host is None else ctypes.cast(host, ctypes.c_void_p), _ptr(slot_mapping), T,
+            q.stride(0) if T > 1 else qrow, k.stride(0) if T > 1 else row, v.stride(0) if T > 1 else row,
+            pos_stride, axes, H, kvh, d, rot, int(bool(interleaved)), max_pos, nb, bs, _DT[q.dtype],
+            _ptr(err_flags), _stream_handle(stream, dev))
+    return args, tensors + (host, err_flags), dev
+
+
+def pkv_rope_write(q_out, k_cache, v_cache, q, k, v, cos_sin, positions, slot_mapping, pair_axis=None,
+                   interleaved: bool = False, err_flags=None, stream=None):
+    """Rotate q [T, H, D] into ``q_out`` (returned; may be q itself when q is
+    contiguous) and k [T, KVH, D] into the paged cache, and copy v there, at
+    slot_mapping [T] (negative = padding, skipped).  cos_sin [max_position,
+    rot_dim] float32 holds the pairs' cosines, then sines; positions is int32
+    [T] or [axes, T]; pair_axis names the axis of each of the rot_dim / 2
+    pairs (a host sequence; None = axis 0)."""
+    lib = load_library()
+    args, _, dev = _rope_write_args(q_out, k_cache, v_cache, q, k, v, cos_sin, positions, slot_mapping,
+                                    pair_axis, interleaved, err_flags, stream)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_rope_write(*args), "pkv_rope_write")
+    return q_out
+
+
+def prepare_rope_write(q_out, k_cache, v_cache, q, k, v, cos_sin, positions, slot_mapping, pair_axis=None,
+                       interleaved: bool = False, err_flags=None, stream=None) -> PreparedCall:
+    """pkv_rope_write, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _rope_write_args(q_out, k_cache, v_cache, q, k, v, cos_sin, positions, slot_mapping,
+                                     pair_axis, interleaved, err_flags, stream)
+    return PreparedCall(lib.pkv_rope_write, args, "pkv_rope_write", keep, dev)
+
+
+def pkv_chunk_workspace_size(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len=0,
+                             max_context_len=0, partition_size=0) -> int:
+    return int(load_library().pkv_chunk_workspace_size(B, total_q, H, num_kv_heads, head_dim, block_size,
+                                                       max_blocks, max_q_len, max_context_len, partition_size))
+
+
+def pkv_chunk_plan(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len=0,
+                   max_context_len=0, window=0, has_prefix=False, partition_size=0, dtype=torch.bfloat16):
+    """(keys per part, parts per row, kernel) pkv_chunk_attention would use
+    (kernel 2 = tcgen05, 1 = mma.sync, 0 = CUDA cores); host only."""
+    mp, kern = ctypes.c_int(0), ctypes.c_int(0)
+    P = load_library().pkv_chunk_plan(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len,
+                                      max_context_len, window, int(bool(has_prefix)), partition_size, _DT[dtype],
+                                      ctypes.byref(mp), ctypes.byref(kern))
+    return P, mp.value, kern.value
+
+
+class ChunkWorkspace:
+    """A zero-filled device workspace sized for pkv_chunk_attention."""
+
+    def __init__(self, B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len=0,
+                 max_context_len=0, partition_size=0, device="cuda"):
+        self.nbytes = pkv_chunk_workspace_size(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks,
+                                               max_q_len, max_context_len, partition_size)
+        self.buffer = torch.zeros(max(self.nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _chunk_args(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, scale, softcap, window,
+                slopes, prefix_lens, kv_starts, max_q_len, max_context_len, partition_size, workspace,
+                err_flags, stream):
+    _require(q.dim() == 3 and out.shape == q.shape, "q and out must be [total_q, H, D]")
+    total_q, H, D = q.shape
+    _require(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.shape[3] == D,
+             "caches must be [nb, bs, KVH, D]")
+    nb, bs, kvh, _ = k_cache.shape
+    _require(q.dtype == out.dtype == k_cache.dtype == v_cache.dtype and q.dtype in _DT, "dtype mismatch")
+    _require(context_lens.dtype == torch.int32 and context_lens.dim() == 1, "context_lens must be int32 [B]")
+    B = context_lens.shape[0]
+    _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == B,
+             "block_tables must be int32 [B, max_blocks]")
+    _require(cu_seqlens_q.dtype == torch.int32 and cu_seqlens_q.shape == (B + 1,),
+             "cu_seqlens_q must be int32 [B + 1]")
+    _require(slopes is None or (slopes.dtype == torch.float32 and slopes.shape == (H,)), "slopes must be float32 [H]")
+    _require(prefix_lens is None or (prefix_lens.dtype == torch.int32 and prefix_lens.shape == (B,)),
+             "prefix_lens must be int32 [B]")
+    _require(kv_starts is None or (kv_starts.dtype == torch.int32 and kv_starts.shape == (total_q,)),
+             "kv_starts must be int32 [total_q]")
+    buf = workspace.buffer if isinstance(workspace, ChunkWorkspace) else workspace
+    tensors = tuple(t for t in (out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, slopes,
+                                prefix_lens, kv_starts, buf) if t is not None)
+    for t in tensors:
+        _require(t.is_contiguous(), "tensors must be contiguous")
+    dev = q.device
+    _require(dev.type == "cuda" and all(t.device == dev for t in tensors),
+             "all tensors must be on the same CUDA device")
+    _flags_ok(err_flags, dev)
+    args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(cu_seqlens_q),
+            _ptr(context_lens), _ptr(slopes), _ptr(prefix_lens), _ptr(kv_starts), B, total_q, H, kvh, D, bs,
+            block_tables.shape[1], nb, float(scale), float(softcap), int(window), _DT[q.dtype], int(max_q_len),
+            int(max_context_len), int(partition_size), _ptr(buf),
+            0 if buf is None else buf.numel() * buf.element_size(), _ptr(err_flags), _stream_handle(stream, dev))
+    return args, tensors + (err_flags,), dev
+
+
+def pkv_chunk_attention(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, scale: float,
+                        softcap: float = 0.0, window: int = 0, slopes=None, prefix_lens=None, kv_starts=None,
+                        max_q_len: int = 0, max_context_len: int = 0, partition_size: int = 0, workspace=None,
+                        err_flags=None, stream=None):
+    """Attention of each sequence's newest tokens over its paged context into
+    ``out`` [total_q, H, D] (returned), with capped scores (``softcap``), a
+    sliding ``window``, a distance bias (``slopes`` [H]), a prefix mask
+    (``prefix_lens`` [B]) or a first visible key per query (``kv_starts``
+    [total_q]); one new token per sequence is decode.  A query that sees no
+    key gives zeros."""
+    lib = load_library()
+    args, _, dev = _chunk_args(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, scale, softcap,
+                               window, slopes, prefix_lens, kv_starts, max_q_len, max_context_len, partition_size,
+                               workspace, err_flags, stream)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_chunk_attention(*args), "pkv_chunk_attention")
+    return out
+
+
+def prepare_chunk_attention(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, scale: float,
+                            softcap: float = 0.0, window: int = 0, slopes=None, prefix_lens=None, kv_starts=None,
+                            max_q_len: int = 0, max_context_len: int = 0, partition_size: int = 0, workspace=None,
+                            err_flags=None, stream=None) -> PreparedCall:
+    """pkv_chunk_attention, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _chunk_args(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, scale, softcap,
+                                window, slopes, prefix_lens, kv_starts, max_q_len, max_context_len, partition_size,
+                                workspace, err_flags, stream)
+    return PreparedCall(lib.pkv_chunk_attention, args, "pkv_chunk_attention", keep, dev)
 
 
 PKV_ERR_OUT_OF_BLOCKS = 5

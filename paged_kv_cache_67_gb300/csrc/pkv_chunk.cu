@@ -1,0 +1,200 @@
+// pkv_chunk.cu -- host side of chunk attention: argument checks, the choice
+// of kernel and split, the workspace's layout, the launch.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "pkv_chunk.cuh"
+
+namespace pkv {
+
+pkv_status launch_chunk_simt(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
+size_t chunk_simt_smem(int D);
+
+// The plan uses the SM count of the one GPU this library is built for, so
+// that the workspace's size needs no device.
+constexpr int kPlanSms = 152;
+constexpr int kChunkRows = 16;     // packed rows per CTA of the CUDA-core and mma.sync kernels
+constexpr int kChunkMaxParts = 64;
+constexpr long long kChunkMaxKeys = 1LL << 30;  // keys of a context: positions plus a part stay in 32 bits
+
+struct ChunkPlan {
+  int kernel;         // 2 tcgen05, 1 mma.sync, 0 CUDA cores
+  int P, max_parts;   // keys per part, parts per row
+  int most_parts;     // parts per row of any call of these sizes (the workspace's)
+  long long chunks;   // row chunks per (sequence, KV head)
+};
+
+static long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+static bool chunk_sizes_ok(int B, int64_t total_q, int H, int KVH, int D, int bs, int max_blocks, int max_q,
+                           int max_n, int partition_size) {
+  return B >= 0 && B <= 65535 && total_q >= 0 && total_q <= 0x7fffffffLL && H > 0 && H <= 65535 && KVH > 0 &&
+         H % KVH == 0 && D > 0 && D <= 512 && bs > 0 && max_blocks >= 0 && max_q >= 0 && max_n >= 0 &&
+         partition_size >= 0 && partition_size % 128 == 0;
+}
+
+static long long chunk_cap(int bs, int max_blocks, int max_n) {
+  long long cap = std::min<long long>((long long)max_blocks * bs, kChunkMaxKeys);
+  if (max_n > 0 && max_n < cap) cap = max_n;
+  return std::max<long long>(cap, 1);
+}
+
+static int chunk_max_q(int64_t total_q, int max_q) {
+  return (int)std::max<int64_t>(1, max_q > 0 ? std::min<int64_t>(max_q, total_q) : total_q);
+}
+
+// Parts wanted for a unit: enough that the units fill `slots` CTA places
+// about twice over.
+static long long parts_wanted(long long units, long long slots) {
+  return std::min<long long>(kChunkMaxParts, std::max<long long>(1, 2 * slots / std::max<long long>(units, 1)));
+}
+
+// `span`: the most keys a unit sees, from its first one's 16-key chunk on
+// (where its first part begins); each part has `min_p` keys or more.
+static void chunk_split(long long wanted, long long span, int min_p, int partition_size, ChunkPlan *p) {
+  long long P = partition_size;
+  if (P == 0) P = std::max<long long>(min_p, ceil_div(ceil_div(span, wanted), 128) * 128);
+  P = std::min(P, ceil_div(span, 128) * 128);
+  p->P = (int)P;
+  p->max_parts = (int)ceil_div(span, P);
+  p->most_parts = partition_size > 0 ? p->max_parts : (int)std::min(wanted, ceil_div(span, min_p));
+}
+
+static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, int max_blocks, int max_q, int max_n,
+                       int window, bool has_prefix, int partition_size, pkv_dtype dt, bool aligned16, ChunkPlan *p) {
+  if (!chunk_sizes_ok(B, total_q, H, KVH, D, bs, max_blocks, max_q, max_n, partition_size) || window < 0) return false;
+  if (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16) return false;
+  const long long mq = chunk_max_q(total_q, max_q), cap = chunk_cap(bs, max_blocks, max_n);
+  p->kernel = 0;
+  p->chunks = ceil_div(mq * (H / KVH), kChunkRows);
+  // a window bounds the keys a unit sees, unless a prefix reaches past it
+  const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 15) : cap;
+  chunk_split(parts_wanted((long long)B * KVH * p->chunks, kPlanSms * 4), span, 256, partition_size, p);
+  return true;
+}
+
+// Workspace bytes of a plan.
+static size_t chunk_ws_bytes(int64_t total_q, int H, int D, long long parts) {
+  size_t bytes = kChunkCnt * sizeof(int);
+  if (parts > 1) {
+    const size_t rows = (size_t)total_q * H;
+    bytes += 2 * align256(rows * parts * sizeof(float)) + align256(rows * parts * (size_t)D * sizeof(float));
+  }
+  return bytes;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+PKV_API size_t pkv_chunk_workspace_size(int B, int64_t total_q, int H, int num_kv_heads, int head_dim, int block_size,
+                                        int max_blocks, int max_q_len, int max_context_len, int partition_size) {
+  size_t most = 0;
+  for (int dt = 0; dt < 2; ++dt) {   // fp32's kernel and the 16-bit types'
+    ChunkPlan p;
+    if (!chunk_plan(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len, max_context_len, 0, false,
+                    partition_size, (pkv_dtype)dt, true, &p))
+      return 0;
+    most = std::max(most, chunk_ws_bytes(total_q, H, head_dim, p.most_parts));
+  }
+  return most;
+}
+
+PKV_API int pkv_chunk_plan(int B, int64_t total_q, int H, int num_kv_heads, int head_dim, int block_size, int max_blocks,
+                           int max_q_len, int max_context_len, int window, int has_prefix, int partition_size,
+                           pkv_dtype dt, int *max_parts, int *kernel) {
+  ChunkPlan p;
+  if (!chunk_plan(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len, max_context_len, window,
+                  has_prefix != 0, partition_size, dt, true, &p))
+    return 0;
+  if (max_parts) *max_parts = p.max_parts;
+  if (kernel) *kernel = p.kernel;
+  return p.P;
+}
+
+PKV_API pkv_status pkv_chunk_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+    const int32_t *cu_seqlens_q, const int32_t *context_lens, const float *slopes, const int32_t *prefix_lens,
+    const int32_t *kv_starts, int B, int64_t total_q, int H, int num_kv_heads, int head_dim, int block_size,
+    int max_blocks, int64_t num_blocks, float scale, float softcap, int window, pkv_dtype dt, int max_q_len,
+    int max_context_len, int partition_size, void *workspace, size_t workspace_bytes, int *err_flags,
+    pkv_stream_t stream) {
+  if (head_dim > 512) return PKV_ERR_UNSUPPORTED;
+  if (!chunk_sizes_ok(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len, max_context_len,
+                      partition_size) ||
+      num_blocks < 0 || num_blocks > 0x7fffffffLL || window < 0 || !(softcap >= 0.f) || isinf(softcap))
+    return PKV_ERR_INVALID_ARG;
+  if (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16) return PKV_ERR_INVALID_ARG;
+  if (B == 0 || total_q == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !context_lens)
+    return PKV_ERR_INVALID_ARG;
+  const uintptr_t el = dt == PKV_F32 ? 4 : 2;
+  const void *ptrs[4] = {out, q, k_cache, v_cache};
+  bool aligned16 = true;
+  for (const void *p : ptrs) {
+    if (reinterpret_cast<uintptr_t>(p) % el) return PKV_ERR_INVALID_ARG;
+    aligned16 = aligned16 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  }
+  const void *p4[] = {block_tables, cu_seqlens_q, context_lens, slopes, prefix_lens, kv_starts, err_flags};
+  for (const void *p : p4)
+    if (reinterpret_cast<uintptr_t>(p) % 4) return PKV_ERR_INVALID_ARG;
+  ChunkPlan plan;
+  if (!chunk_plan(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len, max_context_len, window,
+                  prefix_lens != nullptr, partition_size, dt, aligned16, &plan))
+    return PKV_ERR_INVALID_ARG;
+  const size_t need = chunk_ws_bytes(total_q, H, head_dim, plan.max_parts);
+  if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256) return PKV_ERR_WORKSPACE;
+  if (plan.chunks * num_kv_heads * plan.max_parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  if (plan.max_parts > 1 && (long long)B * num_kv_heads * plan.chunks > kChunkCnt - kChunkCntFirst)
+    return PKV_ERR_UNSUPPORTED;
+
+  ChunkArgs a;
+  memset(&a, 0, sizeof a);
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.tables = block_tables;
+  a.cu_q = cu_seqlens_q;
+  a.lens = context_lens;
+  a.slopes = slopes;
+  a.prefix = prefix_lens;
+  a.starts = kv_starts;
+  a.err = err_flags;
+  a.num_blocks = num_blocks;
+  a.total_q = total_q;
+  a.B = B;
+  a.H = H;
+  a.KVH = num_kv_heads;
+  a.D = head_dim;
+  a.G = H / num_kv_heads;
+  a.bs = block_size;
+  a.max_blocks = max_blocks;
+  a.max_q = chunk_max_q(total_q, max_q_len);
+  a.max_n = (int)chunk_cap(block_size, max_blocks, max_context_len);
+  a.window = window;
+  a.P = plan.P;
+  a.max_parts = plan.max_parts;
+  a.chunks = (int)plan.chunks;
+  a.scale_log2 = softcap > 0.f ? scale / softcap : scale * kLog2e;
+  a.cap_log2 = softcap * kLog2e;
+  char *ws = static_cast<char *>(workspace);
+  a.ws_cnt = reinterpret_cast<int *>(ws);
+  if (plan.max_parts > 1) {
+    const size_t rows = (size_t)total_q * H;
+    ws += kChunkCnt * sizeof(int);
+    a.ws_m = reinterpret_cast<float *>(ws);
+    ws += align256(rows * plan.max_parts * sizeof(float));
+    a.ws_l = reinterpret_cast<float *>(ws);
+    ws += align256(rows * plan.max_parts * sizeof(float));
+    a.ws_o = reinterpret_cast<float *>(ws);
+  }
+  return launch_chunk_simt(a, dt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,276 @@
+// pkv_rope_write.cu -- rotary positions over several axes, fused with the
+// paged write: q rotated into q_out, k rotated into the cache, v copied there.
+//
+// Pair j of a head, (x, y), turns by the angle of position pos[axis(j)]:
+//   (x, y) -> (x c - y s, y c + x s),   c, s = cos_sin[pos][j], [pairs + j]
+// in fp32, rounded once.  Every element is read once and written once, so
+// memory bounds it; what it must not do is read the angle table (8 bytes a
+// pair, more than the 4 bytes of a 16-bit pair itself) once per head.
+//
+// So a lane keeps to one unit of a head -- VEC pairs, two vectors of VEC
+// elements: columns j and j + pairs, or 2 VEC neighbours when interleaved --
+// with its cosines and sines in registers, and runs over the token's heads.
+// A warp's lanes cover 32 / U heads of U units side by side (coalesced), a
+// token is shared by `wpt` warps.  The columns behind rot_dim are units that
+// copy, the value heads are copied by every unit.
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+constexpr int kRopeWarps = 4;
+constexpr int kRopeBatch = 4;       // heads of a lane in flight
+constexpr int kRopeMaxPairs = 256;
+
+struct RopeArgs {
+  char *q_out, *kc, *vc;
+  const char *q, *k, *v;
+  const float *cos_sin;
+  const int32_t *pos;
+  const int64_t *slots;
+  int *err;
+  long long T, q_stride, k_stride, v_stride, pos_stride;  // strides in elements
+  long long max_pos, capacity;
+  int axes, H, KVH, D, pairs, interleaved;
+  int wpt;                              // warps per token
+  uint32_t axis2[kRopeMaxPairs / 16];   // axis of pair j: two bits
+};
+
+template <typename T, int VEC>
+struct __align__(sizeof(T) * VEC) RopeVec {
+  T e[VEC];
+};
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(32 * kRopeWarps) pkv_rope_write_kernel(const __grid_constant__ RopeArgs a) {
+  using V = RopeVec<T, VEC>;
+  const int lane = threadIdx.x & 31;
+  const long long gw = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const long long t = gw / a.wpt;
+  const int part = (int)(gw - t * a.wpt);
+  if (t >= a.T) return;
+  const long long slot = __ldg(a.slots + t);
+  if (slot < 0) return;                                   // padding token
+  const int pairs = a.pairs, D = a.D;
+  const int rot_units = pairs / VEC;
+  const int units = rot_units + (D - 2 * pairs + 2 * VEC - 1) / (2 * VEC);
+  int pos[4] = {0, 0, 0, 0};
+  bool ok = true;
+#pragma unroll
+  for (int ax = 0; ax < 4; ++ax)
+    if (ax < a.axes) pos[ax] = __ldg(a.pos + ax * a.pos_stride + t);
+  // every axis that a pair uses (bit ax of the mask), not only this lane's
+  uint32_t used = 0;
+  for (int j = lane; j < pairs; j += 32) used |= 1u << ((a.axis2[j >> 4] >> (2 * (j & 15))) & 3);
+  used = __reduce_or_sync(0xffffffffu, used);
+#pragma unroll
+  for (int ax = 0; ax < 4; ++ax)
+    if ((used >> ax) & 1) ok = ok && pos[ax] >= 0 && pos[ax] < a.max_pos;
+  if (!ok) {
+    if (lane == 0 && part == 0) raise_flag(a.err, PKV_FLAG_POSITION);
+    return;
+  }
+  const bool in_pool = slot < a.capacity;
+  if (!in_pool && lane == 0 && part == 0) raise_flag(a.err, PKV_FLAG_SLOT_OUT_OF_RANGE);
+
+  const int hpw = units >= 32 ? 1 : 32 / units;           // heads side by side in a warp
+  const int hl = units >= 32 ? 0 : lane / units;
+  const int heads = a.H + 2 * a.KVH;
+  const T *qs = reinterpret_cast<const T *>(a.q) + t * a.q_stride;
+  const T *ks = reinterpret_cast<const T *>(a.k) + t * a.k_stride;
+  const T *vs = reinterpret_cast<const T *>(a.v) + t * a.v_stride;
+  T *qd = reinterpret_cast<T *>(a.q_out) + t * (long long)a.H * D;
+  T *kd = reinterpret_cast<T *>(a.kc) + (in_pool ? slot : 0) * (long long)a.KVH * D;
+  T *vd = reinterpret_cast<T *>(a.vc) + (in_pool ? slot : 0) * (long long)a.KVH * D;
+
+  for (int u0 = 0; u0 < units; u0 += 32) {                // one pass unless a head has more than 32 units
+    const int unit = units >= 32 ? u0 + lane : lane - hl * units;
+    if (hl >= hpw || unit >= units) continue;
+    const bool turns = unit < rot_units;
+    int e0, e1;                                           // the unit's two vectors
+    if (turns) {
+      e0 = a.interleaved ? 2 * unit * VEC : unit * VEC;
+      e1 = a.interleaved ? e0 + VEC : pairs + unit * VEC;
+    } else {
+      e0 = 2 * pairs + (unit - rot_units) * 2 * VEC;
+      e1 = e0 + VEC;
+    }
+    const bool second = e1 < D;
+    float c[VEC], s[VEC];
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int j = unit * VEC + i;
+        const int ax = (a.axis2[j >> 4] >> (2 * (j & 15))) & 3;
+        const int p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
+        const float *row = a.cos_sin + (long long)p * (2 * pairs) + j;
+        c[i] = __ldg(row);
+        s[i] = __ldg(row + pairs);
+      }
+    }
+    for (int h0 = part * hpw + hl; h0 < heads; h0 += a.wpt * hpw * kRopeBatch) {
+      V x[kRopeBatch], y[kRopeBatch];
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i) {
+        const int h = h0 + i * a.wpt * hpw;
+        if (h < heads) {
+          const T *src = h < a.H ? qs + h * D : h < a.H + a.KVH ? ks + (h - a.H) * D : vs + (h - a.H - a.KVH) * D;
+          x[i] = *reinterpret_cast<const V *>(src + e0);
+          if (second) y[i] = *reinterpret_cast<const V *>(src + e1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i) {
+        const int h = h0 + i * a.wpt * hpw;
+        if (h >= heads || (h >= a.H && !in_pool)) continue;
+        T *dst = h < a.H ? qd + h * D : h < a.H + a.KVH ? kd + (h - a.H) * D : vd + (h - a.H - a.KVH) * D;
+        if (turns && h < a.H + a.KVH) {
+          float fx[VEC], fy[VEC];
+#pragma unroll
+          for (int n = 0; n < VEC; ++n) {
+            fx[n] = to_f32<T>(x[i].e[n]);
+            fy[n] = to_f32<T>(y[i].e[n]);
+          }
+          if (a.interleaved) {                            // pairs are neighbours: x holds the first VEC / 2 of them
+            float z[2 * VEC];
+#pragma unroll
+            for (int n = 0; n < VEC; ++n) {
+              z[n] = fx[n];
+              z[VEC + n] = fy[n];
+            }
+#pragma unroll
+            for (int n = 0; n < VEC; ++n) {
+              const float p = z[2 * n], q = z[2 * n + 1];
+              z[2 * n] = fmaf(p, c[n], -(q * s[n]));
+              z[2 * n + 1] = fmaf(q, c[n], p * s[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < VEC; ++n) {
+              x[i].e[n] = from_f32<T>(z[n]);
+              y[i].e[n] = from_f32<T>(z[VEC + n]);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < VEC; ++n) {
+              x[i].e[n] = from_f32<T>(fmaf(fx[n], c[n], -(fy[n] * s[n])));
+              y[i].e[n] = from_f32<T>(fmaf(fy[n], c[n], fx[n] * s[n]));
+            }
+          }
+        }
+        *reinterpret_cast<V *>(dst + e0) = x[i];
+        if (second) *reinterpret_cast<V *>(dst + e1) = y[i];
+      }
+    }
+  }
+}
+
+// Widest vector (elements) that every row start, stride and unit edge allows.
+static int rope_vec(const RopeArgs &a, int el) {
+  const long long strides[] = {a.q_stride, a.k_stride, a.v_stride};
+  const void *ptrs[] = {a.q_out, a.kc, a.vc, a.q, a.k, a.v};
+  for (int vec = 16 / el; vec > 1; vec >>= 1) {
+    if (a.D % vec || a.pairs % vec) continue;
+    bool ok = true;
+    for (long long s : strides) ok = ok && s % vec == 0;
+    for (const void *p : ptrs) ok = ok && reinterpret_cast<uintptr_t>(p) % (vec * el) == 0;
+    if (ok) return vec;
+  }
+  return 1;
+}
+
+template <typename T, int VEC>
+static pkv_status launch_rope_v(RopeArgs &a, cudaStream_t stream) {
+  const int units = a.pairs / VEC + (a.D - 2 * a.pairs + 2 * VEC - 1) / (2 * VEC);
+  const int hpw = units >= 32 ? 1 : 32 / units;
+  const int groups = (a.H + 2 * a.KVH + hpw - 1) / hpw;   // warp-wide groups of heads of a token
+  // few tokens: spread a token's heads over warps until the GPU holds about
+  // 16 warps an SM; many: one warp walks all heads and reads its angles once
+  const long long want = (152LL * 16 + a.T - 1) / a.T;
+  a.wpt = (int)(want < 1 ? 1 : want > groups ? groups : want);
+  const long long blocks = (a.T * a.wpt + kRopeWarps - 1) / kRopeWarps;
+  if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  pkv_rope_write_kernel<T, VEC><<<(unsigned)blocks, 32 * kRopeWarps, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <typename T>
+static pkv_status launch_rope_t(RopeArgs &a, cudaStream_t stream) {
+  switch (rope_vec(a, (int)sizeof(T))) {
+    case 8:
+      if constexpr (sizeof(T) == 2) return launch_rope_v<T, 8>(a, stream);
+    case 4: return launch_rope_v<T, 4>(a, stream);
+    case 2: return launch_rope_v<T, 2>(a, stream);
+  }
+  return launch_rope_v<T, 1>(a, stream);
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" PKV_API pkv_status pkv_rope_write(
+    void *q_out, void *k_cache, void *v_cache, const void *q, const void *k, const void *v,
+    const float *cos_sin, const int32_t *positions, const uint8_t *pair_axis,
+    const int64_t *slot_mapping, int64_t num_tokens, int64_t q_token_stride,
+    int64_t k_token_stride, int64_t v_token_stride, int64_t positions_stride, int num_axes, int H,
+    int num_kv_heads, int head_dim, int rot_dim, int interleaved, int64_t max_position,
+    int64_t num_blocks, int block_size, pkv_dtype dt, int *err_flags, pkv_stream_t stream) {
+  if (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16) return PKV_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_tokens > 0x7fffffffLL || num_blocks < 0 || num_blocks > 0x7fffffffLL ||
+      block_size <= 0 || H <= 0 || H > 65535 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+      head_dim <= 0 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 || num_axes < 1 ||
+      num_axes > 4 || max_position < 0 || positions_stride < 0 ||
+      (num_axes > 1 && positions_stride < num_tokens))
+    return PKV_ERR_INVALID_ARG;
+  if (head_dim > 512) return PKV_ERR_UNSUPPORTED;
+  if (q_token_stride < (int64_t)H * head_dim || k_token_stride < (int64_t)num_kv_heads * head_dim ||
+      v_token_stride < (int64_t)num_kv_heads * head_dim ||
+      (q_out == q && q_token_stride != (int64_t)H * head_dim))
+    return PKV_ERR_INVALID_ARG;
+  RopeArgs a = {};
+  for (int j = 0; pair_axis && j < rot_dim / 2; ++j) {
+    if (pair_axis[j] >= num_axes) return PKV_ERR_INVALID_ARG;
+    a.axis2[j >> 4] |= (uint32_t)pair_axis[j] << (2 * (j & 15));
+  }
+  if (num_tokens == 0) return PKV_OK;
+  if (!q_out || !k_cache || !v_cache || !q || !k || !v || !positions || !slot_mapping ||
+      (rot_dim > 0 && !cos_sin))
+    return PKV_ERR_INVALID_ARG;
+  const uintptr_t el = dt == PKV_F32 ? 4 : 2;
+  const void *ptrs[] = {q_out, k_cache, v_cache, q, k, v};
+  for (const void *p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % el) return PKV_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(cos_sin) % 4 || reinterpret_cast<uintptr_t>(positions) % 4 ||
+      reinterpret_cast<uintptr_t>(err_flags) % 4 || reinterpret_cast<uintptr_t>(slot_mapping) % 8)
+    return PKV_ERR_INVALID_ARG;
+  a.q_out = static_cast<char *>(q_out);
+  a.kc = static_cast<char *>(k_cache);
+  a.vc = static_cast<char *>(v_cache);
+  a.q = static_cast<const char *>(q);
+  a.k = static_cast<const char *>(k);
+  a.v = static_cast<const char *>(v);
+  a.cos_sin = cos_sin;
+  a.pos = positions;
+  a.slots = slot_mapping;
+  a.err = err_flags;
+  a.T = num_tokens;
+  a.q_stride = q_token_stride;
+  a.k_stride = k_token_stride;
+  a.v_stride = v_token_stride;
+  a.pos_stride = positions_stride;
+  a.max_pos = max_position;
+  a.capacity = num_blocks * block_size;
+  a.axes = num_axes;
+  a.H = H;
+  a.KVH = num_kv_heads;
+  a.D = head_dim;
+  a.pairs = rot_dim / 2;
+  a.interleaved = interleaved != 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (dt) {
+    case PKV_F32: return launch_rope_t<float>(a, s);
+    case PKV_BF16: return launch_rope_t<__nv_bfloat16>(a, s);
+    case PKV_F16: return launch_rope_t<__half>(a, s);
+  }
+  return PKV_ERR_INVALID_ARG;
+}

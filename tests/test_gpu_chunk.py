@@ -1,0 +1,331 @@
+"""pkv_chunk_attention on the GPU against its 64-bit restatement.
+
+Tolerance.  Products of 16-bit inputs are exact in fp32 and summed in fp32;
+the weights are rounded to the input type before the second product (relative
+eps / 2 each), the result once (eps / 2).  An output is a mean of values with
+weights w that sum to 1, so rounding the weights moves it by at most
+eps / 2 * sum(w |v|) <= eps / 2 * max|v|, and the output's rounding by
+eps / 2 * |o|.  Scores t (log2 units, |t| <= 64 here) carry a few fp32
+roundings: 2^-20 covers their effect on a weight.  Hence
+|got - want| <= (eps + 2^-18) * max|v| over the values, |o| <= max|v|;
+for fp32, where sums run over up to a few thousand terms, 2^-17 * max|v|."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_67_gb300 as pkv
+from step_reference import chunk
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda")
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def case(seed, lens, qlens, H, KVH, D, bs, dtype, gain=2.0, poison=True):
+    """Shuffled blocks, garbage tails, NaN in every cache row behind a context."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // bs) for n in lens]
+    nb = sum(need) + 3
+    perm = torch.randperm(nb, generator=g).to(torch.int32)
+    tables = torch.full((len(lens), max(need + [1]) + 2), 99999, dtype=torch.int32)
+    k = torch.randn(nb, bs, KVH, D, generator=g).to(dtype)
+    v = torch.randn(nb, bs, KVH, D, generator=g).to(dtype)
+    at, used = 0, torch.zeros(nb, bs, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        tables[b, :need[b]] = perm[at:at + need[b]]
+        for t in range(0, n, bs):
+            used[int(perm[at + t // bs]), :min(bs, n - t)] = True
+        at += need[b]
+    if poison:
+        k[~used] = float("nan")
+        v[~used] = float("nan")
+    cu = torch.tensor([0] + qlens).cumsum(0).to(torch.int32)
+    q = (torch.randn(int(cu[-1]), H, D, generator=g) * gain).to(dtype)
+    return dict(q=q, k=k, v=v, tables=tables, cu=cu, lens=torch.tensor(lens, dtype=torch.int32), scale=1.0 / math.sqrt(D))
+
+
+def run(c, max_q_len=0, max_context_len=0, partition_size=0, ws=None, stream=None, out=None, **form):
+    d = lambda t: None if t is None else t.to(DEV)
+    q = d(c["q"])
+    total, H, D = q.shape
+    B, MB = c["tables"].shape
+    _, bs, KVH, _ = c["k"].shape
+    if out is None:
+        out = torch.full_like(q, 7.0)
+    if ws is None:
+        ws = pkv.ChunkWorkspace(B, total, H, KVH, D, bs, MB, max_q_len, max_context_len, partition_size)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.pkv_chunk_attention(out, q, d(c["k"]), d(c["v"]), d(c["tables"]), d(c["cu"]), d(c["lens"]), c["scale"],
+                            max_q_len=max_q_len, max_context_len=max_context_len, partition_size=partition_size,
+                            workspace=ws, err_flags=err, stream=stream, **{k: d(v) if torch.is_tensor(v) else v for k, v in form.items()})
+    torch.cuda.synchronize()
+    assert not ws.buffer[:65536 * 4].any(), "counters are zero between calls"
+    return out.cpu(), int(err)
+
+
+def reference(c, softcap=0.0, window=0, slopes=None, prefix_lens=None, kv_starts=None):
+    return chunk(c["q"], c["k"], c["v"], c["tables"], c["cu"], c["lens"], c["scale"], softcap, window, slopes, prefix_lens, kv_starts)
+
+
+def close(got, want, c, what=""):
+    dt = c["q"].dtype
+    vmax = c["v"].double().abs().nan_to_num(0.0, 0.0, 0.0).max()
+    tol = (2.0 ** -17 if dt == F32 else torch.finfo(dt).eps + 2.0 ** -18) * vmax
+    assert torch.equal(got.isnan(), want.isnan()), f"{what}: NaN at other places"
+    off = (got.double() - want).abs().nan_to_num(0.0)
+    assert off.max() <= tol, f"{what}: {off.max().item():.3e} > {tol.item():.3e} at {(off == off.max()).nonzero()[0].tolist()}"
+
+
+def slopes_of(H):
+    return torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)])
+
+
+def forms(c, seed=0):
+    """Every score form, and all of them at once."""
+    g = torch.Generator().manual_seed(seed)
+    H, total, B = c["q"].shape[1], c["q"].shape[0], len(c["lens"])
+    n = int(c["lens"].max()) if B else 1
+    starts = torch.zeros(total, dtype=torch.int32)
+    for b in range(B):
+        r0, r1 = int(c["cu"][b]), int(c["cu"][b + 1])
+        p = torch.arange(int(c["lens"][b]) - (r1 - r0), int(c["lens"][b]))
+        size = int(torch.randint(1, max(2, int(c["lens"][b])), (1,), generator=g))
+        starts[r0:r1] = (p // size * size).to(torch.int32)
+    prefix = torch.randint(0, n + 2, (B,), generator=g, dtype=torch.int32)
+    return [{}, {"softcap": 15.0}, {"slopes": slopes_of(H)}, {"window": 1}, {"window": max(1, n // 3)},
+            {"prefix_lens": prefix}, {"kv_starts": starts},
+            {"softcap": 4.0, "slopes": slopes_of(H), "window": max(1, n // 2), "prefix_lens": prefix, "kv_starts": starts}]
+
+
+def check(c, what="", partition_size=0, **form):
+    got, err = run(c, partition_size=partition_size, **form)
+    assert err == 0, f"{what}: flags {err:#x}"
+    close(got, reference(c, **form), c, what)
+
+
+# (dtype, H, KVH, D, block size): each kernel, grouped heads, odd sizes
+SHAPES = [(F32, 4, 2, 64, 16), (F32, 7, 1, 80, 5), (F32, 2, 2, 130, 1), (F32, 3, 3, 512, 16), (BF, 5, 1, 72, 16),
+          (HF, 4, 2, 64, 24), (BF, 8, 2, 64, 16), (BF, 8, 2, 128, 16), (HF, 4, 1, 128, 32), (BF, 7, 1, 128, 16),
+          (HF, 6, 2, 64, 64), (BF, 12, 1, 128, 16), (HF, 4, 4, 192, 16), (BF, 8, 1, 256, 32), (HF, 16, 1, 256, 16),
+          (BF, 32, 1, 64, 16), (BF, 40, 2, 128, 16)]
+
+
+@pytest.mark.parametrize("dtype,H,KVH,D,bs", SHAPES)
+def test_decode_forms(dtype, H, KVH, D, bs):
+    c = case(D + H, [1, 2, 15, 16, 17, 100, 127, 129, 300], [1] * 9, H, KVH, D, bs, dtype)
+    for f in forms(c, 1):
+        check(c, f"{sorted(f)}", **f)
+        check(c, f"{sorted(f)} split", partition_size=128, **f)
+
+
+@pytest.mark.parametrize("dtype,H,KVH,D,bs", SHAPES)
+def test_chunk_forms(dtype, H, KVH, D, bs):
+    c = case(D * 3 + H, [1, 40, 33, 200, 129, 260], [1, 3, 33, 150, 64, 17], H, KVH, D, bs, dtype)
+    for f in forms(c, 2):
+        check(c, f"{sorted(f)}", **f)
+        check(c, f"{sorted(f)} split", partition_size=128, **f)
+
+
+@pytest.mark.parametrize("dtype,H,KVH,D", [(BF, 8, 2, 128), (BF, 4, 4, 64), (HF, 8, 1, 256), (F32, 4, 2, 64)])
+def test_drafts_over_long_contexts_split_automatically(dtype, H, KVH, D):
+    lens = [5000, 130, 3001]
+    c = case(D, lens, [4, 2, 7], H, KVH, D, 16, dtype)
+    assert pkv.pkv_chunk_plan(3, 13, H, KVH, D, 16, c["tables"].shape[1], 0, 0, 0, False, 0, dtype)[1] > 1
+    for f in ({"softcap": 20.0}, {"slopes": slopes_of(H)}, {"window": 700}):
+        check(c, f"{sorted(f)}", **f)
+
+
+@pytest.mark.parametrize("dtype,H,KVH,D", [(BF, 4, 2, 128), (HF, 2, 2, 64), (BF, 3, 1, 128)])
+def test_long_chunks(dtype, H, KVH, D):
+    """Many row tiles and keys per tile edge: whole prompts and chunks on a prefix."""
+    c = case(D + 1, [900, 1300, 513], [900, 257, 512], H, KVH, D, 16, dtype)
+    for f in forms(c, 3):
+        check(c, f"{sorted(f)}", **f)
+
+
+def test_large_scores_and_cap():
+    """Scores far past the cap: tanh saturates, the softmax stays exact."""
+    for dtype, D in ((BF, 128), (F32, 64), (HF, 256)):
+        c = case(7, [300, 64], [20, 1], 4, 2, D, 16, dtype, gain=12.0)
+        for cap in (1.0, 8.0, 30.0):
+            check(c, f"cap {cap}", softcap=cap)
+
+
+def test_equal_scores_average_the_values():
+    """q = 0: every visible key weighs the same, with and without a cap."""
+    c = case(8, [77, 500], [5, 130], 4, 2, 128, 16, BF)
+    c["q"].zero_()
+    check(c, "zero")
+    check(c, "zero, capped", softcap=3.0)
+    check(c, "zero, window", window=64)
+
+
+@pytest.mark.parametrize("dtype,H,KVH,D", [(F32, 4, 2, 64), (BF, 4, 2, 128), (HF, 16, 1, 256), (BF, 4, 1, 64)])
+@pytest.mark.parametrize("qlen", [1, 3, 70])
+def test_rows_that_see_nothing_are_zero(dtype, H, KVH, D, qlen):
+    """Starts behind the query's position: zeros, next to rows that see keys."""
+    c = case(9, [90, 300], [qlen, qlen], H, KVH, D, 16, dtype)
+    starts = torch.zeros(2 * qlen, dtype=torch.int32)
+    starts[::2] = 1000
+    for part in (0, 128):
+        got, err = run(c, kv_starts=starts, partition_size=part)
+        assert err == 0 and not got[::2].any()
+        close(got, reference(c, kv_starts=starts), c)
+        starts_all = torch.full_like(starts, 2 ** 31 - 1)
+        got, err = run(c, kv_starts=starts_all, partition_size=part)
+        assert err == 0 and not got.any()
+
+
+@pytest.mark.parametrize("dtype,H,KVH,D", [(F32, 4, 2, 64), (BF, 4, 2, 128), (HF, 16, 1, 256), (BF, 4, 1, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("qlen", [1, 6, 150])
+def test_what_a_row_does_not_see_never_reaches_it(dtype, H, KVH, D, bad, qlen):
+    """Non-finite keys and values behind a window, in another document or at a
+    later position leave every row that does not see them as it was."""
+    c = case(10, [260, 400], [qlen, qlen], H, KVH, D, 16, dtype)
+    form = {"window": 100, "kv_starts": torch.randint(0, 300, (2 * qlen,), generator=torch.Generator().manual_seed(1), dtype=torch.int32)}
+    clean = reference(c, **form)
+    for b, n in enumerate((260, 400)):
+        for t in (0, 37, n - 140, n - 3, n - 1):
+            blk = int(c["tables"][b, t // 16])
+            c["k"][blk, t % 16] = bad
+            c["v"][blk, t % 16] = bad
+    want = reference(c, **form)
+    got, err = run(c, **form)
+    assert err == 0
+    untouched = want.isfinite().all(-1) & (want == clean).all(-1)
+    assert untouched.any() or qlen == 1
+    g, w = got[untouched], want[untouched]
+    vmax = c["v"].double().abs().nan_to_num(0.0, 0.0, 0.0).max()
+    tol = (2.0 ** -17 if dtype == F32 else torch.finfo(dtype).eps + 2.0 ** -18) * vmax
+    assert (g.double() - w).abs().max() <= tol if g.numel() else True
+    # rows that do see one are not finite either
+    assert not got[~untouched].isfinite().all(-1).any() if (~untouched).any() and bad != float("-inf") else True
+
+
+def test_blocks_outside_the_window_are_not_read():
+    """Freed blocks' table entries may be garbage once no query sees them."""
+    for dtype, D in ((BF, 128), (F32, 64), (HF, 256)):
+        c = case(11, [500, 333], [4, 40], 4, 2, D, 16, dtype)
+        want = reference(c, window=64)
+        for b, (n, q) in enumerate(((500, 4), (333, 40))):
+            first = max(0, n - q - 64 + 1) // 16
+            c["tables"][b, :first] = torch.tensor([-5, 123456] * 40, dtype=torch.int32)[:first]
+        got, err = run(c, window=64)
+        assert err == 0
+        close(got, want, c)
+
+
+def test_prefix_mask_sees_ahead():
+    """Whole prompts whose first tokens see one another (an image, a prefix)."""
+    for dtype, H, KVH, D in ((BF, 4, 2, 128), (F32, 2, 1, 64), (HF, 4, 1, 256)):
+        c = case(12, [300, 70, 140], [300, 70, 5], H, KVH, D, 16, dtype)
+        for prefix in ([0, 0, 0], [150, 70, 140], [10 ** 9, -4, 139]):
+            pl = torch.tensor(prefix, dtype=torch.int32)
+            check(c, f"{prefix}", prefix_lens=pl)
+            check(c, f"{prefix} window", prefix_lens=pl, window=33, slopes=slopes_of(H))
+
+
+def test_rows_behind_the_last_sequence_and_padding():
+    """Padded requests (no queries, no context) and rows behind cu[B]."""
+    for dtype, D in ((BF, 128), (F32, 64), (BF, 256)):
+        c = case(13, [50, 0, 200, 0], [3, 0, 90, 0], 4, 2, D, 16, dtype)
+        c["q"] = torch.cat([c["q"], torch.full((5, 4, D), float("nan"), dtype=dtype)])
+        got, err = run(c, softcap=9.0)
+        assert err == 0 and (got[93:] == 7).all()
+        close(got[:93], reference(c, softcap=9.0)[:93], c)
+        got, err = run(c, softcap=9.0, max_q_len=90, max_context_len=200)
+        assert err == 0
+        close(got[:93], reference(c, softcap=9.0)[:93], c)
+
+
+def test_flags():
+    for dtype, D in ((BF, 128), (F32, 64), (HF, 256)):
+        c = case(14, [50, 200], [3, 90], 4, 2, D, 16, dtype)
+        want = reference(c)
+        good = {**c, "lens": torch.tensor([2, 200], dtype=torch.int32)}     # fewer tokens than queries
+        got, err = run(good)
+        assert err == pkv.FLAG_QUERY_LEN
+        close(got[3:], want[3:], c)
+        got, err = run({**c, "lens": torch.tensor([50, 10 ** 6], dtype=torch.int32)})
+        assert err == pkv.FLAG_QUERY_LEN
+        close(got[:3], want[:3], c)
+        got, err = run(c, max_q_len=80)
+        assert err == pkv.FLAG_QUERY_OVER_HINT
+        close(got[:3], want[:3], c)
+        got, err = run(c, max_context_len=150)
+        assert err == pkv.FLAG_CONTEXT_OVER_HINT
+        close(got[:3], want[:3], c)
+        t = c["tables"].clone()
+        t[0, 1] = 10 ** 6
+        got, err = run({**c, "tables": t})
+        assert err == pkv.FLAG_BLOCK_OUT_OF_RANGE
+        close(got[3:], want[3:], c)
+
+
+def test_plain_form_agrees_with_decode_and_prefill():
+    """Without any score form: decode and causal prefill, as offered already."""
+    c = case(15, [300, 17, 129], [1, 1, 1], 8, 2, 128, 16, BF, poison=False)
+    d = lambda t: t.to(DEV)
+    got, _ = run(c)
+    out = torch.empty_like(d(c["q"]))
+    ws = pkv.DecodeWorkspace(3, 8, 2, 128, 16, c["tables"].shape[1])
+    pkv.pkv_decode_attention(out, d(c["q"]), d(c["k"]), d(c["v"]), d(c["tables"]), d(c["lens"]), c["scale"], workspace=ws)
+    close(got, out.cpu().double(), c)
+    c = case(16, [300, 17, 129], [300, 5, 129], 8, 2, 128, 16, BF, poison=False)
+    got, _ = run(c)
+    out = torch.empty_like(d(c["q"]))
+    pkv.pkv_prefill_attention(out, d(c["q"]), d(c["k"]), d(c["v"]), d(c["tables"]), d(c["cu"]), d(c["lens"]), c["scale"])
+    close(got, out.cpu().double(), c)
+
+
+def test_one_workspace_for_calls_of_different_shapes():
+    """A workspace sized for the largest of a loop's shapes serves them all."""
+    cs = [case(17, [3000, 900], [2, 1], 8, 2, 128, 16, BF), case(18, [400] * 3, [100, 1, 64], 8, 2, 128, 16, BF),
+          case(19, [2000], [5], 16, 1, 256, 16, HF), case(20, [700, 5], [1, 1], 4, 2, 64, 16, F32)]
+    big = max((pkv.ChunkWorkspace(len(c["lens"]), c["q"].shape[0], c["q"].shape[1], c["k"].shape[2], c["q"].shape[2], 16,
+                                  c["tables"].shape[1], 0, 0, 128) for c in cs), key=lambda w: w.nbytes)
+    for _ in range(2):
+        for c in cs:
+            got, err = run(c, ws=big, partition_size=128, softcap=20.0)
+            assert err == 0
+            close(got, reference(c, softcap=20.0), c)
+
+
+def test_streams_and_graphs():
+    """Two streams with workspaces of their own, and a captured call replayed
+    with other inputs and lengths."""
+    c = case(21, [2500, 700], [3, 4], 8, 2, 128, 16, BF)
+    want = reference(c, softcap=20.0)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got, err = run(c, softcap=20.0, stream=s)
+    assert err == 0
+    close(got, want, c)
+    for qlens, maxq in (([3, 4], 8), ([100, 90], 128)):
+        c = case(22, [2500, 700], qlens, 8, 2, 128, 16, BF)
+        d = {k: c[k].to(DEV) for k in ("q", "k", "v", "tables", "cu", "lens")}
+        out = torch.zeros_like(d["q"])
+        ws = pkv.ChunkWorkspace(2, out.shape[0], 8, 2, 128, 16, d["tables"].shape[1], maxq)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            pkv.pkv_chunk_attention(out, d["q"], d["k"], d["v"], d["tables"], d["cu"], d["lens"], c["scale"], softcap=20.0,
+                                    max_q_len=maxq, workspace=ws, err_flags=err, stream=s)
+        for lens in ([2500, 700], [900, 120]):
+            c["lens"] = torch.tensor(lens, dtype=torch.int32)
+            d["lens"].copy_(c["lens"])
+            out.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert int(err) == 0
+            close(out.cpu(), reference(c, softcap=20.0), c, f"{lens}")
+
+
+def test_results_repeat_bit_by_bit():
+    for dtype, D, q in ((BF, 128, [3, 5]), (BF, 128, [200, 100]), (HF, 256, [2, 2]), (F32, 64, [20, 3])):
+        c = case(23, [1500, 400], q, 8, 2, D, 16, dtype)
+        a, b = (run(c, softcap=10.0, partition_size=128)[0] for _ in range(2))
+        assert torch.equal(a, b)

@@ -1,0 +1,147 @@
+"""The step operators on the CPU: what their C entry points refuse before any
+CUDA call, the chunk plan and workspace sizes, and the binding's checks."""
+import ctypes
+
+import pytest
+import torch
+
+from paged_kv_cache_67_gb300 import build as libbuild
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 4
+FAKE = 1 << 20  # an aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    libbuild.build()
+    import paged_kv_cache_67_gb300 as m
+    m.load_library()
+    return m
+
+
+def _step(lib, **kw):
+    names = ("tables", "held", "held_out", "free", "count", "count_out", "cached", "new", "lens", "cu", "slots", "pos")
+    ptr = {n: FAKE + (i << 24) for i, n in enumerate(names)}
+    ptr.update({k: v for k, v in kw.items() if k in names})
+    return lib.pkv_build_step(*[ptr[n] for n in names], kw.get("B", 4), kw.get("mb", 8), kw.get("nb", 64),
+                              kw.get("bs", 16), kw.get("cap", 64), kw.get("T", 32), kw.get("err"), None)
+
+
+def test_build_step_refusals(pkv):
+    lib = pkv.load_library()
+    assert _step(lib, B=0, T=0) == OK
+    for bad in ({"B": -1}, {"mb": -1}, {"nb": -1}, {"bs": 0}, {"cap": -1}, {"T": -1}, {"nb": 1 << 31}):
+        assert _step(lib, **bad) == INVALID, bad
+    assert _step(lib, B=16385) == UNSUPPORTED
+    assert _step(lib, T=1 << 30) == UNSUPPORTED
+    for name in ("tables", "held", "held_out", "free", "count", "count_out", "cached", "new", "lens", "cu", "slots",
+                 "pos"):
+        assert _step(lib, **{name: None}) == INVALID, name
+        assert _step(lib, **{name: FAKE + 2}) == INVALID, name
+    assert _step(lib, slots=FAKE + (20 << 24) + 4) == INVALID       # int64, 4-byte aligned only
+    # overlaps: an output inside another argument, or an in-place pair that is shifted
+    assert _step(lib, lens=FAKE + (7 << 24)) == INVALID             # context_lens on new_lens
+    assert _step(lib, held_out=FAKE + (1 << 24) + 4) == INVALID     # held_out one entry into held
+    assert _step(lib, cu=FAKE + (6 << 24)) == INVALID
+    assert _step(lib, pos=FAKE + (10 << 24) + 64) == INVALID
+
+
+def _rope(lib, **kw):
+    D, H, KVH = kw.get("D", 64), kw.get("H", 4), kw.get("KVH", 2)
+    axis = kw.get("axis")
+    arr = None if axis is None else (ctypes.c_uint8 * len(axis))(*axis)
+    return lib.pkv_rope_write(
+        kw.get("q_out", FAKE), kw.get("kc", FAKE), kw.get("vc", FAKE), kw.get("q", FAKE + 4096), kw.get("k", FAKE),
+        kw.get("v", FAKE), kw.get("cs", FAKE), kw.get("pos", FAKE), arr, kw.get("slots", FAKE), kw.get("T", 3),
+        kw.get("qs", H * D), kw.get("ks", KVH * D), kw.get("vs", KVH * D), kw.get("ps", 3), kw.get("axes", 1), H, KVH,
+        D, kw.get("rot", 64), 0, kw.get("maxp", 128), kw.get("nb", 8), kw.get("bs", 16), kw.get("dt", 1), None, None)
+
+
+def test_rope_write_refusals(pkv):
+    lib = pkv.load_library()
+    assert _rope(lib, T=0) == OK
+    for bad in ({"T": -1}, {"T": 1 << 31}, {"D": 0, "rot": 0}, {"rot": 63}, {"rot": 66}, {"rot": -2}, {"axes": 0},
+                {"axes": 5}, {"maxp": -1}, {"nb": -1}, {"bs": 0}, {"H": 0}, {"KVH": 0}, {"dt": 7}, {"qs": 255},
+                {"ks": 127}, {"vs": 127}, {"axes": 3, "ps": 2}, {"axis": [0] * 31 + [1]}, {"q_out": None},
+                {"kc": None}, {"vc": None}, {"q": None}, {"k": None}, {"v": None}, {"cs": None}, {"pos": None},
+                {"slots": None}, {"q": FAKE + 1}, {"cs": FAKE + 2}, {"pos": FAKE + 2}, {"slots": FAKE + 4},
+                {"q_out": FAKE + 4096, "qs": 512}):
+        assert _rope(lib, **bad) == INVALID, bad
+    assert _rope(lib, D=513, rot=64) == UNSUPPORTED
+
+
+def _chunk(lib, **kw):
+    g = kw.get
+    return lib.pkv_chunk_attention(
+        g("out", FAKE), g("q", FAKE), g("kc", FAKE), g("vc", FAKE), g("tables", FAKE), g("cu", FAKE), g("lens", FAKE),
+        g("slopes"), g("prefix"), g("starts"), g("B", 2), g("total", 6), g("H", 4), g("KVH", 2), g("D", 64),
+        g("bs", 16), g("mb", 4), g("nb", 8), ctypes.c_float(0.1), ctypes.c_float(g("cap", 0.0)), g("window", 0),
+        g("dt", 1), g("max_q", 0), g("max_n", 0), g("P", 0), g("ws"), g("wsb", 0), None, None)
+
+
+def test_chunk_refusals(pkv):
+    lib = pkv.load_library()
+    assert _chunk(lib, B=0) == OK and _chunk(lib, total=0) == OK
+    for bad in ({"B": -1}, {"B": 65536}, {"total": -1}, {"H": 3}, {"KVH": 0}, {"D": 0}, {"bs": 0}, {"mb": -1},
+                {"nb": -1}, {"cap": -1.0}, {"cap": float("nan")}, {"cap": float("inf")}, {"window": -1}, {"dt": 5},
+                {"max_q": -1}, {"max_n": -1}, {"P": 64}, {"P": -128}, {"out": None}, {"q": None}, {"kc": None},
+                {"vc": None}, {"tables": None}, {"cu": None}, {"lens": None}, {"q": FAKE + 1}, {"slopes": FAKE + 2},
+                {"prefix": FAKE + 2}, {"starts": FAKE + 1}, {"tables": FAKE + 2}):
+        assert _chunk(lib, **bad) == INVALID, bad
+    assert _chunk(lib, D=513) == UNSUPPORTED
+    assert _chunk(lib) == WORKSPACE                               # none given
+    need = pkv.pkv_chunk_workspace_size(2, 6, 4, 2, 64, 16, 4)
+    assert _chunk(lib, ws=FAKE, wsb=1024) == WORKSPACE            # too small
+    assert _chunk(lib, ws=FAKE + 128, wsb=need) == WORKSPACE      # misaligned
+
+
+def test_chunk_plan_and_workspace(pkv):
+    size, plan = pkv.pkv_chunk_workspace_size, pkv.pkv_chunk_plan
+    assert size(2, 6, 3, 2, 64, 16, 4) == 0                       # H % KVH
+    assert size(2, 6, 4, 2, 64, 16, 4, 0, 0, 100) == 0            # partition not a multiple of 128
+    assert plan(2, 6, 3, 2, 64, 16, 4)[0] == 0
+    front = 65536 * 4
+    for dt in (torch.bfloat16, torch.float32):
+        for B, q, H, KVH, D, bs, mb in ((1, 1, 8, 1, 64, 16, 2048), (64, 64, 32, 8, 128, 16, 256), (3, 700, 6, 2, 80, 24, 99),
+                                        (8, 8 * 4, 32, 8, 128, 16, 2048), (1, 8192, 32, 8, 128, 16, 512)):
+            for window in (0, 1, 100, 1000, 5000):
+                for part in (0, 128, 1024):
+                    for max_q in (0, -(-q // B)):
+                        P, parts, kernel = plan(B, q, H, KVH, D, bs, mb, max_q, 0, window, False, part, dt)
+                        assert P % 128 == 0 and (part == 0 or P <= part) and 1 <= parts <= max(64, -(-bs * mb // P))
+                        # every part a unit can touch has a place
+                        mq = max_q or q
+                        span = min(bs * mb, window + mq + 15) if window else bs * mb
+                        assert parts == -(-span // P)
+                        assert part == 0 or P == min(part, -(-span // 128) * 128)
+                        rows = q * H
+                        al = lambda x: (x + 255) // 256 * 256
+                        need = front + (0 if parts == 1 else 2 * al(rows * parts * 4) + rows * parts * D * 4)
+                        assert size(B, q, H, KVH, D, bs, mb, max_q, 0, part) >= need
+
+
+def test_binding_refuses_before_any_call(pkv):
+    """Wrong shapes, types and devices raise ValueError on the host."""
+    z = lambda *s, dt=torch.int32: torch.zeros(*s, dtype=dt)
+    args = [z(2, 4), z(2), z(2), z(8), z(1), z(1), z(2), z(2), z(2), z(3), z(6, dt=torch.int64), z(6)]
+    with pytest.raises(ValueError):
+        pkv.pkv_build_step(*args, 8, 16)                          # host tensors
+    for i, wrong in ((0, z(2, 4, dt=torch.int64)), (1, z(3)), (3, z(2, 4)), (4, z(2)), (9, z(2)), (10, z(6)), (11, z(5))):
+        bad = list(args)
+        bad[i] = wrong
+        with pytest.raises(ValueError):
+            pkv.pkv_build_step(*bad, 8, 16)
+    f = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    rope = dict(q_out=f(3, 4, 64), k_cache=f(2, 16, 2, 64), v_cache=f(2, 16, 2, 64), q=f(3, 4, 64), k=f(3, 2, 64),
+                v=f(3, 2, 64), cos_sin=torch.zeros(8, 64), positions=z(3), slot_mapping=z(3, dt=torch.int64))
+    for change in ({}, {"q": f(3, 4, 32)}, {"k": f(2, 2, 64)}, {"q_out": f(3, 4, 64).float()}, {"cos_sin": torch.zeros(8, 66)},
+                   {"cos_sin": torch.zeros(8, 64).double()}, {"positions": z(4)}, {"slot_mapping": z(3)},
+                   {"pair_axis": [0] * 31}, {"pair_axis": [1] * 32}, {"q": f(3, 64, 4).transpose(1, 2)}):
+        with pytest.raises(ValueError):
+            pkv.pkv_rope_write(**{**rope, **change})
+    chunk = dict(out=f(3, 4, 64), q=f(3, 4, 64), k_cache=f(2, 16, 2, 64), v_cache=f(2, 16, 2, 64), block_tables=z(2, 2),
+                 cu_seqlens_q=z(3), context_lens=z(2), scale=0.1)
+    for change in ({}, {"out": f(2, 4, 64)}, {"cu_seqlens_q": z(2)}, {"slopes": torch.zeros(3)}, {"prefix_lens": z(3)},
+                   {"kv_starts": z(2)}, {"block_tables": z(3, 2)}, {"q": f(3, 4, 64).float()}):
+        with pytest.raises(ValueError):
+            pkv.pkv_chunk_attention(**{**chunk, **change})
