@@ -10,7 +10,7 @@
 namespace pkv {
 
 pkv_status launch_chunk_simt(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
-size_t chunk_simt_smem(int D);
+pkv_status launch_chunk_mma(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
 
 // The plan uses the SM count of the one GPU this library is built for, so
 // that the workspace's size needs no device.
@@ -68,11 +68,13 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   if (!chunk_sizes_ok(B, total_q, H, KVH, D, bs, max_blocks, max_q, max_n, partition_size) || window < 0) return false;
   if (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16) return false;
   const long long mq = chunk_max_q(total_q, max_q), cap = chunk_cap(bs, max_blocks, max_n);
-  p->kernel = 0;
+  // 16-bit tensors that TMA can read, in tokens chunks that never span two blocks
+  p->kernel = tc_eligible(dt, D, bs) && aligned16 ? 1 : 0;
   p->chunks = ceil_div(mq * (H / KVH), kChunkRows);
   // a window bounds the keys a unit sees, unless a prefix reaches past it
   const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 15) : cap;
-  chunk_split(parts_wanted((long long)B * KVH * p->chunks, kPlanSms * 4), span, 256, partition_size, p);
+  const int per_sm = p->kernel == 0 ? 4 : D <= 128 ? 2 : 1;   // resident CTAs
+  chunk_split(parts_wanted((long long)B * KVH * p->chunks, kPlanSms * per_sm), span, 256, partition_size, p);
   return true;
 }
 
@@ -183,6 +185,7 @@ PKV_API pkv_status pkv_chunk_attention(
   a.chunks = (int)plan.chunks;
   a.scale_log2 = softcap > 0.f ? scale / softcap : scale * kLog2e;
   a.cap_log2 = softcap * kLog2e;
+  a.scale_y = softcap > 0.f ? 2.f * kLog2e * scale / softcap : scale * kLog2e;
   char *ws = static_cast<char *>(workspace);
   a.ws_cnt = reinterpret_cast<int *>(ws);
   if (plan.max_parts > 1) {
@@ -194,7 +197,9 @@ PKV_API pkv_status pkv_chunk_attention(
     ws += align256(rows * plan.max_parts * sizeof(float));
     a.ws_o = reinterpret_cast<float *>(ws);
   }
-  return launch_chunk_simt(a, dt, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (plan.kernel == 1) return launch_chunk_mma(a, dt, s);
+  return launch_chunk_simt(a, dt, s);
 }
 
 }  // extern "C"

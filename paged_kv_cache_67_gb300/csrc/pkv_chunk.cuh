@@ -48,6 +48,7 @@ struct ChunkArgs {
   int chunks;                    // row chunks per (sequence, KV head): the grid's and the counters'
   float scale_log2;              // scale * log2(e), or with a cap: scale / cap
   float cap_log2;                // 0, or cap * log2(e)
+  float scale_y;                 // scale * log2(e), or with a cap: chunk_capped's 2 log2(e) scale / cap
 };
 
 struct ChunkSeq {
@@ -109,6 +110,138 @@ __device__ __forceinline__ float chunk_score(const ChunkArgs &a, float dot, floa
   if (a.cap_log2 > 0.f) t = a.cap_log2 * chunk_tanh(t);
   if (a.slopes) t = fmaf(-slope_log2, fabsf((float)(p - j)), t);
   return t;
+}
+
+// The capped score of the 16-bit kernels, with y = 2 log2(e) scale / cap
+// (q . k):  cap tanh(x) = cap - 2 cap / (1 + 2^y).  Off by a few 2^-23 of cap,
+// far below what rounding a weight to 16 bits does to it.
+__device__ __forceinline__ float chunk_capped(float y, float cap_log2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(y)));
+  return fmaf(-2.f * cap_log2, r, cap_log2);
+}
+
+// Reference for a running max that may still be -inf (nothing seen yet): with
+// 0 in its place every weight is 2^(-inf) = 0 and not NaN.
+__device__ __forceinline__ float chunk_ref(float m) { return m == -INFINITY ? 0.f : m; }
+
+// One row over keys [t0, t1), all of them visible, key by key on one warp:
+// m, l and the lane's D / 32 columns of the weighted sum, unnormalised.  The
+// tensor-core kernels multiply a whole tile by weights that are 0 for hidden
+// keys; where a hidden value is not finite that gives NaN, and the rows that
+// show one are done again here, from what they see alone.
+template <typename T, int EPL>
+__device__ __noinline__ void chunk_row_exact(const ChunkArgs &a, int b, int kvh, size_t q_row, float slope_log2, int p,
+                                             int t0, int t1, float &m, float &l, float (&o)[EPL]) {
+  const int lane = threadIdx.x & 31;
+  const T *q = reinterpret_cast<const T *>(a.q) + q_row * a.D;
+  float qv[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) {
+    const int d = lane + 32 * e;
+    qv[e] = d < a.D ? to_f32<T>(q[d]) : 0.f;
+    o[e] = 0.f;
+  }
+  m = -INFINITY;
+  l = 0.f;
+  for (int t = t0; t < t1; ++t) {
+    int phys = __ldg(a.tables + (size_t)b * a.max_blocks + t / a.bs);
+    if (phys < 0 || (long long)phys >= a.num_blocks) phys = 0;   // flagged where it was first read
+    const size_t row = (((size_t)phys * a.bs + t % a.bs) * a.KVH + kvh) * a.D;
+    const T *k = reinterpret_cast<const T *>(a.k_cache) + row, *v = reinterpret_cast<const T *>(a.v_cache) + row;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      const int d = lane + 32 * e;
+      if (d < a.D) s = fmaf(qv[e], to_f32<T>(k[d]), s);
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+    const float x = chunk_score(a, s, slope_log2, p, t);
+    const float mn = fmaxf(m, x), ref = chunk_ref(mn);
+    const float c = fast_exp2(m - ref), w = fast_exp2(x - ref);
+    l = fmaf(l, c, w);
+    m = mn;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      const int d = lane + 32 * e;
+      if (d < a.D) o[e] = fmaf(o[e], c, w * to_f32<T>(v[d]));
+    }
+  }
+}
+
+// The end of part `part` of `nparts` of a unit of `rows` rows, by the whole
+// CTA: s_m, s_l, s_o (row r at r * ostride) hold the part's state; row_out(r)
+// is row r's output row; seen(r) says whether it sees any key at all.  One
+// part writes o / l.  Several leave their state in the workspace, and the one
+// that `counter` shows to be last merges:
+//   M = max m_p,  out = sum o_p 2^(m_p - M) / sum l_p 2^(m_p - M).
+// s_scratch: 1 int.
+template <typename T, typename RowOut, typename Seen>
+__device__ void chunk_finish(const ChunkArgs &a, int rows, int part, int nparts, const float *s_m, const float *s_l,
+                             const float *s_o, int ostride, int *s_scratch, int *counter, const RowOut &row_out,
+                             const Seen &seen) {
+  const int tid = threadIdx.x, nthr = blockDim.x, D = a.D, DV = D / 4;
+  T *out = reinterpret_cast<T *>(a.out);
+  auto put4 = [&](size_t row, int d4, float x, float y, float z, float w) {
+    T v[4] = {from_f32<T>(x), from_f32<T>(y), from_f32<T>(z), from_f32<T>(w)};
+    *reinterpret_cast<uint2 *>(out + row * D + 4 * d4) = *reinterpret_cast<const uint2 *>(v);
+  };
+  if (nparts == 1) {
+    for (int i = tid; i < rows * DV; i += nthr) {
+      const int r = i / DV, d4 = i - r * DV;
+      const float4 v = *reinterpret_cast<const float4 *>(s_o + r * ostride + 4 * d4);
+      const float inv = seen(r) ? 1.f / s_l[r] : 0.f;
+      if (seen(r)) put4(row_out(r), d4, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      else put4(row_out(r), d4, 0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  for (int r = tid; r < rows; r += nthr) {
+    const size_t at = row_out(r) * a.max_parts + part;
+    a.ws_m[at] = s_m[r];
+    a.ws_l[at] = s_l[r];
+  }
+  for (int i = tid; i < rows * DV; i += nthr) {
+    const int r = i / DV, d4 = i - r * DV;
+    reinterpret_cast<float4 *>(a.ws_o + (row_out(r) * a.max_parts + part) * D)[d4] =
+        *reinterpret_cast<const float4 *>(s_o + r * ostride + 4 * d4);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int prev;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                 : "=r"(prev)
+                 : "l"(reinterpret_cast<uint64_t>(counter))
+                 : "memory");
+    *s_scratch = prev == nparts - 1;
+  }
+  __syncthreads();
+  if (!*s_scratch) return;
+  for (int i = tid; i < rows * DV; i += nthr) {
+    const int r = i / DV, d4 = i - r * DV;
+    const size_t at = row_out(r) * a.max_parts;
+    float M = -INFINITY;
+#pragma unroll 4
+    for (int p = 0; p < nparts; ++p) M = fmaxf(M, __ldcg(a.ws_m + at + p));
+    const float ref = chunk_ref(M);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < nparts; ++p) {
+      const float w = fast_exp2(__ldcg(a.ws_m + at + p) - ref);
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (at + p) * D) + d4);
+      L = fmaf(__ldcg(a.ws_l + at + p), w, L);
+      acc.x = fmaf(v.x, w, acc.x);
+      acc.y = fmaf(v.y, w, acc.y);
+      acc.z = fmaf(v.z, w, acc.z);
+      acc.w = fmaf(v.w, w, acc.w);
+    }
+    const float inv = 1.f / L;
+    if (seen(r)) put4(row_out(r), d4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else put4(row_out(r), d4, 0.f, 0.f, 0.f, 0.f);
+  }
+  if (tid == 0) *counter = 0;  // ready for the next call
 }
 
 }  // namespace pkv

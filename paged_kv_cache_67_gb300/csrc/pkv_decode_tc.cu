@@ -509,8 +509,8 @@ bool encode_cache_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long lo
 // 1 block, 128-byte swizzle.  A box lands as D / 64 tiles of 16 rows x 128
 // bytes, one after another: the layout of one 4-D box per 64 values, in one
 // copy.
-static bool encode_chunk_map(CUtensorMap *map, const void *cache, pkv_dtype dt,
-                             long long num_blocks, int bs, int KVH, int D) {
+bool encode_chunk_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long long num_blocks,
+                      int bs, int KVH, int D) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t el = 2;

@@ -72,6 +72,11 @@ pkv_status launch_write(void *k_cache, void *v_cache, const void *k, const void 
 bool encode_cache_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long long num_blocks,
                       int bs, int KVH, int D);
 
+// The same cache in 5-D: box of 64 elements x 16 rows x D / 64 blocks of 64 x
+// 1 head x 1 block, so one box is a 16-token chunk of a KV head.
+bool encode_chunk_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long long num_blocks,
+                      int bs, int KVH, int D);
+
 // Tensor map of a [rows, H, D] 16-bit tensor: box of 64 elements x 1 head x
 // box_rows rows, 128-byte swizzle, zero past the last row.
 bool encode_rows_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,
