@@ -11,6 +11,9 @@ namespace pkv {
 
 pkv_status launch_chunk_simt(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
 pkv_status launch_chunk_mma(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
+pkv_status launch_chunk_tc(const ChunkArgs &a, pkv_dtype dt, char *scratch, int sms, cudaStream_t stream);
+long long chunk_tc_items(int B, long long total_q, int H, int G, int max_q);
+size_t chunk_tc_scratch(int B, long long total_q, int G, int max_q, long long parts);
 
 // The plan uses the SM count of the one GPU this library is built for, so
 // that the workspace's size needs no device.
@@ -28,6 +31,16 @@ struct ChunkPlan {
 
 static long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+static bool device_sms(int *sms) {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+  *sms = dev < 64 ? cached[dev] : 0;
+  if (*sms == 0 && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+  if (dev < 64) cached[dev] = *sms;
+  return *sms > 0;
+}
 
 static bool chunk_sizes_ok(int B, int64_t total_q, int H, int KVH, int D, int bs, int max_blocks, int max_q,
                            int max_n, int partition_size) {
@@ -70,17 +83,23 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   const long long mq = chunk_max_q(total_q, max_q), cap = chunk_cap(bs, max_blocks, max_n);
   // 16-bit tensors that TMA can read, in tokens chunks that never span two blocks
   p->kernel = tc_eligible(dt, D, bs) && aligned16 ? 1 : 0;
+  if (p->kernel == 1 && D <= 128 && mq * (H / KVH) > kChunkRows) p->kernel = 2;
   p->chunks = ceil_div(mq * (H / KVH), kChunkRows);
   // a window bounds the keys a unit sees, unless a prefix reaches past it
   const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 15) : cap;
+  if (p->kernel == 2) {
+    chunk_split(parts_wanted(chunk_tc_items(B, total_q, H, H / KVH, (int)mq), kPlanSms), span, 512, partition_size, p);
+    return true;
+  }
   const int per_sm = p->kernel == 0 ? 4 : D <= 128 ? 2 : 1;   // resident CTAs
   chunk_split(parts_wanted((long long)B * KVH * p->chunks, kPlanSms * per_sm), span, 256, partition_size, p);
   return true;
 }
 
 // Workspace bytes of a plan.
-static size_t chunk_ws_bytes(int64_t total_q, int H, int D, long long parts) {
+static size_t chunk_ws_bytes(int kernel, int B, int64_t total_q, int H, int KVH, int D, int max_q, long long parts) {
   size_t bytes = kChunkCnt * sizeof(int);
+  if (kernel == 2) bytes += chunk_tc_scratch(B, total_q, H / KVH, chunk_max_q(total_q, max_q), parts);
   if (parts > 1) {
     const size_t rows = (size_t)total_q * H;
     bytes += 2 * align256(rows * parts * sizeof(float)) + align256(rows * parts * (size_t)D * sizeof(float));
@@ -97,12 +116,12 @@ extern "C" {
 PKV_API size_t pkv_chunk_workspace_size(int B, int64_t total_q, int H, int num_kv_heads, int head_dim, int block_size,
                                         int max_blocks, int max_q_len, int max_context_len, int partition_size) {
   size_t most = 0;
-  for (int dt = 0; dt < 2; ++dt) {   // fp32's kernel and the 16-bit types'
+  for (int dt = 0; dt < 3; ++dt) {   // fp32, 16-bit, and 16-bit tensors that TMA cannot read
     ChunkPlan p;
     if (!chunk_plan(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len, max_context_len, 0, false,
-                    partition_size, (pkv_dtype)dt, true, &p))
+                    partition_size, (pkv_dtype)dt, dt == 1, &p))
       return 0;
-    most = std::max(most, chunk_ws_bytes(total_q, H, head_dim, p.most_parts));
+    most = std::max(most, chunk_ws_bytes(p.kernel, B, total_q, H, num_kv_heads, head_dim, max_q_len, p.most_parts));
   }
   return most;
 }
@@ -149,12 +168,14 @@ PKV_API pkv_status pkv_chunk_attention(
   if (!chunk_plan(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len, max_context_len, window,
                   prefix_lens != nullptr, partition_size, dt, aligned16, &plan))
     return PKV_ERR_INVALID_ARG;
-  const size_t need = chunk_ws_bytes(total_q, H, head_dim, plan.max_parts);
+  const size_t need = chunk_ws_bytes(plan.kernel, B, total_q, H, num_kv_heads, head_dim, max_q_len, plan.max_parts);
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256) return PKV_ERR_WORKSPACE;
   if (plan.chunks * num_kv_heads * plan.max_parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  if (plan.max_parts > 1 && (long long)B * num_kv_heads * plan.chunks > kChunkCnt - kChunkCntFirst)
+  if (plan.kernel != 2 && plan.max_parts > 1 && (long long)B * num_kv_heads * plan.chunks > kChunkCnt - kChunkCntFirst)
     return PKV_ERR_UNSUPPORTED;
 
+  int sms = 0;
+  if (!device_sms(&sms)) return PKV_ERR_CUDA;
   ChunkArgs a;
   memset(&a, 0, sizeof a);
   a.out = out;
@@ -188,9 +209,11 @@ PKV_API pkv_status pkv_chunk_attention(
   a.scale_y = softcap > 0.f ? 2.f * kLog2e * scale / softcap : scale * kLog2e;
   char *ws = static_cast<char *>(workspace);
   a.ws_cnt = reinterpret_cast<int *>(ws);
+  ws += kChunkCnt * sizeof(int);
+  char *scratch = ws;
+  if (plan.kernel == 2) ws += chunk_tc_scratch(B, total_q, a.G, a.max_q, plan.max_parts);
   if (plan.max_parts > 1) {
     const size_t rows = (size_t)total_q * H;
-    ws += kChunkCnt * sizeof(int);
     a.ws_m = reinterpret_cast<float *>(ws);
     ws += align256(rows * plan.max_parts * sizeof(float));
     a.ws_l = reinterpret_cast<float *>(ws);
@@ -198,6 +221,7 @@ PKV_API pkv_status pkv_chunk_attention(
     a.ws_o = reinterpret_cast<float *>(ws);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (plan.kernel == 2) return launch_chunk_tc(a, dt, scratch, sms, s);
   if (plan.kernel == 1) return launch_chunk_mma(a, dt, s);
   return launch_chunk_simt(a, dt, s);
 }

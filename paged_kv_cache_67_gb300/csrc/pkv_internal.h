@@ -81,6 +81,10 @@ bool encode_chunk_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long lo
 // box_rows rows, 128-byte swizzle, zero past the last row.
 bool encode_rows_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,
                      int box_rows);
+// The same tensor with box_heads heads in a box: box_rows x box_heads rows of
+// 64 elements, heads of one token next to one another.
+bool encode_packed_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,
+                       int box_heads, int box_rows);
 
 // One-time opt-in to a kernel's dynamic shared memory, per device
 // (`configured` is the kernel's own per-device record).
