@@ -207,6 +207,17 @@ PKV_API pkv_status pkv_chunk_attention(
   a.scale_log2 = softcap > 0.f ? scale / softcap : scale * kLog2e;
   a.cap_log2 = softcap * kLog2e;
   a.scale_y = softcap > 0.f ? 2.f * kLog2e * scale / softcap : scale * kLog2e;
+  // the series' powers of scale / cap have to stay in range, and a running
+  // max commutes with the cap for a positive scale only
+  const double ratio = softcap > 0.f ? (double)scale / softcap : 0.0;
+  a.cap_small = a.cap_mid = -1.f;
+  if (ratio > 1e-4 && ratio < 1e2) {
+    double power = ratio;
+    for (int i = 0; i < 4; ++i, power *= ratio * ratio) a.cap_k[i] = (float)(softcap * 1.4426950408889634 * kTanh4[i] * power);
+    for (int i = 0; i < 6; ++i) a.cap_c[i] = (float)(softcap * 1.4426950408889634 * kTanh6[i]);
+    a.cap_small = (float)(0.5 / ratio);
+    a.cap_mid = (float)(1.0 / ratio);
+  }
   char *ws = static_cast<char *>(workspace);
   a.ws_cnt = reinterpret_cast<int *>(ws);
   ws += kChunkCnt * sizeof(int);

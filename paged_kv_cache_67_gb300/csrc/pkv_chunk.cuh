@@ -48,6 +48,8 @@ struct ChunkArgs {
   int chunks;                    // row chunks per (sequence, KV head): the grid's and the counters'
   float scale_log2;              // scale * log2(e), or with a cap: scale / cap
   float cap_log2;                // 0, or cap * log2(e)
+  float cap_k[4], cap_small;     // chunk_cap_fit: the near series in the raw product, and its range there
+  float cap_c[6], cap_mid;       // the middle one in scale / cap (q . k), times cap * log2(e); its range in the raw product
   float scale_y;                 // scale * log2(e), or with a cap: chunk_capped's 2 log2(e) scale / cap
 };
 
@@ -120,6 +122,13 @@ __device__ __forceinline__ float chunk_capped(float y, float cap_log2) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(y)));
   return fmaf(-2.f * cap_log2, r, cap_log2);
 }
+
+// tanh(x) = x P(x^2) on the FMA pipe: P fitted to tanh(x) / x by reweighted
+// least squares (towards the least maximum), relative error 6e-7 for |x| <= 1/2
+// with 4 terms and 7e-7 for |x| <= 1 with 6.
+constexpr float kTanh4[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222308039665f};
+constexpr float kTanh6[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f,
+                             -0.051605671644210815f, 0.016743112355470657f, -0.0030670592095702887f};
 
 // Reference for a running max that may still be -inf (nothing seen yet): with
 // 0 in its place every weight is 2^(-inf) = 0 and not NaN.

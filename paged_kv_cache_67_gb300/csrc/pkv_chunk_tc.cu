@@ -632,9 +632,37 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           sc[c] = __uint_as_float(sa[c]);
           sc[64 + c] = __uint_as_float(sb[c]);
         }
+        const bool cut = t0 < lo || t0 + kCtTile > hi;   // some of the tile is hidden from the row
+        // Capped scores: |q . k| over the tile picks the way to its tanh.  The
+        // usual tile is near 0, where 4 terms do; without a bias they are
+        // then evaluated inside the exponent, straight from the raw scores.
+        bool fused = false;
+        float mx_raw = -INFINITY;
         if (CAP) {
+          float mn_raw = INFINITY;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) sc[c] = chunk_capped(sc[c] * sl2, a.cap_log2);
+          for (int c = 0; c < 128; c += 2) {
+            mx_raw = max3f(mx_raw, sc[c], sc[c + 1]);
+            mn_raw = min3f(mn_raw, sc[c], sc[c + 1]);
+          }
+          const float far = fmaxf(mx_raw, -mn_raw);
+          fused = !BIAS && __all_sync(0xffffffffu, !cut && far <= a.cap_small);
+          if (!fused && __all_sync(0xffffffffu, far <= a.cap_mid)) {
+            const float2 rt = make_float2(a.scale_log2, a.scale_log2);
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+              const float2 x = fmul2(make_float2(sc[c], sc[c + 1]), rt), z = fmul2(x, x);
+              float2 q = ffma2(z, make_float2(a.cap_c[5], a.cap_c[5]), make_float2(a.cap_c[4], a.cap_c[4]));
+#pragma unroll
+              for (int e = 3; e >= 0; --e) q = ffma2(z, q, make_float2(a.cap_c[e], a.cap_c[e]));
+              q = fmul2(x, q);
+              sc[c] = q.x;
+              sc[c + 1] = q.y;
+            }
+          } else if (!fused) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sc[c] = chunk_capped(sc[c] * sl2, a.cap_log2);
+          }
         } else if (!raw && !BIAS) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) sc[c] *= sl2;
@@ -657,15 +685,20 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             for (int c = 0; c < 128; ++c) sc[c] = fmaf(sc[c], f, -slope * fabsf(away + (float)c));
           }
         }
-        if (t0 < lo || t0 + kCtTile > hi) {
+        if (cut) {
           const int vlo = lo - t0, vhi = hi - t0;
 #pragma unroll
           for (int c = 0; c < 128; ++c) sc[c] = c >= vlo && c < vhi ? sc[c] : -INFINITY;
         }
         float mx = -INFINITY;
+        if (fused) {
+          const float z = mx_raw * mx_raw;
+          mx = mx_raw * fmaf(z, fmaf(z, fmaf(z, a.cap_k[3], a.cap_k[2]), a.cap_k[1]), a.cap_k[0]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) mx = max3f(mx, sc[c], sc[c + 1]);
-        if (raw) mx *= sl2;
+          for (int c = 0; c < 128; c += 2) mx = max3f(mx, sc[c], sc[c + 1]);
+          if (raw) mx *= sl2;
+        }
         // the reference max moves only when the row max exceeds it by 2^8
         const float m_new = (mx > m_used + 8.f) ? mx : m_used;
         const float ref = chunk_ref(m_new);            // nothing seen yet: weights 0, not NaN
@@ -674,20 +707,34 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         l *= alpha;
         m_used = m_new;
         float2 lsum = make_float2(0.f, 0.f);
+        auto weights = [&](const auto &exponent) {       // P = 2^exponent(pair), and its sum
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[32];
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int c2 = 0; c2 < 32; ++c2) {
-            const int c = 64 * hf + 2 * c2;
-            float2 x = raw ? ffma2(make_float2(sc[c], sc[c + 1]), make_float2(mul, mul), make_float2(-ref, -ref))
-                           : fadd2(make_float2(sc[c], sc[c + 1]), make_float2(-ref, -ref));
-            x.x = fast_exp2(x.x);
-            x.y = fast_exp2(x.y);
-            lsum = fadd2(lsum, x);
-            pk[c2] = PackPair<T>::pack(x.x, x.y);
+            for (int c2 = 0; c2 < 32; ++c2) {
+              const int c = 64 * hf + 2 * c2;
+              float2 x = exponent(make_float2(sc[c], sc[c + 1]));
+              x.x = fast_exp2(x.x);
+              x.y = fast_exp2(x.y);
+              lsum = fadd2(lsum, x);
+              pk[c2] = PackPair<T>::pack(x.x, x.y);
+            }
+            tmem_st32u_nowait(tmem_sp + 32 * hf, pk);
           }
-          tmem_st32u_nowait(tmem_sp + 32 * hf, pk);
+        };
+        const float2 nref = make_float2(-ref, -ref);
+        if (CAP && !BIAS && fused) {
+          const float2 k0 = make_float2(a.cap_k[0], a.cap_k[0]), k1 = make_float2(a.cap_k[1], a.cap_k[1]);
+          const float2 k2 = make_float2(a.cap_k[2], a.cap_k[2]), k3 = make_float2(a.cap_k[3], a.cap_k[3]);
+          weights([&](float2 x) {
+            const float2 z = fmul2(x, x);
+            return ffma2(x, ffma2(z, ffma2(z, ffma2(z, k3, k2), k1), k0), nref);
+          });
+        } else if (CAP || BIAS) {
+          weights([&](float2 x) { return fadd2(x, nref); });
+        } else {
+          weights([&](float2 x) { return ffma2(x, make_float2(mul, mul), nref); });
         }
         tmem_wait_st();
         l += lsum.x + lsum.y;
