@@ -64,6 +64,14 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return *reinterpret_cast<float2 *>(&d);
 }
 
+// (x, x) in a register pair that the compiler keeps: as a plain constant it
+// is moved together again before every use when registers are short.
+__device__ __forceinline__ float2 kept_pair(float x) {
+  unsigned long long d;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
 template <typename T>
 struct PackPair;
 template <>

@@ -65,6 +65,25 @@ static long long parts_wanted(long long units, long long slots) {
   return std::min<long long>(kChunkMaxParts, std::max<long long>(1, 2 * slots / std::max<long long>(units, 1)));
 }
 
+// Parts of the persistent tcgen05 kernel's items (256 rows x a part): the
+// number that gives the shortest estimate, in key tiles of 128, of
+//   rounds of items over the SMs x (tiles of a part + 2 to start and end one)
+//   + joining the parts (0.015 a part of an item: its 270 KB to and from
+//   memory against 2.7 us a tile on one SM of 152; 2 for the launch).
+static long long tc_parts_wanted(long long items, long long span) {
+  long long best = 1;
+  double least = 0;
+  for (long long p = 1; p <= kChunkMaxParts && p <= ceil_div(span, 512); ++p) {
+    const double cost = (double)ceil_div(items * p, kPlanSms) * (ceil_div(ceil_div(span, p), 128) + 2) +
+                        (p > 1 ? 0.015 * items * p + 2 : 0.0);
+    if (p == 1 || cost < least) {
+      least = cost;
+      best = p;
+    }
+  }
+  return best;
+}
+
 // `span`: the most keys a unit sees, from its first one's 16-key chunk on
 // (where its first part begins); each part has `min_p` keys or more.
 static void chunk_split(long long wanted, long long span, int min_p, int partition_size, ChunkPlan *p) {
@@ -88,7 +107,9 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   // a window bounds the keys a unit sees, unless a prefix reaches past it
   const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 15) : cap;
   if (p->kernel == 2) {
-    chunk_split(parts_wanted(chunk_tc_items(B, total_q, H, H / KVH, (int)mq), kPlanSms), span, 512, partition_size, p);
+    const long long items = chunk_tc_items(B, total_q, H, H / KVH, (int)mq);
+    // (never more than without a window: the workspace is sized for that)
+    chunk_split(std::min(tc_parts_wanted(items, span), tc_parts_wanted(items, cap)), span, 512, partition_size, p);
     return true;
   }
   const int per_sm = p->kernel == 0 ? 4 : D <= 128 ? 2 : 1;   // resident CTAs

@@ -140,7 +140,7 @@ __device__ __forceinline__ float chunk_ref(float m) { return m == -INFINITY ? 0.
 // keys; where a hidden value is not finite that gives NaN, and the rows that
 // show one are done again here, from what they see alone.
 template <typename T, int EPL>
-__device__ __noinline__ void chunk_row_exact(const ChunkArgs &a, int b, int kvh, size_t q_row, float slope_log2, int p,
+__device__ __forceinline__ void chunk_row_exact(const ChunkArgs &a, int b, int kvh, size_t q_row, float slope_log2, int p,
                                              int t0, int t1, float &m, float &l, float (&o)[EPL]) {
   const int lane = threadIdx.x & 31;
   const T *q = reinterpret_cast<const T *>(a.q) + q_row * a.D;

@@ -7,16 +7,20 @@
 //          tiles) of a sequence x one part of the keys they see, most key
 //          tiles first, so that the long ones start first.
 //   main   persistent, a CTA per SM, claims (unit, head subgroup) items from
-//          a counter; 11 warps as in causal prefill: a scheduler that claims,
-//          works out and publishes items and loads their queries, a producer
-//          that streams the K and V tiles (128 keys), a thread that issues
-//          S = Q K^T and O += P V into tensor memory, and two softmax
-//          warpgroups, one per tile and one row per thread.
+//          a counter; roles as in causal prefill: two softmax warpgroups, one
+//          per tile and one row per thread, a producer that streams the K and
+//          V tiles (128 keys), a thread that issues S = Q K^T and O += P V
+//          into tensor memory, and a scheduler that claims, works out and
+//          publishes items and loads their queries.
 //   merge  (only when the keys are split) joins the parts' (m, l, O).
 // Packing.  With G' the largest power of two that divides the G query heads
 // of a KV head, a tile is 128 / G' queries x G' heads: one TMA box brings it
 // into the tile's row order, a K/V tile serves G' heads at once, and a tile
 // spans fewer positions, so fewer keys are multiplied only to be masked.
+// A unit of one row tile (128 rows or fewer) gives both warpgroups the same
+// rows and every other key tile each: one group's softmax hides behind the
+// other's products, and group 0 joins the two states at the end, reading
+// group 1's O from tensor memory.
 // Units whose keys a window or document mask cuts start at the first key any
 // of their rows sees (its 16-key chunk): tiles before it are never loaded.
 // Values that no row sees are zeroed in the tile; a row that still ends not
@@ -36,8 +40,15 @@ constexpr int kCtRows = 128;     // packed rows per softmax warpgroup (MMA M)
 constexpr int kCtGroups = 2;     // row tiles per item
 constexpr int kCtTile = 128;     // keys per tile
 constexpr int kCtStages = 2;     // K/V ring depth
-constexpr int kCtSched = 2 + 4 * kCtGroups;    // scheduler warp
-constexpr int kCtThreads = 32 * (3 + 4 * kCtGroups);
+constexpr int kCtSoftmaxWarps = 4 * kCtGroups; // warps 0-3, 4-7; then producer, MMA, scheduler and an idle one
+constexpr int kCtThreads = 32 * (kCtSoftmaxWarps + 4);
+// Registers: the launch has 384 x 168 = 64512; the softmax warps take 200
+// each and the others 104 (256 x 200 + 128 x 104 = 64512).  At 216 / 72 the
+// MMA issuer spills (plain scores 1065 TFLOP/s against 1121), at 184 / 136
+// the softmax does.
+constexpr int kCtRegsLaunch = 168, kCtRegsSoftmax = 200, kCtRegsOther = 104;
+static_assert(32 * kCtSoftmaxWarps * kCtRegsSoftmax + 128 * kCtRegsOther <= kCtThreads * kCtRegsLaunch,
+              "the split cannot exceed what the launch holds");
 constexpr int kCtQRegion = kCtRows * 128;      // 128 rows x 64 elements of 16 bits
 constexpr int kCtKVRegion = kCtTile * 128;
 constexpr int kCtReaders = 2 + 4 * kCtGroups;  // of a published item
@@ -52,7 +63,7 @@ struct CtUnit {                  // 32 bytes, written by the plan
 struct CtArgs {
   ChunkArgs c;
   int *n_units;                  // written by the plan
-  int2 *tiles;                   // [tiles_cap] (sequence, tile)
+  int4 *tiles;                   // [tiles_cap] (sequence, tile, first key seen, one past the last)
   CtUnit *units;                 // [units_cap]
   int tiles_cap, units_cap;
   int gshift;                    // log2 of the packed heads G'
@@ -76,6 +87,7 @@ __device__ __forceinline__ void ct_span(const ChunkArgs &a, const ChunkSeq &s, i
     }
   };
   if (a.starts) {
+#pragma unroll 8                 // independent loads in flight together
     for (int i = i0 + sub; i < i1; i += kCtLanes) take(i);
   } else if (i1 > i0) {          // both bounds rise with the query
     take(i0);
@@ -123,7 +135,7 @@ __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const Ct
     total += __shfl_sync(0xffffffffu, v, 31);
     // (query offsets that overlap could list more tiles than there is room for)
     for (int t = 0; t < cnt; ++t) {
-      if (at + t < a.tiles_cap) a.tiles[at + t] = make_int2(b, t);
+      if (at + t < a.tiles_cap) a.tiles[at + t] = make_int4(b, t, 0, 0);
       else raise_flag(a.c.err, PKV_FLAG_QUERY_LEN);
     }
     __syncthreads();
@@ -134,17 +146,19 @@ __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const Ct
   for (int pass = 0; pass < 2; ++pass) {
     for (int n0 = 0; n0 < total; n0 += kCtPlanThreads / kCtLanes) {
       const int n = n0 + tid / kCtLanes, sub = tid & (kCtLanes - 1);
-      int2 bt = make_int2(0, 0);
-      ChunkSeq s = {0, 0, 0, 0};
-      int i0 = 0, i1 = 0;
-      if (n < total) {
-        bt = a.tiles[n];
-        s = chunk_seq(a.c, bt.x, false);
-        i0 = bt.y * per;
-        i1 = min(s.qlen, i0 + per);
+      int4 bt = make_int4(0, 0, 0, 0);
+      if (n < total) bt = a.tiles[n];
+      const int i0 = bt.y * per;
+      int lo = bt.z, hi = bt.w;
+      if (pass == 0) {
+        ChunkSeq s = {0, 0, 0, 0};
+        if (n < total) s = chunk_seq(a.c, bt.x, false);
+        ct_span(a.c, s, i0, min(s.qlen, i0 + per), sub, lo, hi);
+        if (n < total && sub == 0) {
+          a.tiles[n].z = lo;
+          a.tiles[n].w = hi;
+        }
       }
-      int lo, hi;
-      ct_span(a.c, s, i0, i1, sub, lo, hi);
       if (n >= total) continue;
       const int base = hi > 0 ? lo & ~15 : 0;
       const int nparts = max(1, (hi - base + a.c.P - 1) / a.c.P);
@@ -191,7 +205,8 @@ struct CtShape {
   static constexpr int kQOff = 0;                               // [group]
   static constexpr int kKVOff = kQOff + kCtGroups * kQBytes;    // [stage][K, V]
   static constexpr int kBarOff = kKVOff + kCtStages * 2 * kKVBytes;
-  static constexpr int kSmem = kBarOff + 1024 + 1024;           // barriers, item ring; + alignment slack
+  static constexpr int kPairOff = kBarOff + 1024;               // group 1's m, l of 128 rows
+  static constexpr int kSmem = kPairOff + 1024 + 1024;          // + alignment slack
   static constexpr uint32_t kTmemCols = 512;  // per group: S (128 columns, P over its first half), O (D columns)
 };
 
@@ -201,8 +216,11 @@ struct __align__(16) CtItem {
   int kind, sub, b, i0;          // head subgroup, sequence, first query in the sequence
   int q0, qlen, n, queries;      // the sequence's first row; queries of the item
   int t0, t1, lo, part;          // the part's keys, the unit's first seen key
-  int nt[kCtGroups];             // key tiles each row tile needs
-  int ntiles, nparts;
+  int nt[kCtGroups];             // key tiles each group works on
+  int ntiles;                    // key tiles the item loads
+  int nparts;                    // negative: both groups share one row tile (then -nparts parts)
+  __device__ __forceinline__ bool pair() const { return nparts < 0; }
+  __device__ __forceinline__ int parts() const { return nparts < 0 ? -nparts : nparts; }
 };
 static_assert(sizeof(CtItem) == 64, "four 16-byte words");
 
@@ -226,10 +244,13 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   uint64_t *o_done = bars + 16;     // [kCtGroups]: the group's last P . V of an item done
   uint64_t *item_full = bars + 18;  // [2]
   uint64_t *item_empty = bars + 20; // [2]
-  uint64_t *mma_done = bars + 22;
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 23);
-  int *abort_flag = reinterpret_cast<int *>(bars + 24);
-  CtItem *items = reinterpret_cast<CtItem *>(bars + 26);  // [2], 16-byte aligned
+  uint64_t *pair_full = bars + 22;  // group 1's state of a shared row tile is there
+  uint64_t *pair_empty = bars + 23; // group 0 has read it
+  uint64_t *mma_done = bars + 24;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 25);
+  int *abort_flag = reinterpret_cast<int *>(bars + 26);
+  CtItem *items = reinterpret_cast<CtItem *>(bars + 28);  // [2], 16-byte aligned
+  float *s_pair = reinterpret_cast<float *>(sm + Sh::kPairOff);  // [2][128]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -250,6 +271,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       mbar_init(&item_full[s], 1);
       mbar_init(&item_empty[s], kCtReaders);
     }
+    mbar_init(pair_full, 128);
+    mbar_init(pair_empty, 128);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -257,7 +280,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
-  if (warp == 0) tmem_alloc(tmem_holder, Sh::kTmemCols);
+  if (warp == kCtSoftmaxWarps) tmem_alloc(tmem_holder, Sh::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -272,7 +295,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   };
   auto aborted = [&]() { return *(volatile int *)abort_flag != 0; };
 
-  if (warp == kCtSched) {
+  if (warp >= kCtSoftmaxWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtRegsOther));
+  if (warp == kCtSoftmaxWarps + 2) {
     // ------------------------------------------------------------ scheduler
     griddep_wait();                                // the plan's units (every other role waits for an item)
     const unsigned total = (unsigned)*(volatile int *)ta.n_units * (unsigned)ta.subs;
@@ -310,6 +335,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           item.nt[0] = tiles_to(item.i0 + min(per, item.queries) - 1);
           item.nt[1] = item.queries > per ? tiles_to(item.i0 + item.queries - 1) : 0;
           item.ntiles = max(item.nt[0], item.nt[1]);
+          if (item.queries <= per) {
+            item.nparts = -item.nparts;
+            item.nt[1] = item.ntiles / 2;
+            item.nt[0] = item.ntiles - item.nt[1];
+          }
         }
       }
       const int slot = it & 1;
@@ -336,7 +366,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           __syncwarp();
           if (lane < Sh::kRegions)
             tma_load_3d_keep(sm + Sh::kQOff + g * Sh::kQBytes + lane * kCtQRegion, &tmQ, &q_full[g], 64 * lane,
-                             item.sub << ta.gshift, item.q0 + item.i0 + g * per);
+                             item.sub << ta.gshift, item.q0 + item.i0 + (item.pair() ? 0 : g * per));
           ++ig[g];
         }
         if (!ok) break;
@@ -351,7 +381,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
     for (int g = 0; g < kCtGroups; ++g)
       if (ig[g] > 0) mbar_wait_bounded(&q_full[g], (ig[g] - 1) & 1);
-  } else if (warp == 0) {
+  } else if (warp == kCtSoftmaxWarps) {
     // ------------------------------------------------------------ producer
     // per item and tile: the K boxes (one per lane: a 16-key chunk of one
     // 64-column region) once the keys two ring tiles back are read, then V
@@ -408,7 +438,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       mbar_wait_bounded(&k_full[r % kCtStages], (r / kCtStages) & 1);
     for (int r = max(0, v_issued - kCtStages); r < v_issued; ++r)
       mbar_wait_bounded(&v_full[r % kCtStages], (r / kCtStages) & 1);
-  } else if (warp == 1) {
+  } else if (warp == kCtSoftmaxWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t idesc_s = umma_idesc_f16(128, kCtTile, bf16, false);
@@ -468,6 +498,39 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (item.ntiles == 0) continue;
         const bool pre = early;
         early = false;
+        if (item.pair()) {
+          // tile j belongs to group j & 1
+          auto start_s = [&](int j) {  // S of tile j, and what its products free
+            const int g = j & 1, ring = ring0 + j;
+            if (!(j == 0 && pre)) {
+              ok = ok && mbar_wait_bounded(&k_full[ring % kCtStages], (ring / kCtStages) & 1);
+              if (ok && j < 2) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
+              if (!ok) return;
+              tc_fence_after();
+              issue_s(g, ring);
+              if (j + 2 >= item.ntiles) umma_commit(&q_empty[g]);
+            }
+            umma_commit(&k_empty[ring % kCtStages]);
+          };
+          for (int j = 0; ok && j < min(2, item.ntiles); ++j) start_s(j);
+          for (int j = 0; ok && j < item.ntiles; ++j) {
+            const int g = j & 1, ring = ring0 + j;
+            ok = mbar_wait_bounded(&p_full[g], tcnt[g] & 1);
+            ++tcnt[g];
+            if (ok) ok = mbar_wait_bounded(&v_full[ring % kCtStages], (ring / kCtStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(g, ring, j >= 2);
+            umma_commit(&v_empty[ring % kCtStages]);
+            if (j + 2 < item.ntiles) start_s(j + 2);
+            else umma_commit(&o_done[g]);
+          }
+          ring0 += item.ntiles;
+          if (ok && aborted()) ok = false;
+#pragma unroll
+          for (int g = 0; g < kCtGroups; ++g) ig[g] += item.nt[g] > 0;
+          continue;
+        }
         ok = mbar_wait_bounded(&k_full[ring0 % kCtStages], (ring0 / kCtStages) & 1);
 #pragma unroll
         for (int g = 0; g < kCtGroups; ++g)
@@ -558,9 +621,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       mbar_wait_bounded(mma_done, 0);
     }
     __syncwarp();
+  }
   } else {
     // ------------------------------------------------------------ softmax
-    const int g = (warp - 2) >> 2;                      // warpgroup = row tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCtRegsSoftmax));
+    const int g = warp >> 2;                            // warpgroup = row tile
     const int quarter = warp & 3;
     const int r = 32 * quarter + lane;                  // row in the tile = tensor-memory lane
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
@@ -571,7 +636,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // scale stands between (the max commutes with it)
     const bool raw = !CAP && !BIAS && sl2 > 0.f;
     const float mul = raw ? sl2 : 1.f;
-    int it = 0, ring0 = 0, ig = 0, tcnt = 0;
+    int it = 0, ring0 = 0, ig = 0, tcnt = 0, npair = 0;
     bool ok = true;
     while (true) {
       const int slot = it & 1;
@@ -587,7 +652,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (item.kind < 0) break;
       // this thread's row: query i of the sequence, head h (rows past the
       // item's last query mirror it and are not written)
-      const int qi = g * per + (r >> ta.gshift);
+      const bool pair = item.pair();
+      const int qi = (pair ? 0 : g * per) + (r >> ta.gshift);
       const bool real_row = qi < item.queries;
       const int i = item.i0 + min(qi, item.queries - 1);
       const int h = (item.sub << ta.gshift) + (r & (gheads - 1));
@@ -610,6 +676,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       chunk_visible(a, sq, i, lo, hi);
       const int p = item.n - item.qlen + i;
       const float slope = BIAS ? __ldg(a.slopes + h) * kLog2e : 0.f;
+      float2 d_bias[4];                                 // slope x columns 0 .. 7
+#pragma unroll
+      for (int c = 0; c < 4; ++c) d_bias[c] = make_float2(slope * (float)(2 * c), slope * (float)(2 * c + 1));
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < my_tiles; ++j) {
         ok = mbar_wait_bounded(&s_full[g], tcnt & 1);
@@ -619,8 +688,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           break;
         }
         tc_fence_after();
-        const int t0 = item.t0 + j * kCtTile;
-        const int ring = ring0 + j;
+        const int jt = pair ? 2 * j + g : j;           // the item's tile
+        const int t0 = item.t0 + jt * kCtTile;
+        const int ring = ring0 + jt;
         uint32_t sa[64], sb[64];
         tmem_ld64_nowait(tmem_sp, sa);
         tmem_ld64_nowait(tmem_sp + 64, sb);
@@ -633,12 +703,19 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           sc[64 + c] = __uint_as_float(sb[c]);
         }
         const bool cut = t0 < lo || t0 + kCtTile > hi;   // some of the tile is hidden from the row
+        // Where no key lies past a row's position, its bias slope (j - p) is
+        // linear in the column: slope (c mod 8) goes in with the score, and
+        // the rest, one number per 8 columns, only into the max and the
+        // exponent.
+        const bool linear = BIAS && __all_sync(0xffffffffu, t0 + kCtTile - 1 <= p);
+        const float base = BIAS ? slope * (float)(t0 - p) : 0.f;
+        auto block_bias = [&](int c) { return linear ? fmaf(slope, (float)(c & ~7), base) : 0.f; };
         // Capped scores: |q . k| over the tile picks the way to its tanh.  The
         // usual tile is near 0, where 4 terms do; without a bias they are
         // then evaluated inside the exponent, straight from the raw scores.
         bool fused = false;
         float mx_raw = -INFINITY;
-        if (CAP) {
+        if (CAP && !BIAS) {
           float mn_raw = INFINITY;
 #pragma unroll
           for (int c = 0; c < 128; c += 2) {
@@ -646,15 +723,18 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             mn_raw = min3f(mn_raw, sc[c], sc[c + 1]);
           }
           const float far = fmaxf(mx_raw, -mn_raw);
-          fused = !BIAS && __all_sync(0xffffffffu, !cut && far <= a.cap_small);
+          fused = __all_sync(0xffffffffu, !cut && far <= a.cap_small);
           if (!fused && __all_sync(0xffffffffu, far <= a.cap_mid)) {
-            const float2 rt = make_float2(a.scale_log2, a.scale_log2);
+            const float2 rt = kept_pair(a.scale_log2);
+            float2 kc[6];
+#pragma unroll
+            for (int e = 0; e < 6; ++e) kc[e] = kept_pair(a.cap_c[e]);
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
               const float2 x = fmul2(make_float2(sc[c], sc[c + 1]), rt), z = fmul2(x, x);
-              float2 q = ffma2(z, make_float2(a.cap_c[5], a.cap_c[5]), make_float2(a.cap_c[4], a.cap_c[4]));
+              float2 q = ffma2(z, kc[5], kc[4]);
 #pragma unroll
-              for (int e = 3; e >= 0; --e) q = ffma2(z, q, make_float2(a.cap_c[e], a.cap_c[e]));
+              for (int e = 3; e >= 0; --e) q = ffma2(z, q, kc[e]);
               q = fmul2(x, q);
               sc[c] = q.x;
               sc[c + 1] = q.y;
@@ -663,24 +743,25 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
             for (int c = 0; c < 128; ++c) sc[c] = chunk_capped(sc[c] * sl2, a.cap_log2);
           }
+        } else if (CAP) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) sc[c] = chunk_capped(sc[c] * sl2, a.cap_log2);
         } else if (!raw && !BIAS) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) sc[c] *= sl2;
         }
         if (BIAS) {
-          const float away = (float)(t0 - p);          // j - p of the tile's first key
           const float f = CAP ? 1.f : sl2;
-          if (t0 + kCtTile - 1 <= p) {                 // |p - j| = p - j: linear in the column
-            const float2 f2 = make_float2(f, f);
-            const float base = slope * away;
+          if (linear) {
+            const float2 f2 = kept_pair(f);
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
-              const float2 bias = make_float2(fmaf(slope, (float)c, base), fmaf(slope, (float)(c + 1), base));
-              const float2 x = ffma2(make_float2(sc[c], sc[c + 1]), f2, bias);
+              const float2 x = ffma2(make_float2(sc[c], sc[c + 1]), f2, d_bias[(c >> 1) & 3]);
               sc[c] = x.x;
               sc[c + 1] = x.y;
             }
           } else {
+            const float away = (float)(t0 - p);
 #pragma unroll
             for (int c = 0; c < 128; ++c) sc[c] = fmaf(sc[c], f, -slope * fabsf(away + (float)c));
           }
@@ -694,6 +775,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (fused) {
           const float z = mx_raw * mx_raw;
           mx = mx_raw * fmaf(z, fmaf(z, fmaf(z, a.cap_k[3], a.cap_k[2]), a.cap_k[1]), a.cap_k[0]);
+        } else if (BIAS) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            float m8 = max3f(sc[c], sc[c + 1], sc[c + 2]);
+            m8 = max3f(m8, sc[c + 3], sc[c + 4]);
+            m8 = max3f(m8, sc[c + 5], sc[c + 6]);
+            mx = fmaxf(mx, fmaxf(m8, sc[c + 7]) + block_bias(c));
+          }
         } else {
 #pragma unroll
           for (int c = 0; c < 128; c += 2) mx = max3f(mx, sc[c], sc[c + 1]);
@@ -714,7 +803,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
             for (int c2 = 0; c2 < 32; ++c2) {
               const int c = 64 * hf + 2 * c2;
-              float2 x = exponent(make_float2(sc[c], sc[c + 1]));
+              float2 x = exponent(make_float2(sc[c], sc[c + 1]), c);
               x.x = fast_exp2(x.x);
               x.y = fast_exp2(x.y);
               lsum = fadd2(lsum, x);
@@ -723,18 +812,24 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             tmem_st32u_nowait(tmem_sp + 32 * hf, pk);
           }
         };
-        const float2 nref = make_float2(-ref, -ref);
+        const float2 nref = kept_pair(-ref);
         if (CAP && !BIAS && fused) {
-          const float2 k0 = make_float2(a.cap_k[0], a.cap_k[0]), k1 = make_float2(a.cap_k[1], a.cap_k[1]);
-          const float2 k2 = make_float2(a.cap_k[2], a.cap_k[2]), k3 = make_float2(a.cap_k[3], a.cap_k[3]);
-          weights([&](float2 x) {
+          const float2 k0 = kept_pair(a.cap_k[0]), k1 = kept_pair(a.cap_k[1]);
+          const float2 k2 = kept_pair(a.cap_k[2]), k3 = kept_pair(a.cap_k[3]);
+          weights([&](float2 x, int) {
             const float2 z = fmul2(x, x);
             return ffma2(x, ffma2(z, ffma2(z, ffma2(z, k3, k2), k1), k0), nref);
           });
-        } else if (CAP || BIAS) {
-          weights([&](float2 x) { return fadd2(x, nref); });
+        } else if (BIAS) {
+          weights([&](float2 x, int c) {
+            const float e = block_bias(c) - ref;
+            return fadd2(x, make_float2(e, e));
+          });
+        } else if (CAP) {
+          weights([&](float2 x, int) { return fadd2(x, nref); });
         } else {
-          weights([&](float2 x) { return ffma2(x, make_float2(mul, mul), nref); });
+          const float2 mul2 = kept_pair(mul);
+          weights([&](float2 x, int) { return ffma2(x, mul2, nref); });
         }
         tmem_wait_st();
         l += lsum.x + lsum.y;
@@ -780,6 +875,30 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         break;
       }
       tc_fence_after();
+      float scale0 = 1.f, scale1 = 0.f;                 // of this group's O, and of group 1's in a shared tile
+      if (pair && item.nt[1] > 0) {
+        if (g == 1) {                                   // hand the state over, and go on once it has been read
+          s_pair[r] = m_used;
+          s_pair[kCtRows + r] = l;
+          tc_fence_before();
+          mbar_arrive(pair_full);
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(pair_empty, npair & 1));
+          ++npair;
+          if (!ok) break;
+          ring0 += item.ntiles;
+          continue;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(pair_full, npair & 1));
+        ++npair;
+        if (!ok) break;
+        tc_fence_after();
+        const float m1 = s_pair[r], l1 = s_pair[kCtRows + r];
+        const float M = fmaxf(m_used, m1), ref = chunk_ref(M);
+        scale0 = fast_exp2(m_used - ref);
+        scale1 = fast_exp2(m1 - ref);
+        m_used = M;
+        l = l * scale0 + l1 * scale1;
+      }
       // the row: O / l, or with several parts (m, l, O) to the workspace
       const bool seen = hi > lo;
       const float inv_l = seen ? 1.f / l : 0.f;
@@ -789,10 +908,16 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
         tmem_ld32(tmem_o + 32 * c, v);
+        if (pair && item.nt[1] > 0) {
+          float v1[32];
+          tmem_ld32(tmem_o + 256 + 32 * c, v1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], scale0, v1[e] * scale1);
+        }
 #pragma unroll
         for (int e = 0; e < 32; ++e) odd = fmaf(v[e], 0.f, odd);
         if (!real_row) continue;
-        if (item.nparts == 1) {
+        if (item.parts() == 1) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -806,7 +931,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           for (int c4 = 0; c4 < 8; ++c4) dst[c4] = make_float4(v[4 * c4], v[4 * c4 + 1], v[4 * c4 + 2], v[4 * c4 + 3]);
         }
       }
-      if (real_row && item.nparts > 1) {
+      if (pair && item.nt[1] > 0) {
+        tc_fence_before();
+        mbar_arrive(pair_empty);
+      }
+      if (real_row && item.parts() > 1) {
         a.ws_m[at] = m_used;
         a.ws_l[at] = l;
       }
@@ -827,12 +956,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
           const int d = lane + 32 * e;
-          if (item.nparts == 1)
+          if (item.parts() == 1)
             reinterpret_cast<T *>(a.out)[row * D + d] = from_f32<T>(any_key ? eo[e] / el : 0.f);
           else
             a.ws_o[ra * D + d] = eo[e];
         }
-        if (item.nparts > 1 && lane == 0) {
+        if (item.parts() > 1 && lane == 0) {
           a.ws_m[ra] = em;
           a.ws_l[ra] = el;
         }
@@ -844,7 +973,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, Sh::kTmemCols);
+  if (warp == kCtSoftmaxWarps) tmem_dealloc(tmem, Sh::kTmemCols);
   if (tid == 0) {
     // the last CTA puts the counters back (every claim's value was used
     // before the barrier, so it is performed already)
@@ -927,7 +1056,7 @@ static size_t ct_align(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t chunk_tc_scratch(int B, long long total_q, int G, int max_q, long long parts) {
   const long long tiles = ct_tiles_cap(B, total_q, max_q, (kCtGroups * kCtRows) >> chunk_tc_gshift(G));
-  return 256 + ct_align(tiles * sizeof(int2)) + ct_align(tiles * parts * sizeof(CtUnit));
+  return 256 + ct_align(tiles * sizeof(int4)) + ct_align(tiles * parts * sizeof(CtUnit));
 }
 
 template <typename... KArgs, typename... Args>
@@ -981,8 +1110,8 @@ pkv_status launch_chunk_tc(const ChunkArgs &c, pkv_dtype dt, char *scratch, int 
   a.units_cap = (int)(tiles * c.max_parts);
   a.n_units = reinterpret_cast<int *>(scratch);
   scratch += 256;
-  a.tiles = reinterpret_cast<int2 *>(scratch);
-  scratch += ct_align(tiles * sizeof(int2));
+  a.tiles = reinterpret_cast<int4 *>(scratch);
+  scratch += ct_align(tiles * sizeof(int4));
   a.units = reinterpret_cast<CtUnit *>(scratch);
   CUtensorMap mq, mk, mv;
   if (!encode_packed_map(&mq, c.q, dt, c.total_q, c.H, c.D, 1 << a.gshift, kCtRows >> a.gshift) ||
