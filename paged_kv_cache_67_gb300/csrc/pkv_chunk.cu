@@ -105,7 +105,7 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   if (p->kernel == 1 && D <= 128 && mq * (H / KVH) > kChunkRows) p->kernel = 2;
   p->chunks = ceil_div(mq * (H / KVH), kChunkRows);
   // a window bounds the keys a unit sees, unless a prefix reaches past it
-  const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 15) : cap;
+  const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 63) : cap;
   if (p->kernel == 2) {
     const long long items = chunk_tc_items(B, total_q, H, H / KVH, (int)mq);
     // (never more than without a window: the workspace is sized for that)

@@ -39,8 +39,8 @@ namespace pkv {
 constexpr int kCtRows = 128;     // packed rows per softmax warpgroup (MMA M)
 constexpr int kCtGroups = 2;     // row tiles per item
 constexpr int kCtTile = 128;     // keys per tile
-constexpr int kCtStages = 2;     // K/V ring depth
-constexpr int kCtSoftmaxWarps = 4 * kCtGroups; // warps 0-3, 4-7; then producer, MMA, scheduler and an idle one
+constexpr int kCtMaxStages = 4;  // of the K ring, and of the V ring
+constexpr int kCtSoftmaxWarps = 4 * kCtGroups; // warps 0-3, 4-7; then K producer, MMA, scheduler, V producer
 constexpr int kCtThreads = 32 * (kCtSoftmaxWarps + 4);
 // Registers: the launch has 384 x 168 = 64512; the softmax warps take 200
 // each and the others 104 (256 x 200 + 128 x 104 = 64512).  At 216 / 72 the
@@ -51,7 +51,7 @@ static_assert(32 * kCtSoftmaxWarps * kCtRegsSoftmax + 128 * kCtRegsOther <= kCtT
               "the split cannot exceed what the launch holds");
 constexpr int kCtQRegion = kCtRows * 128;      // 128 rows x 64 elements of 16 bits
 constexpr int kCtKVRegion = kCtTile * 128;
-constexpr int kCtReaders = 2 + 4 * kCtGroups;  // of a published item
+constexpr int kCtReaders = 3 + 4 * kCtGroups;  // of a published item
 constexpr int kCtPlanThreads = 1024;
 constexpr int kCtClasses = 256;                // plan: key tiles of a unit, the most first
 
@@ -68,6 +68,7 @@ struct CtArgs {
   int tiles_cap, units_cap;
   int gshift;                    // log2 of the packed heads G'
   int subs;                      // head subgroups: H / G'
+  int bshift;                    // log2 of the keys in one TMA box: 16 .. 64, a divisor of block_size
 };
 
 // ---------------------------------------------------------------------- plan
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const Ct
         }
       }
       if (n >= total) continue;
-      const int base = hi > 0 ? lo & ~15 : 0;
+      const int base = hi > 0 ? lo & -(1 << a.bshift) : 0;
       const int nparts = max(1, (hi - base + a.c.P - 1) / a.c.P);
       for (int p = sub; p < nparts; p += kCtLanes) {
         const int t0 = base + p * a.c.P, t1 = min(hi, t0 + a.c.P);
@@ -203,8 +204,10 @@ struct CtShape {
   static constexpr int kQBytes = kRegions * kCtQRegion;         // one group's query tile
   static constexpr int kKVBytes = kRegions * kCtKVRegion;       // one K (or V) tile
   static constexpr int kQOff = 0;                               // [group]
-  static constexpr int kKVOff = kQOff + kCtGroups * kQBytes;    // [stage][K, V]
-  static constexpr int kBarOff = kKVOff + kCtStages * 2 * kKVBytes;
+  static constexpr int kKStages = D == 64 ? 4 : 2, kVStages = D == 64 ? 4 : 3;
+  static constexpr int kKOff = kQOff + kCtGroups * kQBytes;     // [stage]
+  static constexpr int kVOff = kKOff + kKStages * kKVBytes;     // [stage]
+  static constexpr int kBarOff = kVOff + kVStages * kKVBytes;
   static constexpr int kPairOff = kBarOff + 1024;               // group 1's m, l of 128 rows
   static constexpr int kSmem = kPairOff + 1024 + 1024;          // + alignment slack
   static constexpr uint32_t kTmemCols = 512;  // per group: S (128 columns, P over its first half), O (D columns)
@@ -233,28 +236,29 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Sh::kBarOff);
-  uint64_t *k_full = bars + 0;      // [kCtStages]
-  uint64_t *v_full = bars + 2;      // [kCtStages]
-  uint64_t *k_empty = bars + 4;     // [kCtStages]
-  uint64_t *v_empty = bars + 6;     // [kCtStages]
-  uint64_t *q_full = bars + 8;      // [kCtGroups]: the group's query tile landed
-  uint64_t *q_empty = bars + 10;    // [kCtGroups]: the group's last S of an item done
-  uint64_t *s_full = bars + 12;     // [kCtGroups]: S of the group's current tile
-  uint64_t *p_full = bars + 14;     // [kCtGroups]: P of the group's current tile
-  uint64_t *o_done = bars + 16;     // [kCtGroups]: the group's last P . V of an item done
-  uint64_t *item_full = bars + 18;  // [2]
-  uint64_t *item_empty = bars + 20; // [2]
-  uint64_t *pair_full = bars + 22;  // group 1's state of a shared row tile is there
-  uint64_t *pair_empty = bars + 23; // group 0 has read it
-  uint64_t *mma_done = bars + 24;
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 25);
-  int *abort_flag = reinterpret_cast<int *>(bars + 26);
-  CtItem *items = reinterpret_cast<CtItem *>(bars + 28);  // [2], 16-byte aligned
+  uint64_t *k_full = bars;                       // [kCtMaxStages]: K and V arrive and are
+  uint64_t *v_full = k_full + kCtMaxStages;      // released separately, each through its
+  uint64_t *k_empty = v_full + kCtMaxStages;     // own ring and producer
+  uint64_t *v_empty = k_empty + kCtMaxStages;
+  uint64_t *q_full = v_empty + kCtMaxStages;     // [kCtGroups]: the group's query tile landed
+  uint64_t *q_empty = q_full + kCtGroups;        // its last S of an item done
+  uint64_t *s_full = q_empty + kCtGroups;        // S of its current tile
+  uint64_t *p_full = s_full + kCtGroups;         // P of its current tile
+  uint64_t *o_done = p_full + kCtGroups;         // its last P . V of an item done
+  uint64_t *item_full = o_done + kCtGroups;      // [2]
+  uint64_t *item_empty = item_full + 2;          // [2]
+  uint64_t *pair_full = item_empty + 2;          // group 1's state of a shared row tile is there
+  uint64_t *pair_empty = pair_full + 1;          // group 0 has read it
+  uint64_t *mma_done = pair_empty + 1;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
+  int *abort_flag = reinterpret_cast<int *>(mma_done + 2);
+  CtItem *items = reinterpret_cast<CtItem *>(bars + 36);  // [2], 16-byte aligned
+  static_assert(4 * kCtMaxStages + 5 * kCtGroups + 4 + 3 + 2 <= 36, "the barriers end before the items");
   float *s_pair = reinterpret_cast<float *>(sm + Sh::kPairOff);  // [2][128]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int s = 0; s < kCtStages; ++s) {
+    for (int s = 0; s < kCtMaxStages; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -381,13 +385,21 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
     for (int g = 0; g < kCtGroups; ++g)
       if (ig[g] > 0) mbar_wait_bounded(&q_full[g], (ig[g] - 1) & 1);
-  } else if (warp == kCtSoftmaxWarps) {
-    // ------------------------------------------------------------ producer
-    // per item and tile: the K boxes (one per lane: a 16-key chunk of one
-    // 64-column region) once the keys two ring tiles back are read, then V
-    const int per_tensor = 8 * Sh::kRegions;
-    const int region = (lane % per_tensor) >> 3, chunk = lane & 7;
-    int it = 0, k_issued = 0, v_issued = 0;
+  } else if (warp == kCtSoftmaxWarps || warp == kCtSoftmaxWarps + 3) {
+    // ----------------------------------------------------------- producers
+    // one warp streams the keys, one the values: per item and tile the boxes
+    // (one per lane: some keys of one 64-column region) once the tile that
+    // used the stage before has been read.  In one warp a tile's keys would
+    // wait behind the values before them.
+    const bool is_v = warp != kCtSoftmaxWarps;
+    const int stages = is_v ? Sh::kVStages : Sh::kKStages;
+    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+    const CUtensorMap *map = is_v ? &tmV : &tmK;
+    uint8_t *ring_base = sm + (is_v ? Sh::kVOff : Sh::kKOff);
+    const int nboxes = kCtTile >> ta.bshift, per_tensor = nboxes * Sh::kRegions;
+    const int region = (lane % per_tensor) / nboxes, chunk = lane % nboxes;
+    int it = 0, issued = 0, stage = 0;
+    uint32_t parity = 1;            // of the stage's release: passes at once in the first round
     bool ok = true;
     while (ok) {
       const int slot = it & 1;
@@ -399,53 +411,44 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       ++it;
       if (item.kind < 0) break;
       const int kvh = (item.sub << ta.gshift) / a.G;
-      for (int j = 0; j < item.ntiles && ok; ++j) {
-        const int ring = k_issued, stage = ring % kCtStages, use = ring / kCtStages;
+      for (int j = 0; j < item.ntiles; ++j) {
         const int tok0 = item.t0 + j * kCtTile;
-        const int valid_chunks = min(8, (item.t1 - tok0 + 15) >> 4);
-        const uint32_t bytes = (uint32_t)(valid_chunks * Sh::kRegions * 2048);
+        const int valid_chunks = min(nboxes, (item.t1 - tok0 + (1 << ta.bshift) - 1) >> ta.bshift);
+        const uint32_t bytes = (uint32_t)(valid_chunks * Sh::kRegions * (128 << ta.bshift));
         int phys = 0;
-        if (lane < valid_chunks) phys = __ldg(a.tables + (size_t)item.b * a.max_blocks + (tok0 + 16 * lane) / a.bs);
-        for (int v = 0; v < 2 && ok; ++v) {
-          if (ring >= kCtStages) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(v ? &v_empty[stage] : &k_empty[stage], (use - 1) & 1)) &&
-                 !aborted();
-            if (!ok) break;
-          }
-          if (v == 0) {
-            if (lane < valid_chunks && (phys < 0 || (long long)phys >= a.num_blocks)) {
-              raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
-              phys = 0;
-            }
-            phys = __shfl_sync(0xffffffffu, phys, chunk);
-          }
-          uint64_t *full = v ? &v_full[stage] : &k_full[stage];
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-          __syncwarp();
-          if (lane < per_tensor && chunk < valid_chunks) {
-            const int t = tok0 + 16 * chunk;
-            uint8_t *dst = sm + Sh::kKVOff + stage * 2 * Sh::kKVBytes + (v ? Sh::kKVBytes : 0) +
-                           region * kCtKVRegion + chunk * 2048;
-            tma_load_4d_keep(dst, v ? &tmV : &tmK, full, region * 64, kvh, t % a.bs, phys);
-          }
-          if (v) ++v_issued; else ++k_issued;
+        if (lane < valid_chunks) phys = __ldg(a.tables + (size_t)item.b * a.max_blocks + (tok0 + (lane << ta.bshift)) / a.bs);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], parity)) && !aborted();
+        if (!ok) break;
+        if (lane < valid_chunks && (phys < 0 || (long long)phys >= a.num_blocks)) {
+          raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
+          phys = 0;
+        }
+        phys = __shfl_sync(0xffffffffu, phys, chunk);
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+        __syncwarp();
+        if (lane < per_tensor && chunk < valid_chunks) {
+          const int t = tok0 + (chunk << ta.bshift);
+          tma_load_4d_keep(ring_base + stage * Sh::kKVBytes + region * kCtKVRegion + chunk * (128 << ta.bshift), map,
+                           &full[stage], region * 64, kvh, t % a.bs, phys);
+        }
+        ++issued;
+        if (++stage == stages) {
+          stage = 0;
+          parity ^= 1;
         }
       }
     }
     if (!ok && lane == 0) abort_cta();
     // the last fills land before the CTA can end (bounded)
-    for (int r = max(0, k_issued - kCtStages); r < k_issued; ++r)
-      mbar_wait_bounded(&k_full[r % kCtStages], (r / kCtStages) & 1);
-    for (int r = max(0, v_issued - kCtStages); r < v_issued; ++r)
-      mbar_wait_bounded(&v_full[r % kCtStages], (r / kCtStages) & 1);
+    for (int r = max(0, issued - stages); r < issued; ++r) mbar_wait_bounded(&full[r % stages], (r / stages) & 1);
   } else if (warp == kCtSoftmaxWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t idesc_s = umma_idesc_f16(128, kCtTile, bf16, false);
       const uint32_t idesc_o = umma_idesc_f16(128, D, bf16, true);
       auto kv_base = [&](int ring, bool v) {
-        return smem_u32(sm + Sh::kKVOff + (ring % kCtStages) * 2 * Sh::kKVBytes +
-                        (v ? Sh::kKVBytes : 0));
+        return smem_u32(v ? sm + Sh::kVOff + (ring % Sh::kVStages) * Sh::kKVBytes
+                          : sm + Sh::kKOff + (ring % Sh::kKStages) * Sh::kKVBytes);
       };
       auto issue_s = [&](int g, int ring) {  // S_g = Q_g . K^T over D in 16-wide steps
         const uint32_t qb = smem_u32(sm + Sh::kQOff + g * Sh::kQBytes), kb = kv_base(ring, false);
@@ -503,25 +506,25 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           auto start_s = [&](int j) {  // S of tile j, and what its products free
             const int g = j & 1, ring = ring0 + j;
             if (!(j == 0 && pre)) {
-              ok = ok && mbar_wait_bounded(&k_full[ring % kCtStages], (ring / kCtStages) & 1);
+              ok = ok && mbar_wait_bounded(&k_full[ring % Sh::kKStages], (ring / Sh::kKStages) & 1);
               if (ok && j < 2) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
               if (!ok) return;
               tc_fence_after();
               issue_s(g, ring);
               if (j + 2 >= item.ntiles) umma_commit(&q_empty[g]);
             }
-            umma_commit(&k_empty[ring % kCtStages]);
+            umma_commit(&k_empty[ring % Sh::kKStages]);
           };
           for (int j = 0; ok && j < min(2, item.ntiles); ++j) start_s(j);
           for (int j = 0; ok && j < item.ntiles; ++j) {
             const int g = j & 1, ring = ring0 + j;
             ok = mbar_wait_bounded(&p_full[g], tcnt[g] & 1);
             ++tcnt[g];
-            if (ok) ok = mbar_wait_bounded(&v_full[ring % kCtStages], (ring / kCtStages) & 1);
+            if (ok) ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
             if (!ok) break;
             tc_fence_after();
             issue_pv(g, ring, j >= 2);
-            umma_commit(&v_empty[ring % kCtStages]);
+            umma_commit(&v_empty[ring % Sh::kVStages]);
             if (j + 2 < item.ntiles) start_s(j + 2);
             else umma_commit(&o_done[g]);
           }
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           for (int g = 0; g < kCtGroups; ++g) ig[g] += item.nt[g] > 0;
           continue;
         }
-        ok = mbar_wait_bounded(&k_full[ring0 % kCtStages], (ring0 / kCtStages) & 1);
+        ok = mbar_wait_bounded(&k_full[ring0 % Sh::kKStages], (ring0 / Sh::kKStages) & 1);
 #pragma unroll
         for (int g = 0; g < kCtGroups; ++g)
           if (ok && item.nt[g] > 0 && !(g == 0 && pre)) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           issue_s(g, ring0);
           if (item.nt[g] == 1) umma_commit(&q_empty[g]);  // the group's last S of the item
         }
-        umma_commit(&k_empty[ring0 % kCtStages]);
+        umma_commit(&k_empty[ring0 % Sh::kKStages]);
         const int ring_next = ring0 + item.ntiles;
         // group 0's first S of the next item, if everything it reads is
         // there (never waits)
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             have_nx = true;
           }
           if (nx.kind != 1) return;
-          if (!mbar_test_wait(&k_full[ring_next % kCtStages], (ring_next / kCtStages) & 1) ||
+          if (!mbar_test_wait(&k_full[ring_next % Sh::kKStages], (ring_next / Sh::kKStages) & 1) ||
               !mbar_test_wait(&q_full[0], (ig[0] + 1) & 1))
             return;
           tc_fence_after();
@@ -588,17 +591,17 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             ++tcnt[g];
             if (!ok) break;
             if (!v_ready) {
-              ok = mbar_wait_bounded(&v_full[ring % kCtStages], (ring / kCtStages) & 1);
+              ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
               if (!ok) break;
               v_ready = true;
             }
             tc_fence_after();
             issue_pv(g, ring, j > 0);
             // the tile's last P . V: its V slot is free once that has run
-            if (g == kCtGroups - 1 || j >= item.nt[g + 1]) umma_commit(&v_empty[ring % kCtStages]);
+            if (g == kCtGroups - 1 || j >= item.nt[g + 1]) umma_commit(&v_empty[ring % Sh::kVStages]);
             if (j + 1 < item.nt[g]) {
               if (!k_ready) {
-                ok = mbar_wait_bounded(&k_full[(ring + 1) % kCtStages], ((ring + 1) / kCtStages) & 1);
+                ok = mbar_wait_bounded(&k_full[(ring + 1) % Sh::kKStages], ((ring + 1) / Sh::kKStages) & 1);
                 if (!ok) break;
                 k_ready = true;
               }
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
           }
           if (!ok) break;
-          if (j + 1 < item.ntiles) umma_commit(&k_empty[(ring + 1) % kCtStages]);
+          if (j + 1 < item.ntiles) umma_commit(&k_empty[(ring + 1) % Sh::kKStages]);
         }
         ring0 = ring_next;
         if (ok && aborted()) ok = false;
@@ -655,6 +658,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const bool pair = item.pair();
       const int qi = (pair ? 0 : g * per) + (r >> ta.gshift);
       const bool real_row = qi < item.queries;
+      const bool live = __any_sync(0xffffffffu, real_row);  // a warp without rows only keeps the barriers going
       const int i = item.i0 + min(qi, item.queries - 1);
       const int h = (item.sub << ta.gshift) + (r & (gheads - 1));
       const size_t q_row = (size_t)(item.q0 + i) * a.H + h;
@@ -691,6 +695,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         const int jt = pair ? 2 * j + g : j;           // the item's tile
         const int t0 = item.t0 + jt * kCtTile;
         const int ring = ring0 + jt;
+        if (live) {
         uint32_t sa[64], sb[64];
         tmem_ld64_nowait(tmem_sp, sa);
         tmem_ld64_nowait(tmem_sp + 64, sb);
@@ -716,13 +721,18 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         bool fused = false;
         float mx_raw = -INFINITY;
         if (CAP && !BIAS) {
+          if (cut) {  // hidden columns hold whatever was there: they have no say
+            const int vlo = lo - t0, vhi = hi - t0;
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sc[c] = c >= vlo && c < vhi ? sc[c] : 0.f;
+          }
           float mn_raw = INFINITY;
 #pragma unroll
           for (int c = 0; c < 128; c += 2) {
             mx_raw = max3f(mx_raw, sc[c], sc[c + 1]);
             mn_raw = min3f(mn_raw, sc[c], sc[c + 1]);
           }
-          const float far = fmaxf(mx_raw, -mn_raw);
+          const float far = real_row ? fmaxf(mx_raw, -mn_raw) : 0.f;
           fused = __all_sync(0xffffffffu, !cut && far <= a.cap_small);
           if (!fused && __all_sync(0xffffffffu, far <= a.cap_mid)) {
             const float2 rt = kept_pair(a.scale_log2);
@@ -845,17 +855,18 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             tmem_st32(tmem_o + 32 * c, v);
           }
         }
+        }
         // the tile's values that no row of the unit sees become 0 (they may
         // hold anything, and 0 * NaN would poison the product)
         const bool ragged = t0 < item.lo || t0 + kCtTile > item.t1;
         if (ragged) {
-          ok = mbar_wait_bounded(&v_full[ring % kCtStages], (ring / kCtStages) & 1);
+          ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           if (t0 + r < item.lo || t0 + r >= item.t1) {
-            uint8_t *vrow = sm + Sh::kKVOff + (ring % kCtStages) * 2 * Sh::kKVBytes + Sh::kKVBytes + r * 128;
+            uint8_t *vrow = sm + Sh::kVOff + (ring % Sh::kVStages) * Sh::kKVBytes + r * 128;
 #pragma unroll
             for (int rg = 0; rg < Sh::kRegions; ++rg)
 #pragma unroll
@@ -906,6 +917,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       float odd = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
+        if (!live) break;
         float v[32];
         tmem_ld32(tmem_o + 32 * c, v);
         if (pair && item.nt[1] > 0) {
@@ -1104,6 +1116,7 @@ pkv_status launch_chunk_tc(const ChunkArgs &c, pkv_dtype dt, char *scratch, int 
   a.c = c;
   a.gshift = chunk_tc_gshift(c.G);
   a.subs = c.H >> a.gshift;
+  a.bshift = c.bs % 64 == 0 ? 6 : c.bs % 32 == 0 ? 5 : 4;
   const long long tiles = ct_tiles_cap(c.B, c.total_q, c.max_q, (kCtGroups * kCtRows) >> a.gshift);
   if (tiles * c.max_parts * a.subs > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   a.tiles_cap = (int)tiles;
@@ -1115,8 +1128,8 @@ pkv_status launch_chunk_tc(const ChunkArgs &c, pkv_dtype dt, char *scratch, int 
   a.units = reinterpret_cast<CtUnit *>(scratch);
   CUtensorMap mq, mk, mv;
   if (!encode_packed_map(&mq, c.q, dt, c.total_q, c.H, c.D, 1 << a.gshift, kCtRows >> a.gshift) ||
-      !encode_cache_map(&mk, c.k_cache, dt, c.num_blocks, c.bs, c.KVH, c.D) ||
-      !encode_cache_map(&mv, c.v_cache, dt, c.num_blocks, c.bs, c.KVH, c.D))
+      !encode_cache_map(&mk, c.k_cache, dt, c.num_blocks, c.bs, c.KVH, c.D, 1 << a.bshift) ||
+      !encode_cache_map(&mv, c.v_cache, dt, c.num_blocks, c.bs, c.KVH, c.D, 1 << a.bshift))
     return PKV_ERR_CUDA;
   const bool bf = dt == PKV_BF16;
   if (c.D == 128)

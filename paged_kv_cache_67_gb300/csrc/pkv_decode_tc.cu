@@ -488,15 +488,15 @@ static CUtensorMapDataType map_type(pkv_dtype dt) {
 }
 
 // Tensor map of a [num_blocks, bs, KVH, D] cache: dims innermost first, box of
-// 64 elements x 1 head x 16 rows x 1 block, 128-byte swizzle.
+// 64 elements x 1 head x box_rows rows x 1 block, 128-byte swizzle.
 bool encode_cache_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long long num_blocks,
-                             int bs, int KVH, int D) {
+                             int bs, int KVH, int D, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t el = 2;
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)KVH, (cuuint64_t)bs, (cuuint64_t)num_blocks};
   cuuint64_t strides[3] = {D * el, (cuuint64_t)KVH * D * el, (cuuint64_t)bs * KVH * D * el};
-  cuuint32_t box[4] = {kBoxElems, 1, kChunk, 1};
+  cuuint32_t box[4] = {kBoxElems, 1, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, map_type(dt), 4, const_cast<void *>(cache), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

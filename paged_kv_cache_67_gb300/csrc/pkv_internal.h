@@ -68,9 +68,9 @@ pkv_status launch_write(void *k_cache, void *v_cache, const void *k, const void 
                         cudaStream_t stream);
 
 // Tensor map of a [num_blocks, bs, KVH, D] 16-bit cache: box of 64 elements
-// x 1 head x 16 rows x 1 block, 128-byte swizzle (false if unavailable).
+// x 1 head x box_rows rows x 1 block, 128-byte swizzle (false if unavailable).
 bool encode_cache_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long long num_blocks,
-                      int bs, int KVH, int D);
+                      int bs, int KVH, int D, int box_rows = 16);
 
 // The same cache in 5-D: box of 64 elements x 16 rows x D / 64 blocks of 64 x
 // 1 head x 1 block, so one box is a 16-token chunk of a KV head.

@@ -111,7 +111,7 @@ def test_chunk_plan_and_workspace(pkv):
                         assert P % 128 == 0 and (part == 0 or P <= part) and 1 <= parts <= max(64, -(-bs * mb // P))
                         # every part a unit can touch has a place
                         mq = max_q or q
-                        span = min(bs * mb, window + mq + 15) if window else bs * mb
+                        span = min(bs * mb, window + mq + 63) if window else bs * mb
                         assert parts == -(-span // P)
                         assert part == 0 or P == min(part, -(-span // 128) * 128)
                         rows = q * H
