@@ -19,6 +19,7 @@ size_t chunk_tc_scratch(int B, long long total_q, int G, int max_q, long long pa
 // that the workspace's size needs no device.
 constexpr int kPlanSms = 152;
 constexpr int kChunkRows = 16;     // packed rows per CTA of the CUDA-core and mma.sync kernels
+constexpr int kMmaRows = 32;       // packed rows up to which the mma.sync kernel is taken where tcgen05 could be
 constexpr int kChunkMaxParts = 64;
 constexpr long long kChunkMaxKeys = 1LL << 30;  // keys of a context: positions plus a part stay in 32 bits
 
@@ -59,10 +60,23 @@ static int chunk_max_q(int64_t total_q, int max_q) {
   return (int)std::max<int64_t>(1, max_q > 0 ? std::min<int64_t>(max_q, total_q) : total_q);
 }
 
-// Parts wanted for a unit: enough that the units fill `slots` CTA places
-// about twice over.
-static long long parts_wanted(long long units, long long slots) {
-  return std::min<long long>(kChunkMaxParts, std::max<long long>(1, 2 * slots / std::max<long long>(units, 1)));
+// Parts of a unit of the CUDA-core and mma.sync kernels, `slots` CTAs resident.
+//  - Units that fill the GPU: a CTA's start and end cost its slot some 7 us,
+//    so only contexts of 4096 keys and more are split, 2048 keys or more a
+//    part, to even out ragged lengths (512 units: 64 sequences of 2304 keys
+//    92 us whole, 105 in two; 512 to 4096 keys 104.4 us at 2048, 108.8 whole).
+//  - Fewer units, long contexts: two CTAs a slot of 1024 keys or more (drafts
+//    over 16-32k keys: 132 us at 8192 keys, 150 at 2048).
+//  - Fewer units, short contexts: one round of CTAs, 128 keys or more, at most
+//    32 parts (one sequence of 8192 keys, 8 KV heads: 17 us at 256 keys, 19 at
+//    1024, 25 at 128; 128 one-head units of 1087 keys, 152 slots: 25.4 us
+//    whole, 33.8 in two).
+static long long parts_wanted(long long units, long long slots, long long span) {
+  units = std::max<long long>(units, 1);
+  if (units >= slots) return std::max<long long>(1, std::min(ceil_div(4 * slots, units), span / 2048));
+  const long long two = std::min<long long>(2 * slots / units, kChunkMaxParts);
+  if (span / two >= 1024) return two;
+  return std::max<long long>(1, std::min<long long>({slots / units, 32, ceil_div(span, 128)}));
 }
 
 // Parts of the persistent tcgen05 kernel's items (256 rows x a part): the
@@ -102,7 +116,7 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   const long long mq = chunk_max_q(total_q, max_q), cap = chunk_cap(bs, max_blocks, max_n);
   // 16-bit tensors that TMA can read, in tokens chunks that never span two blocks
   p->kernel = tc_eligible(dt, D, bs) && aligned16 ? 1 : 0;
-  if (p->kernel == 1 && D <= 128 && mq * (H / KVH) > kChunkRows) p->kernel = 2;
+  if (p->kernel == 1 && D <= 128 && mq * (H / KVH) > kMmaRows) p->kernel = 2;
   p->chunks = ceil_div(mq * (H / KVH), kChunkRows);
   // a window bounds the keys a unit sees, unless a prefix reaches past it
   const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 63) : cap;
@@ -112,8 +126,9 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
     chunk_split(std::min(tc_parts_wanted(items, span), tc_parts_wanted(items, cap)), span, 512, partition_size, p);
     return true;
   }
-  const int per_sm = p->kernel == 0 ? 4 : D <= 128 ? 2 : 1;   // resident CTAs
-  chunk_split(parts_wanted((long long)B * KVH * p->chunks, kPlanSms * per_sm), span, 256, partition_size, p);
+  const int per_sm = p->kernel == 0 ? 4 : D <= 192 ? 2 : 1;   // resident CTAs
+  const long long units = (long long)B * KVH * p->chunks, slots = (long long)kPlanSms * per_sm;
+  chunk_split(std::min(parts_wanted(units, slots, span), parts_wanted(units, slots, cap)), span, 128, partition_size, p);
   return true;
 }
 

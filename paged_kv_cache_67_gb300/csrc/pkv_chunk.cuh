@@ -185,10 +185,10 @@ __device__ __forceinline__ void chunk_row_exact(const ChunkArgs &a, int b, int k
 // part writes o / l.  Several leave their state in the workspace, and the one
 // that `counter` shows to be last merges:
 //   M = max m_p,  out = sum o_p 2^(m_p - M) / sum l_p 2^(m_p - M).
-// s_scratch: 1 int.
+// s_scratch: 1 int.  s_o is overwritten (it holds rows x nparts floats or more).
 template <typename T, typename RowOut, typename Seen>
 __device__ void chunk_finish(const ChunkArgs &a, int rows, int part, int nparts, const float *s_m, const float *s_l,
-                             const float *s_o, int ostride, int *s_scratch, int *counter, const RowOut &row_out,
+                             float *s_o, int ostride, int *s_scratch, int *counter, const RowOut &row_out,
                              const Seen &seen) {
   const int tid = threadIdx.x, nthr = blockDim.x, D = a.D, DV = D / 4;
   T *out = reinterpret_cast<T *>(a.out);
@@ -227,28 +227,67 @@ __device__ void chunk_finish(const ChunkArgs &a, int rows, int part, int nparts,
   }
   __syncthreads();
   if (!*s_scratch) return;
-  for (int i = tid; i < rows * DV; i += nthr) {
-    const int r = i / DV, d4 = i - r * DV;
+  // the rows' weights 2^(m_p - M) / L once, in shared memory (the part's own
+  // state is in the workspace, its place is free) ...
+  float *s_w = s_o;                                   // [rows][nparts]
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int r = warp; r < rows; r += nthr >> 5) {
     const size_t at = row_out(r) * a.max_parts;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int p = 0; p < nparts; ++p) M = fmaxf(M, __ldcg(a.ws_m + at + p));
+    float M = -INFINITY, L = 0.f;
+    for (int p = lane; p < nparts; p += 32) M = fmaxf(M, __ldcg(a.ws_m + at + p));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float ref = chunk_ref(M);
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = 0; p < nparts; ++p) {
+    for (int p = lane; p < nparts; p += 32) {
       const float w = fast_exp2(__ldcg(a.ws_m + at + p) - ref);
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (at + p) * D) + d4);
+      s_w[r * nparts + p] = w;
       L = fmaf(__ldcg(a.ws_l + at + p), w, L);
-      acc.x = fmaf(v.x, w, acc.x);
-      acc.y = fmaf(v.y, w, acc.y);
-      acc.z = fmaf(v.z, w, acc.z);
-      acc.w = fmaf(v.w, w, acc.w);
     }
-    const float inv = 1.f / L;
-    if (seen(r)) put4(row_out(r), d4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    else put4(row_out(r), d4, 0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = seen(r) ? 1.f / L : 0.f;
+    __syncwarp();
+    for (int p = lane; p < nparts; p += 32) s_w[r * nparts + p] *= inv;
+  }
+  __syncthreads();
+  // ... then the sums: a round trip to L2 brings kR rows x kP parts of a thread
+  constexpr int kR = 4, kP = 4;
+  const int tpr = DV < nthr ? DV : nthr;              // threads along a row
+  const int step = nthr / tpr;                        // rows side by side
+  for (int d4 = tid % tpr; d4 < DV; d4 += tpr) {
+    for (int r0 = tid / tpr; r0 < rows && tid < step * tpr; r0 += step * kR) {
+      float4 acc[kR];
+      const float4 *po[kR];
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        po[k] = reinterpret_cast<const float4 *>(a.ws_o + row_out(min(r0 + k * step, rows - 1)) * a.max_parts * D) + d4;
+      }
+      for (int p0 = 0; p0 < nparts; p0 += kP) {
+        float4 v[kR][kP];
+#pragma unroll
+        for (int k = 0; k < kR; ++k)
+#pragma unroll
+          for (int p = 0; p < kP; ++p) v[k][p] = __ldcg(po[k] + (size_t)min(p0 + p, nparts - 1) * DV);
+#pragma unroll
+        for (int k = 0; k < kR; ++k)
+#pragma unroll
+          for (int p = 0; p < kP; ++p) {
+            const float w = p0 + p < nparts ? s_w[min(r0 + k * step, rows - 1) * nparts + p0 + p] : 0.f;
+            acc[k].x = fmaf(v[k][p].x, w, acc[k].x);
+            acc[k].y = fmaf(v[k][p].y, w, acc[k].y);
+            acc[k].z = fmaf(v[k][p].z, w, acc[k].z);
+            acc[k].w = fmaf(v[k][p].w, w, acc[k].w);
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        const int r = r0 + k * step;
+        if (r >= rows) continue;
+        if (seen(r)) put4(row_out(r), d4, acc[k].x, acc[k].y, acc[k].z, acc[k].w);
+        else put4(row_out(r), d4, 0.f, 0.f, 0.f, 0.f);
+      }
+    }
   }
   if (tid == 0) *counter = 0;  // ready for the next call
 }

@@ -59,8 +59,10 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
   int *s_scratch = s_hi + kCmRows;
 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int b = blockIdx.y, part = blockIdx.x % a.max_parts, unit = blockIdx.x / a.max_parts;
-  const int kvh = unit / a.chunks, chunk = unit - kvh * a.chunks;
+  // row chunks of the same keys are neighbours in the grid, so that the second
+  // finds in L2 what the first has read
+  const int b = blockIdx.y, chunk = blockIdx.x % a.chunks, unit = blockIdx.x / a.chunks;
+  const int kvh = unit / a.max_parts, part = unit - kvh * a.max_parts;
   const ChunkSeq sq = chunk_seq(a, b, blockIdx.x == 0 && tid == 0);
   const int rows = min(kCmRows, sq.qlen * a.G - chunk * kCmRows);
   if (rows <= 0) return;
