@@ -445,7 +445,7 @@ PKV_API pkv_status pkv_build_step(int32_t *block_tables, const int32_t *held, in
  *   interleaved   0: pair j is elements (j, j + rot_dim / 2); else (2j, 2j + 1)
  * With (x, y) a pair and c, s its table entries: (x c - y s, y c + x s), in
  * fp32, rounded once to dtype.  A negative slot is a padding token: nothing
- * is read or written for it (its q_out row stays as it was).  A kept token
+ * is written for it (its q_out row stays as it was).  A kept token
  * with a used axis' position outside [0, max_position) raises
  * PKV_FLAG_POSITION and is skipped the same way; a slot past the pool raises
  * PKV_FLAG_SLOT_OUT_OF_RANGE, its q_out row is written and the cache is not.

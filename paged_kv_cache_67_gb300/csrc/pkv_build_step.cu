@@ -12,7 +12,7 @@
 // needed and released blocks).
 //
 // One cluster does the step: every CTA makes the three sums for itself in
-// shared memory (B <= 16384 requests, a few tiles of 1024), then takes its
+// shared memory (B <= 16384 requests, up to 16 of a thread), then takes its
 // share of the tokens, the needed and the released blocks, finding a token's
 // request by a binary search of the sums.  No CTA waits for another until the
 // end: table and stack entries that are written are never ones that are read
@@ -25,9 +25,16 @@
 
 namespace pkv {
 
-constexpr int kStepThreads = 1024;
+constexpr int kStepMaxThreads = 1024;
 constexpr int kStepMaxB = 16384;    // three sums of 4 bytes each in shared memory
+constexpr int kStepSmemB = 8192;    // up to here the cached and held lengths stay there too
+constexpr size_t kStepMaxSmem = (size_t)3 * (kStepMaxB + 4) * sizeof(int);  // the most a step asks for
+static_assert(kStepMaxSmem >= (size_t)5 * (kStepSmemB + 4) * sizeof(int), "both layouts fit");
+constexpr int kStepSmall = 256;     // threads of a small step
 constexpr int kStepCluster = 8;     // CTAs of a large step
+constexpr int kStepWide = 16;       // of a very large one, where the device has room for it
+constexpr int kStepWideFrom = 16384;
+constexpr int kStepOneCta = 1024;   // requests or tokens up to which one CTA does the step
 constexpr int kStepSat = 0x40000000;  // sums saturate here: above every valid total
 
 struct StepArgs {
@@ -46,14 +53,20 @@ struct StepArgs {
   int *err;
   long long num_blocks, free_capacity;
   int B, max_blocks, bs, max_tokens;
+  uint32_t bs_mul, bs_shift;        // x / bs = (umulhi(x, bs_mul) + x) >> bs_shift for 0 <= x < 2^31
 };
 
 __device__ __forceinline__ int sat_add(int a, int b) {  // both in [0, kStepSat]
   return min(a + b, kStepSat);
 }
 
-__device__ __forceinline__ int blocks_for(int tokens, int bs) {  // ceil, no overflow
-  return tokens / bs + (tokens % bs != 0);
+__device__ __forceinline__ int div_bs(const StepArgs &a, int x) {
+  return (int)((__umulhi((uint32_t)x, a.bs_mul) + (uint32_t)x) >> a.bs_shift);
+}
+
+__device__ __forceinline__ int blocks_for(const StepArgs &a, int tokens) {  // ceil, no overflow
+  const int q = div_bs(a, tokens);
+  return q + (q * a.bs != tokens);
 }
 
 // Last b in [0, B) with start[b] <= x (start[0] = 0 <= x).
@@ -67,78 +80,106 @@ __device__ __forceinline__ int owner_of(const int *start, int B, int x) {
   return lo;
 }
 
+// The same from b on (start[b] <= x), for an owner that is likely near: steps
+// that double, then halve.
+__device__ __forceinline__ int owner_from(const int *start, int B, int b, int x) {
+  int step = 1;
+  while (b + step < B && start[b + step] <= x) {
+    b += step;
+    step <<= 1;
+  }
+  for (step >>= 1; step > 0; step >>= 1)
+    if (b + step < B && start[b + step] <= x) b += step;
+  return b;
+}
+
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kStepThreads) pkv_build_step_kernel(const StepArgs a) {
-  extern __shared__ int s_dyn[];
-  int *s_new = s_dyn;              // [B] exclusive sums of new tokens
-  int *s_need = s_new + a.B;       // [B] of needed blocks
-  int *s_back = s_need + a.B;      // [B] of released blocks
+// IPT requests of a thread, neighbours, so that one scan over the block makes
+// the sums.
+template <int IPT>
+__global__ void __launch_bounds__(kStepMaxThreads) pkv_build_step_kernel(const StepArgs a) {
+  extern __shared__ __align__(16) int s_dyn[];
+  const int pad = (a.B + 4) & ~3;  // entries of an array, one more than the requests
+  int *s_new = s_dyn;              // [B + 1] exclusive sums of new tokens
+  int *s_need = s_new + pad;       // [B + 1] of needed blocks
+  int *s_back = s_need + pad;      // [B + 1] of released blocks
+  int *s_cached = s_back + pad;    // [B] with B <= kStepSmemB
+  int *s_held = s_cached + pad;
+  const bool local = a.B <= kStepSmemB;
   __shared__ int s_warp[3][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
   const int rank = blockIdx.x, ncta = gridDim.x;
 
   const int count = *a.free_count;
   int bad = count < 0 || count > a.free_capacity;
-  int sum_new = 0, sum_need = 0, sum_back = 0;   // totals of the tiles before
-  for (int base = 0; base < a.B; base += kStepThreads) {
-    const int b = base + tid;
-    int x[3] = {0, 0, 0};
-    if (b < a.B) {
-      const int c = a.cached[b], n = a.fresh[b], h = a.held[b];
-      const bool ok = c >= 0 && n >= 0 && h >= 0 && h <= a.max_blocks &&
-                      (long long)c + n <= (long long)a.max_blocks * a.bs &&
-                      (long long)c + n <= 0x7fffffffLL && blocks_for(c, a.bs) <= h;
-      if (ok) {
-        const int w = blocks_for(c + n, a.bs);
-        x[0] = min(n, kStepSat);
-        x[1] = min(max(w - h, 0), kStepSat);
-        x[2] = min(max(h - w, 0), kStepSat);
-      }
-      bad |= !ok;
+  int c[IPT], n[IPT], h[IPT];
+  const int b0 = tid * IPT;
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const bool in = b0 + i < a.B;
+    c[i] = in ? a.cached[b0 + i] : 0;
+    n[i] = in ? a.fresh[b0 + i] : 0;
+    h[i] = in ? a.held[b0 + i] : 0;
+  }
+  int sum[3] = {0, 0, 0}, x[3][IPT];   // this thread's totals, and its requests' own numbers
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const bool ok = c[i] >= 0 && n[i] >= 0 && h[i] >= 0 && h[i] <= a.max_blocks &&
+                    (long long)c[i] + n[i] <= (long long)a.max_blocks * a.bs &&
+                    (long long)c[i] + n[i] <= 0x7fffffffLL && blocks_for(a, c[i]) <= h[i];
+    const int w = ok ? blocks_for(a, c[i] + n[i]) : 0;
+    x[0][i] = ok ? min(n[i], kStepSat) : 0;
+    x[1][i] = ok ? min(max(w - h[i], 0), kStepSat) : 0;
+    x[2][i] = ok ? min(max(h[i] - w, 0), kStepSat) : 0;
+    bad |= !ok;
+    if (local && b0 + i < a.B) {
+      s_cached[b0 + i] = c[i];
+      s_held[b0 + i] = h[i];
     }
-    int inc[3] = {x[0], x[1], x[2]};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k] = sat_add(sum[k], x[k][i]);
+  }
+  int inc[3] = {sum[0], sum[1], sum[2]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, inc[k], o);
+      if (lane >= o) inc[k] = sat_add(inc[k], y);
+    }
+  }
+  if (lane == 31) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s_warp[k][warp] = inc[k];
+  }
+  bad = __syncthreads_or(bad);
+  int total[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int v = lane < nthr / 32 ? s_warp[k][lane] : 0;  // the warps' totals, scanned by every warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int y = __shfl_up_sync(0xffffffffu, inc[i], o);
-        if (lane >= o) inc[i] = sat_add(inc[i], y);
-      }
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = sat_add(v, y);
     }
-    if (lane == 31) {
+    total[k] = __shfl_sync(0xffffffffu, v, 31);
+    const int before = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
+    // (a sum past the saturation point belongs to a step that is refused below)
+    int at = sat_add(warp ? before : 0, inc[k] - sum[k]);
+    int *dst = k == 0 ? s_new : k == 1 ? s_need : s_back;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) s_warp[i][warp] = inc[i];
+    for (int i = 0; i < IPT; ++i) {
+      if (b0 + i < a.B) dst[b0 + i] = at;
+      at = sat_add(at, x[k][i]);
     }
-    __syncthreads();
-    int tot[3], pre[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      int v = s_warp[i][lane];                    // the 32 warps' totals, scanned by every warp
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = sat_add(v, y);
-      }
-      tot[i] = __shfl_sync(0xffffffffu, v, 31);
-      const int before = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
-      pre[i] = warp ? before : 0;
-    }
-    if (b < a.B) {
-      // a sum past the saturation point belongs to a step that is refused below
-      s_new[b] = sat_add(sum_new, sat_add(pre[0], inc[0] - x[0]));
-      s_need[b] = sat_add(sum_need, sat_add(pre[1], inc[1] - x[1]));
-      s_back[b] = sat_add(sum_back, sat_add(pre[2], inc[2] - x[2]));
-    }
-    sum_new = sat_add(sum_new, tot[0]);
-    sum_need = sat_add(sum_need, tot[1]);
-    sum_back = sat_add(sum_back, tot[2]);
-    __syncthreads();                              // s_warp is written again
+    if (tid == 0) dst[a.B] = total[k];
   }
+  __syncthreads();
+  int sum_new = total[0], sum_need = total[1], sum_back = total[2];
   bad |= sum_new >= kStepSat || sum_back >= kStepSat || (long long)count + sum_back > a.free_capacity;
-  bad = __syncthreads_or(bad);
   const int top = bad ? 0 : count + sum_back;     // |F'| (at most free_capacity)
   const bool short_of = !bad && sum_need > top;
   const bool ok = !bad && !short_of;
@@ -149,11 +190,12 @@ __global__ void __launch_bounds__(kStepThreads) pkv_build_step_kernel(const Step
   }
   if (!ok) sum_new = sum_need = sum_back = 0;
 
-  // entry i of the table row that request b returns (i counts from w_b)
-  auto returned = [&](int r) {
+  auto cached_of = [&](int b) { return local ? s_cached[b] : a.cached[b]; };
+  auto held_of = [&](int b) { return local ? s_held[b] : a.held[b]; };
+  auto want_of = [&](int b) { return blocks_for(a, cached_of(b) + (s_new[b + 1] - s_new[b])); };
+  auto returned = [&](int r) {                    // released block r, from its table row
     const int b = owner_of(s_back, a.B, r);
-    const int w = blocks_for(a.cached[b] + a.fresh[b], a.bs);
-    return a.tables[(size_t)b * a.max_blocks + w + (r - s_back[b])];
+    return a.tables[(size_t)b * a.max_blocks + want_of(b) + (r - s_back[b])];
   };
   auto needed = [&](int k) {                      // F'[top - 1 - k]
     const int i = top - 1 - k;
@@ -161,64 +203,95 @@ __global__ void __launch_bounds__(kStepThreads) pkv_build_step_kernel(const Step
   };
   auto in_pool = [&](int blk) { return blk >= 0 && (long long)blk < a.num_blocks; };
 
-  const int gid = rank * kStepThreads + tid, gstep = ncta * kStepThreads;
-  // tokens (those that the lists have room for): kU of a thread's in flight at once (each is a chain of a search
-  // and two dependent loads)
-  constexpr int kU = 4;
-  for (long long t0 = gid; t0 < a.max_tokens; t0 += (long long)gstep * kU) {
-    int pos[kU];
-    long long slot[kU];
+  // Tokens (those that the lists have room for) from the first warps on,
+  // needed blocks from the last on, released ones from the middle, so that
+  // the three run side by side in a small step.
+  const int gid = rank * nthr + tid, gstep = ncta * nthr;
+  constexpr int kU = 2;                           // chains of a lane in flight in a large one
+  const int nu = a.max_tokens > gstep ? kU : 1;
+  for (int w0 = gid >> 5; (long long)w0 * 32 * nu < a.max_tokens; w0 += gstep >> 5) {
+    const int first = w0 * 32 * nu + lane;
+    int pos[kU], blk[kU], off[kU], b = 0;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const long long t = t0 + (long long)u * gstep;
-      pos[u] = 0;
-      slot[u] = -1;
-      if (t < sum_new) {
-        const int b = owner_of(s_new, a.B, (int)t);
-        pos[u] = a.cached[b] + ((int)t - s_new[b]);
-        const int lb = pos[u] / a.bs, h = a.held[b];
-        const int blk = lb < h ? a.tables[(size_t)b * a.max_blocks + lb] : needed(s_need[b] + (lb - h));
-        if (in_pool(blk)) slot[u] = (long long)blk * a.bs + (pos[u] - lb * a.bs);
-        else raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
+      const int t = first + 32 * u;
+      pos[u] = off[u] = 0;
+      blk[u] = -1;
+      if (u < nu && t < sum_new && t < a.max_tokens) {
+        b = u == 0 ? owner_of(s_new, a.B, t) : owner_from(s_new, a.B, b, t);
+        pos[u] = cached_of(b) + (t - s_new[b]);
+        const int lb = div_bs(a, pos[u]), held = held_of(b);
+        off[u] = pos[u] - lb * a.bs;
+        blk[u] = lb < held ? a.tables[(size_t)b * a.max_blocks + lb] : needed(s_need[b] + (lb - held));
       }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const long long t = t0 + (long long)u * gstep;
-      if (t < a.max_tokens) {
-        a.slots[t] = slot[u];
+      const int t = first + 32 * u;
+      if (u < nu && t < a.max_tokens) {
+        const bool fits = in_pool(blk[u]);
+        if (!fits && t < sum_new) raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
+        a.slots[t] = fits ? (long long)blk[u] * a.bs + off[u] : -1;
         a.positions[t] = pos[u];
       }
     }
   }
-  for (int k = gid; k < sum_need; k += gstep) {
+  for (int k = gstep - 1 - gid; k < sum_need; k += gstep) {
     const int b = owner_of(s_need, a.B, k);
     const int blk = needed(k);
     if (!in_pool(blk)) raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
-    a.tables[(size_t)b * a.max_blocks + a.held[b] + (k - s_need[b])] = blk;
+    a.tables[(size_t)b * a.max_blocks + held_of(b) + (k - s_need[b])] = blk;
   }
-  for (int r = gid; r < sum_back; r += gstep) a.free_blocks[count + r] = returned(r);
-  for (int b = gid; b <= a.B; b += gstep) a.cu[b] = !ok ? 0 : b < a.B ? s_new[b] : sum_new;
+  const int mid = gid >= gstep / 2 ? gid - gstep / 2 : gid + gstep - gstep / 2;
+  for (int r = mid; r < sum_back; r += gstep) a.free_blocks[count + r] = returned(r);
+  for (int b = gid; b <= a.B; b += gstep) a.cu[b] = ok ? s_new[b] : 0;
 
   // behind every CTA's last read: the outputs that may be the inputs' memory
   if (ncta > 1) cluster_sync_all();
   else __syncthreads();
   for (int b = gid; b < a.B; b += gstep) {
-    const int c = a.cached[b], n = a.fresh[b], h = a.held[b];
-    a.lens[b] = ok ? c + n : 0;
-    a.held_out[b] = ok ? blocks_for(c + n, a.bs) : h;
+    const int cb = cached_of(b), hb = held_of(b);
+    a.lens[b] = ok ? cb + (s_new[b + 1] - s_new[b]) : 0;
+    a.held_out[b] = ok ? want_of(b) : hb;
   }
   if (gid == 0) *a.free_count_out = ok ? top - sum_need : count;
 }
 
-pkv_status launch_build_step(const StepArgs &a, cudaStream_t stream) {
-  const size_t smem = (size_t)3 * a.B * sizeof(int);
+// Whether clusters of kStepWide CTAs (past the portable 8) fit this device.
+template <int IPT>
+static bool wide_fits() {
+  static int known[64] = {0};      // 0 unknown, 1 yes, 2 no
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  if (known[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kStepWide);
+    cfg.blockDim = dim3(kStepMaxThreads);
+    cfg.dynamicSmemBytes = kStepMaxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kStepWide;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok = cudaFuncSetAttribute(pkv_build_step_kernel<IPT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, pkv_build_step_kernel<IPT>, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();
+    known[dev] = ok ? 1 : 2;
+  }
+  return known[dev] == 1;
+}
+
+template <int IPT>
+static pkv_status launch_step(const StepArgs &a, int ctas, int threads, cudaStream_t stream) {
+  const size_t smem = (size_t)(a.B <= kStepSmemB ? 5 : 3) * ((a.B + 4) & ~3) * sizeof(int);
   static int configured[64] = {0};
-  if (!allow_smem(pkv_build_step_kernel, smem, configured)) return PKV_ERR_CUDA;
-  const int ctas = a.max_tokens > 4 * kStepThreads ? kStepCluster : 1;
+  if (!allow_smem(pkv_build_step_kernel<IPT>, kStepMaxSmem, configured)) return PKV_ERR_CUDA;
+  if (ctas == kStepWide && !wide_fits<IPT>()) ctas = kStepCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kStepThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -228,8 +301,17 @@ pkv_status launch_build_step(const StepArgs &a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, pkv_build_step_kernel, a) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, pkv_build_step_kernel<IPT>, a) != cudaSuccess) return PKV_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status launch_build_step(const StepArgs &a, cudaStream_t stream) {
+  const int most = a.B > a.max_tokens ? a.B : a.max_tokens;
+  const int ctas = most > kStepWideFrom ? kStepWide : most > kStepOneCta ? kStepCluster : 1;
+  const int threads = most <= kStepSmall ? kStepSmall : kStepMaxThreads;   // fewer warps start and meet faster
+  if (a.B <= threads) return launch_step<1>(a, ctas, threads, stream);
+  if (a.B <= 4 * threads) return launch_step<4>(a, ctas, threads, stream);
+  return launch_step<kStepMaxB / kStepMaxThreads>(a, ctas, threads, stream);
 }
 
 }  // namespace pkv
@@ -275,6 +357,10 @@ extern "C" PKV_API pkv_status pkv_build_step(
     }
   StepArgs a = {block_tables, held, held_out, free_blocks, free_count, free_count_out, cached_lens,
                 new_lens, context_lens, cu_seqlens_q, slot_mapping, positions, err_flags,
-                num_blocks, free_capacity, B, max_blocks, block_size, (int)max_tokens};
+                num_blocks, free_capacity, B, max_blocks, block_size, (int)max_tokens, 0, 0};
+  // x / bs for 31-bit x by one product (Granlund and Montgomery 1994): with
+  // s = ceil(log2 bs), m = floor(2^32 (2^s - bs) / bs) + 1
+  while ((1LL << a.bs_shift) < block_size) ++a.bs_shift;
+  a.bs_mul = (uint32_t)(((1ULL << 32) * ((1ULL << a.bs_shift) - block_size)) / block_size + 1);
   return launch_build_step(a, reinterpret_cast<cudaStream_t>(stream));
 }

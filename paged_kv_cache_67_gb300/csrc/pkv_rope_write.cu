@@ -19,7 +19,6 @@
 namespace pkv {
 
 constexpr int kRopeWarps = 4;
-constexpr int kRopeBatch = 4;       // heads of a lane in flight
 constexpr int kRopeMaxPairs = 256;
 
 struct RopeArgs {
@@ -33,6 +32,8 @@ struct RopeArgs {
   long long max_pos, capacity;
   int axes, H, KVH, D, pairs, interleaved;
   int wpt;                              // warps per token
+  uint32_t used_axes;                   // axes that turn a pair
+  int quads;                            // the table's four-pair groups can be read as vectors
   uint32_t axis2[kRopeMaxPairs / 16];   // axis of pair j: two bits
 };
 
@@ -49,43 +50,28 @@ __global__ void __launch_bounds__(32 * kRopeWarps) pkv_rope_write_kernel(const _
   const long long t = gw / a.wpt;
   const int part = (int)(gw - t * a.wpt);
   if (t >= a.T) return;
+  // slot, positions and the first heads' vectors are independent loads: all in
+  // flight before the first is looked at
   const long long slot = __ldg(a.slots + t);
-  if (slot < 0) return;                                   // padding token
-  const int pairs = a.pairs, D = a.D;
-  const int rot_units = pairs / VEC;
-  const int units = rot_units + (D - 2 * pairs + 2 * VEC - 1) / (2 * VEC);
   int pos[4] = {0, 0, 0, 0};
-  bool ok = true;
 #pragma unroll
   for (int ax = 0; ax < 4; ++ax)
     if (ax < a.axes) pos[ax] = __ldg(a.pos + ax * a.pos_stride + t);
-  // every axis that a pair uses (bit ax of the mask), not only this lane's
-  uint32_t used = 0;
-  for (int j = lane; j < pairs; j += 32) used |= 1u << ((a.axis2[j >> 4] >> (2 * (j & 15))) & 3);
-  used = __reduce_or_sync(0xffffffffu, used);
-#pragma unroll
-  for (int ax = 0; ax < 4; ++ax)
-    if ((used >> ax) & 1) ok = ok && pos[ax] >= 0 && pos[ax] < a.max_pos;
-  if (!ok) {
-    if (lane == 0 && part == 0) raise_flag(a.err, PKV_FLAG_POSITION);
-    return;
-  }
-  const bool in_pool = slot < a.capacity;
-  if (!in_pool && lane == 0 && part == 0) raise_flag(a.err, PKV_FLAG_SLOT_OUT_OF_RANGE);
-
+  const int pairs = a.pairs, D = a.D;
+  const int rot_units = pairs / VEC;
+  const int units = rot_units + (D - 2 * pairs + 2 * VEC - 1) / (2 * VEC);
   const int hpw = units >= 32 ? 1 : 32 / units;           // heads side by side in a warp
   const int hl = units >= 32 ? 0 : lane / units;
   const int heads = a.H + 2 * a.KVH;
   const T *qs = reinterpret_cast<const T *>(a.q) + t * a.q_stride;
   const T *ks = reinterpret_cast<const T *>(a.k) + t * a.k_stride;
   const T *vs = reinterpret_cast<const T *>(a.v) + t * a.v_stride;
-  T *qd = reinterpret_cast<T *>(a.q_out) + t * (long long)a.H * D;
-  T *kd = reinterpret_cast<T *>(a.kc) + (in_pool ? slot : 0) * (long long)a.KVH * D;
-  T *vd = reinterpret_cast<T *>(a.vc) + (in_pool ? slot : 0) * (long long)a.KVH * D;
+  const bool in_pool = slot < a.capacity;
+  const int hstep = a.wpt * hpw;
 
   for (int u0 = 0; u0 < units; u0 += 32) {                // one pass unless a head has more than 32 units
     const int unit = units >= 32 ? u0 + lane : lane - hl * units;
-    if (hl >= hpw || unit >= units) continue;
+    const bool has = hl < hpw && unit < units;
     const bool turns = unit < rot_units;
     int e0, e1;                                           // the unit's two vectors
     if (turns) {
@@ -96,70 +82,99 @@ __global__ void __launch_bounds__(32 * kRopeWarps) pkv_rope_write_kernel(const _
       e1 = e0 + VEC;
     }
     const bool second = e1 < D;
+    V x, y;
+    auto load = [&](int h) {
+      if (has && h < heads) {
+        const T *src = h < a.H ? qs + h * D : h < a.H + a.KVH ? ks + (h - a.H) * D : vs + (h - a.H - a.KVH) * D;
+        x = *reinterpret_cast<const V *>(src + e0);
+        if (second) y = *reinterpret_cast<const V *>(src + e1);
+      }
+    };
+    int h = part * hpw + hl;
+    load(h);
+    if (u0 == 0) {
+      if (slot < 0) return;                               // padding token
+      bool ok = true;
+#pragma unroll
+      for (int ax = 0; ax < 4; ++ax)
+        if ((a.used_axes >> ax) & 1) ok = ok && pos[ax] >= 0 && pos[ax] < a.max_pos;
+      if (!ok) {
+        if (lane == 0 && part == 0) raise_flag(a.err, PKV_FLAG_POSITION);
+        return;
+      }
+      if (!in_pool && lane == 0 && part == 0) raise_flag(a.err, PKV_FLAG_SLOT_OUT_OF_RANGE);
+    }
+    if (!has) continue;
+    T *qd = reinterpret_cast<T *>(a.q_out) + t * (long long)a.H * D;
+    T *kd = reinterpret_cast<T *>(a.kc) + (in_pool ? slot : 0) * (long long)a.KVH * D;
+    T *vd = reinterpret_cast<T *>(a.vc) + (in_pool ? slot : 0) * (long long)a.KVH * D;
     float c[VEC], s[VEC];
     if (turns) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int j = unit * VEC + i;
+      auto row_of = [&](int j) {
         const int ax = (a.axis2[j >> 4] >> (2 * (j & 15))) & 3;
         const int p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
-        const float *row = a.cos_sin + (long long)p * (2 * pairs) + j;
-        c[i] = __ldg(row);
-        s[i] = __ldg(row + pairs);
+        return a.cos_sin + (long long)p * (2 * pairs) + j;
+      };
+      if (VEC % 4 == 0 && a.quads) {                      // four pairs of one axis: one load
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+          const float *row = row_of(unit * VEC + 4 * i);
+          const float4 cv = __ldg(reinterpret_cast<const float4 *>(row));
+          const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + pairs));
+          c[4 * i] = cv.x; c[4 * i + 1] = cv.y; c[4 * i + 2] = cv.z; c[4 * i + 3] = cv.w;
+          s[4 * i] = sv.x; s[4 * i + 1] = sv.y; s[4 * i + 2] = sv.z; s[4 * i + 3] = sv.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float *row = row_of(unit * VEC + i);
+          c[i] = __ldg(row);
+          s[i] = __ldg(row + pairs);
+        }
       }
     }
-    for (int h0 = part * hpw + hl; h0 < heads; h0 += a.wpt * hpw * kRopeBatch) {
-      V x[kRopeBatch], y[kRopeBatch];
+    // one head at a time: more loads in flight a lane cost registers and with
+    // them warps (two heads 93 us, four 103, one 77 at 16384 tokens of 32 + 8
+    // + 8 heads of 128)
+    for (; h < heads; h += hstep) {
+      if (h != part * hpw + hl) load(h);
+      if (h >= a.H && !in_pool) continue;
+      T *dst = h < a.H ? qd + h * D : h < a.H + a.KVH ? kd + (h - a.H) * D : vd + (h - a.H - a.KVH) * D;
+      if (turns && h < a.H + a.KVH) {
+        float fx[VEC], fy[VEC];
 #pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i) {
-        const int h = h0 + i * a.wpt * hpw;
-        if (h < heads) {
-          const T *src = h < a.H ? qs + h * D : h < a.H + a.KVH ? ks + (h - a.H) * D : vs + (h - a.H - a.KVH) * D;
-          x[i] = *reinterpret_cast<const V *>(src + e0);
-          if (second) y[i] = *reinterpret_cast<const V *>(src + e1);
+        for (int n = 0; n < VEC; ++n) {
+          fx[n] = to_f32<T>(x.e[n]);
+          fy[n] = to_f32<T>(y.e[n]);
         }
-      }
-#pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i) {
-        const int h = h0 + i * a.wpt * hpw;
-        if (h >= heads || (h >= a.H && !in_pool)) continue;
-        T *dst = h < a.H ? qd + h * D : h < a.H + a.KVH ? kd + (h - a.H) * D : vd + (h - a.H - a.KVH) * D;
-        if (turns && h < a.H + a.KVH) {
-          float fx[VEC], fy[VEC];
+        if (a.interleaved) {                              // pairs are neighbours: x holds the first VEC / 2 of them
+          float z[2 * VEC];
 #pragma unroll
           for (int n = 0; n < VEC; ++n) {
-            fx[n] = to_f32<T>(x[i].e[n]);
-            fy[n] = to_f32<T>(y[i].e[n]);
+            z[n] = fx[n];
+            z[VEC + n] = fy[n];
           }
-          if (a.interleaved) {                            // pairs are neighbours: x holds the first VEC / 2 of them
-            float z[2 * VEC];
 #pragma unroll
-            for (int n = 0; n < VEC; ++n) {
-              z[n] = fx[n];
-              z[VEC + n] = fy[n];
-            }
+          for (int n = 0; n < VEC; ++n) {
+            const float p = z[2 * n], q = z[2 * n + 1];
+            z[2 * n] = fmaf(p, c[n], -(q * s[n]));
+            z[2 * n + 1] = fmaf(q, c[n], p * s[n]);
+          }
 #pragma unroll
-            for (int n = 0; n < VEC; ++n) {
-              const float p = z[2 * n], q = z[2 * n + 1];
-              z[2 * n] = fmaf(p, c[n], -(q * s[n]));
-              z[2 * n + 1] = fmaf(q, c[n], p * s[n]);
-            }
+          for (int n = 0; n < VEC; ++n) {
+            x.e[n] = from_f32<T>(z[n]);
+            y.e[n] = from_f32<T>(z[VEC + n]);
+          }
+        } else {
 #pragma unroll
-            for (int n = 0; n < VEC; ++n) {
-              x[i].e[n] = from_f32<T>(z[n]);
-              y[i].e[n] = from_f32<T>(z[VEC + n]);
-            }
-          } else {
-#pragma unroll
-            for (int n = 0; n < VEC; ++n) {
-              x[i].e[n] = from_f32<T>(fmaf(fx[n], c[n], -(fy[n] * s[n])));
-              y[i].e[n] = from_f32<T>(fmaf(fy[n], c[n], fx[n] * s[n]));
-            }
+          for (int n = 0; n < VEC; ++n) {
+            x.e[n] = from_f32<T>(fmaf(fx[n], c[n], -(fy[n] * s[n])));
+            y.e[n] = from_f32<T>(fmaf(fy[n], c[n], fx[n] * s[n]));
           }
         }
-        *reinterpret_cast<V *>(dst + e0) = x[i];
-        if (second) *reinterpret_cast<V *>(dst + e1) = y[i];
       }
+      *reinterpret_cast<V *>(dst + e0) = x;
+      if (second) *reinterpret_cast<V *>(dst + e1) = y;
     }
   }
 }
@@ -228,9 +243,13 @@ extern "C" PKV_API pkv_status pkv_rope_write(
       (q_out == q && q_token_stride != (int64_t)H * head_dim))
     return PKV_ERR_INVALID_ARG;
   RopeArgs a = {};
-  for (int j = 0; pair_axis && j < rot_dim / 2; ++j) {
-    if (pair_axis[j] >= num_axes) return PKV_ERR_INVALID_ARG;
-    a.axis2[j >> 4] |= (uint32_t)pair_axis[j] << (2 * (j & 15));
+  a.quads = rot_dim % 8 == 0 && reinterpret_cast<uintptr_t>(cos_sin) % 16 == 0;
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    const int axis = pair_axis ? pair_axis[j] : 0;
+    if (axis >= num_axes) return PKV_ERR_INVALID_ARG;
+    a.axis2[j >> 4] |= (uint32_t)axis << (2 * (j & 15));
+    a.used_axes |= 1u << axis;
+    if (pair_axis && axis != pair_axis[j & ~3]) a.quads = 0;   // a group over two axes
   }
   if (num_tokens == 0) return PKV_OK;
   if (!q_out || !k_cache || !v_cache || !q || !k || !v || !positions || !slot_mapping ||
