@@ -1,10 +1,10 @@
 // pkv_chunk_tc.cu -- chunk attention for bf16 / fp16 and many rows per key
-// (long chunks, drafts of grouped heads), head_dim 64 or 128, on the
+// (long chunks, drafts of grouped heads), head_dim 64 to 256, on the
 // 5th-generation tensor cores (see pkv_chunk.cuh for rows, masks and scores).
 //
 // Three launches.
 //   plan   (one CTA) lists the units of work: 256 packed rows (two 128-row
-//          tiles) of a sequence x one part of the keys they see, most key
+//          tiles; one at head_dim 192 and 256) of a sequence x one part of the keys they see, most key
 //          tiles first, so that the long ones start first.
 //   main   persistent, a CTA per SM, claims (unit, head subgroup) items from
 //          a counter; roles as in causal prefill: two softmax warpgroups, one
@@ -37,21 +37,20 @@
 namespace pkv {
 
 constexpr int kCtRows = 128;     // packed rows per softmax warpgroup (MMA M)
-constexpr int kCtGroups = 2;     // row tiles per item
+constexpr int kCtMaxGroups = 2;  // row tiles per item: 2, or 1 where O's columns leave no room for a second (D > 128)
 constexpr int kCtTile = 128;     // keys per tile
 constexpr int kCtMaxStages = 4;  // of the K ring, and of the V ring
-constexpr int kCtSoftmaxWarps = 4 * kCtGroups; // warps 0-3, 4-7; then K producer, MMA, scheduler, V producer
-constexpr int kCtThreads = 32 * (kCtSoftmaxWarps + 4);
-// Registers: the launch has 384 x 168 = 64512; the softmax warps take 200
-// each and the others 104 (256 x 200 + 128 x 104 = 64512).  At 216 / 72 the
-// MMA issuer spills (plain scores 1065 TFLOP/s against 1121), at 184 / 136
-// the softmax does.
+// Warps: four softmax warps per group, then K producer, MMA, scheduler and V
+// producer.  Registers with two groups: the launch has 384 x 168 = 64512; the
+// softmax warps take 200 each and the others 104 (256 x 200 + 128 x 104 =
+// 64512).  At 216 / 72 the MMA issuer spills (plain scores 1065 TFLOP/s
+// against 1121), at 184 / 136 the softmax does.  One group needs no split.
 constexpr int kCtRegsLaunch = 168, kCtRegsSoftmax = 200, kCtRegsOther = 104;
-static_assert(32 * kCtSoftmaxWarps * kCtRegsSoftmax + 128 * kCtRegsOther <= kCtThreads * kCtRegsLaunch,
+static_assert(32 * 4 * kCtMaxGroups * kCtRegsSoftmax + 128 * kCtRegsOther <= 32 * (4 * kCtMaxGroups + 4) * kCtRegsLaunch,
               "the split cannot exceed what the launch holds");
+__host__ __device__ constexpr int ct_groups(int D) { return D <= 128 ? 2 : 1; }
 constexpr int kCtQRegion = kCtRows * 128;      // 128 rows x 64 elements of 16 bits
 constexpr int kCtKVRegion = kCtTile * 128;
-constexpr int kCtReaders = 3 + 4 * kCtGroups;  // of a published item
 constexpr int kCtPlanThreads = 1024;
 constexpr int kCtClasses = 256;                // plan: key tiles of a unit, the most first
 
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const Ct
   __shared__ int s_warp[32];
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (kCtGroups * kCtRows) >> a.gshift;   // queries per unit
+  const int per = (ct_groups(a.c.D) * kCtRows) >> a.gshift;   // queries per unit
   for (int i = tid; i < kCtClasses; i += kCtPlanThreads) s_cls[i] = 0;
   // the (sequence, tile) list
   int total = 0;
@@ -200,12 +199,16 @@ __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const Ct
 
 template <int D>
 struct CtShape {
+  static constexpr int kGroups = ct_groups(D);
+  static constexpr int kSoftmaxWarps = 4 * kGroups;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+  static constexpr int kReaders = 3 + kSoftmaxWarps;            // of a published item
   static constexpr int kRegions = D / 64;
   static constexpr int kQBytes = kRegions * kCtQRegion;         // one group's query tile
   static constexpr int kKVBytes = kRegions * kCtKVRegion;       // one K (or V) tile
   static constexpr int kQOff = 0;                               // [group]
-  static constexpr int kKStages = D == 64 ? 4 : 2, kVStages = D == 64 ? 4 : 3;
-  static constexpr int kKOff = kQOff + kCtGroups * kQBytes;     // [stage]
+  static constexpr int kKStages = D == 64 ? 4 : D <= 192 ? 2 : 1, kVStages = D == 64 ? 4 : D == 128 ? 3 : 1;
+  static constexpr int kKOff = kQOff + kGroups * kQBytes;       // [stage]
   static constexpr int kVOff = kKOff + kKStages * kKVBytes;     // [stage]
   static constexpr int kBarOff = kVOff + kVStages * kKVBytes;
   static constexpr int kPairOff = kBarOff + 1024;               // group 1's m, l of 128 rows
@@ -219,7 +222,7 @@ struct __align__(16) CtItem {
   int kind, sub, b, i0;          // head subgroup, sequence, first query in the sequence
   int q0, qlen, n, queries;      // the sequence's first row; queries of the item
   int t0, t1, lo, part;          // the part's keys, the unit's first seen key
-  int nt[kCtGroups];             // key tiles each group works on
+  int nt[kCtMaxGroups];             // key tiles each group works on
   int ntiles;                    // key tiles the item loads
   int nparts;                    // negative: both groups share one row tile (then -nparts parts)
   __device__ __forceinline__ bool pair() const { return nparts < 0; }
@@ -228,10 +231,11 @@ struct __align__(16) CtItem {
 static_assert(sizeof(CtItem) == 64, "four 16-byte words");
 
 template <int D, typename T, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kCtThreads, 1)
+__global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
     pkv_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CtArgs ta) {
   using Sh = CtShape<D>;
+  constexpr int kGroups = Sh::kGroups, kSoftmaxWarps = Sh::kSoftmaxWarps;
   const ChunkArgs &a = ta.c;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -240,12 +244,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   uint64_t *v_full = k_full + kCtMaxStages;      // released separately, each through its
   uint64_t *k_empty = v_full + kCtMaxStages;     // own ring and producer
   uint64_t *v_empty = k_empty + kCtMaxStages;
-  uint64_t *q_full = v_empty + kCtMaxStages;     // [kCtGroups]: the group's query tile landed
-  uint64_t *q_empty = q_full + kCtGroups;        // its last S of an item done
-  uint64_t *s_full = q_empty + kCtGroups;        // S of its current tile
-  uint64_t *p_full = s_full + kCtGroups;         // P of its current tile
-  uint64_t *o_done = p_full + kCtGroups;         // its last P . V of an item done
-  uint64_t *item_full = o_done + kCtGroups;      // [2]
+  uint64_t *q_full = v_empty + kCtMaxStages;     // [groups]: the group's query tile landed
+  uint64_t *q_empty = q_full + kCtMaxGroups;        // its last S of an item done
+  uint64_t *s_full = q_empty + kCtMaxGroups;        // S of its current tile
+  uint64_t *p_full = s_full + kCtMaxGroups;         // P of its current tile
+  uint64_t *o_done = p_full + kCtMaxGroups;         // its last P . V of an item done
+  uint64_t *item_full = o_done + kCtMaxGroups;      // [2]
   uint64_t *item_empty = item_full + 2;          // [2]
   uint64_t *pair_full = item_empty + 2;          // group 1's state of a shared row tile is there
   uint64_t *pair_empty = pair_full + 1;          // group 0 has read it
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
   int *abort_flag = reinterpret_cast<int *>(mma_done + 2);
   CtItem *items = reinterpret_cast<CtItem *>(bars + 36);  // [2], 16-byte aligned
-  static_assert(4 * kCtMaxStages + 5 * kCtGroups + 4 + 3 + 2 <= 36, "the barriers end before the items");
+  static_assert(4 * kCtMaxStages + 5 * kCtMaxGroups + 4 + 3 + 2 <= 36, "the barriers end before the items");
   float *s_pair = reinterpret_cast<float *>(sm + Sh::kPairOff);  // [2][128]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    for (int g = 0; g < kCtGroups; ++g) {
+    for (int g = 0; g < kGroups; ++g) {
       mbar_init(&q_full[g], 1);
       mbar_init(&q_empty[g], 1);
       mbar_init(&s_full[g], 1);
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&item_full[s], 1);
-      mbar_init(&item_empty[s], kCtReaders);
+      mbar_init(&item_empty[s], Sh::kReaders);
     }
     mbar_init(pair_full, 128);
     mbar_init(pair_empty, 128);
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
-  if (warp == kCtSoftmaxWarps) tmem_alloc(tmem_holder, Sh::kTmemCols);
+  if (warp == kSoftmaxWarps) tmem_alloc(tmem_holder, Sh::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -299,14 +303,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   };
   auto aborted = [&]() { return *(volatile int *)abort_flag != 0; };
 
-  if (warp >= kCtSoftmaxWarps) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtRegsOther));
-  if (warp == kCtSoftmaxWarps + 2) {
+  if (warp >= kSoftmaxWarps) {
+  if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtRegsOther));
+  if (warp == kSoftmaxWarps + 2) {
     // ------------------------------------------------------------ scheduler
     griddep_wait();                                // the plan's units (every other role waits for an item)
     const unsigned total = (unsigned)*(volatile int *)ta.n_units * (unsigned)ta.subs;
     unsigned w = blockIdx.x;
-    int it = 0, ig[kCtGroups] = {0, 0};
+    int it = 0, ig[kCtMaxGroups] = {0, 0};
     bool ok = true;
     while (true) {
       CtItem item;
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         item.q0 = s.q0;
         item.qlen = s.qlen;
         item.n = s.n;
-        item.queries = min(kCtGroups * per, s.qlen - item.i0);
+        item.queries = min(kGroups * per, s.qlen - item.i0);
         item.kind = item.t1 > 0 ? 1 : 2;
         if (item.kind == 1) {
           // one past the last key the group's rows see before the part's end
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           item.nt[0] = tiles_to(item.i0 + min(per, item.queries) - 1);
           item.nt[1] = item.queries > per ? tiles_to(item.i0 + item.queries - 1) : 0;
           item.ntiles = max(item.nt[0], item.nt[1]);
-          if (item.queries <= per) {
+          if (kGroups == 2 && item.queries <= per) {
             item.nparts = -item.nparts;
             item.nt[1] = item.ntiles / 2;
             item.nt[0] = item.ntiles - item.nt[1];
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (item.kind < 0) break;
       if (item.kind == 1) {
 #pragma unroll
-        for (int g = 0; g < kCtGroups; ++g) {
+        for (int g = 0; g < kGroups; ++g) {
           if (!ok || item.nt[g] == 0) continue;
           if (ig[g] > 0) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_empty[g], (ig[g] - 1) & 1)) && !aborted();
@@ -383,15 +387,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     if (a.max_parts > 1) griddep_launch_dependents();  // the merge: it reads nothing before it has waited
     // the last query tiles land before the CTA can end (bounded)
 #pragma unroll
-    for (int g = 0; g < kCtGroups; ++g)
+    for (int g = 0; g < kGroups; ++g)
       if (ig[g] > 0) mbar_wait_bounded(&q_full[g], (ig[g] - 1) & 1);
-  } else if (warp == kCtSoftmaxWarps || warp == kCtSoftmaxWarps + 3) {
+  } else if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 3) {
     // ----------------------------------------------------------- producers
     // one warp streams the keys, one the values: per item and tile the boxes
     // (one per lane: some keys of one 64-column region) once the tile that
     // used the stage before has been read.  In one warp a tile's keys would
     // wait behind the values before them.
-    const bool is_v = warp != kCtSoftmaxWarps;
+    const bool is_v = warp != kSoftmaxWarps;
     const int stages = is_v ? Sh::kVStages : Sh::kKStages;
     uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
     const CUtensorMap *map = is_v ? &tmV : &tmK;
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     if (!ok && lane == 0) abort_cta();
     // the last fills land before the CTA can end (bounded)
     for (int r = max(0, issued - stages); r < issued; ++r) mbar_wait_bounded(&full[r % stages], (r / stages) & 1);
-  } else if (warp == kCtSoftmaxWarps + 1) {
+  } else if (warp == kSoftmaxWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t idesc_s = umma_idesc_f16(128, kCtTile, bf16, false);
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       // the next item is issued as soon as that item, its query tile and its
       // first keys are there, so group 0's softmax starts on the next item
       // while group 1 finishes this one.
-      int it = 0, ring0 = 0, ig[kCtGroups] = {0, 0}, tcnt[kCtGroups] = {0, 0};
+      int it = 0, ring0 = 0, ig[kCtMaxGroups] = {0, 0}, tcnt[kCtMaxGroups] = {0, 0};
       CtItem nx;
       bool have_nx = false;   // the next item is read already
       bool early = false;     // ... and group 0's first S of it issued
@@ -501,7 +505,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (item.ntiles == 0) continue;
         const bool pre = early;
         early = false;
-        if (item.pair()) {
+        if (kGroups == 2 && item.pair()) {
           // tile j belongs to group j & 1
           auto start_s = [&](int j) {  // S of tile j, and what its products free
             const int g = j & 1, ring = ring0 + j;
@@ -531,12 +535,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           ring0 += item.ntiles;
           if (ok && aborted()) ok = false;
 #pragma unroll
-          for (int g = 0; g < kCtGroups; ++g) ig[g] += item.nt[g] > 0;
+          for (int g = 0; g < kGroups; ++g) ig[g] += item.nt[g] > 0;
           continue;
         }
         ok = mbar_wait_bounded(&k_full[ring0 % Sh::kKStages], (ring0 / Sh::kKStages) & 1);
 #pragma unroll
-        for (int g = 0; g < kCtGroups; ++g)
+        for (int g = 0; g < kGroups; ++g)
           if (ok && item.nt[g] > 0 && !(g == 0 && pre)) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
         if (!ok || aborted()) {
           ok = false;
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < kCtGroups; ++g) {
+        for (int g = 0; g < kGroups; ++g) {
           if (item.nt[g] == 0 || (g == 0 && pre)) continue;
           issue_s(g, ring0);
           if (item.nt[g] == 1) umma_commit(&q_empty[g]);  // the group's last S of the item
@@ -576,7 +580,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           const int ring = ring0 + j;
           bool v_ready = false, k_ready = false;
 #pragma unroll
-          for (int g = 0; g < kCtGroups; ++g) {
+          for (int g = 0; g < kGroups; ++g) {
             if (!ok || j >= item.nt[g]) continue;
             if (g == 1 && j + 1 >= item.nt[0]) {
               // group 0 is done with this item: look for its next one while
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             tc_fence_after();
             issue_pv(g, ring, j > 0);
             // the tile's last P . V: its V slot is free once that has run
-            if (g == kCtGroups - 1 || j >= item.nt[g + 1]) umma_commit(&v_empty[ring % Sh::kVStages]);
+            if (g == kGroups - 1 || j >= item.nt[1]) umma_commit(&v_empty[ring % Sh::kVStages]);
             if (j + 1 < item.nt[g]) {
               if (!k_ready) {
                 ok = mbar_wait_bounded(&k_full[(ring + 1) % Sh::kKStages], ((ring + 1) / Sh::kKStages) & 1);
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         ring0 = ring_next;
         if (ok && aborted()) ok = false;
 #pragma unroll
-        for (int g = 0; g < kCtGroups; ++g) ig[g] += item.nt[g] > 0;
+        for (int g = 0; g < kGroups; ++g) ig[g] += item.nt[g] > 0;
       }
       if (!ok) abort_cta();
       umma_commit(mma_done);  // every product issued above has completed when this arrives
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCtRegsSoftmax));
+    if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCtRegsSoftmax));
     const int g = warp >> 2;                            // warpgroup = row tile
     const int quarter = warp & 3;
     const int r = 32 * quarter + lane;                  // row in the tile = tensor-memory lane
@@ -655,7 +659,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (item.kind < 0) break;
       // this thread's row: query i of the sequence, head h (rows past the
       // item's last query mirror it and are not written)
-      const bool pair = item.pair();
+      const bool pair = kGroups == 2 && item.pair();
       const int qi = (pair ? 0 : g * per) + (r >> ta.gshift);
       const bool real_row = qi < item.queries;
       const bool live = __any_sync(0xffffffffu, real_row);  // a warp without rows only keeps the barriers going
@@ -985,7 +989,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kCtSoftmaxWarps) tmem_dealloc(tmem, Sh::kTmemCols);
+  if (warp == kSoftmaxWarps) tmem_dealloc(tmem, Sh::kTmemCols);
   if (tid == 0) {
     // the last CTA puts the counters back (every claim's value was used
     // before the barrier, so it is performed already)
@@ -1006,15 +1010,16 @@ __global__ void __launch_bounds__(256) pkv_chunk_merge_kernel(const __grid_const
   griddep_wait();
   const ChunkArgs &a = ta.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (kCtGroups * kCtRows) >> ta.gshift;
+  constexpr int kRows = ct_groups(D) * kCtRows;
+  const int per = kRows >> ta.gshift;
   const int units = *ta.n_units;
-  // 8 rows (one per warp) of a unit's 256 x subs per block of work
-  const long long blocks_per_unit = (long long)ta.subs * (kCtGroups * kCtRows / 8);
+  // 8 rows (one per warp) of a unit's rows x subs per block of work
+  const long long blocks_per_unit = (long long)ta.subs * (kRows / 8);
   for (long long w = blockIdx.x; w < units * blocks_per_unit; w += gridDim.x) {
     const int un = (int)(w / blocks_per_unit), rest = (int)(w - un * blocks_per_unit);
     const CtUnit u = ta.units[un];
     if (u.part != 0 || u.nparts == 1) continue;
-    const int sub = rest / (kCtGroups * kCtRows / 8), r = (rest % (kCtGroups * kCtRows / 8)) * 8 + warp;
+    const int sub = rest / (kRows / 8), r = (rest % (kRows / 8)) * 8 + warp;
     const ChunkSeq s = chunk_seq(a, u.b, false);
     const int i = u.i0 + (r >> ta.gshift);
     if (i >= min(s.qlen, u.i0 + per)) continue;
@@ -1059,15 +1064,15 @@ int chunk_tc_gshift(int G) {     // log2 of the heads packed in a tile
   return s;
 }
 
-long long chunk_tc_items(int B, long long total_q, int H, int G, int max_q) {
+long long chunk_tc_items(int B, long long total_q, int H, int G, int D, int max_q) {
   const int sh = chunk_tc_gshift(G);
-  return ct_tiles_cap(B, total_q, max_q, (kCtGroups * kCtRows) >> sh) * (H >> sh);
+  return ct_tiles_cap(B, total_q, max_q, (ct_groups(D) * kCtRows) >> sh) * (H >> sh);
 }
 
 static size_t ct_align(size_t x) { return (x + 255) & ~size_t(255); }
 
-size_t chunk_tc_scratch(int B, long long total_q, int G, int max_q, long long parts) {
-  const long long tiles = ct_tiles_cap(B, total_q, max_q, (kCtGroups * kCtRows) >> chunk_tc_gshift(G));
+size_t chunk_tc_scratch(int B, long long total_q, int G, int D, int max_q, long long parts) {
+  const long long tiles = ct_tiles_cap(B, total_q, max_q, (ct_groups(D) * kCtRows) >> chunk_tc_gshift(G));
   return 256 + ct_align(tiles * sizeof(int4)) + ct_align(tiles * parts * sizeof(CtUnit));
 }
 
@@ -1096,7 +1101,7 @@ static pkv_status launch_ct(const CtArgs &a, const CUtensorMap &mq, const CUtens
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   const long long most = (long long)a.units_cap * a.subs;
   const int ctas = (int)(most < sms ? most : sms);
-  if (!launch_after(kern, ctas, kCtThreads, CtShape<D>::kSmem, stream, mq, mk, mv, a)) return PKV_ERR_CUDA;
+  if (!launch_after(kern, ctas, CtShape<D>::kThreads, CtShape<D>::kSmem, stream, mq, mk, mv, a)) return PKV_ERR_CUDA;
   if (a.c.max_parts > 1 && !launch_after(pkv_chunk_merge_kernel<D, T>, sms * 8, 256, 0, stream, a)) return PKV_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
@@ -1117,7 +1122,7 @@ pkv_status launch_chunk_tc(const ChunkArgs &c, pkv_dtype dt, char *scratch, int 
   a.gshift = chunk_tc_gshift(c.G);
   a.subs = c.H >> a.gshift;
   a.bshift = c.bs % 64 == 0 ? 6 : c.bs % 32 == 0 ? 5 : 4;
-  const long long tiles = ct_tiles_cap(c.B, c.total_q, c.max_q, (kCtGroups * kCtRows) >> a.gshift);
+  const long long tiles = ct_tiles_cap(c.B, c.total_q, c.max_q, (ct_groups(c.D) * kCtRows) >> a.gshift);
   if (tiles * c.max_parts * a.subs > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   a.tiles_cap = (int)tiles;
   a.units_cap = (int)(tiles * c.max_parts);
@@ -1131,11 +1136,17 @@ pkv_status launch_chunk_tc(const ChunkArgs &c, pkv_dtype dt, char *scratch, int 
       !encode_cache_map(&mk, c.k_cache, dt, c.num_blocks, c.bs, c.KVH, c.D, 1 << a.bshift) ||
       !encode_cache_map(&mv, c.v_cache, dt, c.num_blocks, c.bs, c.KVH, c.D, 1 << a.bshift))
     return PKV_ERR_CUDA;
-  const bool bf = dt == PKV_BF16;
-  if (c.D == 128)
-    return bf ? launch_ct_form<128, __nv_bfloat16>(a, mq, mk, mv, sms, stream) : launch_ct_form<128, __half>(a, mq, mk, mv, sms, stream);
-  if (c.D == 64)
-    return bf ? launch_ct_form<64, __nv_bfloat16>(a, mq, mk, mv, sms, stream) : launch_ct_form<64, __half>(a, mq, mk, mv, sms, stream);
+  auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return dt == PKV_BF16 ? launch_ct_form<D, __nv_bfloat16>(a, mq, mk, mv, sms, stream)
+                          : launch_ct_form<D, __half>(a, mq, mk, mv, sms, stream);
+  };
+  switch (c.D) {
+    case 64: return pick(std::integral_constant<int, 64>());
+    case 128: return pick(std::integral_constant<int, 128>());
+    case 192: return pick(std::integral_constant<int, 192>());
+    case 256: return pick(std::integral_constant<int, 256>());
+  }
   return PKV_ERR_UNSUPPORTED;
 }
 
