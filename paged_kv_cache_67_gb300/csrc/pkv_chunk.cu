@@ -9,7 +9,7 @@
 
 namespace pkv {
 
-pkv_status launch_chunk_simt(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
+pkv_status launch_chunk_simt(const ChunkArgs &a, int rows, pkv_dtype dt, cudaStream_t stream);
 pkv_status launch_chunk_mma(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
 pkv_status launch_chunk_tc(const ChunkArgs &a, pkv_dtype dt, char *scratch, int sms, cudaStream_t stream);
 long long chunk_tc_items(int B, long long total_q, int H, int G, int D, int max_q);
@@ -19,6 +19,7 @@ size_t chunk_tc_scratch(int B, long long total_q, int G, int D, int max_q, long 
 // that the workspace's size needs no device.
 constexpr int kPlanSms = 152;
 constexpr int kChunkRows = 16;     // packed rows per CTA of the CUDA-core and mma.sync kernels
+constexpr int kChunkManyRows = 64; // of the CUDA-core kernel for long chunks
 constexpr int kMmaRows = 32;       // packed rows up to which the mma.sync kernel is taken where tcgen05 could be
 constexpr int kChunkMaxParts = 64;
 constexpr long long kChunkMaxKeys = 1LL << 30;  // keys of a context: positions plus a part stay in 32 bits
@@ -27,6 +28,7 @@ struct ChunkPlan {
   int kernel;         // 2 tcgen05, 1 mma.sync, 0 CUDA cores
   int P, max_parts;   // keys per part, parts per row
   int most_parts;     // parts per row of any call of these sizes (the workspace's)
+  int rows;           // packed rows per CTA (kernels 0 and 1)
   long long chunks;   // row chunks per (sequence, KV head)
 };
 
@@ -117,7 +119,8 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   // 16-bit tensors that TMA can read, in tokens chunks that never span two blocks
   p->kernel = tc_eligible(dt, D, bs) && aligned16 ? 1 : 0;
   if (p->kernel == 1 && mq * (H / KVH) > kMmaRows) p->kernel = 2;
-  p->chunks = ceil_div(mq * (H / KVH), kChunkRows);
+  p->rows = p->kernel == 0 && D <= 256 && mq * (H / KVH) > 2 * kChunkRows ? kChunkManyRows : kChunkRows;
+  p->chunks = ceil_div(mq * (H / KVH), p->rows);
   // a window bounds the keys a unit sees, unless a prefix reaches past it
   const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 63) : cap;
   if (p->kernel == 2) {
@@ -126,7 +129,7 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
     chunk_split(std::min(tc_parts_wanted(items, span), tc_parts_wanted(items, cap)), span, 512, partition_size, p);
     return true;
   }
-  const int per_sm = p->kernel == 0 ? 4 : D <= 192 ? 2 : 1;   // resident CTAs
+  const int per_sm = p->kernel == 0 ? (p->rows == kChunkRows ? 4 : 2) : D <= 192 ? 2 : 1;   // resident CTAs
   const long long units = (long long)B * KVH * p->chunks, slots = (long long)kPlanSms * per_sm;
   chunk_split(std::min(parts_wanted(units, slots, span), parts_wanted(units, slots, cap)), span, 128, partition_size, p);
   return true;
@@ -270,7 +273,7 @@ PKV_API pkv_status pkv_chunk_attention(
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (plan.kernel == 2) return launch_chunk_tc(a, dt, scratch, sms, s);
   if (plan.kernel == 1) return launch_chunk_mma(a, dt, s);
-  return launch_chunk_simt(a, dt, s);
+  return launch_chunk_simt(a, plan.rows, dt, s);
 }
 
 }  // extern "C"
