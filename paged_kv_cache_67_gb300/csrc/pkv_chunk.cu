@@ -20,6 +20,7 @@ size_t chunk_tc_scratch(int B, long long total_q, int G, int D, int max_q, long 
 constexpr int kPlanSms = 152;
 constexpr int kChunkRows = 16;     // packed rows per CTA of the CUDA-core and mma.sync kernels
 constexpr int kChunkManyRows = 64; // of the CUDA-core kernel for long chunks
+constexpr int kChunkFewRows = 4;   // and for single tokens of small groups
 constexpr int kMmaRows = 32;       // packed rows up to which the mma.sync kernel is taken where tcgen05 could be
 constexpr int kChunkMaxParts = 64;
 constexpr long long kChunkMaxKeys = 1LL << 30;  // keys of a context: positions plus a part stay in 32 bits
@@ -119,7 +120,9 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   // 16-bit tensors that TMA can read, in tokens chunks that never span two blocks
   p->kernel = tc_eligible(dt, D, bs) && aligned16 ? 1 : 0;
   if (p->kernel == 1 && mq * (H / KVH) > kMmaRows) p->kernel = 2;
-  p->rows = p->kernel == 0 && D <= 256 && mq * (H / KVH) > 2 * kChunkRows ? kChunkManyRows : kChunkRows;
+  const long long unit_rows = mq * (H / KVH);
+  p->rows = kChunkRows;
+  if (p->kernel == 0) p->rows = unit_rows <= kChunkFewRows ? kChunkFewRows : D <= 256 && unit_rows > 2 * kChunkRows ? kChunkManyRows : kChunkRows;
   p->chunks = ceil_div(mq * (H / KVH), p->rows);
   // a window bounds the keys a unit sees, unless a prefix reaches past it
   const long long span = window > 0 && !has_prefix ? std::min(cap, (long long)window + mq + 63) : cap;
@@ -129,7 +132,7 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
     chunk_split(std::min(tc_parts_wanted(items, span), tc_parts_wanted(items, cap)), span, 512, partition_size, p);
     return true;
   }
-  const int per_sm = p->kernel == 0 ? (p->rows == kChunkRows ? 4 : 2) : D <= 192 ? 2 : 1;   // resident CTAs
+  const int per_sm = p->kernel == 0 ? (p->rows == kChunkManyRows ? 2 : 4) : D <= 192 ? 2 : 1;   // resident CTAs
   const long long units = (long long)B * KVH * p->chunks, slots = (long long)kPlanSms * per_sm;
   chunk_split(std::min(parts_wanted(units, slots, span), parts_wanted(units, slots, cap)), span, 128, partition_size, p);
   return true;

@@ -5,15 +5,18 @@
 //
 // CTA = (part of the context, RT packed rows of a KV head, sequence), 128
 // threads; 32 keys at a time pass through shared memory.
-//   RT = 16, few rows per key, bound by the loads:
-//     S    thread = key x 4 rows: a key vector against four query vectors
-//     O    thread = columns tid, tid + 128, ... x 16 rows
+//   RT = 4 and 16, few rows per key, bound by instructions and loads:
+//     S    RT = 16: thread = key x 4 rows, a key vector against four query
+//          vectors; RT = 4: thread = key x 4 rows x a quarter of D (its warp's),
+//          the quarters added up by the softmax
+//     O    thread = columns tid, tid + 128, ... x RT rows
 //   RT = 64, long chunks, bound by the multiply-adds: 8 row groups x 16 columns
 //     S    thread = 8 rows x 2 keys: 10 shared loads feed 64 multiply-adds per
 //          4 columns of D, the query loads broadcast over 16 lanes
 //     O    thread = 8 rows x columns 4 tx + 64 j
 // The next tile's keys load while this one's softmax and O run, its values
-// while the next S runs (cp.async, one buffer each); block-table entries are
+// while the next S runs (cp.async, one buffer each: with two, fewer CTAs fit an
+// SM and decode at head_dim 128 took 880 us for 489); block-table entries are
 // read a tile ahead of that.
 #include "pkv_chunk.cuh"
 
@@ -31,7 +34,7 @@ __host__ __device__ constexpr int cs_stride(int D) {
 template <typename T, int RT>
 static size_t cs_smem(int D) {
   return (size_t)RT * cs_stride<float>(D) * 4 + 2 * (size_t)kCsTok * cs_stride<T>(D) * sizeof(T) +
-         4 * (size_t)(RT * (kCsTok + 4) + kCsTok * (RT + 4) + 4 * RT) + 4 * (2 * RT + 4) + 2 * kCsTok * sizeof(long long);
+         4 * (size_t)((RT == 4 ? 16 : RT) * (kCsTok + 4) + kCsTok * (RT + 4) + 4 * RT) + 4 * (2 * RT + 4) + 2 * kCsTok * sizeof(long long);
 }
 
 __device__ __forceinline__ void cs_copy16(uint32_t dst, const void *src, bool live) {  // zeros when not live
@@ -50,7 +53,7 @@ __device__ __forceinline__ float4 cs_ld4(const T *p) {
   return make_float4(to_f32<T>(e[0]), to_f32<T>(e[1]), to_f32<T>(e[2]), to_f32<T>(e[3]));
 }
 
-// EP: column steps of a thread in O (RT = 16: of 128, RT = 64: of 64).  AL:
+// EP: column steps of a thread in O (RT = 64: of 64, else of 128).  AL:
 // rows are whole, aligned 16-byte vectors.
 template <typename T, int RT, int EP, bool AL>
 __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkArgs a) {
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
   T *sK = reinterpret_cast<T *>(sQ + RT * QS);        // [32][KS]
   T *sV = sK + kCsTok * KS;                           // [32][KS]
   float *sS = reinterpret_cast<float *>(sV + kCsTok * KS);  // [RT][kSS] scores
-  float *sP = sS + RT * kSS;                          // [32][kPS] weights, transposed
+  float *sP = sS + (RT == 4 ? 16 : RT) * kSS;         // [32][kPS] weights, transposed  (RT = 4: sS is [4 quarters][4])
   float *s_alpha = sP + kCsTok * kPS;                 // [RT]
   float *s_m = s_alpha + RT, *s_l = s_m + RT, *s_slope = s_l + RT;  // [RT]
   int *s_lo = reinterpret_cast<int *>(s_slope + RT);  // [RT]
@@ -107,25 +110,31 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
   const int t0 = max(lo_min, base + slotp * a.P), t1 = min(hi_max, base + (slotp + 1) * a.P);
 
   // element offset of key t's row, -1 past the part's end
-  auto key_row = [&](int t) -> long long {
+  auto table_entry = [&](int t) { return t < t1 ? __ldg(a.tables + (size_t)b * a.max_blocks + t / a.bs) : 0; };
+  auto key_row = [&](int t, int phys) -> long long {
     if (t >= t1) return -1;
     const int lb = t / a.bs;
-    int phys = __ldg(a.tables + (size_t)b * a.max_blocks + lb);
     if (phys < 0 || (long long)phys >= a.num_blocks) {
       raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
       phys = 0;
     }
     return (((long long)phys * a.bs + (t - lb * a.bs)) * a.KVH + kvh) * D;
   };
+  const int row_pieces = max(1, D * (int)sizeof(T) / 16), first_row = tid / row_pieces, first_piece = tid % row_pieces;
   auto fetch = [&](T *dst, const void *cache, int tile) {  // 32 rows into shared memory
     const T *src = reinterpret_cast<const T *>(cache);
     const long long *rowp = s_row + (tile & 1) * kCsTok;
     if constexpr (AL) {
-      const int pieces = D * (int)sizeof(T) / 16;
-      for (int i = tid; i < kCsTok * pieces; i += kCsThreads) {
-        const int t = i / pieces, c = i - t * pieces;
+      const int pieces = row_pieces;
+      auto copy = [&](int t, int c) {
         const long long row = rowp[t];
         cs_copy16(smem_u32(dst + t * KS) + 16 * c, reinterpret_cast<const uint4 *>(src + (row < 0 ? 0 : row)) + c, row >= 0);
+      };
+      if (kCsThreads % pieces == 0) {           // a thread keeps to one piece of the row
+#pragma unroll 4
+        for (int t = first_row; t < kCsTok; t += kCsThreads / pieces) copy(t, first_piece);
+      } else {
+        for (int i = tid; i < kCsTok * pieces; i += kCsThreads) copy(i / pieces, i % pieces);
       }
     } else {
       for (int t = warp; t < kCsTok; t += kCsThreads / 32) {
@@ -136,7 +145,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
     cs_commit();
   };
   const int ntiles = t1 > t0 ? (t1 - t0 + kCsTok - 1) / kCsTok : 0;
-  if (tid < 2 * kCsTok) s_row[tid] = key_row(t0 + tid);   // the first two tiles
+  if (tid < 2 * kCsTok) s_row[tid] = key_row(t0 + tid, table_entry(t0 + tid));   // the first two tiles
   __syncthreads();
   if (ntiles > 0) {
     fetch(sK, a.k_cache, 0);
@@ -146,7 +155,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
     for (int d = lane; d < QS; d += 32)
       sQ[r * QS + d] = (r < rows && d < D) ? to_f32<T>(reinterpret_cast<const T *>(a.q)[out_row(r) * D + d]) : 0.f;
 
-  constexpr int kOR = RT == 16 ? 16 : 8, kOC = RT == 16 ? EP : 4 * EP;  // rows and columns of O a thread holds
+  constexpr int kOR = RT == 64 ? 8 : RT, kOC = RT == 64 ? 4 * EP : EP;  // rows and columns of O a thread holds
   float o[kOR][kOC];
 #pragma unroll
   for (int r = 0; r < kOR; ++r)
@@ -160,7 +169,23 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
     const int key0 = t0 + tile * kCsTok;
     cs_wait<1>();
     __syncthreads();                            // this tile's keys are there
-    if constexpr (RT == 16) {                   // key `lane`, rows 4 * warp ..
+    if constexpr (RT == 4) {                    // key `lane`, four rows, the warp's quarter of the columns
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const T *kr = sK + lane * KS;
+      const float4 *qr = reinterpret_cast<const float4 *>(sQ);
+      const int quads = (D + 3) / 4, from = quads * warp / 4, to = quads * (warp + 1) / 4;
+#pragma unroll 4
+      for (int d = from; d < to; ++d) {
+        const float4 kx = cs_ld4(kr + 4 * d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 qx = qr[r * (QS / 4) + d];
+          acc[r] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, acc[r]))));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sS[(4 * warp + r) * kSS + lane] = acc[r];
+    } else if constexpr (RT == 16) {            // key `lane`, rows 4 * warp ..
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       const T *kr = sK + lane * KS;
       const float4 *qr = reinterpret_cast<const float4 *>(sQ + 4 * warp * QS);
@@ -207,8 +232,8 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
         }
       }
     }
-    long long next_row = -1;                    // table entries of the tile after the next
-    if (tid < kCsTok) next_row = key_row(key0 + 2 * kCsTok + tid);
+    // table entries of the tile after the next, looked at only at the end
+    const int next_key = key0 + 2 * kCsTok + tid, next_phys = tid < kCsTok ? table_entry(next_key) : 0;
     __syncthreads();                            // scores there, keys free
     if (tile + 1 < ntiles) fetch(sK, a.k_cache, tile + 1);
     else cs_commit();
@@ -216,7 +241,14 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
       float x[kXs], mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kXs; ++i) {
-        x[i] = sS[srow * kSS + sub + kTpr * i];
+        if constexpr (RT == 4) {                // the quarters' sum, and the score
+          const float dot = (sS[srow * kSS + sub] + sS[(4 + srow) * kSS + sub]) + (sS[(8 + srow) * kSS + sub] + sS[(12 + srow) * kSS + sub]);
+          const int j = key0 + sub;
+          const bool vis = j < t1 && j >= s_lo[srow] && j < s_hi[srow];
+          x[i] = vis ? chunk_score(a, dot, s_slope[srow], sq.n - sq.qlen + row_query(srow), j) : -INFINITY;
+        } else {
+          x[i] = sS[srow * kSS + sub + kTpr * i];
+        }
         mx = fmaxf(mx, x[i]);
       }
 #pragma unroll
@@ -238,7 +270,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
     }
     cs_wait<1>();
     __syncthreads();                            // weights and this tile's values are there
-    const int r0 = RT == 16 ? 0 : 8 * ty;
+    const int r0 = RT == 64 ? 8 * ty : 0;
 #pragma unroll
     for (int r = 0; r < kOR; ++r) {
       const float al = s_alpha[r0 + r];
@@ -253,13 +285,13 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
         const float4 v = *reinterpret_cast<const float4 *>(sP + t * kPS + r0 + 4 * r4);
         p[4 * r4] = v.x; p[4 * r4 + 1] = v.y; p[4 * r4 + 2] = v.z; p[4 * r4 + 3] = v.w;
       }
-      if constexpr (RT == 16) {
+      if constexpr (RT != 64) {
 #pragma unroll
         for (int e = 0; e < EP; ++e) {
           const int d = tid + kCsThreads * e;
           const float v = d < D ? to_f32<T>(sV[t * KS + d]) : 0.f;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r][e] = fmaf(p[r], v, o[r][e]);
+          for (int r = 0; r < RT; ++r) o[r][e] = fmaf(p[r], v, o[r][e]);
         }
       } else {
 #pragma unroll
@@ -280,7 +312,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
     if (tile + 1 < ntiles) fetch(sV, a.v_cache, tile + 1);
     else cs_commit();
     // (read again only after the next barriers: K of tile + 2 is fetched behind two of them)
-    if (tid < kCsTok) s_row[(tile & 1) * kCsTok + tid] = next_row;
+    if (tid < kCsTok) s_row[(tile & 1) * kCsTok + tid] = key_row(next_key, next_phys);
   }
   cs_wait<0>();
   if (sub == 0) {
@@ -297,14 +329,14 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
   T *out = reinterpret_cast<T *>(a.out);
 #pragma unroll
   for (int r = 0; r < kOR; ++r) {
-    const int rr = RT == 16 ? r : 8 * ty + r;
+    const int rr = RT == 64 ? 8 * ty + r : r;
     if (rr >= rows) continue;
     const size_t row = out_row(rr), at = row * a.max_parts + slotp;
     const bool seen = s_hi[rr] > s_lo[rr];
     float odd = 0.f;
 #pragma unroll
     for (int e = 0; e < kOC; ++e) {
-      const int d = RT == 16 ? tid + kCsThreads * e : 4 * tx + 64 * (e / 4) + e % 4;
+      const int d = RT == 64 ? 4 * tx + 64 * (e / 4) + e % 4 : tid + kCsThreads * e;
       if (d >= D) continue;
       odd = fmaf(o[r][e], 0.f, odd);
       if (nparts == 1) out[row * D + d] = from_f32<T>(seen ? o[r][e] / s_l[rr] : 0.f);
@@ -321,7 +353,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
   const unsigned long long again = *s_again;
   for (int r = warp; again && r < rows; r += kCsThreads / 32) {
     if (!((again >> r) & 1)) continue;
-    constexpr int kE = RT == 16 ? 4 * EP : 2 * EP;  // 32-column steps of a row
+    constexpr int kE = RT == 64 ? 2 * EP : 4 * EP;  // 32-column steps of a row
     float em, el, eo[kE];
     chunk_row_exact<T, kE>(a, b, kvh, out_row(r), s_slope[r], sq.n - sq.qlen + row_query(r), max(t0, s_lo[r]),
                            min(t1, s_hi[r]), em, el, eo);
@@ -392,11 +424,15 @@ static pkv_status launch_cs_dt(const ChunkArgs &a, int rows, cudaStream_t stream
     if (a.D <= 64) return launch_cs<T, 64, 1>(a, stream);
     return a.D <= 128 ? launch_cs<T, 64, 2>(a, stream) : launch_cs<T, 64, 4>(a, stream);
   }
+  if (rows == 4) {
+    if (a.D <= 128) return launch_cs<T, 4, 1>(a, stream);
+    return a.D <= 256 ? launch_cs<T, 4, 2>(a, stream) : launch_cs<T, 4, 4>(a, stream);
+  }
   if (a.D <= 128) return launch_cs<T, 16, 1>(a, stream);
   return a.D <= 256 ? launch_cs<T, 16, 2>(a, stream) : launch_cs<T, 16, 4>(a, stream);
 }
 
-// rows: packed rows per CTA, 16 or (head_dim up to 256) 64.
+// rows: packed rows per CTA, 4, 16 or (head_dim up to 256) 64.
 pkv_status launch_chunk_simt(const ChunkArgs &a, int rows, pkv_dtype dt, cudaStream_t stream) {
   switch (dt) {
     case PKV_F32: return launch_cs_dt<float>(a, rows, stream);
