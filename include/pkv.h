@@ -498,7 +498,8 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  *                 block_size); a longer one raises PKV_FLAG_CONTEXT_OVER_HINT,
  *                 its output rows are unspecified
  *   partition_size  0 = automatic, else a positive multiple of 128: keys per
- *                 part of the split over the context
+ *                 part of the split over the context (raised where it would
+ *                 give more than 256 parts)
  *   workspace     pkv_chunk_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use; every call that completes
  *                 without PKV_FLAG_TIMEOUT leaves it ready for the next on the

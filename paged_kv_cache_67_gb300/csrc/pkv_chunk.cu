@@ -22,7 +22,8 @@ constexpr int kChunkRows = 16;     // packed rows per CTA of the CUDA-core and m
 constexpr int kChunkManyRows = 64; // of the CUDA-core kernel for long chunks
 constexpr int kChunkFewRows = 4;   // and for single tokens of small groups
 constexpr int kMmaRows = 32;       // packed rows up to which the mma.sync kernel is taken where tcgen05 could be
-constexpr int kChunkMaxParts = 64;
+constexpr int kChunkMaxParts = 64;    // of the automatic split
+constexpr int kChunkManyParts = 256;  // of any (a row's weights have to fit the join's shared memory)
 constexpr long long kChunkMaxKeys = 1LL << 30;  // keys of a context: positions plus a part stay in 32 bits
 
 struct ChunkPlan {
@@ -106,7 +107,7 @@ static long long tc_parts_wanted(long long items, long long span) {
 static void chunk_split(long long wanted, long long span, int min_p, int partition_size, ChunkPlan *p) {
   long long P = partition_size;
   if (P == 0) P = std::max<long long>(min_p, ceil_div(ceil_div(span, wanted), 128) * 128);
-  P = std::min(P, ceil_div(span, 128) * 128);
+  P = std::min(std::max(P, ceil_div(ceil_div(span, kChunkManyParts), 128) * 128), ceil_div(span, 128) * 128);
   p->P = (int)P;
   p->max_parts = (int)ceil_div(span, P);
   p->most_parts = partition_size > 0 ? p->max_parts : (int)std::min(wanted, ceil_div(span, min_p));

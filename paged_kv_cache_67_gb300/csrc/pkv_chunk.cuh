@@ -179,30 +179,140 @@ __device__ __forceinline__ void chunk_row_exact(const ChunkArgs &a, int b, int k
   }
 }
 
+// Four (or one) output elements of a row.
+template <typename T, int VEC>
+__device__ __forceinline__ void chunk_put(T *dst, const float (&v)[VEC]) {
+  struct __align__(VEC * sizeof(T)) Pack {
+    T e[VEC];
+  } p;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) p.e[i] = from_f32<T>(v[i]);
+  *reinterpret_cast<Pack *>(dst) = p;
+}
+
+// Joins the nparts parts of `rows` rows from the workspace, by the whole CTA:
+//   M = max m_p,  out = sum o_p 2^(m_p - M) / sum l_p 2^(m_p - M).
+// The weights 2^(m_p - M) / L are made once, in s_w (room for `room` floats,
+// nparts or more), for as many rows at a time as fit; a round trip to L2 then
+// brings kR rows x kP parts of a thread.  VEC: columns a thread takes at once
+// (4: head_dim a multiple of 4, `out` aligned to 4 elements).
+template <typename T, int VEC, typename RowOut, typename Seen>
+__device__ void chunk_merge(const ChunkArgs &a, int rows, int nparts, float *s_w, int room, const RowOut &row_out,
+                            const Seen &seen) {
+  constexpr int kR = 2, kP = 8;
+  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31;
+  const int D = a.D, DV = D / VEC, group = min(rows, room / nparts);
+  T *out = reinterpret_cast<T *>(a.out);
+  for (int g0 = 0; g0 < rows; g0 += group) {
+    const int gn = min(group, rows - g0);
+    __syncthreads();                                  // s_w is free
+    for (int r = warp; r < gn; r += nthr >> 5) {
+      const size_t at = row_out(g0 + r) * a.max_parts;
+      float M = -INFINITY, L = 0.f;
+      for (int p = lane; p < nparts; p += 32) M = fmaxf(M, __ldcg(a.ws_m + at + p));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float ref = chunk_ref(M);
+      for (int p = lane; p < nparts; p += 32) {
+        const float w = fast_exp2(__ldcg(a.ws_m + at + p) - ref);
+        s_w[r * nparts + p] = w;
+        L = fmaf(__ldcg(a.ws_l + at + p), w, L);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      const float inv = 1.f / L;
+      __syncwarp();
+      for (int p = lane; p < nparts; p += 32) s_w[r * nparts + p] *= inv;
+    }
+    __syncthreads();
+    const int tpr = min(DV, nthr);                    // threads along a row
+    const int step = nthr / tpr;                      // rows side by side
+    for (int dv = tid % tpr; dv < DV; dv += tpr) {
+      for (int r0 = tid / tpr; r0 < gn && tid < step * tpr; r0 += step * kR) {
+        float acc[kR][VEC];
+        const float *po[kR];
+#pragma unroll
+        for (int k = 0; k < kR; ++k) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[k][i] = 0.f;
+          po[k] = a.ws_o + row_out(g0 + min(r0 + k * step, gn - 1)) * a.max_parts * D + dv * VEC;
+        }
+        for (int p0 = 0; p0 < nparts; p0 += kP) {
+          float v[kR][kP][VEC];
+#pragma unroll
+          for (int k = 0; k < kR; ++k)
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+              const float *src = po[k] + (size_t)min(p0 + p, nparts - 1) * D;
+              if constexpr (VEC == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                v[k][p][0] = x.x; v[k][p][1] = x.y; v[k][p][2] = x.z; v[k][p][3] = x.w;
+              } else {
+                v[k][p][0] = __ldcg(src);
+              }
+            }
+#pragma unroll
+          for (int k = 0; k < kR; ++k)
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+              if (p0 + p >= nparts) continue;
+              const float w = s_w[min(r0 + k * step, gn - 1) * nparts + p0 + p];
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) acc[k][i] = fmaf(v[k][p][i], w, acc[k][i]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kR; ++k) {
+          const int r = r0 + k * step;
+          if (r >= gn) continue;
+          if (!seen(g0 + r)) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[k][i] = 0.f;
+          }
+          chunk_put<T, VEC>(out + row_out(g0 + r) * D + dv * VEC, acc[k]);
+        }
+      }
+    }
+  }
+}
+
+// Counts a finished part of a unit (every thread's partial results are
+// written); whether it was the last.  One thread publishes for the CTA with
+// an acquire-release atomic.  s_scratch: 1 int.
+__device__ __forceinline__ bool chunk_last_part(int *counter, int nparts, int *s_scratch) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int prev;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                 : "=r"(prev)
+                 : "l"(reinterpret_cast<uint64_t>(counter))
+                 : "memory");
+    *s_scratch = prev == nparts - 1;
+  }
+  __syncthreads();
+  return *s_scratch != 0;
+}
+
 // The end of part `part` of `nparts` of a unit of `rows` rows, by the whole
 // CTA: s_m, s_l, s_o (row r at r * ostride) hold the part's state; row_out(r)
 // is row r's output row; seen(r) says whether it sees any key at all.  One
 // part writes o / l.  Several leave their state in the workspace, and the one
-// that `counter` shows to be last merges:
-//   M = max m_p,  out = sum o_p 2^(m_p - M) / sum l_p 2^(m_p - M).
-// s_scratch: 1 int.  s_o is overwritten (it holds rows x nparts floats or more).
+// that `counter` shows to be last joins them.  s_o is overwritten then
+// (`room` floats).
 template <typename T, typename RowOut, typename Seen>
 __device__ void chunk_finish(const ChunkArgs &a, int rows, int part, int nparts, const float *s_m, const float *s_l,
-                             float *s_o, int ostride, int *s_scratch, int *counter, const RowOut &row_out,
+                             float *s_o, int ostride, int room, int *s_scratch, int *counter, const RowOut &row_out,
                              const Seen &seen) {
   const int tid = threadIdx.x, nthr = blockDim.x, D = a.D, DV = D / 4;
   T *out = reinterpret_cast<T *>(a.out);
-  auto put4 = [&](size_t row, int d4, float x, float y, float z, float w) {
-    T v[4] = {from_f32<T>(x), from_f32<T>(y), from_f32<T>(z), from_f32<T>(w)};
-    *reinterpret_cast<uint2 *>(out + row * D + 4 * d4) = *reinterpret_cast<const uint2 *>(v);
-  };
   if (nparts == 1) {
     for (int i = tid; i < rows * DV; i += nthr) {
       const int r = i / DV, d4 = i - r * DV;
       const float4 v = *reinterpret_cast<const float4 *>(s_o + r * ostride + 4 * d4);
-      const float inv = seen(r) ? 1.f / s_l[r] : 0.f;
-      if (seen(r)) put4(row_out(r), d4, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-      else put4(row_out(r), d4, 0.f, 0.f, 0.f, 0.f);
+      const bool sees = seen(r);
+      const float inv = sees ? 1.f / s_l[r] : 0.f;
+      const float x[4] = {sees ? v.x * inv : 0.f, sees ? v.y * inv : 0.f, sees ? v.z * inv : 0.f, sees ? v.w * inv : 0.f};
+      chunk_put<T, 4>(out + row_out(r) * D + 4 * d4, x);
     }
     return;
   }
@@ -216,79 +326,8 @@ __device__ void chunk_finish(const ChunkArgs &a, int rows, int part, int nparts,
     reinterpret_cast<float4 *>(a.ws_o + (row_out(r) * a.max_parts + part) * D)[d4] =
         *reinterpret_cast<const float4 *>(s_o + r * ostride + 4 * d4);
   }
-  __syncthreads();
-  if (tid == 0) {
-    int prev;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
-                 : "=r"(prev)
-                 : "l"(reinterpret_cast<uint64_t>(counter))
-                 : "memory");
-    *s_scratch = prev == nparts - 1;
-  }
-  __syncthreads();
-  if (!*s_scratch) return;
-  // the rows' weights 2^(m_p - M) / L once, in shared memory (the part's own
-  // state is in the workspace, its place is free) ...
-  float *s_w = s_o;                                   // [rows][nparts]
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int r = warp; r < rows; r += nthr >> 5) {
-    const size_t at = row_out(r) * a.max_parts;
-    float M = -INFINITY, L = 0.f;
-    for (int p = lane; p < nparts; p += 32) M = fmaxf(M, __ldcg(a.ws_m + at + p));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = chunk_ref(M);
-    for (int p = lane; p < nparts; p += 32) {
-      const float w = fast_exp2(__ldcg(a.ws_m + at + p) - ref);
-      s_w[r * nparts + p] = w;
-      L = fmaf(__ldcg(a.ws_l + at + p), w, L);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float inv = seen(r) ? 1.f / L : 0.f;
-    __syncwarp();
-    for (int p = lane; p < nparts; p += 32) s_w[r * nparts + p] *= inv;
-  }
-  __syncthreads();
-  // ... then the sums: a round trip to L2 brings kR rows x kP parts of a thread
-  constexpr int kR = 4, kP = 4;
-  const int tpr = DV < nthr ? DV : nthr;              // threads along a row
-  const int step = nthr / tpr;                        // rows side by side
-  for (int d4 = tid % tpr; d4 < DV; d4 += tpr) {
-    for (int r0 = tid / tpr; r0 < rows && tid < step * tpr; r0 += step * kR) {
-      float4 acc[kR];
-      const float4 *po[kR];
-#pragma unroll
-      for (int k = 0; k < kR; ++k) {
-        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        po[k] = reinterpret_cast<const float4 *>(a.ws_o + row_out(min(r0 + k * step, rows - 1)) * a.max_parts * D) + d4;
-      }
-      for (int p0 = 0; p0 < nparts; p0 += kP) {
-        float4 v[kR][kP];
-#pragma unroll
-        for (int k = 0; k < kR; ++k)
-#pragma unroll
-          for (int p = 0; p < kP; ++p) v[k][p] = __ldcg(po[k] + (size_t)min(p0 + p, nparts - 1) * DV);
-#pragma unroll
-        for (int k = 0; k < kR; ++k)
-#pragma unroll
-          for (int p = 0; p < kP; ++p) {
-            const float w = p0 + p < nparts ? s_w[min(r0 + k * step, rows - 1) * nparts + p0 + p] : 0.f;
-            acc[k].x = fmaf(v[k][p].x, w, acc[k].x);
-            acc[k].y = fmaf(v[k][p].y, w, acc[k].y);
-            acc[k].z = fmaf(v[k][p].z, w, acc[k].z);
-            acc[k].w = fmaf(v[k][p].w, w, acc[k].w);
-          }
-      }
-#pragma unroll
-      for (int k = 0; k < kR; ++k) {
-        const int r = r0 + k * step;
-        if (r >= rows) continue;
-        if (seen(r)) put4(row_out(r), d4, acc[k].x, acc[k].y, acc[k].z, acc[k].w);
-        else put4(row_out(r), d4, 0.f, 0.f, 0.f, 0.f);
-      }
-    }
-  }
+  if (!chunk_last_part(counter, nparts, s_scratch)) return;
+  chunk_merge<T, 4>(a, rows, nparts, s_o, room, row_out, seen);
   if (tid == 0) *counter = 0;  // ready for the next call
 }
 

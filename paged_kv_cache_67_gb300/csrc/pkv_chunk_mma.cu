@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
     }
     __syncthreads();
   }
-  chunk_finish<T>(a, rows, part, nparts, s_m, s_l, sO, Sh::kOStride, s_scratch,
+  chunk_finish<T>(a, rows, part, nparts, s_m, s_l, sO, Sh::kOStride, Sh::kRing / 4, s_scratch,
                   a.ws_cnt + kChunkCntFirst + ((size_t)b * a.KVH + kvh) * a.chunks + chunk, row_out,
                   [&](int r) { return s_hi[r] > s_lo[r]; });
 }

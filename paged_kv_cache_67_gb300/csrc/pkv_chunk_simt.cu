@@ -371,34 +371,15 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
     }
   }
   if (nparts == 1) return;
-  __syncthreads();
   int *counter = a.ws_cnt + kChunkCntFirst + ((size_t)b * a.KVH + kvh) * a.chunks + chunk;
-  if (tid == 0) {
-    int prev;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
-                 : "=r"(prev)
-                 : "l"(reinterpret_cast<uint64_t>(counter))
-                 : "memory");
-    s_flag[0] = prev == nparts - 1;
-  }
-  __syncthreads();
-  if (!s_flag[0]) return;
-  // the last part joins them: out = sum_p o_p 2^(m_p - M) / sum_p l_p 2^(m_p - M)
-  for (int i = tid; i < rows * D; i += kCsThreads) {
-    const int r = i / D, d = i - r * D;
-    const size_t at = out_row(r) * a.max_parts;
-    float M = -INFINITY, L = 0.f, acc = 0.f;
-#pragma unroll 8
-    for (int p = 0; p < nparts; ++p) M = fmaxf(M, __ldcg(a.ws_m + at + p));
-    const float ref = chunk_ref(M);
-#pragma unroll 8
-    for (int p = 0; p < nparts; ++p) {
-      const float w = fast_exp2(__ldcg(a.ws_m + at + p) - ref);
-      L = fmaf(__ldcg(a.ws_l + at + p), w, L);
-      acc = fmaf(__ldcg(a.ws_o + (at + p) * D + d), w, acc);
-    }
-    out[out_row(r) * D + d] = from_f32<T>(s_hi[r] > s_lo[r] ? acc / L : 0.f);
-  }
+  if (!chunk_last_part(counter, nparts, s_flag)) return;
+  // (everything before the rows' bounds is free now)
+  const int room = (int)(reinterpret_cast<float *>(s_alpha) - reinterpret_cast<float *>(s_raw));
+  auto seen = [&](int r) { return s_hi[r] > s_lo[r]; };
+  if (D % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(T)) == 0)
+    chunk_merge<T, 4>(a, rows, nparts, reinterpret_cast<float *>(s_raw), room, out_row, seen);
+  else
+    chunk_merge<T, 1>(a, rows, nparts, reinterpret_cast<float *>(s_raw), room, out_row, seen);
   if (tid == 0) *counter = 0;
 }
 

@@ -74,7 +74,7 @@ struct CtArgs {
 
 // Keys that the rows of queries [i0, i1) see: the first, and one past the
 // last.  kCtLanes lanes of a warp work on a tile together.
-constexpr int kCtLanes = 8;
+constexpr int kCtLanes = 4;
 __device__ __forceinline__ void ct_span(const ChunkArgs &a, const ChunkSeq &s, int i0, int i1, int sub, int &lo, int &hi) {
   lo = 0x7fffffff;
   hi = 0;
@@ -87,7 +87,7 @@ __device__ __forceinline__ void ct_span(const ChunkArgs &a, const ChunkSeq &s, i
     }
   };
   if (a.starts) {
-#pragma unroll 8                 // independent loads in flight together
+#pragma unroll 16                // independent loads in flight together
     for (int i = i0 + sub; i < i1; i += kCtLanes) take(i);
   } else if (i1 > i0) {          // both bounds rise with the query
     take(i0);
@@ -712,11 +712,11 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           sc[64 + c] = __uint_as_float(sb[c]);
         }
         const bool cut = t0 < lo || t0 + kCtTile > hi;   // some of the tile is hidden from the row
-        // Where no key lies past a row's position, its bias slope (j - p) is
+        // Where a row sees no key past its position, its bias slope (j - p) is
         // linear in the column: slope (c mod 8) goes in with the score, and
         // the rest, one number per 8 columns, only into the max and the
         // exponent.
-        const bool linear = BIAS && __all_sync(0xffffffffu, t0 + kCtTile - 1 <= p);
+        const bool linear = BIAS && (!a.prefix || __all_sync(0xffffffffu, t0 + kCtTile - 1 <= p));
         const float base = BIAS ? slope * (float)(t0 - p) : 0.f;
         auto block_bias = [&](int c) { return linear ? fmaf(slope, (float)(c & ~7), base) : 0.f; };
         // Capped scores: |q . k| over the tile picks the way to its tanh.  The
