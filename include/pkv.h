@@ -481,8 +481,9 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  * query that sees no key gives a row of zeros.
  *
  *   out, q, cu_seqlens_q, k_cache, v_cache, block_tables, context_lens
- *                 as in pkv_prefill_attention; out rows behind
- *                 cu_seqlens_q[B] are left as they were
+ *                 as in pkv_prefill_attention (out overlaps no other
+ *                 argument); out rows behind cu_seqlens_q[B] are left as they
+ *                 were
  *   softcap       0 = none, else > 0
  *   window        0 = none, else a query sees at most the last `window` keys
  *                 up to itself (and the prefix positions above p)
@@ -515,10 +516,11 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  * Supported: fp32, bf16, fp16; head_dim <= 512; any block size; element-
  * aligned pointers.  bf16 / fp16 with 16-byte aligned tensors, block_size a
  * multiple of 16 and head_dim 64, 128, 192 or 256 run tensor-core kernels:
- * chunks of up to 16 (query, head) rows per KV head, and every chunk at
- * head_dim 192 and 256, an mma.sync kernel; longer chunks at head_dim 64 and
- * 128 a tcgen05 kernel.  Everything else runs on the CUDA cores.
- * Errors: PKV_ERR_INVALID_ARG (also a negative or NaN softcap, a negative
+ * an mma.sync kernel where max_q_len * H / num_kv_heads is 32 at most, else a
+ * tcgen05 kernel (three launches: plan, attention and, when split, join).
+ * Everything else runs on the CUDA cores.
+ * Errors: PKV_ERR_INVALID_ARG (also a scale that is not finite, a softcap
+ * that is negative, not finite or too small for scale / softcap, a negative
  * window), PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA.  B == 0 or
  * total_q == 0 enqueues nothing.
  */

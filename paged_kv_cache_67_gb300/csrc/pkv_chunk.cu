@@ -191,7 +191,8 @@ PKV_API pkv_status pkv_chunk_attention(
   if (head_dim > 512) return PKV_ERR_UNSUPPORTED;
   if (!chunk_sizes_ok(B, total_q, H, num_kv_heads, head_dim, block_size, max_blocks, max_q_len, max_context_len,
                       partition_size) ||
-      num_blocks < 0 || num_blocks > 0x7fffffffLL || window < 0 || !(softcap >= 0.f) || isinf(softcap))
+      num_blocks < 0 || num_blocks > 0x7fffffffLL || window < 0 || !(softcap >= 0.f) || isinf(softcap) || !isfinite(scale) ||
+      (softcap > 0.f && !isfinite(2.f * kLog2e * scale / softcap)))
     return PKV_ERR_INVALID_ARG;
   if (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16) return PKV_ERR_INVALID_ARG;
   if (B == 0 || total_q == 0) return PKV_OK;

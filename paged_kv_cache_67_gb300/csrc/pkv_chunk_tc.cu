@@ -52,6 +52,7 @@ __host__ __device__ constexpr int ct_groups(int D) { return D <= 128 ? 2 : 1; }
 constexpr int kCtQRegion = kCtRows * 128;      // 128 rows x 64 elements of 16 bits
 constexpr int kCtKVRegion = kCtTile * 128;
 constexpr int kCtPlanThreads = 1024;
+constexpr int kCtSat = 1 << 29;                // sums of tiles stop here (query offsets that overlap can add up to anything)
 constexpr int kCtClasses = 256;                // plan: key tiles of a unit, the most first
 
 struct CtUnit {                  // 32 bytes, written by the plan
@@ -73,25 +74,34 @@ struct CtArgs {
 // ---------------------------------------------------------------------- plan
 
 // Keys that the rows of queries [i0, i1) see: the first, and one past the
-// last.  kCtLanes lanes of a warp work on a tile together.
+// last.  kCtLanes lanes of a warp work on a tile together.  Without kv_starts
+// both bounds rise with the query; with them the first key is the least over
+// the queries that see any, 16 loads of a lane in flight.
 constexpr int kCtLanes = 4;
 __device__ __forceinline__ void ct_span(const ChunkArgs &a, const ChunkSeq &s, int i0, int i1, int sub, int &lo, int &hi) {
   lo = 0x7fffffff;
   hi = 0;
-  auto take = [&](int i) {
-    int l, h;
-    chunk_visible(a, s, i, l, h);
-    if (h > l) {
+  auto take = [&](int i, int start) {
+    const int p = s.n - s.qlen + i, h = max(p + 1, s.prefix);
+    const int l = max(a.window > 0 ? max(0, p - a.window + 1) : 0, start);
+    if (l < h) {
       lo = min(lo, l);
       hi = max(hi, h);
     }
   };
   if (a.starts) {
-#pragma unroll 16                // independent loads in flight together
-    for (int i = i0 + sub; i < i1; i += kCtLanes) take(i);
-  } else if (i1 > i0) {          // both bounds rise with the query
-    take(i0);
-    take(i1 - 1);
+    constexpr int kU = 16;
+    for (int i = i0 + sub; i < i1; i += kCtLanes * kU) {
+      int st[kU];
+#pragma unroll
+      for (int k = 0; k < kU; ++k) st[k] = i + kCtLanes * k < i1 ? __ldg(a.starts + s.q0 + i + kCtLanes * k) : 0x7fffffff;
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (i + kCtLanes * k < i1) take(i + kCtLanes * k, st[k]);
+    }
+  } else if (i1 > i0) {
+    take(i0, 0);
+    take(i1 - 1, 0);
   }
 #pragma unroll
   for (int o = kCtLanes / 2; o > 0; o >>= 1) {
@@ -103,24 +113,27 @@ __device__ __forceinline__ void ct_span(const ChunkArgs &a, const ChunkSeq &s, i
 __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const CtArgs a) {
   __shared__ int s_cls[kCtClasses];
   __shared__ int s_warp[32];
+  __shared__ int s_first[kCtPlanThreads];    // B <= kCtPlanThreads: a sequence's first tile
+  __shared__ ChunkSeq s_seq[kCtPlanThreads];
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (ct_groups(a.c.D) * kCtRows) >> a.gshift;   // queries per unit
+  const bool one_scan = a.c.B <= kCtPlanThreads;   // tiles are then found by a search, else listed first
   for (int i = tid; i < kCtClasses; i += kCtPlanThreads) s_cls[i] = 0;
-  // the (sequence, tile) list
   int total = 0;
   for (int base = 0; base < a.c.B; base += kCtPlanThreads) {
     const int b = base + tid;
     int cnt = 0;
     if (b < a.c.B) {
       const ChunkSeq s = chunk_seq(a.c, b, true);
-      cnt = (s.qlen + per - 1) / per;
+      cnt = min((s.qlen + per - 1) / per, kCtSat);
+      if (one_scan) s_seq[b] = s;
     }
     int inc = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      if (lane >= o) inc = min(inc + y, kCtSat);
     }
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
@@ -128,18 +141,20 @@ __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const Ct
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
+      if (lane >= o) v = min(v + y, kCtSat);
     }
     const int before = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
-    const int at = total + (warp ? before : 0) + inc - cnt;
-    total += __shfl_sync(0xffffffffu, v, 31);
-    // (query offsets that overlap could list more tiles than there is room for)
-    for (int t = 0; t < cnt; ++t) {
-      if (at + t < a.tiles_cap) a.tiles[at + t] = make_int4(b, t, 0, 0);
-      else raise_flag(a.c.err, PKV_FLAG_QUERY_LEN);
+    const int at = min(total + min((warp ? before : 0) + (inc - cnt), kCtSat), kCtSat);
+    total = min(total + __shfl_sync(0xffffffffu, v, 31), kCtSat);
+    if (one_scan) {
+      s_first[tid] = at;
+    } else {
+      for (int t = 0; t < cnt && at + t < a.tiles_cap; ++t) a.tiles[at + t] = make_int4(b, t, 0, 0);
     }
     __syncthreads();
   }
+  // (query offsets that overlap could make more tiles than there is room for)
+  if (total > a.tiles_cap && tid == 0) raise_flag(a.c.err, PKV_FLAG_QUERY_LEN);
   total = min(total, a.tiles_cap);
   __syncthreads();
   // each tile's parts: counted by their key tiles, then placed by them
@@ -147,18 +162,27 @@ __global__ void __launch_bounds__(kCtPlanThreads) pkv_chunk_plan_kernel(const Ct
     for (int n0 = 0; n0 < total; n0 += kCtPlanThreads / kCtLanes) {
       const int n = n0 + tid / kCtLanes, sub = tid & (kCtLanes - 1);
       int4 bt = make_int4(0, 0, 0, 0);
-      if (n < total) bt = a.tiles[n];
-      const int i0 = bt.y * per;
+      if (n < total && (pass == 1 || !one_scan)) bt = a.tiles[n];
       int lo = bt.z, hi = bt.w;
       if (pass == 0) {
         ChunkSeq s = {0, 0, 0, 0};
-        if (n < total) s = chunk_seq(a.c, bt.x, false);
-        ct_span(a.c, s, i0, min(s.qlen, i0 + per), sub, lo, hi);
-        if (n < total && sub == 0) {
-          a.tiles[n].z = lo;
-          a.tiles[n].w = hi;
+        if (n < total && one_scan) {           // the last sequence that starts at or before tile n
+          int b = 0, len = a.c.B;
+          while (len > 1) {
+            const int half = len >> 1;
+            if (s_first[b + half] <= n) b += half;
+            len -= half;
+          }
+          bt.x = b;
+          bt.y = n - s_first[b];
+          s = s_seq[b];
+        } else if (n < total) {
+          s = chunk_seq(a.c, bt.x, false);
         }
+        ct_span(a.c, s, bt.y * per, min(s.qlen, bt.y * per + per), sub, lo, hi);
+        if (n < total && sub == 0) a.tiles[n] = make_int4(bt.x, bt.y, lo, hi);
       }
+      const int i0 = bt.y * per;
       if (n >= total) continue;
       const int base = hi > 0 ? lo & -(1 << a.bshift) : 0;
       const int nparts = max(1, (hi - base + a.c.P - 1) / a.c.P);
@@ -1123,7 +1147,7 @@ pkv_status launch_chunk_tc(const ChunkArgs &c, pkv_dtype dt, char *scratch, int 
   a.subs = c.H >> a.gshift;
   a.bshift = c.bs % 64 == 0 ? 6 : c.bs % 32 == 0 ? 5 : 4;
   const long long tiles = ct_tiles_cap(c.B, c.total_q, c.max_q, (ct_groups(c.D) * kCtRows) >> a.gshift);
-  if (tiles * c.max_parts * a.subs > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  if (tiles >= kCtSat || tiles * c.max_parts * a.subs > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   a.tiles_cap = (int)tiles;
   a.units_cap = (int)(tiles * c.max_parts);
   a.n_units = reinterpret_cast<int *>(scratch);

@@ -144,6 +144,67 @@ def test_long_chunks(dtype, H, KVH, D):
         check(c, f"{sorted(f)}", **f)
 
 
+@pytest.mark.parametrize("dtype,H,KVH,D", [(HF, 2, 2, 192), (BF, 4, 1, 256)])
+def test_long_chunks_wide_heads(dtype, H, KVH, D):
+    """One row tile an item: several items and key tiles, split and whole."""
+    c = case(D + 2, [700, 400, 129], [300, 257, 129], H, KVH, D, 16, dtype)
+    for f in forms(c, 4):
+        check(c, f"{sorted(f)}", **f)
+    check(c, "split", partition_size=128, softcap=15.0)
+
+
+@pytest.mark.parametrize("H,KVH,D", [(128, 1, 64), (96, 1, 128), (24, 2, 64), (66, 1, 64)])
+def test_large_and_odd_groups(H, KVH, D):
+    """Up to 128 heads packed in a tile; groups with an odd factor pack fewer."""
+    c = case(H, [40, 150, 17], [5, 9, 2], H, KVH, D, 16, BF)
+    for f in ({}, {"softcap": 9.0, "window": 50}, {"slopes": slopes_of(H)}):
+        check(c, f"{sorted(f)}", **f)
+        check(c, f"{sorted(f)} split", partition_size=128, **f)
+
+
+@pytest.mark.parametrize("bs", [32, 48, 64, 80, 256])
+def test_block_sizes(bs):
+    for dtype, D, q in ((BF, 128, [3, 1]), (BF, 64, [100, 40]), (HF, 256, [90, 3]), (F32, 64, [40, 3])):
+        c = case(bs + D, [333, 500], q, 4, 2, D, bs, dtype)
+        check(c, f"{bs} {D}", softcap=12.0, window=170)
+
+
+@pytest.mark.parametrize("B", [1023, 1100, 2500])
+def test_many_sequences(B):
+    """More sequences than one scan of the plan covers, and just fewer."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(1, 40, (B,), generator=g).tolist()
+    qlens = [min(n, int(torch.randint(0, 12, (1,), generator=g))) for n in lens]
+    qlens[5] = lens[5] = 35
+    c = case(B, lens, qlens, 4, 2, 64, 16, BF)
+    assert pkv.pkv_chunk_plan(B, sum(qlens), 4, 2, 64, 16, c["tables"].shape[1], 35)[2] == 2
+    got, err = run(c, max_q_len=35, softcap=9.0)
+    assert err == 0
+    close(got, reference(c, softcap=9.0), c)
+
+
+def test_scale_signs():
+    """Negative and zero scales, with and without a cap and a bias."""
+    for dtype, D, q in ((BF, 128, [3, 2]), (BF, 64, [70, 100]), (HF, 256, [60, 2]), (F32, 64, [3, 50])):
+        c = case(31, [200, 300], q, 4, 2, D, 16, dtype)
+        for scale in (-0.1, 0.0, 1e-7):
+            c["scale"] = scale
+            for f in ({}, {"softcap": 8.0}, {"slopes": -slopes_of(4), "window": 90}):
+                check(c, f"{scale} {sorted(f)}", **f)
+
+
+def test_query_offsets_that_overlap():
+    """Offsets that go back and forth are flagged; sequences that are fine
+    stay right, and nothing outside is touched."""
+    for D in (64, 128, 256):
+        c = case(33, [60, 60, 60, 60], [50, 50, 50, 50], 4, 2, D, 16, BF)
+        want = reference(c)
+        c["cu"] = torch.tensor([0, 50, 10, 200, 190], dtype=torch.int32)    # lengths 50, -40, 190, -10
+        got, err = run(c)
+        assert err & pkv.FLAG_QUERY_LEN
+        close(got[:50], want[:50], c)
+
+
 def test_large_scores_and_cap():
     """Scores far past the cap: tanh saturates, the softmax stays exact."""
     for dtype, D in ((BF, 128), (F32, 64), (HF, 256)):

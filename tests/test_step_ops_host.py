@@ -75,7 +75,7 @@ def _chunk(lib, **kw):
     return lib.pkv_chunk_attention(
         g("out", FAKE), g("q", FAKE), g("kc", FAKE), g("vc", FAKE), g("tables", FAKE), g("cu", FAKE), g("lens", FAKE),
         g("slopes"), g("prefix"), g("starts"), g("B", 2), g("total", 6), g("H", 4), g("KVH", 2), g("D", 64),
-        g("bs", 16), g("mb", 4), g("nb", 8), ctypes.c_float(0.1), ctypes.c_float(g("cap", 0.0)), g("window", 0),
+        g("bs", 16), g("mb", 4), g("nb", 8), ctypes.c_float(g("scale", 0.1)), ctypes.c_float(g("cap", 0.0)), g("window", 0),
         g("dt", 1), g("max_q", 0), g("max_n", 0), g("P", 0), g("ws"), g("wsb", 0), None, None)
 
 
@@ -83,7 +83,7 @@ def test_chunk_refusals(pkv):
     lib = pkv.load_library()
     assert _chunk(lib, B=0) == OK and _chunk(lib, total=0) == OK
     for bad in ({"B": -1}, {"B": 65536}, {"total": -1}, {"H": 3}, {"KVH": 0}, {"D": 0}, {"bs": 0}, {"mb": -1},
-                {"nb": -1}, {"cap": -1.0}, {"cap": float("nan")}, {"cap": float("inf")}, {"window": -1}, {"dt": 5},
+                {"nb": -1}, {"cap": -1.0}, {"cap": float("nan")}, {"cap": float("inf")}, {"cap": 1e-40}, {"scale": float("nan")}, {"scale": float("inf")}, {"window": -1}, {"dt": 5},
                 {"max_q": -1}, {"max_n": -1}, {"P": 64}, {"P": -128}, {"out": None}, {"q": None}, {"kc": None},
                 {"vc": None}, {"tables": None}, {"cu": None}, {"lens": None}, {"q": FAKE + 1}, {"slopes": FAKE + 2},
                 {"prefix": FAKE + 2}, {"starts": FAKE + 1}, {"tables": FAKE + 2}):
