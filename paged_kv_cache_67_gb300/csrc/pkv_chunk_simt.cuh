@@ -55,20 +55,8 @@ __device__ __forceinline__ float4 cs_ld4(const T *p) {
   return make_float4(to_f32<T>(e[0]), to_f32<T>(e[1]), to_f32<T>(e[2]), to_f32<T>(e[3]));
 }
 
-// Out of line: seldom run, and many instances.
-template <typename T, int EPL>
-__device__ __noinline__ void cs_row_exact(const ChunkArgs &a, int b, int kvh, size_t q_row, float slope_log2, int p, int t0,
-                                          int t1, float &m, float &l, float (&o)[EPL]) {
-  chunk_row_exact<T, EPL>(a, b, kvh, q_row, slope_log2, p, t0, t1, m, l, o);
-}
-template <typename T, int VEC, typename RowOut, typename Seen>
-__device__ __noinline__ void cs_merge(const ChunkArgs &a, int rows, int nparts, float *s_w, int room, const RowOut &row_out,
-                                      const Seen &seen) {
-  chunk_merge<T, VEC>(a, rows, nparts, s_w, room, row_out, seen);
-}
-
 // EP: column steps of a thread in O (RT = 64: of 64, else of 128).  AL:
-// rows are whole, aligned 16-byte vectors.
+// cache rows are whole, aligned 16-byte vectors, and out is aligned.
 template <typename T, int RT, int EP, bool AL>
 __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
@@ -369,7 +357,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
     if (!((again >> r) & 1)) continue;
     constexpr int kE = RT == 64 ? 2 * EP : 4 * EP;  // 32-column steps of a row
     float em, el, eo[kE];
-    cs_row_exact<T, kE>(a, b, kvh, out_row(r), s_slope[r], sq.n - sq.qlen + row_query(r), max(t0, s_lo[r]),
+    chunk_row_exact<T, kE>(a, b, kvh, out_row(r), s_slope[r], sq.n - sq.qlen + row_query(r), max(t0, s_lo[r]),
                            min(t1, s_hi[r]), em, el, eo);
     const size_t row = out_row(r), at = row * a.max_parts + slotp;
 #pragma unroll
@@ -390,10 +378,7 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
   // (everything before the rows' bounds is free now)
   const int room = (int)(reinterpret_cast<float *>(s_alpha) - reinterpret_cast<float *>(s_raw));
   auto seen = [&](int r) { return s_hi[r] > s_lo[r]; };
-  if (D % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(T)) == 0)
-    cs_merge<T, 4>(a, rows, nparts, reinterpret_cast<float *>(s_raw), room, out_row, seen);
-  else
-    cs_merge<T, 1>(a, rows, nparts, reinterpret_cast<float *>(s_raw), room, out_row, seen);
+  chunk_merge<T, AL ? 4 : 1>(a, rows, nparts, reinterpret_cast<float *>(s_raw), room, out_row, seen);
   if (tid == 0) *counter = 0;
 }
 
@@ -402,7 +387,8 @@ static pkv_status launch_cs(const ChunkArgs &a, cudaStream_t stream) {
   const dim3 grid((unsigned)((long long)a.max_parts * a.KVH * a.chunks), a.B);
   const size_t smem = cs_smem<T, RT>(a.D);
   const bool aligned = a.D * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k_cache) % 16 == 0 &&
-                       reinterpret_cast<uintptr_t>(a.v_cache) % 16 == 0;
+                       reinterpret_cast<uintptr_t>(a.v_cache) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   auto go = [&](auto kern, int *configured) {
     if (!allow_smem(kern, smem, configured)) return PKV_ERR_CUDA;
     kern<<<grid, kCsThreads, smem, stream>>>(a);
