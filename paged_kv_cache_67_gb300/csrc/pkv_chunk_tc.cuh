@@ -590,6 +590,15 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           sc[64 + c] = __uint_as_float(sb[c]);
         }
         const bool cut = t0 < lo || t0 + kCtTile > hi;   // some of the tile is hidden from the row
+        auto hide = [&](float v) {  // v in the hidden columns: a bit per column, not two comparisons
+#pragma unroll
+          for (int k = 0; k < 128; k += 32) {
+            const int from = min(max(lo - t0 - k, 0), 32), to = min(max(hi - t0 - k, 0), 32);
+            const uint32_t seen_bits = (uint32_t)((1ull << to) - 1ull) & ~(uint32_t)((1ull << from) - 1ull);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sc[k + c] = (seen_bits >> c) & 1u ? sc[k + c] : v;
+          }
+        };
         // Where a row sees no key past its position, its bias slope (j - p) is
         // linear in the column: slope (c mod 8) goes in with the score, and
         // the rest, one number per 8 columns, only into the max and the
@@ -604,9 +613,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
         float mx_raw = -INFINITY;
         if (CAP && !BIAS) {
           if (cut) {  // hidden columns hold whatever was there: they have no say
-            const int vlo = lo - t0, vhi = hi - t0;
-#pragma unroll
-            for (int c = 0; c < 128; ++c) sc[c] = c >= vlo && c < vhi ? sc[c] : 0.f;
+            hide(0.f);
           }
           float mn_raw = INFINITY;
 #pragma unroll
@@ -659,9 +666,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           }
         }
         if (cut) {
-          const int vlo = lo - t0, vhi = hi - t0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c) sc[c] = c >= vlo && c < vhi ? sc[c] : -INFINITY;
+          hide(-INFINITY);
         }
         float mx = -INFINITY;
         if (fused) {
