@@ -430,7 +430,8 @@ PKV_API pkv_status pkv_build_step(int32_t *block_tables, const int32_t *held, in
  *   q             [num_tokens, H, head_dim], token i at element i * q_token_stride
  *   k, v          [num_tokens, num_kv_heads, head_dim], strides as in pkv_write
  *   q_out         [num_tokens, H, head_dim] contiguous; may be q itself (with
- *                 q_token_stride = H * head_dim), else no overlap
+ *                 q_token_stride = H * head_dim), else overlaps neither q, k
+ *                 nor v
  *   k_cache, v_cache, slot_mapping  as in pkv_write
  *   cos_sin       [max_position, rot_dim] float32: row p holds the cosines of
  *                 the rot_dim / 2 pairs' angles at position p, then the sines
@@ -500,7 +501,8 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  *                 its output rows are unspecified
  *   partition_size  0 = automatic, else a positive multiple of 128: keys per
  *                 part of the split over the context (raised where it would
- *                 give more than 256 parts)
+ *                 give more than 256 parts; with more than 65520 units of
+ *                 16 rows nothing is split)
  *   workspace     pkv_chunk_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use; every call that completes
  *                 without PKV_FLAG_TIMEOUT leaves it ready for the next on the

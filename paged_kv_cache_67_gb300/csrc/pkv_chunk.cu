@@ -110,7 +110,10 @@ static void chunk_split(long long wanted, long long span, int min_p, int partiti
   P = std::min(std::max(P, ceil_div(ceil_div(span, kChunkManyParts), 128) * 128), ceil_div(span, 128) * 128);
   p->P = (int)P;
   p->max_parts = (int)ceil_div(span, P);
-  p->most_parts = partition_size > 0 ? p->max_parts : (int)std::min(wanted, ceil_div(span, min_p));
+  // (of a window's shorter span too: its parts may be a few more where this P
+  // was raised)
+  p->most_parts = partition_size > 0 ? (int)std::min<long long>(kChunkManyParts, ceil_div(span, partition_size))
+                                     : (int)std::min(wanted, ceil_div(span, min_p));
 }
 
 static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, int max_blocks, int max_q, int max_n,
@@ -135,7 +138,10 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   }
   const int per_sm = p->kernel == 0 ? (p->rows == kChunkManyRows ? 2 : 4) : D <= 192 ? 2 : 1;   // resident CTAs
   const long long units = (long long)B * KVH * p->chunks, slots = (long long)kPlanSms * per_sm;
-  chunk_split(std::min(parts_wanted(units, slots, span), parts_wanted(units, slots, cap)), span, 128, partition_size, p);
+  if (units > kChunkCnt - kChunkCntFirst)   // more than can be counted: whole, whatever the caller asked for
+    chunk_split(1, span, 128, 0, p);
+  else
+    chunk_split(std::min(parts_wanted(units, slots, span), parts_wanted(units, slots, cap)), span, 128, partition_size, p);
   return true;
 }
 
@@ -215,9 +221,6 @@ PKV_API pkv_status pkv_chunk_attention(
   const size_t need = chunk_ws_bytes(plan.kernel, B, total_q, H, num_kv_heads, head_dim, max_q_len, plan.max_parts);
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256) return PKV_ERR_WORKSPACE;
   if (plan.chunks * num_kv_heads * plan.max_parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  if (plan.kernel != 2 && plan.max_parts > 1 && (long long)B * num_kv_heads * plan.chunks > kChunkCnt - kChunkCntFirst)
-    return PKV_ERR_UNSUPPORTED;
-
   int sms = 0;
   if (!device_sms(&sms)) return PKV_ERR_CUDA;
   ChunkArgs a;

@@ -51,7 +51,7 @@ def _rope(lib, **kw):
     axis = kw.get("axis")
     arr = None if axis is None else (ctypes.c_uint8 * len(axis))(*axis)
     return lib.pkv_rope_write(
-        kw.get("q_out", FAKE), kw.get("kc", FAKE), kw.get("vc", FAKE), kw.get("q", FAKE + 4096), kw.get("k", FAKE),
+        kw.get("q_out", 4 * FAKE), kw.get("kc", FAKE), kw.get("vc", FAKE), kw.get("q", FAKE + 4096), kw.get("k", FAKE),
         kw.get("v", FAKE), kw.get("cs", FAKE), kw.get("pos", FAKE), arr, kw.get("slots", FAKE), kw.get("T", 3),
         kw.get("qs", H * D), kw.get("ks", KVH * D), kw.get("vs", KVH * D), kw.get("ps", 3), kw.get("axes", 1), H, KVH,
         D, kw.get("rot", 64), 0, kw.get("maxp", 128), kw.get("nb", 8), kw.get("bs", 16), kw.get("dt", 1), None, None)
@@ -65,7 +65,7 @@ def test_rope_write_refusals(pkv):
                 {"ks": 127}, {"vs": 127}, {"axes": 3, "ps": 2}, {"axis": [0] * 31 + [1]}, {"q_out": None},
                 {"kc": None}, {"vc": None}, {"q": None}, {"k": None}, {"v": None}, {"cs": None}, {"pos": None},
                 {"slots": None}, {"q": FAKE + 1}, {"cs": FAKE + 2}, {"pos": FAKE + 2}, {"slots": FAKE + 4},
-                {"q_out": FAKE + 4096, "qs": 512}):
+                {"q_out": FAKE + 4096, "qs": 512}, {"q_out": FAKE + 4100}, {"q_out": FAKE - 8}):
         assert _rope(lib, **bad) == INVALID, bad
     assert _rope(lib, D=513, rot=64) == UNSUPPORTED
 
@@ -103,17 +103,18 @@ def test_chunk_plan_and_workspace(pkv):
     front = 65536 * 4
     for dt in (torch.bfloat16, torch.float32):
         for B, q, H, KVH, D, bs, mb in ((1, 1, 8, 1, 64, 16, 2048), (64, 64, 32, 8, 128, 16, 256), (3, 700, 6, 2, 80, 24, 99),
-                                        (8, 8 * 4, 32, 8, 128, 16, 2048), (1, 8192, 32, 8, 128, 16, 512)):
-            for window in (0, 1, 100, 1000, 5000):
+                                        (8, 8 * 4, 32, 8, 128, 16, 2048), (1, 8192, 32, 8, 128, 16, 512), (2, 40, 8, 2, 64, 16, 12000)):
+            for window in (0, 1, 100, 1000, 5000, 32000, 150000):
                 for part in (0, 128, 1024):
                     for max_q in (0, -(-q // B)):
                         P, parts, kernel = plan(B, q, H, KVH, D, bs, mb, max_q, 0, window, False, part, dt)
-                        assert P % 128 == 0 and (part == 0 or P <= part) and 1 <= parts <= max(64, -(-bs * mb // P))
+                        assert P % 128 == 0 and 1 <= parts <= 256
                         # every part a unit can touch has a place
                         mq = max_q or q
                         span = min(bs * mb, window + mq + 63) if window else bs * mb
                         assert parts == -(-span // P)
-                        assert part == 0 or P == min(part, -(-span // 128) * 128)
+                        least = -(-(-(-span // 256)) // 128) * 128
+                        assert part == 0 or P == min(max(part, least), -(-span // 128) * 128)
                         rows = q * H
                         al = lambda x: (x + 255) // 256 * 256
                         need = front + (0 if parts == 1 else 2 * al(rows * parts * 4) + rows * parts * D * 4)
