@@ -88,13 +88,16 @@ static long long parts_wanted(long long units, long long slots, long long span) 
 //   rounds of items over the SMs x (tiles of a part + 2 to start and end one)
 //   + joining the parts (0.015 a part of an item: its 270 KB to and from
 //   memory against 2.7 us a tile on one SM of 152; 2 for the launch).
+// No part is longer than 2^20 keys (some 25 ms), far inside the kernel's
+// bounded waits, which span an item.
 static long long tc_parts_wanted(long long items, long long span) {
-  long long best = 1;
+  const long long fewest = ceil_div(span, 1LL << 20);
+  long long best = fewest;
   double least = 0;
-  for (long long p = 1; p <= kChunkMaxParts && p <= ceil_div(span, 512); ++p) {
+  for (long long p = fewest; p <= kChunkMaxParts && p <= ceil_div(span, 512); ++p) {
     const double cost = (double)ceil_div(items * p, kPlanSms) * (ceil_div(ceil_div(span, p), 128) + 2) +
                         (p > 1 ? 0.015 * items * p + 2 : 0.0);
-    if (p == 1 || cost < least) {
+    if (p == fewest || cost < least) {
       least = cost;
       best = p;
     }

@@ -91,7 +91,11 @@ struct CtShape {
   static constexpr int kBarOff = kVOff + kVStages * kKVBytes;
   static constexpr int kPairOff = kBarOff + 1024;               // group 1's m, l of 128 rows
   static constexpr int kSmem = kPairOff + 1024 + 1024;          // + alignment slack
-  static constexpr uint32_t kTmemCols = 512;  // per group: S (128 columns, P over its first half), O (D columns)
+  // Tensor memory, 512 columns.  Two groups: S (128 columns, P over its first
+  // half) and O (D columns) in 256 each.  One: S buffer 0, O in columns 128 to
+  // 383, S buffer 1.
+  static constexpr uint32_t kTmemCols = 512;
+  __device__ __forceinline__ static uint32_t s_col(int g) { return (kGroups == 2 ? 256 : 384) * g; }
 };
 
 // One work item as every role sees it.  kind: 1 work, 2 no row sees a key
@@ -123,10 +127,10 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
   uint64_t *k_empty = v_full + kCtMaxStages;     // own ring and producer
   uint64_t *v_empty = k_empty + kCtMaxStages;
   uint64_t *q_full = v_empty + kCtMaxStages;     // [groups]: the group's query tile landed
-  uint64_t *q_empty = q_full + kCtMaxGroups;        // its last S of an item done
-  uint64_t *s_full = q_empty + kCtMaxGroups;        // S of its current tile
-  uint64_t *p_full = s_full + kCtMaxGroups;         // P of its current tile
-  uint64_t *o_done = p_full + kCtMaxGroups;         // its last P . V of an item done
+  uint64_t *q_empty = q_full + kCtMaxGroups;     // its last S of an item done
+  uint64_t *s_full = q_empty + kCtMaxGroups;     // S of its current tile (one group: of S buffer tile & 1)
+  uint64_t *p_full = s_full + kCtMaxGroups;      // P of its current tile (the same)
+  uint64_t *o_done = p_full + kCtMaxGroups;      // its last P . V of an item done (one group: every P . V, [0])
   uint64_t *item_full = o_done + kCtMaxGroups;      // [2]
   uint64_t *item_empty = item_full + 2;          // [2]
   uint64_t *pair_full = item_empty + 2;          // group 1's state of a shared row tile is there
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < kCtMaxGroups; ++g) {
       mbar_init(&q_full[g], 1);
       mbar_init(&q_empty[g], 1);
       mbar_init(&s_full[g], 1);
@@ -182,331 +186,375 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
   auto aborted = [&]() { return *(volatile int *)abort_flag != 0; };
 
   if (warp >= kSoftmaxWarps) {
-  if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtRegsOther));
-  if (warp == kSoftmaxWarps + 2) {
-    // ------------------------------------------------------------ scheduler
-    griddep_wait();                                // the plan's units (every other role waits for an item)
-    const unsigned total = (unsigned)*(volatile int *)ta.n_units * (unsigned)ta.subs;
-    unsigned w = blockIdx.x;
-    int it = 0, ig[kCtMaxGroups] = {0, 0};
-    bool ok = true;
-    while (true) {
-      CtItem item;
-      memset(&item, 0, sizeof item);
-      item.kind = -1;
-      if (w < total) {
-        const int4 *up = reinterpret_cast<const int4 *>(ta.units + w / (unsigned)ta.subs);
-        const int4 u0 = __ldcg(up), u1 = __ldcg(up + 1);
-        const ChunkSeq s = chunk_seq(a, u0.x, false);
-        item.sub = (int)(w % (unsigned)ta.subs);
-        item.b = u0.x;
-        item.i0 = u0.y;
-        item.part = u0.z;
-        item.nparts = u0.w;
-        item.t0 = u1.x;
-        item.t1 = u1.y;
-        item.lo = u1.z;
-        item.q0 = s.q0;
-        item.qlen = s.qlen;
-        item.n = s.n;
-        item.queries = min(kGroups * per, s.qlen - item.i0);
-        item.kind = item.t1 > 0 ? 1 : 2;
-        if (item.kind == 1) {
-          // one past the last key the group's rows see before the part's end
-          // (at least one tile, so that a present group always has work)
-          auto tiles_to = [&](int i) {
-            const int hi = min(item.t1, max(s.n - s.qlen + i + 1, s.prefix));
-            return max(1, (hi - item.t0 + kCtTile - 1) / kCtTile);
-          };
-          item.nt[0] = tiles_to(item.i0 + min(per, item.queries) - 1);
-          item.nt[1] = item.queries > per ? tiles_to(item.i0 + item.queries - 1) : 0;
-          item.ntiles = max(item.nt[0], item.nt[1]);
-          if (kGroups == 2 && item.queries <= per) {
-            item.nparts = -item.nparts;
-            item.nt[1] = item.ntiles / 2;
-            item.nt[0] = item.ntiles - item.nt[1];
+    if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtRegsOther));
+    if (warp == kSoftmaxWarps + 2) {
+      // ------------------------------------------------------------ scheduler
+      griddep_wait();                                // the plan's units (every other role waits for an item)
+      const unsigned total = (unsigned)*(volatile int *)ta.n_units * (unsigned)ta.subs;
+      unsigned w = blockIdx.x;
+      int it = 0, ig[kCtMaxGroups] = {0, 0};
+      bool ok = true;
+      while (true) {
+        CtItem item;
+        memset(&item, 0, sizeof item);
+        item.kind = -1;
+        if (w < total) {
+          const int4 *up = reinterpret_cast<const int4 *>(ta.units + w / (unsigned)ta.subs);
+          const int4 u0 = __ldcg(up), u1 = __ldcg(up + 1);
+          const ChunkSeq s = chunk_seq(a, u0.x, false);
+          item.sub = (int)(w % (unsigned)ta.subs);
+          item.b = u0.x;
+          item.i0 = u0.y;
+          item.part = u0.z;
+          item.nparts = u0.w;
+          item.t0 = u1.x;
+          item.t1 = u1.y;
+          item.lo = u1.z;
+          item.q0 = s.q0;
+          item.qlen = s.qlen;
+          item.n = s.n;
+          item.queries = min(kGroups * per, s.qlen - item.i0);
+          item.kind = item.t1 > 0 ? 1 : 2;
+          if (item.kind == 1) {
+            // one past the last key the group's rows see before the part's end
+            // (at least one tile, so that a present group always has work)
+            auto tiles_to = [&](int i) {
+              const int hi = min(item.t1, max(s.n - s.qlen + i + 1, s.prefix));
+              return max(1, (hi - item.t0 + kCtTile - 1) / kCtTile);
+            };
+            item.nt[0] = tiles_to(item.i0 + min(per, item.queries) - 1);
+            item.nt[1] = item.queries > per ? tiles_to(item.i0 + item.queries - 1) : 0;
+            item.ntiles = max(item.nt[0], item.nt[1]);
+            if (kGroups == 2 && item.queries <= per) {
+              item.nparts = -item.nparts;
+              item.nt[1] = item.ntiles / 2;
+              item.nt[0] = item.ntiles - item.nt[1];
+            }
           }
         }
-      }
-      const int slot = it & 1;
-      if (it >= 2) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&item_empty[slot], ((it >> 1) - 1) & 1));
-        if (!ok) break;
-      }
-      if (lane == 0) {
-        items[slot] = item;
-        mbar_arrive(&item_full[slot]);
-      }
-      __syncwarp();
-      ++it;
-      if (item.kind < 0) break;
-      if (item.kind == 1) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          if (!ok || item.nt[g] == 0) continue;
-          if (ig[g] > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_empty[g], (ig[g] - 1) & 1)) && !aborted();
-            if (!ok) break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&q_full[g], (uint32_t)Sh::kQBytes);
-          __syncwarp();
-          if (lane < Sh::kRegions)
-            tma_load_3d_keep(sm + Sh::kQOff + g * Sh::kQBytes + lane * kCtQRegion, &tmQ, &q_full[g], 64 * lane,
-                             item.sub << ta.gshift, item.q0 + item.i0 + (item.pair() ? 0 : g * per));
-          ++ig[g];
+        const int slot = it & 1;
+        if (it >= 2) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&item_empty[slot], ((it >> 1) - 1) & 1));
+          if (!ok) break;
         }
-        if (!ok) break;
-      }
-      unsigned nw = 0;
-      if (lane == 0) nw = (unsigned)atomicAdd(a.ws_cnt, 1) + gridDim.x;
-      w = __shfl_sync(0xffffffffu, nw, 0);
-    }
-    if (!ok && lane == 0) abort_cta();
-    if (a.max_parts > 1) griddep_launch_dependents();  // the merge: it reads nothing before it has waited
-    // the last query tiles land before the CTA can end (bounded)
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-      if (ig[g] > 0) mbar_wait_bounded(&q_full[g], (ig[g] - 1) & 1);
-  } else if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 3) {
-    // ----------------------------------------------------------- producers
-    // one warp streams the keys, one the values: per item and tile the boxes
-    // (one per lane: some keys of one 64-column region) once the tile that
-    // used the stage before has been read.  In one warp a tile's keys would
-    // wait behind the values before them.
-    const bool is_v = warp != kSoftmaxWarps;
-    const int stages = is_v ? Sh::kVStages : Sh::kKStages;
-    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-    const CUtensorMap *map = is_v ? &tmV : &tmK;
-    uint8_t *ring_base = sm + (is_v ? Sh::kVOff : Sh::kKOff);
-    const int nboxes = kCtTile >> ta.bshift, per_tensor = nboxes * Sh::kRegions;
-    const int region = (lane % per_tensor) / nboxes, chunk = lane % nboxes;
-    int it = 0, issued = 0, stage = 0;
-    uint32_t parity = 1;            // of the stage's release: passes at once in the first round
-    bool ok = true;
-    while (ok) {
-      const int slot = it & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&item_full[slot], (it >> 1) & 1));
-      if (!ok) break;
-      const CtItem item = items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty[slot]);
-      ++it;
-      if (item.kind < 0) break;
-      const int kvh = (item.sub << ta.gshift) / a.G;
-      for (int j = 0; j < item.ntiles; ++j) {
-        const int tok0 = item.t0 + j * kCtTile;
-        const int valid_chunks = min(nboxes, (item.t1 - tok0 + (1 << ta.bshift) - 1) >> ta.bshift);
-        const uint32_t bytes = (uint32_t)(valid_chunks * Sh::kRegions * (128 << ta.bshift));
-        int phys = 0;
-        if (lane < valid_chunks) phys = __ldg(a.tables + (size_t)item.b * a.max_blocks + (tok0 + (lane << ta.bshift)) / a.bs);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], parity)) && !aborted();
-        if (!ok) break;
-        if (lane < valid_chunks && (phys < 0 || (long long)phys >= a.num_blocks)) {
-          raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
-          phys = 0;
+        if (lane == 0) {
+          items[slot] = item;
+          mbar_arrive(&item_full[slot]);
         }
-        phys = __shfl_sync(0xffffffffu, phys, chunk);
-        if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
         __syncwarp();
-        if (lane < per_tensor && chunk < valid_chunks) {
-          const int t = tok0 + (chunk << ta.bshift);
-          tma_load_4d_keep(ring_base + stage * Sh::kKVBytes + region * kCtKVRegion + chunk * (128 << ta.bshift), map,
-                           &full[stage], region * 64, kvh, t % a.bs, phys);
+        ++it;
+        if (item.kind < 0) break;
+        if (item.kind == 1) {
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            if (!ok || item.nt[g] == 0) continue;
+            if (ig[g] > 0) {
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_empty[g], (ig[g] - 1) & 1)) && !aborted();
+              if (!ok) break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&q_full[g], (uint32_t)Sh::kQBytes);
+            __syncwarp();
+            if (lane < Sh::kRegions)
+              tma_load_3d_keep(sm + Sh::kQOff + g * Sh::kQBytes + lane * kCtQRegion, &tmQ, &q_full[g], 64 * lane,
+                               item.sub << ta.gshift, item.q0 + item.i0 + (item.pair() ? 0 : g * per));
+            ++ig[g];
+          }
+          if (!ok) break;
         }
-        ++issued;
-        if (++stage == stages) {
-          stage = 0;
-          parity ^= 1;
-        }
+        unsigned nw = 0;
+        if (lane == 0) nw = (unsigned)atomicAdd(a.ws_cnt, 1) + gridDim.x;
+        w = __shfl_sync(0xffffffffu, nw, 0);
       }
-    }
-    if (!ok && lane == 0) abort_cta();
-    // the last fills land before the CTA can end (bounded)
-    for (int r = max(0, issued - stages); r < issued; ++r) mbar_wait_bounded(&full[r % stages], (r / stages) & 1);
-  } else if (warp == kSoftmaxWarps + 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_s = umma_idesc_f16(128, kCtTile, bf16, false);
-      const uint32_t idesc_o = umma_idesc_f16(128, D, bf16, true);
-      auto kv_base = [&](int ring, bool v) {
-        return smem_u32(v ? sm + Sh::kVOff + (ring % Sh::kVStages) * Sh::kKVBytes
-                          : sm + Sh::kKOff + (ring % Sh::kKStages) * Sh::kKVBytes);
-      };
-      auto issue_s = [&](int g, int ring) {  // S_g = Q_g . K^T over D in 16-wide steps
-        const uint32_t qb = smem_u32(sm + Sh::kQOff + g * Sh::kQBytes), kb = kv_base(ring, false);
+      if (!ok && lane == 0) abort_cta();
+      if (a.max_parts > 1) griddep_launch_dependents();  // the merge: it reads nothing before it has waited
+      // the last query tiles land before the CTA can end (bounded)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_f16(tmem + 256 * g, umma_desc_sw128(qb + (k >> 2) * kCtQRegion + (k & 3) * 32, 16, 1024),
-                   umma_desc_sw128(kb + (k >> 2) * kCtKVRegion + (k & 3) * 32, 16, 1024), idesc_s,
-                   k > 0);
-        umma_commit(&s_full[g]);
-      };
-      auto issue_pv = [&](int g, int ring, bool acc) {  // O_g (+)= P_g . V, P from tensor memory
-        const uint32_t vb = kv_base(ring, true);
-#pragma unroll
-        for (int k = 0; k < kCtTile / 16; ++k)
-          umma_f16_tmem_a(tmem + 256 * g + 128, tmem + 256 * g + 8 * k,
-                          umma_desc_sw128(vb + k * 2048, kCtKVRegion, 1024), idesc_o, acc || k > 0);
-      };
-      // Per item: S of the first tile of both groups; then per tile and
-      // group, as soon as P_g(j) arrives: P_g(j) . V_j, then S_g(j+1).  The
-      // products of one thread run in issue order, so S_g(j+1) -- written
-      // over P_g(j) -- starts after P_g(j) . V_j has read it, and the commit
-      // that signals S_g(j+1) also covers P_g(j) . V_j (O is final for tile
-      // j when the softmax sees S_g(j+1)).  The next item's first product
-      // into O (no accumulate) comes after the softmax's first P of that
-      // item, which the softmax writes only once it has read the previous O.
-      // Group 0 (the earlier query rows) needs no more KV tiles than group
-      // 1: once its last product of an item is issued, group 0's first S of
-      // the next item is issued as soon as that item, its query tile and its
-      // first keys are there, so group 0's softmax starts on the next item
-      // while group 1 finishes this one.
-      int it = 0, ring0 = 0, ig[kCtMaxGroups] = {0, 0}, tcnt[kCtMaxGroups] = {0, 0};
-      CtItem nx;
-      bool have_nx = false;   // the next item is read already
-      bool early = false;     // ... and group 0's first S of it issued
+      for (int g = 0; g < kGroups; ++g)
+        if (ig[g] > 0) mbar_wait_bounded(&q_full[g], (ig[g] - 1) & 1);
+    } else if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 3) {
+      // ----------------------------------------------------------- producers
+      // one warp streams the keys, one the values: per item and tile the boxes
+      // (one per lane: some keys of one 64-column region) once the tile that
+      // used the stage before has been read.  In one warp a tile's keys would
+      // wait behind the values before them.
+      const bool is_v = warp != kSoftmaxWarps;
+      const int stages = is_v ? Sh::kVStages : Sh::kKStages;
+      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+      const CUtensorMap *map = is_v ? &tmV : &tmK;
+      uint8_t *ring_base = sm + (is_v ? Sh::kVOff : Sh::kKOff);
+      const int nboxes = kCtTile >> ta.bshift, per_tensor = nboxes * Sh::kRegions;
+      const int region = (lane % per_tensor) / nboxes, chunk = lane % nboxes;
+      int it = 0, issued = 0, stage = 0;
+      uint32_t parity = 1;            // of the stage's release: passes at once in the first round
       bool ok = true;
       while (ok) {
-        CtItem item;
-        if (have_nx) {
-          item = nx;
-          have_nx = false;
-        } else {
-          const int slot = it & 1;
-          ok = mbar_wait_bounded(&item_full[slot], (it >> 1) & 1);
-          if (!ok) break;
-          item = items[slot];
-          mbar_arrive(&item_empty[slot]);
-          ++it;
-        }
+        const int slot = it & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&item_full[slot], (it >> 1) & 1));
+        if (!ok) break;
+        const CtItem item = items[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[slot]);
+        ++it;
         if (item.kind < 0) break;
-        if (item.ntiles == 0) continue;
-        const bool pre = early;
-        early = false;
-        if (kGroups == 2 && item.pair()) {
-          // tile j belongs to group j & 1
-          auto start_s = [&](int j) {  // S of tile j, and what its products free
-            const int g = j & 1, ring = ring0 + j;
-            if (!(j == 0 && pre)) {
+        const int kvh = (item.sub << ta.gshift) / a.G;
+        for (int j = 0; j < item.ntiles; ++j) {
+          const int tok0 = item.t0 + j * kCtTile;
+          const int valid_chunks = min(nboxes, (item.t1 - tok0 + (1 << ta.bshift) - 1) >> ta.bshift);
+          const uint32_t bytes = (uint32_t)(valid_chunks * Sh::kRegions * (128 << ta.bshift));
+          int phys = 0;
+          if (lane < valid_chunks) phys = __ldg(a.tables + (size_t)item.b * a.max_blocks + (tok0 + (lane << ta.bshift)) / a.bs);
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], parity)) && !aborted();
+          if (!ok) break;
+          if (lane < valid_chunks && (phys < 0 || (long long)phys >= a.num_blocks)) {
+            raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
+            phys = 0;
+          }
+          phys = __shfl_sync(0xffffffffu, phys, chunk);
+          if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          __syncwarp();
+          if (lane < per_tensor && chunk < valid_chunks) {
+            const int t = tok0 + (chunk << ta.bshift);
+            tma_load_4d_keep(ring_base + stage * Sh::kKVBytes + region * kCtKVRegion + chunk * (128 << ta.bshift), map,
+                             &full[stage], region * 64, kvh, t % a.bs, phys);
+          }
+          ++issued;
+          if (++stage == stages) {
+            stage = 0;
+            parity ^= 1;
+          }
+        }
+      }
+      if (!ok && lane == 0) abort_cta();
+      // the last fills land before the CTA can end (bounded)
+      for (int r = max(0, issued - stages); r < issued; ++r) mbar_wait_bounded(&full[r % stages], (r / stages) & 1);
+    } else if (warp == kSoftmaxWarps + 1) {
+      // ------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        const uint32_t idesc_s = umma_idesc_f16(128, kCtTile, bf16, false);
+        const uint32_t idesc_o = umma_idesc_f16(128, D, bf16, true);
+        auto kv_base = [&](int ring, bool v) {
+          return smem_u32(v ? sm + Sh::kVOff + (ring % Sh::kVStages) * Sh::kKVBytes
+                            : sm + Sh::kKOff + (ring % Sh::kKStages) * Sh::kKVBytes);
+        };
+        // g: the group, or with one group the S buffer
+        auto issue_s = [&](int g, int ring) {  // S_g = Q_g . K^T over D in 16-wide steps
+          const uint32_t qb = smem_u32(sm + Sh::kQOff + (kGroups == 2 ? g : 0) * Sh::kQBytes), kb = kv_base(ring, false);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            umma_f16(tmem + Sh::s_col(g), umma_desc_sw128(qb + (k >> 2) * kCtQRegion + (k & 3) * 32, 16, 1024),
+                     umma_desc_sw128(kb + (k >> 2) * kCtKVRegion + (k & 3) * 32, 16, 1024), idesc_s,
+                     k > 0);
+          umma_commit(&s_full[g]);
+        };
+        auto issue_pv = [&](int g, int ring, bool acc) {  // O_g (+)= P_g . V, P from tensor memory
+          const uint32_t vb = kv_base(ring, true);
+#pragma unroll
+          for (int k = 0; k < kCtTile / 16; ++k)
+            umma_f16_tmem_a(tmem + (kGroups == 2 ? 256 * g + 128 : 128), tmem + Sh::s_col(g) + 8 * k,
+                            umma_desc_sw128(vb + k * 2048, kCtKVRegion, 1024), idesc_o, acc || k > 0);
+        };
+        // Per item: S of the first tile of both groups; then per tile and
+        // group, as soon as P_g(j) arrives: P_g(j) . V_j, then S_g(j+1).  The
+        // products of one thread run in issue order, so S_g(j+1) -- written
+        // over P_g(j) -- starts after P_g(j) . V_j has read it, and the commit
+        // that signals S_g(j+1) also covers P_g(j) . V_j (O is final for tile
+        // j when the softmax sees S_g(j+1)).  The next item's first product
+        // into O (no accumulate) comes after the softmax's first P of that
+        // item, which the softmax writes only once it has read the previous O.
+        // Group 0 (the earlier query rows) needs no more KV tiles than group
+        // 1: once its last product of an item is issued, group 0's first S of
+        // the next item is issued as soon as that item, its query tile and its
+        // first keys are there, so group 0's softmax starts on the next item
+        // while group 1 finishes this one.
+        int it = 0, ring0 = 0, ig[kCtMaxGroups] = {0, 0}, tcnt[kCtMaxGroups] = {0, 0};
+        CtItem nx;
+        bool have_nx = false;   // the next item is read already
+        bool early = false;     // ... and group 0's first S of it issued
+        bool ok = true;
+        while (ok) {
+          CtItem item;
+          if (have_nx) {
+            item = nx;
+            have_nx = false;
+          } else {
+            const int slot = it & 1;
+            ok = mbar_wait_bounded(&item_full[slot], (it >> 1) & 1);
+            if (!ok) break;
+            item = items[slot];
+            mbar_arrive(&item_empty[slot]);
+            ++it;
+          }
+          if (item.kind < 0) break;
+          if (item.ntiles == 0) continue;
+          const bool pre = early;
+          early = false;
+          if constexpr (kGroups == 1) {
+            // One row tile: S of tile t goes to buffer t & 1 (t counts over all
+            // items), so the next S is made while the softmax works on this one,
+            // as soon as its keys are there, and before or after P . V as they
+            // and P arrive.  A buffer's P is read by a product issued before
+            // the S that overwrites it.
+            auto start_s = [&](int ring, bool last) {
               ok = ok && mbar_wait_bounded(&k_full[ring % Sh::kKStages], (ring / Sh::kKStages) & 1);
-              if (ok && j < 2) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
               if (!ok) return;
               tc_fence_after();
-              issue_s(g, ring);
-              if (j + 2 >= item.ntiles) umma_commit(&q_empty[g]);
+              issue_s(ring & 1, ring);
+              if (last) umma_commit(&q_empty[0]);
+              umma_commit(&k_empty[ring % Sh::kKStages]);
+            };
+            ok = mbar_wait_bounded(&q_full[0], ig[0] & 1);
+            start_s(ring0, item.ntiles == 1);
+            for (int j = 0; ok && j < item.ntiles; ++j) {
+              const int ring = ring0 + j, nr = ring + 1;
+              bool started = j + 1 >= item.ntiles;
+              const unsigned long long t0 = global_timer_ns();
+              while (!mbar_test_wait(&p_full[ring & 1], (ring >> 1) & 1)) {
+                if (!started && mbar_test_wait(&k_full[nr % Sh::kKStages], (nr / Sh::kKStages) & 1)) {
+                  start_s(nr, j + 2 == item.ntiles);
+                  started = true;
+                }
+                if (global_timer_ns() - t0 > kWaitLimitNs) {
+                  ok = false;
+                  break;
+                }
+              }
+              if (ok) ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(ring & 1, ring, j > 0);
+              umma_commit(&v_empty[ring % Sh::kVStages]);
+              umma_commit(&o_done[0]);
+              if (!started) start_s(nr, j + 2 == item.ntiles);
             }
-            umma_commit(&k_empty[ring % Sh::kKStages]);
-          };
-          for (int j = 0; ok && j < min(2, item.ntiles); ++j) start_s(j);
-          for (int j = 0; ok && j < item.ntiles; ++j) {
-            const int g = j & 1, ring = ring0 + j;
-            ok = mbar_wait_bounded(&p_full[g], tcnt[g] & 1);
-            ++tcnt[g];
-            if (ok) ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(g, ring, j >= 2);
-            umma_commit(&v_empty[ring % Sh::kVStages]);
-            if (j + 2 < item.ntiles) start_s(j + 2);
-            else umma_commit(&o_done[g]);
+            ring0 += item.ntiles;
+            if (ok && aborted()) ok = false;
+            ++ig[0];
+            continue;
           }
-          ring0 += item.ntiles;
+          if (kGroups == 2 && item.pair()) {
+            // tile j belongs to group j & 1
+            auto start_s = [&](int j) {  // S of tile j, and what its products free
+              const int g = j & 1, ring = ring0 + j;
+              if (!(j == 0 && pre)) {
+                ok = ok && mbar_wait_bounded(&k_full[ring % Sh::kKStages], (ring / Sh::kKStages) & 1);
+                if (ok && j < 2) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
+                if (!ok) return;
+                tc_fence_after();
+                issue_s(g, ring);
+                if (j + 2 >= item.ntiles) umma_commit(&q_empty[g]);
+              }
+              umma_commit(&k_empty[ring % Sh::kKStages]);
+            };
+            for (int j = 0; ok && j < min(2, item.ntiles); ++j) start_s(j);
+            for (int j = 0; ok && j < item.ntiles; ++j) {
+              const int g = j & 1, ring = ring0 + j;
+              ok = mbar_wait_bounded(&p_full[g], tcnt[g] & 1);
+              ++tcnt[g];
+              if (ok) ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(g, ring, j >= 2);
+              umma_commit(&v_empty[ring % Sh::kVStages]);
+              if (j + 2 < item.ntiles) start_s(j + 2);
+              else umma_commit(&o_done[g]);
+            }
+            ring0 += item.ntiles;
+            if (ok && aborted()) ok = false;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) ig[g] += item.nt[g] > 0;
+            continue;
+          }
+          ok = mbar_wait_bounded(&k_full[ring0 % Sh::kKStages], (ring0 / Sh::kKStages) & 1);
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+            if (ok && item.nt[g] > 0 && !(g == 0 && pre)) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
+          if (!ok || aborted()) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            if (item.nt[g] == 0 || (g == 0 && pre)) continue;
+            issue_s(g, ring0);
+            if (item.nt[g] == 1) umma_commit(&q_empty[g]);  // the group's last S of the item
+          }
+          umma_commit(&k_empty[ring0 % Sh::kKStages]);
+          const int ring_next = ring0 + item.ntiles;
+          // group 0's first S of the next item, if everything it reads is
+          // there (never waits)
+          auto try_early = [&]() {
+            if (early) return;
+            if (!have_nx) {
+              const int slot = it & 1;
+              if (!mbar_test_wait(&item_full[slot], (it >> 1) & 1)) return;
+              nx = items[slot];
+              mbar_arrive(&item_empty[slot]);
+              ++it;
+              have_nx = true;
+            }
+            if (nx.kind != 1) return;
+            if (!mbar_test_wait(&k_full[ring_next % Sh::kKStages], (ring_next / Sh::kKStages) & 1) ||
+                !mbar_test_wait(&q_full[0], (ig[0] + 1) & 1))
+              return;
+            tc_fence_after();
+            issue_s(0, ring_next);
+            if (nx.nt[0] == 1) umma_commit(&q_empty[0]);
+            early = true;
+          };
+          for (int j = 0; ok && j < item.ntiles; ++j) {
+            const int ring = ring0 + j;
+            bool v_ready = false, k_ready = false;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              if (!ok || j >= item.nt[g]) continue;
+              if (g == 1 && j + 1 >= item.nt[0]) {
+                // group 0 is done with this item: look for its next one while
+                // group 1's P is not there yet
+                const unsigned long long t0 = global_timer_ns();
+                while (!mbar_test_wait(&p_full[1], tcnt[1] & 1)) {
+                  try_early();
+                  if (global_timer_ns() - t0 > kWaitLimitNs) break;
+                }
+              }
+              ok = mbar_wait_bounded(&p_full[g], tcnt[g] & 1);
+              ++tcnt[g];
+              if (!ok) break;
+              if (!v_ready) {
+                ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
+                if (!ok) break;
+                v_ready = true;
+              }
+              tc_fence_after();
+              issue_pv(g, ring, j > 0);
+              // the tile's last P . V: its V slot is free once that has run
+              if (g == kGroups - 1 || j >= item.nt[1]) umma_commit(&v_empty[ring % Sh::kVStages]);
+              if (j + 1 < item.nt[g]) {
+                if (!k_ready) {
+                  ok = mbar_wait_bounded(&k_full[(ring + 1) % Sh::kKStages], ((ring + 1) / Sh::kKStages) & 1);
+                  if (!ok) break;
+                  k_ready = true;
+                }
+                issue_s(g, ring + 1);
+                if (j + 2 == item.nt[g]) umma_commit(&q_empty[g]);
+              } else {
+                umma_commit(&o_done[g]);  // the group's last product of the item
+              }
+            }
+            if (!ok) break;
+            if (j + 1 < item.ntiles) umma_commit(&k_empty[(ring + 1) % Sh::kKStages]);
+          }
+          ring0 = ring_next;
           if (ok && aborted()) ok = false;
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) ig[g] += item.nt[g] > 0;
-          continue;
         }
-        ok = mbar_wait_bounded(&k_full[ring0 % Sh::kKStages], (ring0 / Sh::kKStages) & 1);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-          if (ok && item.nt[g] > 0 && !(g == 0 && pre)) ok = mbar_wait_bounded(&q_full[g], ig[g] & 1);
-        if (!ok || aborted()) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          if (item.nt[g] == 0 || (g == 0 && pre)) continue;
-          issue_s(g, ring0);
-          if (item.nt[g] == 1) umma_commit(&q_empty[g]);  // the group's last S of the item
-        }
-        umma_commit(&k_empty[ring0 % Sh::kKStages]);
-        const int ring_next = ring0 + item.ntiles;
-        // group 0's first S of the next item, if everything it reads is
-        // there (never waits)
-        auto try_early = [&]() {
-          if (early) return;
-          if (!have_nx) {
-            const int slot = it & 1;
-            if (!mbar_test_wait(&item_full[slot], (it >> 1) & 1)) return;
-            nx = items[slot];
-            mbar_arrive(&item_empty[slot]);
-            ++it;
-            have_nx = true;
-          }
-          if (nx.kind != 1) return;
-          if (!mbar_test_wait(&k_full[ring_next % Sh::kKStages], (ring_next / Sh::kKStages) & 1) ||
-              !mbar_test_wait(&q_full[0], (ig[0] + 1) & 1))
-            return;
-          tc_fence_after();
-          issue_s(0, ring_next);
-          if (nx.nt[0] == 1) umma_commit(&q_empty[0]);
-          early = true;
-        };
-        for (int j = 0; ok && j < item.ntiles; ++j) {
-          const int ring = ring0 + j;
-          bool v_ready = false, k_ready = false;
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            if (!ok || j >= item.nt[g]) continue;
-            if (g == 1 && j + 1 >= item.nt[0]) {
-              // group 0 is done with this item: look for its next one while
-              // group 1's P is not there yet
-              const unsigned long long t0 = global_timer_ns();
-              while (!mbar_test_wait(&p_full[1], tcnt[1] & 1)) {
-                try_early();
-                if (global_timer_ns() - t0 > kWaitLimitNs) break;
-              }
-            }
-            ok = mbar_wait_bounded(&p_full[g], tcnt[g] & 1);
-            ++tcnt[g];
-            if (!ok) break;
-            if (!v_ready) {
-              ok = mbar_wait_bounded(&v_full[ring % Sh::kVStages], (ring / Sh::kVStages) & 1);
-              if (!ok) break;
-              v_ready = true;
-            }
-            tc_fence_after();
-            issue_pv(g, ring, j > 0);
-            // the tile's last P . V: its V slot is free once that has run
-            if (g == kGroups - 1 || j >= item.nt[1]) umma_commit(&v_empty[ring % Sh::kVStages]);
-            if (j + 1 < item.nt[g]) {
-              if (!k_ready) {
-                ok = mbar_wait_bounded(&k_full[(ring + 1) % Sh::kKStages], ((ring + 1) / Sh::kKStages) & 1);
-                if (!ok) break;
-                k_ready = true;
-              }
-              issue_s(g, ring + 1);
-              if (j + 2 == item.nt[g]) umma_commit(&q_empty[g]);
-            } else {
-              umma_commit(&o_done[g]);  // the group's last product of the item
-            }
-          }
-          if (!ok) break;
-          if (j + 1 < item.ntiles) umma_commit(&k_empty[(ring + 1) % Sh::kKStages]);
-        }
-        ring0 = ring_next;
-        if (ok && aborted()) ok = false;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) ig[g] += item.nt[g] > 0;
+        if (!ok) abort_cta();
+        umma_commit(mma_done);  // every product issued above has completed when this arrives
+        mbar_wait_bounded(mma_done, 0);
       }
-      if (!ok) abort_cta();
-      umma_commit(mma_done);  // every product issued above has completed when this arrives
-      mbar_wait_bounded(mma_done, 0);
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     // ------------------------------------------------------------ softmax
     if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCtRegsSoftmax));
@@ -514,7 +562,6 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
     const int quarter = warp & 3;
     const int r = 32 * quarter + lane;                  // row in the tile = tensor-memory lane
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    const uint32_t tmem_sp = tmem + 256 * g + lane_off; // S, then P over its first half
     const uint32_t tmem_o = tmem + 256 * g + 128 + lane_off;
     const float sl2 = a.scale_y;
     // scores may stay raw until the exponent when nothing but a positive
@@ -567,16 +614,18 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
       for (int c = 0; c < 4; ++c) d_bias[c] = make_float2(slope * (float)(2 * c), slope * (float)(2 * c + 1));
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < my_tiles; ++j) {
-        ok = mbar_wait_bounded(&s_full[g], tcnt & 1);
+        const int jt = pair ? 2 * j + g : j;           // the item's tile
+        const int t0 = item.t0 + jt * kCtTile;
+        const int ring = ring0 + jt;
+        const int sb = kGroups == 2 ? g : ring & 1;    // its S (and P) and their barriers
+        const uint32_t tmem_sp = tmem + Sh::s_col(sb) + lane_off;
+        ok = mbar_wait_bounded(&s_full[sb], (kGroups == 2 ? tcnt : ring >> 1) & 1);
         ++tcnt;
         if (!__all_sync(0xffffffffu, ok) || aborted()) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int jt = pair ? 2 * j + g : j;           // the item's tile
-        const int t0 = item.t0 + jt * kCtTile;
-        const int ring = ring0 + jt;
         if (live) {
         uint32_t sa[64], sb[64];
         tmem_ld64_nowait(tmem_sp, sa);
@@ -730,9 +779,13 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
         }
         tmem_wait_st();
         l += lsum.x + lsum.y;
-        // O is final for tile j - 1 here (the commit that signalled S_g(j)
-        // covers P_g(j - 1) . V)
+        // O is final for tile j - 1 here with two groups (the commit that
+        // signalled S_g(j) covers P_g(j - 1) . V); with one it may still run
         if (rescale) {
+          if (kGroups == 1) {
+            ok = mbar_wait_bounded(&o_done[0], (ring - 1) & 1);
+            tc_fence_after();
+          }
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
@@ -742,6 +795,15 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
             tmem_st32(tmem_o + 32 * c, v);
           }
         }
+        }
+        if (kGroups == 1) {
+          // the product before the item's last is waited for here, so that the
+          // wait for the last one below looks at its phase and no other
+          if (j > 0 && j + 1 == my_tiles) ok = ok && mbar_wait_bounded(&o_done[0], (ring - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
         }
         // the tile's values that no row of the unit sees become 0 (they may
         // hold anything, and 0 * NaN would poison the product)
@@ -763,10 +825,14 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           fence_proxy_async_shared();  // the zeros before the product reads them
         }
         tc_fence_before();
-        mbar_arrive(&p_full[g]);
+        mbar_arrive(&p_full[sb]);
       }
       if (!ok) break;
-      ok = mbar_wait_bounded(&o_done[g], ig & 1);
+      if (kGroups == 2) {
+        ok = mbar_wait_bounded(&o_done[g], ig & 1);
+      } else {
+        ok = mbar_wait_bounded(&o_done[0], (ring0 + my_tiles - 1) & 1);
+      }
       ++ig;
       if (!__all_sync(0xffffffffu, ok) || aborted()) {
         ok = false;
