@@ -518,9 +518,9 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  * Supported: fp32, bf16, fp16; head_dim <= 512; any block size; element-
  * aligned pointers.  bf16 / fp16 with 16-byte aligned tensors, block_size a
  * multiple of 16 and head_dim 64, 128, 192 or 256 run tensor-core kernels:
- * an mma.sync kernel where max_q_len * H / num_kv_heads is 32 at most, else a
- * tcgen05 kernel (three launches: plan, attention and, when split, join).
- * Everything else runs on the CUDA cores.
+ * an mma.sync kernel where max_q_len * H / num_kv_heads is 32 at most or the
+ * whole call is small, else a tcgen05 kernel (three launches: plan, attention
+ * and, when split, join).  Everything else runs on the CUDA cores.
  * Errors: PKV_ERR_INVALID_ARG (also a scale that is not finite, a softcap
  * that is negative, not finite or too small for scale / softcap, a negative
  * window), PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA.  B == 0 or

@@ -74,12 +74,13 @@ static int chunk_max_q(int64_t total_q, int max_q) {
 //  - Fewer units, short contexts: one round of CTAs, 128 keys or more, at most
 //    32 parts (one sequence of 8192 keys, 8 KV heads: 17 us at 256 keys, 19 at
 //    1024, 25 at 128; 128 one-head units of 1087 keys, 152 slots: 25.4 us
-//    whole, 33.8 in two).
-static long long parts_wanted(long long units, long long slots, long long span) {
+//    whole, 33.8 in two); `whole` keys or fewer are not worth the join.
+static long long parts_wanted(long long units, long long slots, long long span, long long whole) {
   units = std::max<long long>(units, 1);
   if (units >= slots) return std::max<long long>(1, std::min(ceil_div(4 * slots, units), span / 2048));
   const long long two = std::min<long long>(2 * slots / units, kChunkMaxParts);
   if (span / two >= 1024) return two;
+  if (span <= whole) return 1;
   return std::max<long long>(1, std::min<long long>({slots / units, 32, ceil_div(span, 128)}));
 }
 
@@ -126,8 +127,15 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   const long long mq = chunk_max_q(total_q, max_q), cap = chunk_cap(bs, max_blocks, max_n);
   // 16-bit tensors that TMA can read, in tokens chunks that never span two blocks
   p->kernel = tc_eligible(dt, D, bs) && aligned16 ? 1 : 0;
-  if (p->kernel == 1 && mq * (H / KVH) > kMmaRows) p->kernel = 2;
   const long long unit_rows = mq * (H / KVH);
+  // More rows than that go to tcgen05, unless everything is small: 16-row
+  // units that are all resident at once, over 1024 keys or fewer, are done
+  // before the plan and the larger tiles pay (64 tokens on 64 keys, 8 KV
+  // heads: 8.4 us against 16.8; on 1024 keys 22.8 / 27.1; 200 tokens on 1024
+  // keys, 400 units, 35 / 31).  By the table's keys, not a window's, so that
+  // the workspace knows.
+  const bool small = (long long)B * KVH * ceil_div(unit_rows, kChunkRows) <= kPlanSms * (D <= 192 ? 2 : 1) && cap <= 1024;
+  if (p->kernel == 1 && unit_rows > kMmaRows && !small) p->kernel = 2;
   p->rows = kChunkRows;
   if (p->kernel == 0) p->rows = unit_rows <= kChunkFewRows ? kChunkFewRows : D <= 256 && unit_rows > 2 * kChunkRows ? kChunkManyRows : kChunkRows;
   p->chunks = ceil_div(mq * (H / KVH), p->rows);
@@ -141,10 +149,12 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   }
   const int per_sm = p->kernel == 0 ? (p->rows == kChunkManyRows ? 2 : 4) : D <= 192 ? 2 : 1;   // resident CTAs
   const long long units = (long long)B * KVH * p->chunks, slots = (long long)kPlanSms * per_sm;
+  const long long whole = p->kernel == 1 ? 640 : 0;   // a tensor-core CTA takes 640 keys in the time of a join
   if (units > kChunkCnt - kChunkCntFirst)   // more than can be counted: whole, whatever the caller asked for
     chunk_split(1, span, 128, 0, p);
   else
-    chunk_split(std::min(parts_wanted(units, slots, span), parts_wanted(units, slots, cap)), span, 128, partition_size, p);
+    chunk_split(std::min(parts_wanted(units, slots, span, whole), parts_wanted(units, slots, cap, whole)), span, 128,
+                partition_size, p);
   return true;
 }
 

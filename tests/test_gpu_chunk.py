@@ -22,13 +22,15 @@ DEV = torch.device("cuda")
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
 
 
-def case(seed, lens, qlens, H, KVH, D, bs, dtype, gain=2.0, poison=True):
-    """Shuffled blocks, garbage tails, NaN in every cache row behind a context."""
+def case(seed, lens, qlens, H, KVH, D, bs, dtype, gain=2.0, poison=True, room=1100):
+    """Shuffled blocks, garbage tails (tables of `room` keys or more: small calls,
+    up to 1024, may run on another kernel), NaN in every cache row behind a
+    context."""
     g = torch.Generator().manual_seed(seed)
     need = [-(-n // bs) for n in lens]
     nb = sum(need) + 3
     perm = torch.randperm(nb, generator=g).to(torch.int32)
-    tables = torch.full((len(lens), max(need + [1]) + 2), 99999, dtype=torch.int32)
+    tables = torch.full((len(lens), max(need + [1, -(-room // bs)]) + 2), 99999, dtype=torch.int32)
     k = torch.randn(nb, bs, KVH, D, generator=g).to(dtype)
     v = torch.randn(nb, bs, KVH, D, generator=g).to(dtype)
     at, used = 0, torch.zeros(nb, bs, dtype=torch.bool)
@@ -119,12 +121,22 @@ def test_decode_forms(dtype, H, KVH, D, bs):
         check(c, f"{sorted(f)} split", partition_size=128, **f)
 
 
+@pytest.mark.parametrize("room", [1, 1100])
 @pytest.mark.parametrize("dtype,H,KVH,D,bs", SHAPES)
-def test_chunk_forms(dtype, H, KVH, D, bs):
-    c = case(D * 3 + H, [1, 40, 33, 200, 129, 260], [1, 3, 33, 150, 64, 17], H, KVH, D, bs, dtype)
+def test_chunk_forms(dtype, H, KVH, D, bs, room):
+    c = case(D * 3 + H, [1, 40, 33, 200, 129, 260], [1, 3, 33, 150, 64, 17], H, KVH, D, bs, dtype, room=room)
     for f in forms(c, 2):
         check(c, f"{sorted(f)}", **f)
         check(c, f"{sorted(f)} split", partition_size=128, **f)
+
+
+def test_each_kernel_is_reached():
+    """The plan's kernel by rows, type, shape and the call's size."""
+    plan = lambda *a, **k: pkv.pkv_chunk_plan(*a, **k)[2]
+    assert plan(4, 4, 8, 2, 128, 16, 200) == 1 and plan(4, 400, 8, 2, 128, 16, 200) == 2
+    assert plan(4, 400, 8, 2, 256, 16, 200) == 2 and plan(2, 40, 8, 2, 128, 16, 64, 20) == 1
+    assert plan(64, 6400, 8, 2, 128, 16, 64, 100) == 2
+    assert plan(4, 400, 8, 2, 128, 8, 200) == 0 and plan(4, 400, 8, 2, 128, 16, 200, dtype=F32) == 0
 
 
 @pytest.mark.parametrize("dtype,H,KVH,D", [(BF, 8, 2, 128), (BF, 4, 4, 64), (HF, 8, 1, 256), (F32, 4, 2, 64)])
