@@ -73,8 +73,8 @@ static int chunk_max_q(int64_t total_q, int max_q) {
 //    over 16-32k keys: 132 us at 8192 keys, 150 at 2048).
 //  - Fewer units, short contexts: one round of CTAs, 128 keys or more, at most
 //    32 parts (one sequence of 8192 keys, 8 KV heads: 17 us at 256 keys, 19 at
-//    1024, 25 at 128; 128 one-head units of 1087 keys, 152 slots: 25.4 us
-//    whole, 33.8 in two); `whole` keys or fewer are not worth the join.
+//    1024, 25 at 128; 128 one-head units of 1087 keys, 152 slots: 28.9 us
+//    whole, 46.3 in two); `whole` keys or fewer are not worth the join.
 static long long parts_wanted(long long units, long long slots, long long span, long long whole) {
   units = std::max<long long>(units, 1);
   if (units >= slots) return std::max<long long>(1, std::min(ceil_div(4 * slots, units), span / 2048));

@@ -2,16 +2,17 @@
 // single tokens and short drafts, where reading K and V once bounds the call
 // (see pkv_chunk.cuh for the rows, masks and scores).
 //
-// CTA = (part of the context, 16 packed rows of a KV head, sequence), 4 warps.
+// CTA = (part of the context, 16 packed rows of a KV head, sequence), W warps.
 // A part is walked in chunks of 16 tokens (block_size is a multiple of 16, so
-// a chunk lies in one block); warp w takes chunks w, w + 4, ... through its
-// own ring of shared-memory stages, each filled by two 5-D TMA boxes (the
-// chunk's K and V rows of this head).  The 16 rows are one m16n8k16 tile:
+// a chunk lies in one block); warp w takes chunks w, w + W, ...; chunk c passes
+// through stage c mod R of a ring in shared memory, filled by two 5-D TMA boxes
+// (the chunk's K and V rows of this head), and the warp that is done with chunk
+// c fetches chunk c + R into its stage.  The 16 rows are one m16n8k16 tile:
 //   S[16 x 16] = Q K^T, scores and masks, online softmax in registers,
 //   O[16 x D] += P V,
-// and the four warps' states are merged in shared memory at the end.  No
-// barrier separates the warps in between; a chunk that every row sees whole
-// (the usual one) skips the masks.
+// and the warps' states are merged in shared memory at the end.  No barrier
+// separates the warps in between; a chunk that every row sees whole (the usual
+// one) skips the masks.
 #include <string.h>
 
 #include "pkv_chunk.cuh"
@@ -20,7 +21,6 @@ namespace pkv {
 
 constexpr int kCmTok = 16;
 constexpr int kCmRows = 16;
-constexpr int kCmWarps = 4;
 constexpr int kCmBox = 16 * 128;      // one box: 16 rows of 64 elements
 
 template <int D>
@@ -28,35 +28,66 @@ struct CmShape {
   static constexpr int kSteps = D / 16;
   static constexpr int kBoxes = D / 64;
   static constexpr int kStage = 2 * kBoxes * kCmBox;             // K and V of one chunk
-  static constexpr int kStages = D <= 64 ? 6 : D <= 128 ? 3 : D <= 192 ? 2 : 3;
-  static constexpr int kRing = kCmWarps * kStages * kStage;
+  // Two CTAs of 4 warps an SM; at 256, where 12 stages fill the
+  // shared memory, one of 8.  (4 warps there left each scheduler one, which
+  // waited for its own products: 16 heads on 8192 keys 28.9 us, 22.2 with 8; on
+  // 640 whole 18.6 / 16.3; 64 sequences of 4096 62.9 / 58.9.  128 of 1087 lose,
+  // 27.0 / 28.8: fewer stages are ahead of the warps.  Two CTAs of 4 warps and 6
+  // stages: 8192 keys 29.1, 128 of 1087 in two parts 38.5.)
+  static constexpr int kWarps = D <= 192 ? 4 : 8;
+  static constexpr int kStages = D <= 64 ? 24 : D <= 128 ? 12 : D <= 192 ? 8 : 12;
+  // a stage is always the same warp's: its next chunk cannot be looked for
+  // before it is asked for
+  static constexpr bool kOwn = kStages % kWarps == 0;
+  static constexpr int kRing = kStages * kStage;
   static constexpr int kQStride = D + 8;
   static constexpr int kOStride = D + 8;
   static constexpr bool kQInRegs = D <= 128;
-  static constexpr int kSmem = 1024 + kRing + kCmRows * kQStride * 2 + kCmWarps * kStages * 8 +
-                               4 * (2 * kCmWarps * kCmRows + 3 * kCmRows) + 4 * (2 * kCmRows + 4);
-  static_assert(kCmWarps * kCmRows * kOStride * 4 <= kRing, "the warps' states fit the ring");
+  static constexpr int kSmem = 1024 + kRing + kCmRows * kQStride * 2 + kStages * 8 +
+                               4 * (2 * kWarps * kCmRows + 3 * kCmRows) + 4 * (2 * kCmRows + 4 + kStages);
+  static_assert(kWarps * kCmRows * kOStride * 4 <= kRing, "the warps' states fit the ring");
+  static_assert(kStages >= kWarps, "every warp's first chunk is in the first fill");
 };
 
+__device__ __forceinline__ void st_release_cta(int *p, int v) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+
+// Wait until *p is v; false after kWaitLimitNs.
+__device__ __forceinline__ bool flag_wait_bounded(const int *p, int v) {
+  auto is = [&]() {
+    int x;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(x) : "r"(smem_u32(p)) : "memory");
+    return x == v;
+  };
+  if (is()) return true;
+  const unsigned long long t0 = global_timer_ns();
+  while (!is()) {
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return true;
+}
+
 template <int D, typename T, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(32 * kCmWarps, 1)
+__global__ void __launch_bounds__(32 * CmShape<D>::kWarps, 1)
     pkv_chunk_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const ChunkArgs a) {
   using Sh = CmShape<D>;
   using Mma = MmaOp<T>;
-  constexpr int S = Sh::kStages;
+  constexpr int R = Sh::kStages, W = Sh::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   T *sQ = reinterpret_cast<T *>(ring + Sh::kRing);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sQ + kCmRows * Sh::kQStride);
-  float *s_wm = reinterpret_cast<float *>(bars + kCmWarps * S);  // [4][16]
-  float *s_wl = s_wm + kCmWarps * kCmRows;                       // [4][16]
-  float *s_m = s_wl + kCmWarps * kCmRows;                        // [16]
+  float *s_wm = reinterpret_cast<float *>(bars + R);           // [W][16]
+  float *s_wl = s_wm + W * kCmRows;                              // [W][16]
+  float *s_m = s_wl + W * kCmRows;                               // [16]
   float *s_l = s_m + kCmRows;                                    // [16]
   float *s_slope = s_l + kCmRows;                                // [16]
   int *s_lo = reinterpret_cast<int *>(s_slope + kCmRows);        // [16]
   int *s_hi = s_lo + kCmRows;                                    // [16]
   int *s_scratch = s_hi + kCmRows;
+  int *s_asked = s_scratch + 4;                                  // [R] chunk that a stage was last filled with
 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   // row chunks of the same keys are neighbours in the grid, so that the second
@@ -92,22 +123,28 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
   if (part >= nparts) return;
   const int t0 = base + part * a.P, t1 = min(hi_max, t0 + a.P);
   const int nchunks = t1 > t0 ? (t1 - t0 + kCmTok - 1) / kCmTok : 0;
-  const int nch_w = nchunks > w ? (nchunks - w + kCmWarps - 1) / kCmWarps : 0;
+  const int nch_w = nchunks > w ? (nchunks - w + W - 1) / W : 0;
 
   if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&bars[w * S + s], 1);
+    for (int s = w; s < R; s += W) mbar_init(&bars[s], 1);
     fence_mbar_init();
   }
   __syncwarp();
   const uint64_t policy = l2_evict_first_policy();
+  // The chunks this warp asks for: w, w + W, ... of the first fill, then the
+  // ones R behind those it is done with.
+  const int first = (R - w + W - 1) / W;
+  auto asks = [&](int i) { return i < first ? w + W * i : w + R + W * (i - first); };
   int tbl_batch = -1, my_phys = 0;
-  auto issue = [&](int i, int slot) {   // chunk i of this warp into `slot`
+  auto issue = [&](int i) {             // the i-th of them
+    const int c = asks(i);
+    if (c >= nchunks) return;
     if ((i >> 5) != tbl_batch) {        // table entries: one load per lane for 32 chunks
       tbl_batch = i >> 5;
-      const int ii = tbl_batch * 32 + lane;
+      const int cl = asks(tbl_batch * 32 + lane);
       my_phys = 0;
-      if (ii < nch_w) {
-        my_phys = __ldg(a.tables + (size_t)b * a.max_blocks + (t0 + kCmTok * (w + kCmWarps * ii)) / a.bs);
+      if (cl < nchunks) {
+        my_phys = __ldg(a.tables + (size_t)b * a.max_blocks + (t0 + kCmTok * cl) / a.bs);
         if (my_phys < 0 || (long long)my_phys >= a.num_blocks) {
           raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
           my_phys = 0;
@@ -115,15 +152,17 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
       }
     }
     const int phys = __shfl_sync(0xffffffffu, my_phys, i & 31);
-    const int row0 = (t0 + kCmTok * (w + kCmWarps * i)) % a.bs;
-    uint8_t *st = ring + (size_t)(w * S + slot) * Sh::kStage;
-    if (lane == 0) mbar_arrive_expect_tx(&bars[w * S + slot], Sh::kStage);
+    const int row0 = (t0 + kCmTok * c) % a.bs, slot = c % R;
+    uint8_t *st = ring + (size_t)slot * Sh::kStage;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars[slot], Sh::kStage);
+      st_release_cta(&s_asked[slot], c);
+    }
     __syncwarp();
     if (lane < 2)
-      tma_load_5d(st + lane * Sh::kBoxes * kCmBox, lane ? &tmV : &tmK, &bars[w * S + slot], 0, row0, 0, kvh, phys,
-                  policy);
+      tma_load_5d(st + lane * Sh::kBoxes * kCmBox, lane ? &tmV : &tmK, &bars[slot], 0, row0, 0, kvh, phys, policy);
   };
-  for (int i = 0; i < min(S, nch_w); ++i) issue(i, i);
+  for (int i = 0; i < first; ++i) issue(i);
 
   // query rows (zeros past the last) while the first chunks are in flight
   for (int i = tid; i < kCmRows * (D / 8); i += blockDim.x) {
@@ -159,16 +198,18 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
   const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_col = lane >> 4;
   const int sw = lane & 7;
 
-  int slot = 0, i = 0;
-  uint32_t parity = 0;
+  int i = 0;
   for (; i < nch_w; ++i) {
-    const bool ok = mbar_wait_bounded(&bars[w * S + slot], parity);
+    const int c = w + W * i, slot = c % R;
+    // a stage that passes from warp to warp: its barrier's parity says nothing
+    // until the chunk was asked for
+    const bool ok = (Sh::kOwn || flag_wait_bounded(&s_asked[slot], c)) && mbar_wait_bounded(&bars[slot], (c / R) & 1);
     if (!__all_sync(0xffffffffu, ok)) {
       if (lane == 0) raise_flag(a.err, PKV_FLAG_TIMEOUT);
       break;
     }
-    const int c0 = t0 + kCmTok * (w + kCmWarps * i);
-    const uint32_t kb = smem_u32(ring + (size_t)(w * S + slot) * Sh::kStage), vb = kb + Sh::kBoxes * kCmBox;
+    const int c0 = t0 + kCmTok * c;
+    const uint32_t kb = smem_u32(ring + (size_t)slot * Sh::kStage), vb = kb + Sh::kBoxes * kCmBox;
     // S = Q K^T; even and odd steps apart (two shorter chains)
     float sacc[2][2][4] = {};
 #pragma unroll
@@ -247,42 +288,32 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
       Mma::run(o[2 * dp + 1], pa, b2, b3);
     }
     __syncwarp();
-    if (i + S < nch_w) issue(i + S, slot);
-    if (++slot == S) {
-      slot = 0;
-      parity ^= 1u;
-    }
-  }
-  if (i < nch_w) {  // gave up: let the copies already issued land (bounded)
-    for (int j = i; j < min(i + S, nch_w); ++j) {
-      mbar_wait_bounded(&bars[w * S + slot], parity);
-      if (++slot == S) {
-        slot = 0;
-        parity ^= 1u;
-      }
-    }
+    issue(first + i);
   }
   l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
   l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
 
-  // merge the four warps' states (the rings are free now)
+  // merge the warps' states (the ring is free then)
   if ((lane & 3) == 0) {
     s_wm[w * kCmRows + r0] = m0;
     s_wm[w * kCmRows + r1] = m1;
     s_wl[w * kCmRows + r0] = l0;
     s_wl[w * kCmRows + r1] = l1;
   }
-  __syncthreads();
+  if (__syncthreads_or(i < nch_w)) {  // a warp gave up: let the copies already asked for land (bounded)
+    for (int s = w; s < min(R, nchunks); s += W) mbar_wait_bounded(&bars[s], (s_asked[s] / R) & 1);
+    __syncthreads();
+  }
   float M0 = -INFINITY, M1 = -INFINITY;
 #pragma unroll
-  for (int ww = 0; ww < kCmWarps; ++ww) {
+  for (int ww = 0; ww < W; ++ww) {
     M0 = fmaxf(M0, s_wm[ww * kCmRows + r0]);
     M1 = fmaxf(M1, s_wm[ww * kCmRows + r1]);
   }
   const float f0 = fast_exp2(m0 - chunk_ref(M0)), f1 = fast_exp2(m1 - chunk_ref(M1));
-  float *sO = reinterpret_cast<float *>(ring);  // [4][16][kOStride]
+  float *sO = reinterpret_cast<float *>(ring);  // [W][16][kOStride]
   if (r0 < rows) {
 #pragma unroll
     for (int nt = 0; nt < D / 8; ++nt)
@@ -297,8 +328,8 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
   }
   if (tid < kCmRows) {
     float M = -INFINITY, L = 0.f;
-    for (int ww = 0; ww < kCmWarps; ++ww) M = fmaxf(M, s_wm[ww * kCmRows + tid]);
-    for (int ww = 0; ww < kCmWarps; ++ww)
+    for (int ww = 0; ww < W; ++ww) M = fmaxf(M, s_wm[ww * kCmRows + tid]);
+    for (int ww = 0; ww < W; ++ww)
       L += s_wl[ww * kCmRows + tid] * fast_exp2(s_wm[ww * kCmRows + tid] - chunk_ref(M));
     s_m[tid] = M;
     s_l[tid] = L;
@@ -309,7 +340,7 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
     const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
     float4 acc = *reinterpret_cast<const float4 *>(sO + r * Sh::kOStride + d);
 #pragma unroll
-    for (int ww = 1; ww < kCmWarps; ++ww) {
+    for (int ww = 1; ww < W; ++ww) {
       const float4 v = *reinterpret_cast<const float4 *>(sO + (ww * kCmRows + r) * Sh::kOStride + d);
       acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
@@ -322,7 +353,7 @@ __global__ void __launch_bounds__(32 * kCmWarps, 1)
   __syncthreads();
   const int again = *s_scratch;
   if (again) {
-    for (int r = w; r < rows; r += kCmWarps) {
+    for (int r = w; r < rows; r += W) {
       if (!((again >> r) & 1)) continue;
       float m, l, acc[D / 32];
       chunk_row_exact<T, D / 32>(a, b, kvh, row_out(r), BIAS ? s_slope[r] : 0.f, sq.n - sq.qlen + row_query(r),
@@ -347,7 +378,7 @@ static pkv_status launch_cm(const ChunkArgs &a, const CUtensorMap &mk, const CUt
   static int configured[64] = {0};
   if (!allow_smem(kern, CmShape<D>::kSmem, configured)) return PKV_ERR_CUDA;
   const dim3 grid((unsigned)((long long)a.max_parts * a.KVH * a.chunks), a.B);
-  kern<<<grid, 32 * kCmWarps, CmShape<D>::kSmem, stream>>>(mk, mv, a);
+  kern<<<grid, 32 * CmShape<D>::kWarps, CmShape<D>::kSmem, stream>>>(mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
