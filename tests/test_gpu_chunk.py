@@ -130,6 +130,23 @@ def test_chunk_forms(dtype, H, KVH, D, bs, room):
         check(c, f"{sorted(f)} split", partition_size=128, **f)
 
 
+@pytest.mark.parametrize("dtype,H,KVH,D,bs", [(BF, 8, 2, 128, 16), (HF, 4, 4, 64, 16), (BF, 6, 1, 192, 32), (HF, 8, 1, 256, 16),
+                                              (BF, 7, 1, 128, 16)])
+def test_small_chunks_stay_on_mma(dtype, H, KVH, D, bs):
+    """Small calls with many 16-row chunks, more chunks of keys than ring stages, whole and split."""
+    c = case(D * 5 + H, [1, 70, 900], [1, 33, 70], H, KVH, D, bs, dtype, room=1)
+    total, kw = int(c["cu"][-1]), dict(max_q_len=70, max_context_len=900)
+    assert pkv.pkv_chunk_plan(3, total, H, KVH, D, bs, c["tables"].shape[1], 70, 900, dtype=dtype)[2] == 1
+    for f in forms(c, 5):
+        want = reference(c, **f)
+        for part in (0, 128, 1024):
+            got, err = run(c, partition_size=part, **kw, **f)
+            assert err == 0, f"{sorted(f)} {part}: flags {err:#x}"
+            close(got, want, c, f"{sorted(f)} {part}")
+            again, _ = run(c, partition_size=part, **kw, **f)
+            assert torch.equal(got.view(torch.int16), again.view(torch.int16)), f"{sorted(f)} {part}: bits differ"
+
+
 def test_each_kernel_is_reached():
     """The plan's kernel by rows, type, shape and the call's size."""
     plan = lambda *a, **k: pkv.pkv_chunk_plan(*a, **k)[2]
