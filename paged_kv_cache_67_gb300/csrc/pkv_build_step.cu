@@ -250,9 +250,11 @@ __global__ void __launch_bounds__(kStepMaxThreads) pkv_build_step_kernel(const S
   if (ncta > 1) cluster_sync_all();
   else __syncthreads();
   for (int b = gid; b < a.B; b += gstep) {
-    const int cb = cached_of(b), hb = held_of(b);
-    a.lens[b] = ok ? cb + (s_new[b + 1] - s_new[b]) : 0;
-    a.held_out[b] = ok ? want_of(b) : hb;
+    // both read before either is written: above kStepSmemB they are the memory
+    // that lens and held_out may be
+    const int total_b = cached_of(b) + (s_new[b + 1] - s_new[b]), hb = held_of(b);
+    a.lens[b] = ok ? total_b : 0;
+    a.held_out[b] = ok ? blocks_for(a, total_b) : hb;
   }
   if (gid == 0) *a.free_count_out = ok ? top - sum_need : count;
 }

@@ -97,6 +97,38 @@ def test_largest_batch():
     check(case(22, 16384, 16, 30, 2, 3), extra=7)
 
 
+@pytest.mark.parametrize("B", [8192, 8193, 16384])
+def test_largest_batches_in_place(B):
+    """Two steps that carry their state in place, on either side of the batch up
+    to which the lengths stay in shared memory.  Blocks of 4 and up to 9 new
+    tokens: most requests would want other blocks for c + 2n than for c + n."""
+    c = case(B, B, 4, 30, 9, 3)
+    check(c, extra=7, in_place=True)
+    c["tables"] = [row + [99999] * 3 for row in c["tables"]]     # room and blocks for a second step
+    spare = list(range(c["nb"], c["nb"] + 4 * B))
+    c.update(free=spare + c["free"], count=c["count"] + len(spare), nb=c["nb"] + len(spare))
+    t = lambda x: torch.tensor(x, dtype=I32, device=DEV)
+    d = {k: t(c[k]) for k in ("tables", "held", "free", "cached", "new")}
+    count, cu, err = t([c["count"]]), t([0] * (B + 1)), t([0])
+    T = 9 * B + 40 * B // 4
+    slots, pos = torch.zeros(T, dtype=I64, device=DEV), torch.zeros(T, dtype=I32, device=DEV)
+    r = random.Random(B)
+    for step in range(2):
+        want = want_of(c, T)
+        assert "why" not in want
+        pkv.pkv_build_step(d["tables"], d["held"], d["held"], d["free"], count, count, d["cached"], d["new"], d["cached"],
+                           cu, slots, pos, c["nb"], 4, err_flags=err)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        for k, v in (("tables", d["tables"]), ("held", d["held"]), ("free", d["free"]), ("lens", d["cached"]), ("cu", cu),
+                     ("slots", slots), ("positions", pos)):
+            assert v.tolist() == want[k], (step, k)
+        assert int(count) == want["count"]
+        c.update(tables=want["tables"], held=want["held"], free=want["free"], count=want["count"], cached=want["lens"],
+                 new=[r.randint(0, 9) for _ in range(B)])
+        d["new"].copy_(t(c["new"]))
+
+
 def test_all_idle_and_empty():
     c = dict(tables=[[3, 9], [9, 9]], held=[1, 0], free=[0, 1, 2, -1], count=3, cached=[5, 0], new=[0, 0], bs=16, nb=4)
     check(c, extra=3)
