@@ -56,8 +56,8 @@ struct StepArgs {
   uint32_t bs_mul, bs_shift;        // x / bs = (umulhi(x, bs_mul) + x) >> bs_shift for 0 <= x < 2^31
 };
 
-__device__ __forceinline__ int sat_add(int a, int b) {  // both in [0, kStepSat]
-  return min(a + b, kStepSat);
+__device__ __forceinline__ int sat_add(int a, int b) {  // both in [0, kStepSat]: their sum can be 2^31
+  return (int)min((unsigned)a + (unsigned)b, (unsigned)kStepSat);
 }
 
 __device__ __forceinline__ int div_bs(const StepArgs &a, int x) {

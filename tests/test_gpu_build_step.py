@@ -168,6 +168,27 @@ def test_refused_steps_change_nothing(what, change, why, in_place):
     assert got["slots"] == [-1] * T and got["positions"] == [0] * T and got["cu"] == [0, 0, 0] and got["lens"] == [0, 0]
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,new", [(2, 2 ** 30), (4, 2 ** 29), (4096, 2 ** 20), (16384, 131072), (8192, 131072), (1024, 2 ** 20)])
+def test_totals_past_the_bound_are_refused(B, new, in_place):
+    """2^30, 2^31 and 2^32 new tokens in all, a block each: no sum may wrap."""
+    c = dict(tables=[[b] for b in range(B)], held=[1] * B, free=[-1] * 4, count=0, cached=[0] * B, new=[new] * B, bs=new, nb=B)
+    assert want_of(c, 8) == {"why": "invalid"}
+    got, flags = run(c, 8, in_place)
+    assert flags == pkv.FLAG_STEP_INVALID
+    assert got["tables"] == c["tables"] and got["free"] == c["free"] and got["held"] == c["held"] and got["count"] == 0
+    assert got["slots"] == [-1] * 8 and got["positions"] == [0] * 8 and got["cu"] == [0] * (B + 1) and got["lens"] == [0] * B
+
+
+def test_the_largest_total():
+    """One token less than the bound is a step; the lists hold its first tokens."""
+    c = dict(tables=[[0], [1]], held=[1, 0], free=[1, -1], count=1, cached=[0, 0], new=[2 ** 30 - 2, 1], bs=2 ** 30, nb=2)
+    got, flags = run(c, 3)
+    assert flags == pkv.FLAG_TOKENS_OVER
+    assert got["cu"] == [0, 2 ** 30 - 2, 2 ** 30 - 1] and got["lens"] == c["new"] and got["held"] == [1, 1]
+    assert got["slots"] == [0, 1, 2] and got["positions"] == [0, 1, 2] and got["count"] == 0
+
+
 @pytest.mark.parametrize("room", [0, 1, 9, 24])
 def test_more_tokens_than_the_lists_hold(room):
     """The lists hold the first max_tokens; the rest of the step is done."""
