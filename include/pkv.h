@@ -485,7 +485,9 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  *                 as in pkv_prefill_attention (out overlaps no other
  *                 argument); out rows behind cu_seqlens_q[B] are left as they
  *                 were
- *   softcap       0 = none, else > 0
+ *   softcap       0 = none, else > 0; up to 256 is fastest on the tensor-core
+ *                 kernels (larger ones take a form whose error does not grow
+ *                 with the cap)
  *   window        0 = none, else a query sees at most the last `window` keys
  *                 up to itself (and the prefix positions above p)
  *   slopes        [H] float32 or NULL: linear distance bias per query head

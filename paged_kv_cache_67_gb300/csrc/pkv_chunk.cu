@@ -1,5 +1,6 @@
 // pkv_chunk.cu -- host side of chunk attention: argument checks, the choice
 // of kernel and split, the workspace's layout, the launch.
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -264,8 +265,9 @@ PKV_API pkv_status pkv_chunk_attention(
   a.P = plan.P;
   a.max_parts = plan.max_parts;
   a.chunks = (int)plan.chunks;
-  a.scale_log2 = softcap > 0.f ? scale / softcap : scale * kLog2e;
-  a.cap_log2 = softcap * kLog2e;
+  a.scale_log2 = scale * kLog2e;
+  a.cap_ratio = softcap > 0.f ? scale / softcap : 0.f;
+  a.cap_log2 = std::min(softcap * kLog2e, FLT_MAX);   // (caps past 2.3e38 stay finite)
   a.scale_y = softcap > 0.f ? 2.f * kLog2e * scale / softcap : scale * kLog2e;
   // the series' powers of scale / cap have to stay in range, and a running
   // max commutes with the cap for a positive scale only

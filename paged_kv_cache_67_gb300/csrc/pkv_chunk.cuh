@@ -17,6 +17,8 @@
 //   biased   t -= slope * log2(e) * |p - j|.
 #pragma once
 
+#include <type_traits>
+
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -46,11 +48,13 @@ struct ChunkArgs {
   int window;
   int P, max_parts;              // keys per part, parts the workspace holds per row
   int chunks;                    // row chunks per (sequence, KV head): the grid's and the counters'
-  float scale_log2;              // scale * log2(e), or with a cap: scale / cap
+  float scale_log2;              // scale * log2(e)
   float cap_log2;                // 0, or cap * log2(e)
   float cap_k[4], cap_small;     // chunk_cap_fit: the near series in the raw product, and its range there
   float cap_c[6], cap_mid;       // the middle one in scale / cap (q . k), times cap * log2(e); its range in the raw product
   float scale_y;                 // scale * log2(e), or with a cap: chunk_capped's 2 log2(e) scale / cap
+  float cap_ratio;               // with a cap: scale / cap (before cap_k, whose wide constant loads it would shift,
+                                 // it costs capped prompts 6 %: 180 us for 169)
 };
 
 struct ChunkSeq {
@@ -90,33 +94,46 @@ __device__ __forceinline__ void chunk_visible(const ChunkArgs &a, const ChunkSeq
   if (lo >= hi) lo = hi = 0;
 }
 
-// tanh(x) = sign(x) (1 - e) / (1 + e), e = 2^(-2 log2(e) |x|), and below 1/4,
-// where 1 - e cancels, its Taylor series through x^9 (next term 1.4e-9 of x
-// at 1/4): within a few fp32 roundings everywhere.
-__device__ __forceinline__ float chunk_tanh(float x) {
-  const float y = fabsf(x);
-  if (y < 0.25f) {
-    const float z = x * x;
-    float p = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
-    p = fmaf(z, p, 2.f / 15.f);
-    p = fmaf(z, p, -1.f / 3.f);
-    return fmaf(x * z, p, x);
-  }
+// The capped score cap tanh(x), x = scale / cap (q . k), in log2 units, off by
+// a few fp32 roundings of the score itself, however large the cap.  With
+// e = 2^(-2 log2(e) |x|), tanh(x) = sign(x) (1 - e) / (1 + e); below 1/4,
+// where 1 - e cancels, the plain score times the Taylor series of tanh(x) / x
+// through x^8 (next term 1.4e-9 of 1 at 1/4), so that a cap far above the
+// scores leaves them as they are, even where scale / cap is 0 in fp32.
+constexpr float kCapNear = 0.25f;
+__device__ __forceinline__ float chunk_cap_near(const ChunkArgs &a, float dot) {
+  const float x = dot * a.cap_ratio, t = dot * a.scale_log2, z = x * x;
+  float p = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
+  p = fmaf(z, p, 2.f / 15.f);
+  p = fmaf(z, p, -1.f / 3.f);
+  return fmaf(t * z, p, t);
+}
+__device__ __forceinline__ float chunk_cap(const ChunkArgs &a, float dot) {
+  const float x = dot * a.cap_ratio, y = fabsf(x);
+  if (y < kCapNear) return chunk_cap_near(a, dot);
   const float e = exp2f(-2.f * kLog2e * y);
-  return copysignf(__fdividef(1.f - e, 1.f + e), x);
+  return copysignf(a.cap_log2 * __fdividef(1.f - e, 1.f + e), x);
 }
 
 // The row's score of a key in log2 units from the raw product q . k.
 __device__ __forceinline__ float chunk_score(const ChunkArgs &a, float dot, float slope_log2, int p, int j) {
-  float t = dot * a.scale_log2;
-  if (a.cap_log2 > 0.f) t = a.cap_log2 * chunk_tanh(t);
+  float t = a.cap_log2 > 0.f ? chunk_cap(a, dot) : dot * a.scale_log2;
   if (a.slopes) t = fmaf(-slope_log2, fabsf((float)(p - j)), t);
   return t;
 }
 
-// The capped score of the 16-bit kernels, with y = 2 log2(e) scale / cap
-// (q . k):  cap tanh(x) = cap - 2 cap / (1 + 2^y).  Off by a few 2^-23 of cap,
-// far below what rounding a weight to 16 bits does to it.
+// How a 16-bit kernel caps its scores, a template parameter: no cap, a cap up
+// to kCapShort, a larger one.
+constexpr int kCapNone = 0, kCapUsual = 1, kCapLarge = 2;
+
+// The capped score for caps up to kCapShort, with y = 2 log2(e) scale / cap
+// (q . k):  cap tanh(x) = cap - 2 cap / (1 + 2^y).  Half of it cancels near 0:
+// off by some 2^-23 of the cap, which moves a weight by 3e-5 at a cap of 256, a
+// sixteenth of fp16's half step.  That grows with the cap (1.2 % of a weight at
+// 1e5), so larger caps take chunk_cap (kCapLarge), at a price: 64 sequences of
+// 512 to 4096 keys 114 us for 105, 8 drafts with a bias 165 for 135, four
+// prompt chunks 257 for 169.
+constexpr float kCapShort = 256.f * kLog2e;   // in log2 units, as cap_log2
 __device__ __forceinline__ float chunk_capped(float y, float cap_log2) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(y)));
@@ -329,6 +346,17 @@ __device__ void chunk_finish(const ChunkArgs &a, int rows, int part, int nparts,
   if (!chunk_last_part(counter, nparts, s_scratch)) return;
   chunk_merge<T, 4>(a, rows, nparts, s_o, room, row_out, seen);
   if (tid == 0) *counter = 0;  // ready for the next call
+}
+
+// go(cap, bias) with a call's score form as constants (.value: kCap..., bool).
+template <typename F>
+static pkv_status chunk_forms(const ChunkArgs &a, const F &go) {
+  auto biased = [&](auto cap) {
+    return a.slopes ? go(cap, std::true_type()) : go(cap, std::false_type());
+  };
+  if (!(a.cap_log2 > 0.f)) return biased(std::integral_constant<int, kCapNone>());
+  return a.cap_log2 > kCapShort ? biased(std::integral_constant<int, kCapLarge>())
+                                : biased(std::integral_constant<int, kCapUsual>());
 }
 
 }  // namespace pkv

@@ -68,7 +68,7 @@ __device__ __forceinline__ bool flag_wait_bounded(const int *p, int v) {
   return true;
 }
 
-template <int D, typename T, bool CAP, bool BIAS>
+template <int D, typename T, int CAP, bool BIAS>
 __global__ void __launch_bounds__(32 * CmShape<D>::kWarps, 1)
     pkv_chunk_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const ChunkArgs a) {
@@ -229,8 +229,13 @@ __global__ void __launch_bounds__(32 * CmShape<D>::kWarps, 1)
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float t = (sacc[0][nt][e] + sacc[1][nt][e]) * a.scale_y;
-        if (CAP) t = chunk_capped(t, a.cap_log2);
+        float t = sacc[0][nt][e] + sacc[1][nt][e];
+        if (CAP == kCapLarge) {
+          t = chunk_cap(a, t);
+        } else {
+          t *= a.scale_y;
+          if (CAP) t = chunk_capped(t, a.cap_log2);
+        }
         if (BIAS) {
           const int j = c0 + nt * 8 + (lane & 3) * 2 + (e & 1);
           t = fmaf(e < 2 ? -slope0 : -slope1, fabsf((float)((e < 2 ? p0 : p1) - j)), t);
@@ -372,7 +377,7 @@ __global__ void __launch_bounds__(32 * CmShape<D>::kWarps, 1)
                   [&](int r) { return s_hi[r] > s_lo[r]; });
 }
 
-template <int D, typename T, bool CAP, bool BIAS>
+template <int D, typename T, int CAP, bool BIAS>
 static pkv_status launch_cm(const ChunkArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
   auto kern = pkv_chunk_mma_kernel<D, T, CAP, BIAS>;
   static int configured[64] = {0};
@@ -384,9 +389,7 @@ static pkv_status launch_cm(const ChunkArgs &a, const CUtensorMap &mk, const CUt
 
 template <int D, typename T>
 static pkv_status launch_cm_form(const ChunkArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
-  if (a.cap_log2 > 0.f)
-    return a.slopes ? launch_cm<D, T, true, true>(a, mk, mv, stream) : launch_cm<D, T, true, false>(a, mk, mv, stream);
-  return a.slopes ? launch_cm<D, T, false, true>(a, mk, mv, stream) : launch_cm<D, T, false, false>(a, mk, mv, stream);
+  return chunk_forms(a, [&](auto cap, auto bias) { return launch_cm<D, T, cap.value, bias.value>(a, mk, mv, stream); });
 }
 
 template <typename T>

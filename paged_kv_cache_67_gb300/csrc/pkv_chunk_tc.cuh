@@ -112,7 +112,7 @@ struct __align__(16) CtItem {
 };
 static_assert(sizeof(CtItem) == 64, "four 16-byte words");
 
-template <int D, typename T, bool CAP, bool BIAS>
+template <int D, typename T, int CAP, bool BIAS>
 __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
     pkv_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CtArgs ta) {
@@ -660,7 +660,20 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
         // then evaluated inside the exponent, straight from the raw scores.
         bool fused = false;
         float mx_raw = -INFINITY;
-        if (CAP && !BIAS) {
+        if (CAP == kCapLarge) {
+          // the scores of a large cap are near 0 as a rule: then no branch per score
+          if (cut) hide(0.f);
+          float far = 0.f;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) far = fmaxf(far, fabsf(sc[c]));
+          if (__all_sync(0xffffffffu, !real_row || far * fabsf(a.cap_ratio) < kCapNear)) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sc[c] = chunk_cap_near(a, sc[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sc[c] = chunk_cap(a, sc[c]);
+          }
+        } else if (CAP && !BIAS) {
           if (cut) {  // hidden columns hold whatever was there: they have no say
             hide(0.f);
           }
@@ -673,7 +686,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           const float far = real_row ? fmaxf(mx_raw, -mn_raw) : 0.f;
           fused = __all_sync(0xffffffffu, !cut && far <= a.cap_small);
           if (!fused && __all_sync(0xffffffffu, far <= a.cap_mid)) {
-            const float2 rt = kept_pair(a.scale_log2);
+            const float2 rt = kept_pair(a.cap_ratio);
             float2 kc[6];
 #pragma unroll
             for (int e = 0; e < 6; ++e) kc[e] = kept_pair(a.cap_c[e]);
@@ -759,7 +772,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           }
         };
         const float2 nref = kept_pair(-ref);
-        if (CAP && !BIAS && fused) {
+        if (CAP == kCapUsual && !BIAS && fused) {
           const float2 k0 = kept_pair(a.cap_k[0]), k1 = kept_pair(a.cap_k[1]);
           const float2 k2 = kept_pair(a.cap_k[2]), k3 = kept_pair(a.cap_k[3]);
           weights([&](float2 x, int) {
@@ -1020,7 +1033,7 @@ static bool launch_after(void (*kern)(KArgs...), int ctas, int threads, size_t s
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
 }
 
-template <int D, typename T, bool CAP, bool BIAS>
+template <int D, typename T, int CAP, bool BIAS>
 static pkv_status launch_ct(const CtArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, int sms,
                             cudaStream_t stream) {
   auto kern = pkv_chunk_tc_kernel<D, T, CAP, BIAS>;
@@ -1037,9 +1050,7 @@ static pkv_status launch_ct(const CtArgs &a, const CUtensorMap &mq, const CUtens
 template <int D, typename T>
 static pkv_status launch_ct_form(const CtArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                                  int sms, cudaStream_t s) {
-  if (a.c.cap_log2 > 0.f)
-    return a.c.slopes ? launch_ct<D, T, true, true>(a, mq, mk, mv, sms, s) : launch_ct<D, T, true, false>(a, mq, mk, mv, sms, s);
-  return a.c.slopes ? launch_ct<D, T, false, true>(a, mq, mk, mv, sms, s) : launch_ct<D, T, false, false>(a, mq, mk, mv, sms, s);
+  return chunk_forms(a.c, [&](auto cap, auto bias) { return launch_ct<D, T, cap.value, bias.value>(a, mq, mk, mv, sms, s); });
 }
 
 template <int D>

@@ -242,6 +242,41 @@ def test_large_scores_and_cap():
             check(c, f"cap {cap}", softcap=cap)
 
 
+@pytest.mark.parametrize("dtype,H,KVH,D", [(HF, 4, 2, 128), (BF, 4, 2, 64), (HF, 4, 1, 256), (HF, 4, 2, 80), (F32, 4, 2, 64)])
+@pytest.mark.parametrize("cap", [400.0, 1e3, 1e5, 1e8, 3e38])
+def test_caps_far_above_the_scores(dtype, H, KVH, D, cap):
+    """A cap that hardly bends the scores leaves them exact, on every kernel:
+    its error goes with the score, not with the cap."""
+    for qlens in ([3, 5], [100, 90]):
+        c = case(51, [260, 400], qlens, H, KVH, D, 16, dtype)
+        for f in ({}, {"slopes": slopes_of(H)}):
+            check(c, f"{qlens} {sorted(f)}", softcap=cap, **f)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap", [300.0, 1000.0])
+def test_caps_that_bend_scores_of_hundreds(D, cap):
+    """Scores from 0 to 1.2 of a large cap.  The products are exact here (one
+    element of q is not 0), so a score t carries the roundings of its cap form
+    alone: 8 at most, 2^-24 each, of |t| <= cap log2(e).  A weight is off by
+    that of its score and of the row's largest:
+    2 ln 2 * 8 * 2^-24 * cap log2(e) = 2^-20 cap, beside what the module's text
+    counts."""
+    for qlens in ([3, 5], [100, 90]):
+        c = case(52, [260, 400], qlens, 4, 2, D, 16, HF)
+        g = torch.Generator().manual_seed(53)
+        c["q"].zero_()
+        rows = c["q"].view(-1, D)
+        rows[torch.arange(len(rows)), torch.randint(0, D, (len(rows),), generator=g)] = 8.0
+        c["k"] = torch.where(c["k"].isnan(), c["k"], (torch.randint(0, 1001, c["k"].shape, generator=g) / 4).to(HF))
+        c["scale"] = 1.2 * cap / 2000
+        got, err = run(c, softcap=cap)
+        want = reference(c, softcap=cap)
+        vmax = c["v"].double().abs().nan_to_num(0.0, 0.0, 0.0).max()
+        tol = (torch.finfo(HF).eps + 2.0 ** -18 + 2.0 ** -20 * cap) * vmax
+        assert err == 0 and (got.double() - want).abs().max() <= tol, f"{qlens}: {(got.double() - want).abs().max():.3e}"
+
+
 def test_equal_scores_average_the_values():
     """q = 0: every visible key weighs the same, with and without a cap."""
     c = case(8, [77, 500], [5, 130], 4, 2, 128, 16, BF)
