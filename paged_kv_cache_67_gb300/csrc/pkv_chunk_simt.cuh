@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kCsThreads) pkv_chunk_simt_kernel(const ChunkA
   const int base = hi_max > 0 ? lo_min & ~15 : 0;
   const int nparts = max(1, (hi_max - base + a.P - 1) / a.P);
   if (slotp >= nparts) return;
-  const int t0 = max(lo_min, base + slotp * a.P), t1 = min(hi_max, base + (slotp + 1) * a.P);
+  // (no row sees a key: the empty part [0, 0), from which t0 + tid is no overflow)
+  const int t0 = hi_max > 0 ? max(lo_min, base + slotp * a.P) : 0, t1 = min(hi_max, base + (slotp + 1) * a.P);
 
   // element offset of key t's row, -1 past the part's end
   auto table_entry = [&](int t) { return t < t1 ? __ldg(a.tables + (size_t)b * a.max_blocks + t / a.bs) : 0; };

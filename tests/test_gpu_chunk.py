@@ -302,6 +302,18 @@ def test_rows_that_see_nothing_are_zero(dtype, H, KVH, D, qlen):
         assert err == 0 and not got.any()
 
 
+@pytest.mark.parametrize("dtype,H,KVH,D", [(F32, 4, 2, 64), (F32, 4, 2, 512), (BF, 4, 2, 80), (BF, 4, 2, 128), (HF, 16, 1, 256), (BF, 4, 1, 64)])
+@pytest.mark.parametrize("qlen", [1, 6, 70])
+def test_a_sequence_that_sees_nothing_reads_no_table(dtype, H, KVH, D, qlen):
+    """Every table entry is garbage: none is looked at where no query sees a key."""
+    c = case(54, [90, 300], [qlen, qlen], H, KVH, D, 16, dtype)
+    c["tables"].fill_(99999)
+    for start in (1000, 2 ** 31 - 1):
+        for part in (0, 128):
+            got, err = run(c, kv_starts=torch.full((2 * qlen,), start, dtype=torch.int32), partition_size=part)
+            assert err == 0 and not got.any()
+
+
 @pytest.mark.parametrize("dtype,H,KVH,D", [(F32, 4, 2, 64), (BF, 4, 2, 128), (HF, 16, 1, 256), (BF, 4, 1, 64)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("qlen", [1, 6, 150])
