@@ -14,7 +14,7 @@ pkv_status launch_chunk_simt(const ChunkArgs &a, int rows, pkv_dtype dt, cudaStr
 pkv_status launch_chunk_mma(const ChunkArgs &a, pkv_dtype dt, cudaStream_t stream);
 pkv_status launch_chunk_tc(const ChunkArgs &a, pkv_dtype dt, char *scratch, int sms, cudaStream_t stream);
 long long chunk_tc_items(int B, long long total_q, int H, int G, int D, int max_q);
-size_t chunk_tc_scratch(int B, long long total_q, int G, int D, int max_q, long long parts);
+size_t chunk_tc_scratch(int B, long long total_q, int H, int G, int D, int max_q, long long parts);
 
 // The plan uses the SM count of the one GPU this library is built for, so
 // that the workspace's size needs no device.
@@ -162,7 +162,7 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
 // Workspace bytes of a plan.
 static size_t chunk_ws_bytes(int kernel, int B, int64_t total_q, int H, int KVH, int D, int max_q, long long parts) {
   size_t bytes = kChunkCnt * sizeof(int);
-  if (kernel == 2) bytes += chunk_tc_scratch(B, total_q, H / KVH, D, chunk_max_q(total_q, max_q), parts);
+  if (kernel == 2) bytes += chunk_tc_scratch(B, total_q, H, H / KVH, D, chunk_max_q(total_q, max_q), parts);
   if (parts > 1) {
     const size_t rows = (size_t)total_q * H;
     bytes += 2 * align256(rows * parts * sizeof(float)) + align256(rows * parts * (size_t)D * sizeof(float));
@@ -284,7 +284,7 @@ PKV_API pkv_status pkv_chunk_attention(
   a.ws_cnt = reinterpret_cast<int *>(ws);
   ws += kChunkCnt * sizeof(int);
   char *scratch = ws;
-  if (plan.kernel == 2) ws += chunk_tc_scratch(B, total_q, a.G, head_dim, a.max_q, plan.max_parts);
+  if (plan.kernel == 2) ws += chunk_tc_scratch(B, total_q, H, a.G, head_dim, a.max_q, plan.max_parts);
   if (plan.max_parts > 1) {
     const size_t rows = (size_t)total_q * H;
     a.ws_m = reinterpret_cast<float *>(ws);

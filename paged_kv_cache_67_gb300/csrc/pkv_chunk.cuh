@@ -151,12 +151,20 @@ constexpr float kTanh6[6] = {0.9999994039535522f, -0.3332904279232025f, 0.132814
 // 0 in its place every weight is 2^(-inf) = 0 and not NaN.
 __device__ __forceinline__ float chunk_ref(float m) { return m == -INFINITY ? 0.f : m; }
 
-// One row over keys [t0, t1), all of them visible, key by key on one warp:
+// Element offset of key t's row of a KV head (a bad entry is flagged where it
+// was first read).
+__device__ __forceinline__ size_t chunk_row_at(const ChunkArgs &a, int b, int kvh, int t) {
+  int phys = __ldg(a.tables + (size_t)b * a.max_blocks + t / a.bs);
+  if (phys < 0 || (long long)phys >= a.num_blocks) phys = 0;
+  return (((size_t)phys * a.bs + t % a.bs) * a.KVH + kvh) * a.D;
+}
+
+// One row over keys [t0, t1), all of them visible, on one warp, KEYS at a time:
 // m, l and the lane's D / 32 columns of the weighted sum, unnormalised.  The
 // tensor-core kernels multiply a whole tile by weights that are 0 for hidden
 // keys; where a hidden value is not finite that gives NaN, and the rows that
 // show one are done again here, from what they see alone.
-template <typename T, int EPL>
+template <typename T, int EPL, int KEYS = 1>
 __device__ __forceinline__ void chunk_row_exact(const ChunkArgs &a, int b, int kvh, size_t q_row, float slope_log2, int p,
                                              int t0, int t1, float &m, float &l, float (&o)[EPL]) {
   const int lane = threadIdx.x & 31;
@@ -170,28 +178,45 @@ __device__ __forceinline__ void chunk_row_exact(const ChunkArgs &a, int b, int k
   }
   m = -INFINITY;
   l = 0.f;
-  for (int t = t0; t < t1; ++t) {
-    int phys = __ldg(a.tables + (size_t)b * a.max_blocks + t / a.bs);
-    if (phys < 0 || (long long)phys >= a.num_blocks) phys = 0;   // flagged where it was first read
-    const size_t row = (((size_t)phys * a.bs + t % a.bs) * a.KVH + kvh) * a.D;
-    const T *k = reinterpret_cast<const T *>(a.k_cache) + row, *v = reinterpret_cast<const T *>(a.v_cache) + row;
-    float s = 0.f;
+  for (int t = t0; t < t1; t += KEYS) {
+    size_t row[KEYS];
+    float x[KEYS], mn = m;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-      const int d = lane + 32 * e;
-      if (d < a.D) s = fmaf(qv[e], to_f32<T>(k[d]), s);
+    for (int k = 0; k < KEYS; ++k) {
+      row[k] = chunk_row_at(a, b, kvh, KEYS > 1 ? min(t + k, t1 - 1) : t);
+      x[k] = 0.f;
     }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    const float x = chunk_score(a, s, slope_log2, p, t);
-    const float mn = fmaxf(m, x), ref = chunk_ref(mn);
-    const float c = fast_exp2(m - ref), w = fast_exp2(x - ref);
-    l = fmaf(l, c, w);
-    m = mn;
+    for (int k = 0; k < KEYS; ++k)
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-      const int d = lane + 32 * e;
-      if (d < a.D) o[e] = fmaf(o[e], c, w * to_f32<T>(v[d]));
+      for (int e = 0; e < EPL; ++e) {
+        const int d = lane + 32 * e;
+        if (d < a.D) x[k] = fmaf(qv[e], to_f32<T>((reinterpret_cast<const T *>(a.k_cache) + row[k])[d]), x[k]);
+      }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1)
+#pragma unroll
+      for (int k = 0; k < KEYS; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], w);
+#pragma unroll
+    for (int k = 0; k < KEYS; ++k) {
+      x[k] = chunk_score(a, x[k], slope_log2, p, t + k);
+      if (t + k < t1) mn = fmaxf(mn, x[k]);
+    }
+    const float ref = chunk_ref(mn), c = fast_exp2(m - ref);
+    m = mn;
+    l *= c;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] *= c;
+#pragma unroll
+    for (int k = 0; k < KEYS; ++k) {
+      if (t + k >= t1) continue;
+      const float w = fast_exp2(x[k] - ref);
+      l += w;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        const int d = lane + 32 * e;
+        if (d < a.D) o[e] = fmaf(w, to_f32<T>((reinterpret_cast<const T *>(a.v_cache) + row[k])[d]), o[e]);
+      }
     }
   }
 }

@@ -172,9 +172,14 @@ long long chunk_tc_items(int B, long long total_q, int H, int G, int D, int max_
 
 static size_t ct_align(size_t x) { return (x + 255) & ~size_t(255); }
 
-size_t chunk_tc_scratch(int B, long long total_q, int G, int D, int max_q, long long parts) {
-  const long long tiles = ct_tiles_cap(B, total_q, max_q, (ct_groups(D) * kCtRows) >> chunk_tc_gshift(G));
-  return 256 + ct_align(tiles * sizeof(int4)) + ct_align(tiles * parts * sizeof(CtUnit));
+// Notes of rows to do again, of an item: one per softmax warp.
+static size_t ct_notes(int D) { return 4 * ct_groups(D) * sizeof(int2); }
+
+size_t chunk_tc_scratch(int B, long long total_q, int H, int G, int D, int max_q, long long parts) {
+  const int sh = chunk_tc_gshift(G);
+  const long long tiles = ct_tiles_cap(B, total_q, max_q, (ct_groups(D) * kCtRows) >> sh);
+  return 256 + ct_align(tiles * sizeof(int4)) + ct_align(tiles * parts * sizeof(CtUnit)) +
+         ct_align(tiles * parts * (H >> sh) * ct_notes(D));
 }
 
 bool launch_ct_plan(const CtArgs &a, cudaStream_t stream) {
@@ -203,6 +208,8 @@ pkv_status launch_chunk_tc(const ChunkArgs &c, pkv_dtype dt, char *scratch, int 
   a.tiles = reinterpret_cast<int4 *>(scratch);
   scratch += ct_align(tiles * sizeof(int4));
   a.units = reinterpret_cast<CtUnit *>(scratch);
+  scratch += ct_align(tiles * c.max_parts * sizeof(CtUnit));
+  a.redo = reinterpret_cast<int2 *>(scratch);
   CUtensorMap mq, mk, mv;
   if (!encode_packed_map(&mq, c.q, dt, c.total_q, c.H, c.D, 1 << a.gshift, kCtRows >> a.gshift) ||
       !encode_cache_map(&mk, c.k_cache, dt, c.num_blocks, c.bs, c.KVH, c.D, 1 << a.bshift) ||

@@ -24,7 +24,8 @@
 // Units whose keys a window or document mask cuts start at the first key any
 // of their rows sees (its 16-key chunk): tiles before it are never loaded.
 // Values that no row sees are zeroed in the tile; a row that still ends not
-// finite because a hidden value is not (0 * inf) is done again key by key.
+// finite because a hidden value is not (0 * inf) is noted, and its warp does it
+// again key by key once the CTA has no more items: no wait spans that.
 // Every wait is bounded, as in prefill.
 #pragma once
 
@@ -57,7 +58,7 @@ constexpr int kCtPlanThreads = 1024;
 constexpr int kCtSat = 1 << 29;                // sums of tiles stop here (query offsets that overlap can add up to anything)
 constexpr int kCtClasses = 256;                // plan: key tiles of a unit, the most first
 
-struct CtUnit {                  // 32 bytes, written by the plan
+struct __align__(16) CtUnit {    // 32 bytes, written by the plan
   int b, i0, part, nparts;       // sequence, first query; part of the keys
   int t0, t1, lo, pad;           // the part's keys [t0, t1) (t1 = 0: no row sees any); first key seen by the unit
 };
@@ -67,6 +68,7 @@ struct CtArgs {
   int *n_units;                  // written by the plan
   int4 *tiles;                   // [tiles_cap] (sequence, tile, first key seen, one past the last)
   CtUnit *units;                 // [units_cap]
+  int2 *redo;                    // [units_cap * subs][softmax warps] (rows to do again, the warp's next noted item)
   int tiles_cap, units_cap;
   int gshift;                    // log2 of the packed heads G'
   int subs;                      // head subgroups: H / G'
@@ -102,7 +104,7 @@ struct CtShape {
 // (zero rows to write), -1 no more items.
 struct __align__(16) CtItem {
   int kind, sub, b, i0;          // head subgroup, sequence, first query in the sequence
-  int q0, qlen, n, queries;      // the sequence's first row; queries of the item
+  int q0, qlen, n, w;            // the sequence's first row; the item's number
   int t0, t1, lo, part;          // the part's keys, the unit's first seen key
   int nt[kCtMaxGroups];             // key tiles each group works on
   int ntiles;                    // key tiles the item loads
@@ -111,6 +113,85 @@ struct __align__(16) CtItem {
   __device__ __forceinline__ int parts() const { return nparts < 0 ? -nparts : nparts; }
 };
 static_assert(sizeof(CtItem) == 64, "four 16-byte words");
+
+// Rows `rows` (bits: lanes) of the warp's 32 of item w, which ended not finite
+// with a key of the part hidden: where a value that was multiplied by a hidden
+// key's 0 is not finite, again from what the row sees alone.  g, r: the lane's
+// row tile and row, as in the softmax.  (Inlined, it cost the softmax registers:
+// four capped prompt chunks 170 us, 167 so.)
+template <int D, typename T, bool BIAS>
+__device__ __noinline__ void ct_redo(const CtArgs &ta, unsigned w, unsigned rows, int g, int r) {
+  constexpr int kGroups = ct_groups(D), EPL = D / 32;
+  constexpr int kKeys = 32 / EPL;                // keys whose loads are in flight together
+  const ChunkArgs &a = ta.c;
+  const int lane = threadIdx.x & 31;
+  const int per = kCtRows >> ta.gshift;
+  CtUnit u;
+  reinterpret_cast<int4 *>(&u)[0] = __ldcg(reinterpret_cast<const int4 *>(ta.units + w / (unsigned)ta.subs));
+  reinterpret_cast<int4 *>(&u)[1] = __ldcg(reinterpret_cast<const int4 *>(ta.units + w / (unsigned)ta.subs) + 1);
+  const int sub = (int)(w % (unsigned)ta.subs), kvh = (sub << ta.gshift) / a.G;
+  const ChunkSeq s = chunk_seq(a, u.b, false);
+  const int queries = min(kGroups * per, s.qlen - u.i0);
+  const int qi = (kGroups == 2 && queries <= per ? 0 : g * per) + (r >> ta.gshift);
+  const int i = u.i0 + min(qi, queries - 1), p = s.n - s.qlen + i;
+  const int h = (sub << ta.gshift) + (r & ((1 << ta.gshift) - 1));
+  const size_t q_row = (size_t)(s.q0 + i) * a.H + h;
+  const float slope = BIAS ? __ldg(a.slopes + h) * kLog2e : 0.f;
+  int lo, hi;
+  chunk_visible(a, s, i, lo, hi);
+  const bool seen = hi > lo;
+  const int rlo = max(lo, u.t0), rhi = min(hi, u.t1);
+  const bool mine = (rows >> lane) & 1, some = mine && rhi > rlo;
+  // The keys [from, u.t1) were multiplied; the row's are one interval of them,
+  // so what counts is the first key with a value that is not finite before the
+  // rows' own, and the last behind them.
+  const int from = max(u.t0, u.lo);
+  const int before = __reduce_max_sync(0xffffffffu, some ? rlo : from);
+  const int behind = __reduce_min_sync(0xffffffffu, some ? rhi : u.t1);
+  auto odd_value = [&](int t) {                  // key t's row of V, by the warp
+    float z = 0.f;
+    const T *v = reinterpret_cast<const T *>(a.v_cache) + chunk_row_at(a, u.b, kvh, t) + lane;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) z = fmaf(to_f32<T>(v[32 * e]), 0.f, z);
+    return z != 0.f;
+  };
+  int first = 0x7fffffff, last = -1;
+  for (int t = from; t < before && first > t; t += kKeys) {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k)
+      if (t + k < before && odd_value(t + k)) first = min(first, t + k);
+    first = __reduce_min_sync(0xffffffffu, first);
+  }
+  for (int t = u.t1 - 1; t >= behind && last < 0; t -= kKeys) {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k)
+      if (t - k >= behind && odd_value(t - k)) last = max(last, t - k);
+    last = __reduce_max_sync(0xffffffffu, last);
+  }
+  unsigned again = __ballot_sync(0xffffffffu, mine && (!some || first < rlo || last >= rhi));
+  while (again) {
+    const int src = __ffs(again) - 1;
+    again &= again - 1;
+    const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)q_row, src);
+    const bool any_key = __shfl_sync(0xffffffffu, (int)seen, src);
+    float em, el, eo[EPL];
+    chunk_row_exact<T, EPL, kKeys>(a, u.b, kvh, row, __shfl_sync(0xffffffffu, slope, src), __shfl_sync(0xffffffffu, p, src),
+                                   __shfl_sync(0xffffffffu, rlo, src), __shfl_sync(0xffffffffu, rhi, src), em, el, eo);
+    const size_t at = row * a.max_parts + u.part;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      const int d = lane + 32 * e;
+      if (u.nparts == 1)
+        reinterpret_cast<T *>(a.out)[row * D + d] = from_f32<T>(any_key ? eo[e] / el : 0.f);
+      else
+        a.ws_o[at * D + d] = eo[e];
+    }
+    if (u.nparts > 1 && lane == 0) {
+      a.ws_m[at] = em;
+      a.ws_l[at] = el;
+    }
+  }
+}
 
 template <int D, typename T, int CAP, bool BIAS>
 __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
@@ -213,7 +294,8 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           item.q0 = s.q0;
           item.qlen = s.qlen;
           item.n = s.n;
-          item.queries = min(kGroups * per, s.qlen - item.i0);
+          item.w = (int)w;
+          const int queries = min(kGroups * per, s.qlen - item.i0);
           item.kind = item.t1 > 0 ? 1 : 2;
           if (item.kind == 1) {
             // one past the last key the group's rows see before the part's end
@@ -222,10 +304,10 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
               const int hi = min(item.t1, max(s.n - s.qlen + i + 1, s.prefix));
               return max(1, (hi - item.t0 + kCtTile - 1) / kCtTile);
             };
-            item.nt[0] = tiles_to(item.i0 + min(per, item.queries) - 1);
-            item.nt[1] = item.queries > per ? tiles_to(item.i0 + item.queries - 1) : 0;
+            item.nt[0] = tiles_to(item.i0 + min(per, queries) - 1);
+            item.nt[1] = queries > per ? tiles_to(item.i0 + queries - 1) : 0;
             item.ntiles = max(item.nt[0], item.nt[1]);
-            if (kGroups == 2 && item.queries <= per) {
+            if (kGroups == 2 && queries <= per) {
               item.nparts = -item.nparts;
               item.nt[1] = item.ntiles / 2;
               item.nt[0] = item.ntiles - item.nt[1];
@@ -569,6 +651,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
     const bool raw = !CAP && !BIAS && sl2 > 0.f;
     const float mul = raw ? sl2 : 1.f;
     int it = 0, ring0 = 0, ig = 0, tcnt = 0, npair = 0;
+    int redo = -1;                                      // the item noted last
     bool ok = true;
     while (true) {
       const int slot = it & 1;
@@ -586,9 +669,10 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
       // item's last query mirror it and are not written)
       const bool pair = kGroups == 2 && item.pair();
       const int qi = (pair ? 0 : g * per) + (r >> ta.gshift);
-      const bool real_row = qi < item.queries;
+      const int queries = min(kGroups * per, item.qlen - item.i0);
+      const bool real_row = qi < queries;
       const bool live = __any_sync(0xffffffffu, real_row);  // a warp without rows only keeps the barriers going
-      const int i = item.i0 + min(qi, item.queries - 1);
+      const int i = item.i0 + min(qi, queries - 1);
       const int h = (item.sub << ta.gshift) + (r & (gheads - 1));
       const size_t q_row = (size_t)(item.q0 + i) * a.H + h;
       T *orow = reinterpret_cast<T *>(a.out) + q_row * D;
@@ -918,35 +1002,23 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
         a.ws_l[at] = l;
       }
       // rows that are not finite although a key of the part is hidden from
-      // them: again, from what they see alone
-      unsigned again = __ballot_sync(0xffffffffu, real_row && odd != 0.f && (lo > item.t0 || hi < item.t1));
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)q_row, src);
-        const int rlo = max(__shfl_sync(0xffffffffu, lo, src), item.t0);
-        const int rhi = min(__shfl_sync(0xffffffffu, hi, src), item.t1);
-        const bool any_key = __shfl_sync(0xffffffffu, (int)seen, src);
-        float em, el, eo[D / 32];
-        chunk_row_exact<T, D / 32>(a, item.b, (item.sub << ta.gshift) / a.G, row, __shfl_sync(0xffffffffu, slope, src),
-                                   __shfl_sync(0xffffffffu, p, src), rlo, rhi, em, el, eo);
-        const size_t ra = row * a.max_parts + item.part;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-          const int d = lane + 32 * e;
-          if (item.parts() == 1)
-            reinterpret_cast<T *>(a.out)[row * D + d] = from_f32<T>(any_key ? eo[e] / el : 0.f);
-          else
-            a.ws_o[ra * D + d] = eo[e];
-        }
-        if (item.parts() > 1 && lane == 0) {
-          a.ws_m[ra] = em;
-          a.ws_l[ra] = el;
-        }
+      // them: noted for the end
+      const unsigned again = __ballot_sync(0xffffffffu, real_row && odd != 0.f && (lo > item.t0 || hi < item.t1));
+      if (again) {
+        if (lane == 0) ta.redo[(size_t)item.w * kSoftmaxWarps + warp] = make_int2((int)again, redo);
+        redo = item.w;
       }
       ring0 += item.ntiles;
     }
     if (!ok && lane == 0) abort_cta();
+    __syncwarp();
+    while (ok && redo >= 0) {
+      const volatile int2 *note = ta.redo + (size_t)redo * kSoftmaxWarps + warp;
+      const unsigned rows = (unsigned)note->x;
+      const int next = note->y;
+      ct_redo<D, T, BIAS>(ta, (unsigned)redo, rows, g, r);
+      redo = next;
+    }
   }
 
   tc_fence_before();

@@ -341,6 +341,48 @@ def test_what_a_row_does_not_see_never_reaches_it(dtype, H, KVH, D, bad, qlen):
     assert not got[~untouched].isfinite().all(-1).any() if (~untouched).any() and bad != float("-inf") else True
 
 
+@pytest.mark.parametrize("D,n", [(64, 100_000), (128, 100_000), (256, 40_000)])
+@pytest.mark.parametrize("parts", [1, 3])
+def test_an_infinity_holds_nobody_up(D, n, parts):
+    """The last key of a long sequence has an infinite value: its 255 queries
+    that do not see it are done again, over all of their keys, while nothing
+    else waits -- no time limit runs out, and another sequence's items, behind
+    on the same SM, come out as without it."""
+    units, per = 160, 256 if D <= 128 else 128
+    g = torch.Generator(device=DEV).manual_seed(D)
+    nb = -(-n // 16) + units * per // 16
+    k, v = (torch.randn(nb, 16, 1, D, generator=g, device=DEV).to(HF) for _ in range(2))
+    q = torch.randn(256 + units * per, 1, D, generator=g, device=DEV).to(HF)
+    first = -(-n // 16)
+    tables = torch.zeros(2, first + units * per // 16, dtype=torch.int32, device=DEV)
+    tables[0, :first] = torch.arange(first, device=DEV)
+    tables[1, :units * per // 16] = torch.arange(first, nb, device=DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    cu, lens, err = i32([0, 256, 256 + units * per]), i32([n, units * per]), i32([0])
+    part = -(-(-(-n // parts)) // 128) * 128
+    ws = pkv.ChunkWorkspace(2, len(q), 1, 1, D, 16, tables.shape[1], units * per, n, part)
+    assert pkv.pkv_chunk_plan(2, len(q), 1, 1, D, 16, tables.shape[1], units * per, n, partition_size=part, dtype=HF)[1:] == (parts, 2)
+    scale, outs = 1 / math.sqrt(D), []
+    for value in (None, float("inf")):
+        if value is not None:
+            v[(n - 1) // 16, (n - 1) % 16] = value
+        out = torch.zeros_like(q)
+        pkv.pkv_chunk_attention(out, q, k, v, tables, cu, lens, scale, max_q_len=units * per, max_context_len=n,
+                                partition_size=part, workspace=ws, err_flags=err)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        outs.append(out.cpu())
+    assert torch.equal(outs[1][256:], outs[0][256:])
+    assert not outs[1][255].isfinite().any()
+    keys, vals = k.view(-1, D)[:n - 1].cpu().double(), v.view(-1, D)[:n - 1].cpu().double()
+    for i in range(0, 255, 23):
+        x = q[i, 0].cpu().double() @ keys[:n - 256 + i + 1].T * scale
+        want = torch.softmax(x, 0) @ vals[:n - 256 + i + 1]
+        tol = (torch.finfo(HF).eps + 2.0 ** -18) * vals.abs().max()
+        assert (outs[1][i, 0].double() - want).abs().max() <= tol
+    assert (outs[1][:255].double() - outs[0][:255].double()).abs().max() <= 2 * tol
+
+
 def test_blocks_outside_the_window_are_not_read():
     """Freed blocks' table entries may be garbage once no query sees them."""
     for dtype, D in ((BF, 128), (F32, 64), (HF, 256)):
