@@ -503,8 +503,9 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  *                 its output rows are unspecified
  *   partition_size  0 = automatic, else a positive multiple of 128: keys per
  *                 part of the split over the context (raised where it would
- *                 give more than 256 parts; with more than 65520 units of
- *                 16 rows nothing is split)
+ *                 give more than 256 parts, at most 2^20 on the tcgen05 kernel
+ *                 where that gives no more; with more than 65520 units of 16
+ *                 rows nothing is split)
  *   workspace     pkv_chunk_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use; every call that completes
  *                 without PKV_FLAG_TIMEOUT leaves it ready for the next on the

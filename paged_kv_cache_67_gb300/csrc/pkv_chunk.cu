@@ -90,10 +90,12 @@ static long long parts_wanted(long long units, long long slots, long long span, 
 //   rounds of items over the SMs x (tiles of a part + 2 to start and end one)
 //   + joining the parts (0.015 a part of an item: its 270 KB to and from
 //   memory against 2.7 us a tile on one SM of 152; 2 for the launch).
-// No part is longer than 2^20 keys (some 25 ms), far inside the kernel's
-// bounded waits, which span an item.
+// No part is longer than kTcMaxPart keys (some 25 ms), far inside the kernel's
+// bounded waits of 500 ms, which span an item; past 2^28 keys a context's 256
+// parts are longer, up to 2^22 keys (some 100 ms).
+constexpr int kTcMaxPart = 1 << 20;
 static long long tc_parts_wanted(long long items, long long span) {
-  const long long fewest = ceil_div(span, 1LL << 20);
+  const long long fewest = ceil_div(span, kTcMaxPart);
   long long best = fewest;
   double least = 0;
   for (long long p = fewest; p <= kChunkMaxParts && p <= ceil_div(span, 512); ++p) {
@@ -145,7 +147,8 @@ static bool chunk_plan(int B, int64_t total_q, int H, int KVH, int D, int bs, in
   if (p->kernel == 2) {
     const long long items = chunk_tc_items(B, total_q, H, H / KVH, D, (int)mq);
     // (never more than without a window: the workspace is sized for that)
-    chunk_split(std::min(tc_parts_wanted(items, span), tc_parts_wanted(items, cap)), span, 512, partition_size, p);
+    chunk_split(std::min(tc_parts_wanted(items, span), tc_parts_wanted(items, cap)), span, 512,
+                std::min(partition_size, kTcMaxPart), p);
     return true;
   }
   const int per_sm = p->kernel == 0 ? (p->rows == kChunkManyRows ? 2 : 4) : D <= 192 ? 2 : 1;   // resident CTAs

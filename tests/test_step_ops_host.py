@@ -121,6 +121,17 @@ def test_chunk_plan_and_workspace(pkv):
                         assert size(B, q, H, KVH, D, bs, mb, max_q, 0, part) >= need
 
 
+@pytest.mark.parametrize("keys", [1 << 20, (1 << 20) + 16, 1 << 24, (1 << 28) + 16, 1 << 30])
+@pytest.mark.parametrize("part", [0, 1 << 20, 1 << 21, 1 << 29, (1 << 31) - 128])
+def test_parts_stay_inside_the_kernels_time_limits(pkv, keys, part):
+    """tcgen05: no part longer than 2^20 keys, or than a 256th of the context."""
+    P, parts, kernel = pkv.pkv_chunk_plan(2, 512, 8, 2, 128, 16, keys // 16, 256, 0, 0, False, part)
+    assert kernel == 2 and P <= max(1 << 20, -(-keys // 256 // 128) * 128 + 128) and parts == -(-keys // P) <= 256
+    rows = 512 * 8
+    need = 65536 * 4 + (0 if parts == 1 else 2 * rows * parts * 4 + rows * parts * 128 * 4)
+    assert pkv.pkv_chunk_workspace_size(2, 512, 8, 2, 128, 16, keys // 16, 256, 0, part) >= need
+
+
 def test_binding_refuses_before_any_call(pkv):
     """Wrong shapes, types and devices raise ValueError on the host."""
     z = lambda *s, dt=torch.int32: torch.zeros(*s, dtype=dt)
