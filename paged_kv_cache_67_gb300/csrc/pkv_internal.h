@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "pkv.h"
 
 namespace pkv {
@@ -86,17 +88,20 @@ bool encode_rows_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long
 bool encode_packed_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,
                        int box_heads, int box_rows);
 
-// One-time opt-in to a kernel's dynamic shared memory, per device
-// (`configured` is the kernel's own per-device record).
+// Opt-in to a kernel's dynamic shared memory, per device (`configured` is the
+// kernel's own per-device record).  The limit only rises, whatever sizes host
+// threads ask for at once: under a lock, and the record follows the limit.
 template <typename K>
 inline bool allow_smem(K kern, size_t bytes, int *configured) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  if (dev < 64 && configured[dev] >= (int)bytes) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-      cudaSuccess)
-    return false;
-  if (dev < 64) configured[dev] = (int)bytes;
+  if (dev >= 64) return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+  if (__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE) >= (int)bytes) return true;
+  static std::mutex lock;
+  std::lock_guard<std::mutex> held(lock);
+  if (configured[dev] >= (int)bytes) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+  __atomic_store_n(&configured[dev], (int)bytes, __ATOMIC_RELEASE);
   return true;
 }
 
