@@ -430,9 +430,9 @@ PKV_API pkv_status pkv_build_step(int32_t *block_tables, const int32_t *held, in
  *   q             [num_tokens, H, head_dim], token i at element i * q_token_stride
  *   k, v          [num_tokens, num_kv_heads, head_dim], strides as in pkv_write
  *   q_out         [num_tokens, H, head_dim] contiguous; may be q itself (with
- *                 q_token_stride = H * head_dim), else overlaps neither q, k
- *                 nor v
- *   k_cache, v_cache, slot_mapping  as in pkv_write
+ *                 q_token_stride = H * head_dim), else overlaps no other
+ *                 argument
+ *   k_cache, v_cache, slot_mapping  as in pkv_write; the caches do not overlap
  *   cos_sin       [max_position, rot_dim] float32: row p holds the cosines of
  *                 the rot_dim / 2 pairs' angles at position p, then the sines
  *   positions     [num_axes, num_tokens] int32, axis a at element
@@ -482,8 +482,8 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  * query that sees no key gives a row of zeros.
  *
  *   out, q, cu_seqlens_q, k_cache, v_cache, block_tables, context_lens
- *                 as in pkv_prefill_attention (out overlaps no other
- *                 argument); out rows behind cu_seqlens_q[B] are left as they
+ *                 as in pkv_prefill_attention (neither out nor the workspace
+ *                 overlaps another argument); out rows behind cu_seqlens_q[B] are left as they
  *                 were
  *   softcap       0 = none, else > 0; up to 256 is fastest on the tensor-core
  *                 kernels (larger ones take a form whose error does not grow

@@ -237,6 +237,18 @@ PKV_API pkv_status pkv_chunk_attention(
     return PKV_ERR_INVALID_ARG;
   const size_t need = chunk_ws_bytes(plan.kernel, B, total_q, H, num_kv_heads, head_dim, max_q_len, plan.max_parts);
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256) return PKV_ERR_WORKSPACE;
+  const size_t rows_bytes = (size_t)total_q * H * head_dim * el;
+  const size_t cache_bytes = (size_t)num_blocks * block_size * num_kv_heads * head_dim * el;
+  const ArgRange written[] = {{out, rows_bytes}, {workspace, need}};
+  const ArgRange read[] = {{q, rows_bytes}, {k_cache, cache_bytes}, {v_cache, cache_bytes},
+                           {block_tables, (size_t)B * max_blocks * sizeof(int32_t)},
+                           {cu_seqlens_q, (size_t)(B + 1) * sizeof(int32_t)}, {context_lens, (size_t)B * sizeof(int32_t)},
+                           {slopes, (size_t)H * sizeof(float)}, {prefix_lens, (size_t)B * sizeof(int32_t)},
+                           {kv_starts, (size_t)total_q * sizeof(int32_t)}, {err_flags, sizeof(int)}};
+  for (const ArgRange &w : written)
+    for (const ArgRange &r : read)
+      if (overlap(w, r)) return PKV_ERR_INVALID_ARG;
+  if (overlap(written[0], written[1])) return PKV_ERR_INVALID_ARG;
   if (plan.chunks * num_kv_heads * plan.max_parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   int sms = 0;
   if (!device_sms(&sms)) return PKV_ERR_CUDA;

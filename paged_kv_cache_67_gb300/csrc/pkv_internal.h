@@ -88,6 +88,17 @@ bool encode_rows_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long
 bool encode_packed_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,
                        int box_heads, int box_rows);
 
+// Whether two arguments share memory (NULL or empty ones share none).
+struct ArgRange {
+  const void *p;
+  size_t bytes;
+};
+inline bool overlap(const ArgRange &x, const ArgRange &y) {
+  if (!x.p || !y.p || !x.bytes || !y.bytes) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return a < b + y.bytes && b < a + x.bytes;
+}
+
 // Opt-in to a kernel's dynamic shared memory, per device (`configured` is the
 // kernel's own per-device record).  The limit only rises, whatever sizes host
 // threads ask for at once: under a lock, and the record follows the limit.

@@ -272,14 +272,18 @@ extern "C" PKV_API pkv_status pkv_rope_write(
       (rot_dim > 0 && !cos_sin))
     return PKV_ERR_INVALID_ARG;
   const uintptr_t el = dt == PKV_F32 ? 4 : 2;
-  const uintptr_t out0 = reinterpret_cast<uintptr_t>(q_out), out1 = out0 + (uintptr_t)num_tokens * H * head_dim * el;
-  const struct { const void *p; int64_t stride, row; } in[] = {{q, q_token_stride, (int64_t)H * head_dim},
-                                                               {k, k_token_stride, (int64_t)num_kv_heads * head_dim},
-                                                               {v, v_token_stride, (int64_t)num_kv_heads * head_dim}};
-  for (const auto &x : in) {  // rows that lie between another tensor's rows would do, but no caller has them
-    const uintptr_t p0 = reinterpret_cast<uintptr_t>(x.p), p1 = p0 + ((num_tokens - 1) * x.stride + x.row) * el;
-    if (out0 < p1 && p0 < out1 && !(x.p == q && q_out == q)) return PKV_ERR_INVALID_ARG;
-  }
+  // (rows that lie between another tensor's rows would do, but no caller has them)
+  auto rows = [&](const void *p, int64_t stride, int64_t row) { return ArgRange{p, (size_t)((num_tokens - 1) * stride + row) * el}; };
+  const int64_t q_row = (int64_t)H * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+  const size_t cache = (size_t)num_blocks * block_size * kv_row * el;
+  const ArgRange out = rows(q_out, q_row, q_row), kc = {k_cache, cache}, vc = {v_cache, cache};
+  const ArgRange others[] = {rows(k, k_token_stride, kv_row), rows(v, v_token_stride, kv_row), kc, vc,
+                             {cos_sin, (size_t)max_position * rot_dim * sizeof(float)},
+                             {positions, (size_t)((num_axes - 1) * positions_stride + num_tokens) * sizeof(int32_t)},
+                             {slot_mapping, (size_t)num_tokens * sizeof(int64_t)}};
+  for (const ArgRange &x : others)
+    if (overlap(out, x)) return PKV_ERR_INVALID_ARG;
+  if ((q_out != q && overlap(out, rows(q, q_token_stride, q_row))) || overlap(kc, vc)) return PKV_ERR_INVALID_ARG;
   const void *ptrs[] = {q_out, k_cache, v_cache, q, k, v};
   for (const void *p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) % el) return PKV_ERR_INVALID_ARG;

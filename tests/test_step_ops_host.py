@@ -70,6 +70,21 @@ def test_rope_write_refusals(pkv):
     assert _rope(lib, D=513, rot=64) == UNSUPPORTED
 
 
+def test_rope_write_refuses_outputs_on_other_arguments(pkv):
+    """q_out on a cache or a table, first and last byte, and a cache on the other."""
+    lib = pkv.load_library()
+    cache, row = 8 * 16 * 2 * 64 * 2, 4 * 64 * 2          # bytes of a cache, of a token's q
+    far = {"q_out": 16 * FAKE, "q": 32 * FAKE, "k": 48 * FAKE, "v": 64 * FAKE, "kc": 80 * FAKE, "vc": 96 * FAKE,
+           "cs": 112 * FAKE, "pos": 128 * FAKE, "slots": 144 * FAKE}
+    for name, size in (("q", 3 * row), ("k", row // 2 * 3), ("v", row // 2 * 3), ("kc", cache), ("vc", cache),
+                       ("cs", 128 * 64 * 4), ("pos", 12), ("slots", 24)):
+        for at in (far[name], far[name] - 3 * row + 8, (far[name] + size - 1) // 8 * 8):
+            if name != "q" or at != far["q"]:
+                assert _rope(lib, **{**far, "q_out": at}) == INVALID, (name, at - far[name])
+    assert _rope(lib, **{**far, "vc": far["kc"] + cache - 16}) == INVALID
+    assert _rope(lib, **{**far, "vc": far["kc"]}) == INVALID
+
+
 def _chunk(lib, **kw):
     g = kw.get
     return lib.pkv_chunk_attention(
@@ -93,6 +108,24 @@ def test_chunk_refusals(pkv):
     need = pkv.pkv_chunk_workspace_size(2, 6, 4, 2, 64, 16, 4)
     assert _chunk(lib, ws=FAKE, wsb=1024) == WORKSPACE            # too small
     assert _chunk(lib, ws=FAKE + 128, wsb=need) == WORKSPACE      # misaligned
+
+
+def test_chunk_refuses_outputs_on_other_arguments(pkv):
+    """out and the workspace on any other argument, first and last byte."""
+    lib = pkv.load_library()
+    names = ("out", "q", "kc", "vc", "tables", "cu", "lens", "slopes", "prefix", "starts", "ws")
+    far = {n: (i + 1) * 16 * FAKE for i, n in enumerate(names)}
+    need = pkv.pkv_chunk_workspace_size(2, 6, 4, 2, 64, 16, 4)
+    rows, cache = 6 * 4 * 64 * 2, 8 * 16 * 2 * 64 * 2
+    sizes = {"out": rows, "q": rows, "kc": cache, "vc": cache, "tables": 32, "cu": 12, "lens": 8, "slopes": 16,
+             "prefix": 8, "starts": 24, "ws": 65536 * 4}
+    for written in ("out", "ws"):
+        for name in names:
+            if name == written:
+                continue
+            step = 16 if written == "out" else 256
+            for at in (far[name], far[name] - (sizes[written] - 1) // step * step, far[name] + (sizes[name] - 1) // step * step):
+                assert _chunk(lib, **{**far, written: at}, wsb=need) == INVALID, (written, name, at - far[name])
 
 
 def test_chunk_plan_and_workspace(pkv):
