@@ -437,7 +437,8 @@ PKV_API pkv_status pkv_build_step(int32_t *block_tables, const int32_t *held, in
  *                 the rot_dim / 2 pairs' angles at position p, then the sines
  *   positions     [num_axes, num_tokens] int32, axis a at element
  *                 a * positions_stride: a token's position on each axis (for
- *                 images and video: time, height, width)
+ *                 images and video: time, height, width); stride 0 gives every
+ *                 axis the same positions (text)
  *   pair_axis     HOST array of rot_dim / 2 bytes: the axis in [0, num_axes)
  *                 whose position turns pair j (sections, or any interleaving
  *                 of the axes); NULL = axis 0 for all; read during the call

@@ -251,7 +251,7 @@ extern "C" PKV_API pkv_status pkv_rope_write(
       block_size <= 0 || H <= 0 || H > 65535 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
       head_dim <= 0 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 || num_axes < 1 ||
       num_axes > 4 || max_position < 0 || positions_stride < 0 ||
-      (num_axes > 1 && positions_stride < num_tokens))
+      (num_axes > 1 && positions_stride > 0 && positions_stride < num_tokens))
     return PKV_ERR_INVALID_ARG;
   if (head_dim > 512) return PKV_ERR_UNSUPPORTED;
   if (q_token_stride < (int64_t)H * head_dim || k_token_stride < (int64_t)num_kv_heads * head_dim ||

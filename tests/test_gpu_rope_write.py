@@ -127,6 +127,21 @@ def test_one_axis_default():
     assert all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
 
 
+def test_positions_broadcast_over_the_axes():
+    """Text: one position for every axis, as an expanded tensor (stride 0)."""
+    for T in (1, 21):
+        c = case(11, T, 4, 2, 64, 64, 3, torch.bfloat16)
+        c["pos"] = c["pos"][:1].repeat(3, 1)
+        want = run(c)
+        d = lambda t: t.to(DEV)
+        q, k, v = (d(c[n]).contiguous() for n in "qkv")
+        q_out, kc, vc = torch.full_like(q, 7.0), d(c["k_cache"]), d(c["v_cache"])
+        pkv.pkv_rope_write(q_out, kc, vc, q, k, v, d(c["cos_sin"]), d(c["pos"][0]).expand(3, T), d(c["slots"]),
+                           pair_axis=c["pair_axis"])
+        for got, w in zip((q_out, kc, vc), want):
+            assert torch.equal(got.cpu(), w)
+
+
 def test_values_that_are_not_finite_stay_in_their_pair():
     c = case(7, 9, 4, 2, 64, 64, 2, torch.bfloat16)
     c["q"][3, 1, 5] = float("nan")
