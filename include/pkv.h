@@ -400,16 +400,16 @@ PKV_API pkv_status pkv_prefill_attention(void *out, const void *q, const void *k
  * request that holds fewer than ceil(cached_lens[b] / block_size) blocks or
  * needs more than max_blocks, 2^30 new tokens or more in all, or a free list
  * that is (or would become) larger than free_capacity, the call raises
- * PKV_FLAG_STEP_INVALID; with too few free blocks PKV_FLAG_OUT_OF_BLOCKS.  In both cases tables, free list and counts stay
- * as they were (held_out and free_count_out get the old values) and the step
- * is empty: context_lens 0, cu_seqlens_q 0, every slot -1.  More than
- * max_tokens new tokens raise PKV_FLAG_TOKENS_OVER: slot_mapping and positions
+ * PKV_FLAG_STEP_INVALID; with too few free blocks PKV_FLAG_OUT_OF_BLOCKS.  In
+ * both cases tables, free list and counts stay as they were (held_out and
+ * free_count_out get the old values) and the step is empty: context_lens 0,
+ * cu_seqlens_q 0, every slot -1.  More than max_tokens new tokens raise PKV_FLAG_TOKENS_OVER: slot_mapping and positions
  * hold the first max_tokens, everything else is as without the bound (what
  * attends over max_tokens query rows skips and flags the requests past it).
  * An entry outside
  * [0, num_blocks) raises PKV_FLAG_BLOCK_OUT_OF_RANGE where a token or a
  * request would get it; that token's slot is -1.
- * Supported: B <= 16384, max_tokens <= 2^30.  Errors: PKV_ERR_INVALID_ARG
+ * Supported: B <= 16384, max_tokens < 2^30, free_capacity < 2^30.  Errors: PKV_ERR_INVALID_ARG
  * (NULL or misaligned pointers, sizes), PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  * B == 0 with max_tokens == 0 enqueues nothing.
  */

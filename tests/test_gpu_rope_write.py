@@ -127,6 +127,15 @@ def test_one_axis_default():
     assert all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype,T,rot", [(torch.bfloat16, 2101, 128), (torch.float16, 2101, 64), (torch.float32, 1051, 128)])
+def test_more_than_the_cache_level_holds(dtype, T, rot, interleaved):
+    """Past 64 MB of rows the stores are marked as streaming: the same values."""
+    H, KVH, D = 128, 16, 128
+    assert T * (H + 2 * KVH) * D * torch.finfo(dtype).bits // 8 > 64 << 20
+    check(case(12, T, H, KVH, D, rot, 3, dtype, max_pos=3000, pads=100), interleaved)
+
+
 def test_positions_broadcast_over_the_axes():
     """Text: one position for every axis, as an expanded tensor (stride 0)."""
     for T in (1, 21):

@@ -46,6 +46,18 @@ def test_build_step_refusals(pkv):
     assert _step(lib, pos=FAKE + (10 << 24) + 64) == INVALID
 
 
+def test_build_step_bounds(pkv):
+    """The largest sizes and the first ones past them: what is refused says so,
+    what is not fails for want of a device alone."""
+    lib = pkv.load_library()
+    assert _step(lib, cap=1 << 30) == UNSUPPORTED
+    assert _step(lib, cap=1 << 31) == INVALID
+    far = {n: FAKE + (i << 36) for i, n in enumerate(("tables", "held", "held_out", "free", "count", "count_out", "cached",
+                                                      "new", "lens", "cu", "slots", "pos"))}
+    if not torch.cuda.is_available():
+        assert _step(lib, **far, cap=(1 << 30) - 1, T=(1 << 30) - 1, B=16384) not in (OK, INVALID, UNSUPPORTED)
+
+
 def _rope(lib, **kw):
     D, H, KVH = kw.get("D", 64), kw.get("H", 4), kw.get("KVH", 2)
     axis = kw.get("axis")
