@@ -403,14 +403,15 @@ PKV_API pkv_status pkv_prefill_attention(void *out, const void *q, const void *k
  * PKV_FLAG_STEP_INVALID; with too few free blocks PKV_FLAG_OUT_OF_BLOCKS.  In
  * both cases tables, free list and counts stay as they were (held_out and
  * free_count_out get the old values) and the step is empty: context_lens 0,
- * cu_seqlens_q 0, every slot -1.  More than max_tokens new tokens raise PKV_FLAG_TOKENS_OVER: slot_mapping and positions
- * hold the first max_tokens, everything else is as without the bound (what
- * attends over max_tokens query rows skips and flags the requests past it).
- * An entry outside
- * [0, num_blocks) raises PKV_FLAG_BLOCK_OUT_OF_RANGE where a token or a
- * request would get it; that token's slot is -1.
- * Supported: B <= 16384, max_tokens < 2^30, free_capacity < 2^30.  Errors: PKV_ERR_INVALID_ARG
- * (NULL or misaligned pointers, sizes), PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * cu_seqlens_q 0, every slot -1.  More than max_tokens new tokens raise
+ * PKV_FLAG_TOKENS_OVER: slot_mapping and positions hold the first max_tokens,
+ * everything else is as without the bound (what attends over max_tokens query
+ * rows skips and flags the requests past it).  An entry outside [0, num_blocks)
+ * raises PKV_FLAG_BLOCK_OUT_OF_RANGE where a token or a request would get it;
+ * that token's slot is -1.
+ * Supported: B <= 16384, max_tokens < 2^30, free_capacity < 2^30.  Errors:
+ * PKV_ERR_INVALID_ARG (NULL or misaligned pointers, sizes),
+ * PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  * B == 0 with max_tokens == 0 enqueues nothing.
  */
 PKV_API pkv_status pkv_build_step(int32_t *block_tables, const int32_t *held, int32_t *held_out,
@@ -520,7 +521,7 @@ PKV_API pkv_status pkv_rope_write(void *q_out, void *k_cache, void *v_cache, con
  * changes a row, whatever it holds.  Table entries of blocks that no query
  * sees are not read.
  * Supported: fp32, bf16, fp16; head_dim <= 512; any block size; element-
- * aligned pointers.  bf16 / fp16 with 16-byte aligned tensors, block_size a
+ * aligned pointers; max_q_len * H / num_kv_heads < 2^31 - 64.  bf16 / fp16 with 16-byte aligned tensors, block_size a
  * multiple of 16 and head_dim 64, 128, 192 or 256 run tensor-core kernels:
  * an mma.sync kernel where max_q_len * H / num_kv_heads is 32 at most or the
  * whole call is small, else a tcgen05 kernel (three launches: plan, attention

@@ -218,6 +218,8 @@ PKV_API pkv_status pkv_chunk_attention(
       (softcap > 0.f && !isfinite(2.f * kLog2e * scale / softcap)))
     return PKV_ERR_INVALID_ARG;
   if (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16) return PKV_ERR_INVALID_ARG;
+  // packed rows of a (sequence, KV head), rounded up to a chunk, are counted in 32 bits
+  if ((long long)chunk_max_q(total_q, max_q_len) * (H / num_kv_heads) > 0x7fffffffLL - kChunkManyRows) return PKV_ERR_UNSUPPORTED;
   if (B == 0 || total_q == 0) return PKV_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !context_lens)
     return PKV_ERR_INVALID_ARG;

@@ -122,6 +122,16 @@ def test_chunk_refusals(pkv):
     assert _chunk(lib, ws=FAKE + 128, wsb=need) == WORKSPACE      # misaligned
 
 
+def test_chunk_refuses_more_rows_than_32_bits_count(pkv):
+    """2^31 packed (query, head) rows of a KV head and more."""
+    lib = pkv.load_library()
+    for kw in ({"D": 1, "H": 65535, "KVH": 1, "total": 40000}, {"D": 2, "H": 16384, "KVH": 1, "total": 131072, "dt": 0},
+               {"D": 64, "H": 2, "KVH": 1, "total": 1 << 30}):
+        assert _chunk(lib, **kw) == UNSUPPORTED, kw
+        assert _chunk(lib, **kw, max_q=1000) == WORKSPACE, kw     # with a bound on the queries it is a call
+    assert _chunk(lib, D=1, H=65535, KVH=1, total=32767) == WORKSPACE
+
+
 def test_chunk_refuses_outputs_on_other_arguments(pkv):
     """out and the workspace on any other argument, first and last byte."""
     lib = pkv.load_library()
