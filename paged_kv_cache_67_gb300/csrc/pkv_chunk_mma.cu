@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(32 * CmShape<D>::kWarps, 1)
       m1 = mn1;
     }
     const float e0 = chunk_ref(m0), e1 = chunk_ref(m1);
+    // weights in 16 bits, and the sum of the rounded ones: it hides behind the loads here
     uint32_t pa[4];
     pa[0] = Mma::pack(fast_exp2(x[0][0] - e0), fast_exp2(x[0][1] - e0), l0);
     pa[1] = Mma::pack(fast_exp2(x[0][2] - e1), fast_exp2(x[0][3] - e1), l1);

@@ -838,6 +838,11 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
         const bool rescale = __any_sync(0xffffffffu, m_new != m_used) && j > 0;
         l *= alpha;
         m_used = m_new;
+        // The sum takes the weights as they are, the product with V rounds them
+        // to T.  Summing the rounded ones makes up for part of that (against 64
+        // bits, capped prompts 0.00210 for 0.00228, packed documents 0.00180 for
+        // 0.00191; rounding the output alone gives 0.00166) and costs the
+        // unpacking: 184 us for 168, 302 for 279.
         float2 lsum = make_float2(0.f, 0.f);
         auto weights = [&](const auto &exponent) {       // P = 2^exponent(pair), and its sum
 #pragma unroll

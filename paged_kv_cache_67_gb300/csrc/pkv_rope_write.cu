@@ -212,7 +212,9 @@ static pkv_status launch_rope_v(RopeArgs &a, cudaStream_t stream) {
   const int hpw = units >= 32 ? 1 : 32 / units;
   const int groups = (a.H + 2 * a.KVH + hpw - 1) / hpw;   // warp-wide groups of heads of a token
   // few tokens: spread a token's heads over warps until the GPU holds about
-  // 16 warps an SM; many: one warp walks all heads and reads its angles once
+  // 16 warps an SM (152 SMs, those of the one GPU this library is built for;
+  // another count costs speed alone); many: one warp walks all heads and reads
+  // its angles once
   const long long want = (152LL * 16 + a.T - 1) / a.T;
   // what is written stays in L2 for the attention that reads it next, unless
   // it could not (402 MB of rows: 72 us with streaming stores, 77 without)
