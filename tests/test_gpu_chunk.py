@@ -503,6 +503,89 @@ def test_streams_and_graphs():
             close(out.cpu(), reference(c, softcap=20.0), c, f"{lens}")
 
 
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F32, 64), (HF, 256), (BF, 80)])
+def test_blocks_past_32_bit_offsets(dtype, D):
+    """Blocks behind 2^32 elements of the cache (10 to 17 GB)."""
+    base = -(-(1 << 32) // (16 * 8 * D)) + 5
+    for qlens in ([1, 2], [150, 40]):
+        c = case(24, [300, 77], qlens, 16, 8, D, 16, dtype)
+        want = reference(c, softcap=20.0)
+        big = []
+        for name in ("k", "v"):
+            t = torch.empty(base + len(c[name]), 16, 8, D, dtype=dtype, device=DEV)
+            t[base:] = c[name].to(DEV)
+            big.append(t)
+        tables = torch.where(c["tables"] < 99999, c["tables"] + base, 2 ** 31 - 1).to(torch.int32)
+        got, err = run({**c, "k": big[0], "v": big[1], "tables": tables}, softcap=20.0)
+        assert err == 0
+        close(got, want, c, f"{qlens}")
+        del big, t
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("odd", ["q", "k", "v", "out", "qkv", "all"])
+def test_tensors_that_start_anywhere(dtype, odd):
+    """Pointers aligned to an element only: the same values on the CUDA cores."""
+    for D, qlens in ((128, [1, 2]), (128, [60, 90]), (64, [3, 7]), (80, [40, 1])):
+        c = case(25 + D, [200, 333], qlens, 4, 2, D, 16, dtype)
+        want = reference(c, softcap=20.0, window=90)
+
+        def place(t, at):
+            flat = torch.zeros(t.numel() + 1, dtype=dtype, device=DEV)
+            v = flat[at:at + t.numel()].view(t.shape)
+            v.copy_(t)
+            return v
+
+        put = {n: place(c[n], int(n in odd or odd == "all")) for n in ("q", "k", "v")}
+        out = place(torch.full_like(c["q"], 7.0), int(odd in ("out", "all")))
+        for part in (0, 128):
+            got, err = run({**c, **put}, out=out, partition_size=part, softcap=20.0, window=90)
+            assert err == 0
+            close(got, want, c, f"{D} {qlens} {part}")
+
+
+def test_no_queries_at_all():
+    """A padded step in which no sequence has a new token: nothing is written."""
+    for dtype, D in ((BF, 128), (F32, 64), (HF, 256)):
+        for B, total in ((1, 3), (5, 200)):
+            c = case(26, [90] * B, [0] * B, 4, 2, D, 16, dtype)
+            c["q"] = torch.full((total, 4, D), float("nan"), dtype=dtype)
+            for part in (0, 128):
+                got, err = run(c, partition_size=part, softcap=9.0)
+                assert err == 0 and (got == 7).all()
+
+
+def test_calls_that_run_at_once():
+    """Calls on four streams, each with a workspace of its own, give the bits of
+    the calls one by one."""
+    shapes = [(BF, 128, [900, 700], [300, 200]), (BF, 128, [4000, 900], [2, 3]), (F32, 64, [300, 400], [40, 2]),
+              (HF, 256, [600, 333], [90, 100])]
+    state, want = [], []
+    for i, (dtype, D, lens, qlens) in enumerate(shapes):
+        c = case(60 + i, lens, qlens, 8, 2, D, 16, dtype)
+        d = {k: c[k].to(DEV) for k in ("q", "k", "v", "tables", "cu", "lens")}
+        ws = pkv.ChunkWorkspace(2, len(d["q"]), 8, 2, D, 16, d["tables"].shape[1], max(qlens), max(lens), 128)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        call = lambda out, stream, c=c, d=d, ws=ws, err=err, lens=lens, qlens=qlens: pkv.pkv_chunk_attention(
+            out, d["q"], d["k"], d["v"], d["tables"], d["cu"], d["lens"], c["scale"], softcap=20.0, max_q_len=max(qlens),
+            max_context_len=max(lens), partition_size=128, workspace=ws, err_flags=err, stream=stream)
+        out = torch.zeros_like(d["q"])
+        call(out, None)
+        torch.cuda.synchronize()
+        state.append((call, d, err, torch.cuda.Stream()))
+        want.append(out)
+    for _ in range(20):
+        outs = [torch.zeros_like(d["q"]) for _, d, _, _ in state]
+        torch.cuda.synchronize()
+        for (call, _, _, stream), out in zip(state, outs):
+            for _ in range(3):
+                call(out, stream)
+        torch.cuda.synchronize()
+        for (_, _, err, _), out, w in zip(state, outs, want):
+            assert int(err) == 0 and torch.equal(out, w)
+
+
 def test_results_repeat_bit_by_bit():
     for dtype, D, q in ((BF, 128, [3, 5]), (BF, 128, [200, 100]), (HF, 256, [2, 2]), (F32, 64, [20, 3])):
         c = case(23, [1500, 400], q, 8, 2, D, 16, dtype)

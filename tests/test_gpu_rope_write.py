@@ -136,6 +136,25 @@ def test_more_than_the_cache_level_holds(dtype, T, rot, interleaved):
     check(case(12, T, H, KVH, D, rot, 3, dtype, max_pos=3000, pads=100), interleaved)
 
 
+def test_slots_past_32_bit_offsets():
+    """Blocks behind 2^32 elements of the cache."""
+    c = case(13, 40, 8, 8, 128, 128, 3, torch.bfloat16, pads=3)
+    want, base = run(c), (1 << 32) // (16 * 8 * 128) + 7
+    d = lambda t: t.to(DEV)
+    q, k, v = (d(c[n]).contiguous() for n in "qkv")
+    caches = [torch.empty(base + len(c["k_cache"]), 16, 8, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    for big, name in zip(caches, ("k_cache", "v_cache")):
+        big[base:] = d(c[name])
+    q_out = torch.full_like(q, 7.0)
+    pkv.pkv_rope_write(q_out, *caches, q, k, v, d(c["cos_sin"]), d(c["pos"]),
+                       d(torch.where(c["slots"] < 0, c["slots"], c["slots"] + base * 16)), pair_axis=c["pair_axis"])
+    torch.cuda.synchronize()
+    for got, w in zip((q_out, caches[0][base:], caches[1][base:]), want):
+        assert torch.equal(got.cpu(), w)
+    del caches, big
+    torch.cuda.empty_cache()
+
+
 def test_positions_broadcast_over_the_axes():
     """Text: one position for every axis, as an expanded tensor (stride 0)."""
     for T in (1, 21):
