@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
     raise_flag(a.err, PKV_FLAG_TIMEOUT);
     *(volatile int *)abort_flag = 1;
   };
+  // (a warp that goes on or gives up as one takes this into its vote)
   auto aborted = [&]() { return *(volatile int *)abort_flag != 0; };
 
   if (warp >= kSoftmaxWarps) {
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           for (int g = 0; g < kGroups; ++g) {
             if (!ok || item.nt[g] == 0) continue;
             if (ig[g] > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_empty[g], (ig[g] - 1) & 1)) && !aborted();
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_empty[g], (ig[g] - 1) & 1) && !aborted());
               if (!ok) break;
             }
             if (lane == 0) mbar_arrive_expect_tx(&q_full[g], (uint32_t)Sh::kQBytes);
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
           const uint32_t bytes = (uint32_t)(valid_chunks * Sh::kRegions * (128 << ta.bshift));
           int phys = 0;
           if (lane < valid_chunks) phys = __ldg(a.tables + (size_t)item.b * a.max_blocks + (tok0 + (lane << ta.bshift)) / a.bs);
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], parity)) && !aborted();
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], parity) && !aborted());
           if (!ok) break;
           if (lane < valid_chunks && (phys < 0 || (long long)phys >= a.num_blocks)) {
             raise_flag(a.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
         const uint32_t tmem_sp = tmem + Sh::s_col(sb) + lane_off;
         ok = mbar_wait_bounded(&s_full[sb], (kGroups == 2 ? tcnt : ring >> 1) & 1);
         ++tcnt;
-        if (!__all_sync(0xffffffffu, ok) || aborted()) {
+        if (!__all_sync(0xffffffffu, ok && !aborted())) {
           ok = false;
           break;
         }
@@ -936,7 +937,7 @@ __global__ void __launch_bounds__(CtShape<D>::kThreads, 1)
         ok = mbar_wait_bounded(&o_done[0], (ring0 + my_tiles - 1) & 1);
       }
       ++ig;
-      if (!__all_sync(0xffffffffu, ok) || aborted()) {
+      if (!__all_sync(0xffffffffu, ok && !aborted())) {
         ok = false;
         break;
       }
