@@ -101,6 +101,10 @@ typedef enum pkv_dtype {
                                             lists hold the first max_tokens, all else is done */
 #define PKV_FLAG_POSITION 0x800          /* pkv_rope_write: a kept token's position is outside
                                             [0, max_position); the token is skipped */
+#define PKV_FLAG_BEAM 0x2000             /* pkv_beam_reorder: a parent or a length that a beam cannot
+                                            have; the child is unused */
+#define PKV_FLAG_LOGITS 0x4000           /* pkv_beam_select: a beam with a NaN or +inf among its logits
+                                            or as its score; it proposes nothing */
 #define PKV_FLAG_APPEND_MISMATCH 0x40    /* pkv_write_decode_attention: a kept slot is not the
                                             slot of position context_lens[b] - 1 through
                                             block_tables (or context_lens[b] == 0); the token
@@ -566,6 +570,213 @@ PKV_API int pkv_chunk_plan(int B, int64_t total_q, int H, int num_kv_heads, int 
                            int block_size, int max_blocks, int max_q_len, int max_context_len,
                            int window, int has_prefix, int partition_size, pkv_dtype dt,
                            int *max_parts, int *kernel);
+
+/*
+ * A cache held in 8 or 4 bits.  Each row (one token's head_dim values of one
+ * KV head) is quantised by itself:
+ *   PKV_QUANT_INT8  code = rint(x * fl(127 / A)),    value = fl(A / 127) * code
+ *   PKV_QUANT_E4M3  code = e4m3(fl(x * fl(448 / A))), value = fl(A / 448) * code
+ *   PKV_QUANT_INT4  code = clamp(rint(x * inv) + zero, 0, 15), value = scale * (code - zero)
+ * with A the row's largest magnitude, fl() a rounding to float32, rint the
+ * nearest whole number (halves to even) of the exact product; for INT4
+ *   lo = min(x, 0), hi = max(x, 0), R = fl(hi - lo), scale = fl(R / 15),
+ *   inv = fl(15 / R), zero = rint(-lo * inv).
+ * A row with A (R) below 2^-100 is held as zeros (scale 0); one that is not
+ * finite, or whose R is not, has scale NaN and codes 0, so that everything
+ * read from it is NaN.
+ *   codes   [num_blocks, block_size, num_kv_heads, head_dim] bytes; INT4
+ *           head_dim / 2 bytes a row, the even element in the low half
+ *   params  float32 [num_blocks, num_kv_heads, block_size]: scale; INT4
+ *           [num_blocks, num_kv_heads, block_size, 2]: scale, zero.  A head's
+ *           numbers of one block lie together, as the decode reads them.
+ * Scales must not be negative.
+ */
+typedef enum pkv_quant_format {
+  PKV_QUANT_INT8 = 0,
+  PKV_QUANT_E4M3 = 1,
+  PKV_QUANT_INT4 = 2
+} pkv_quant_format;
+
+/*
+ * pkv_quant_write -- pkv_write into a quantised cache: k and v (fp32, bf16 or
+ * fp16; arguments as in pkv_write) are quantised row by row as they are
+ * written.  A negative slot is a padding token and is skipped; one past the
+ * pool raises PKV_FLAG_SLOT_OUT_OF_RANGE and is skipped.  Two kept tokens with
+ * the same slot race.
+ * Supported: head_dim <= 512, for INT4 even; any alignment of elements (codes:
+ * of bytes); 16-byte aligned rows are fastest.  The four written arrays
+ * overlap no other argument.  Errors: PKV_ERR_INVALID_ARG,
+ * PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.  num_tokens == 0 enqueues nothing.
+ */
+PKV_API pkv_status pkv_quant_write(void *k_codes, void *v_codes, float *k_params, float *v_params,
+                                   const void *k, const void *v, const int64_t *slot_mapping,
+                                   int64_t num_tokens, int64_t k_token_stride,
+                                   int64_t v_token_stride, int64_t num_blocks, int block_size,
+                                   int num_kv_heads, int head_dim, pkv_quant_format fmt,
+                                   pkv_dtype dt, int *err_flags, pkv_stream_t stream);
+
+/*
+ * pkv_quant_read -- the values of cached rows: token i of k_out and v_out
+ * [num_tokens, num_kv_heads, head_dim] (dtype dt, token strides in elements)
+ * gets the row at slot_mapping[i], computed in fp32 and rounded once.  For
+ * work that the decode below does not do: a prompt's chunk attends a context
+ * read back into 16-bit blocks, a sequence moves to another cache.  A
+ * negative slot leaves its rows as they were, one past the pool does too and
+ * raises PKV_FLAG_SLOT_OUT_OF_RANGE.  The same slot may come more than once.
+ * Sizes, alignment and errors as in pkv_quant_write; k_out and v_out overlap
+ * no other argument.
+ */
+PKV_API pkv_status pkv_quant_read(void *k_out, void *v_out, const void *k_codes,
+                                  const void *v_codes, const float *k_params,
+                                  const float *v_params, const int64_t *slot_mapping,
+                                  int64_t num_tokens, int64_t k_out_stride, int64_t v_out_stride,
+                                  int64_t num_blocks, int block_size, int num_kv_heads,
+                                  int head_dim, pkv_quant_format fmt, pkv_dtype dt, int *err_flags,
+                                  pkv_stream_t stream);
+
+/*
+ * pkv_quant_decode_attention -- pkv_decode_attention over a quantised cache:
+ * one new token per sequence, q and out [B, H, head_dim] in dtype dt,
+ *   x_j = scale * q . K_j,  x_j = softcap * tanh(x_j / softcap) if softcap > 0,
+ *   out = softmax(x) . V over the visible keys j < n = context_lens[b] and, if
+ *   window > 0, j >= n - window,
+ * with K and V the values that the codes stand for; nothing is rounded to 16
+ * bits on the way but, for bf16 and more than four query heads per KV head,
+ * the weights (fp16: half a step, 2^-11 of each).  Scores, statistics and sums
+ * are fp32.  An empty context gives zeros.
+ *   block_tables, context_lens, max_context_len as in pkv_decode_attention
+ *   (the same flags; a context over the table is clamped)
+ *   partition_size  0 = automatic, else a positive multiple of 128: keys per
+ *                 part of the split over the context (raised where it would
+ *                 give more than 256 parts)
+ *   workspace     pkv_quant_decode_workspace_size(...) bytes, 256-byte
+ *                 aligned, zero-filled before its first use; every call leaves
+ *                 it ready for the next on the same stream.  Calls that may
+ *                 overlap need workspaces of their own (two captured graphs
+ *                 that share one must not replay at the same time).
+ * Rows no query sees may hold anything; they are not read, nor are table
+ * entries of blocks that hold only such rows.  A table entry outside
+ * [0, num_blocks) raises PKV_FLAG_BLOCK_OUT_OF_RANGE, that sequence's output is
+ * unspecified.  A visible row whose scale is NaN makes its KV head's outputs
+ * NaN.  out and the workspace overlap no other argument.
+ * Supported: head_dim <= 512, for INT4 even; any block size and alignment of
+ * elements.  16-byte aligned codes (INT4: parameters 8-byte aligned) with
+ * head_dim 64, 80, 96, 128, 192 or 256 (INT4: not 80) run a tensor-core
+ * kernel, everything else the CUDA cores.  Errors: PKV_ERR_INVALID_ARG (also a
+ * scale that is not finite, a softcap that is negative, not finite or too
+ * small for scale / softcap), PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE,
+ * PKV_ERR_CUDA.  B == 0 enqueues nothing.
+ */
+PKV_API pkv_status pkv_quant_decode_attention(
+    void *out, const void *q, const void *k_codes, const void *v_codes, const float *k_params,
+    const float *v_params, const int32_t *block_tables, const int32_t *context_lens, int B, int H,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks, int64_t num_blocks, float scale,
+    float softcap, int window, pkv_quant_format fmt, pkv_dtype dt, int max_context_len,
+    int partition_size, void *workspace, size_t workspace_bytes, int *err_flags,
+    pkv_stream_t stream);
+
+/*
+ * pkv_quant_decode_workspace_size -- bytes of workspace
+ * pkv_quant_decode_attention needs for these sizes, for every format, dtype
+ * and window (host only).  Returns 0 for invalid sizes.
+ */
+PKV_API size_t pkv_quant_decode_workspace_size(int B, int H, int num_kv_heads, int head_dim,
+                                               int block_size, int max_blocks, int max_context_len,
+                                               int partition_size);
+
+/*
+ * pkv_beam_select -- one step of beam search: the K best continuations of each
+ * request over its W beams and the vocabulary.  Beam w of request b has the
+ * score c = scores[b, w] (its log-probability so far; -inf: the beam is not in
+ * use) and proposes
+ *   every token v with the score c + x_v - log sum_u exp(x_u), x its row of
+ *   logits (a logit of -inf is no proposal), or,
+ *   where finished[b, w] is not 0, itself: end_token with the score c.
+ * Taken are the K best by score; of equal ones the lowest beam, then the lowest
+ * token.  The order is that of the scores in 64 bits (a beam's own proposals
+ * go by their logits), the sum behind the logarithm is accurate to some 1e-7.
+ *   scores_out    [B, K] float32; -inf where fewer than K were proposed
+ *   parents       [B, K] int32: the beam that each one continues, -1 there
+ *   tokens        [B, K] int32: the token it adds, -1 there
+ *   finished_out  [B, K] uint8: 1 where the parent was finished or the token
+ *                 is end_token; 0 there
+ *   logits        [B, W, V] of dtype dt; beam row r = b * W + w at element
+ *                 r * row_stride; rows of finished and unused beams are not read
+ *   finished      [B, W] uint8 or NULL (none is)
+ *   end_token     the token that ends a sequence, or -1
+ * A beam whose logits hold a NaN or +inf, or whose score is NaN or +inf,
+ * raises PKV_FLAG_LOGITS and proposes nothing.
+ *   workspace     pkv_beam_select_workspace_size(...) bytes, 256-byte aligned,
+ *                 zero-filled before its first use; every call leaves it ready
+ *                 for the next of any sizes on the same stream.  Calls that may
+ *                 overlap need workspaces of their own.
+ * scores_out may be scores and finished_out finished where K == W; no other
+ * written array overlaps another argument.  Supported: W, K <= 32, B <= 16384,
+ * V <= 2^21, any alignment of elements (rows that are 16-byte aligned are
+ * fastest).  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED,
+ * PKV_ERR_WORKSPACE, PKV_ERR_CUDA.  B == 0 enqueues nothing.
+ */
+PKV_API pkv_status pkv_beam_select(float *scores_out, int32_t *parents, int32_t *tokens,
+                                   uint8_t *finished_out, const void *logits, const float *scores,
+                                   const uint8_t *finished, int B, int W, int K, int64_t V,
+                                   int64_t row_stride, int end_token, pkv_dtype dt,
+                                   void *workspace, size_t workspace_bytes, int *err_flags,
+                                   pkv_stream_t stream);
+
+/* Bytes of workspace pkv_beam_select needs for these sizes, for every dtype
+ * (host only); 0 for invalid sizes. */
+PKV_API size_t pkv_beam_select_workspace_size(int B, int W, int K, int64_t V);
+
+/*
+ * pkv_beam_reorder -- the paged cache follows the beams that were chosen:
+ * child k of request b continues beam parents[b, k] (-1: none).  Full blocks
+ * are shared by naming them in both tables; a last block that is not full goes
+ * to the first child that has it, and every other one gets a block of the
+ * request's own and a copy of its rows, so that no two beams ever write the
+ * same block.
+ *   tables        [B, W, max_blocks] int32: the beams' block tables
+ *   lens          [B, W] int32: their tokens in the cache
+ *   parents       [B, K] int32, as from pkv_beam_select
+ *   owned         [B, K, max_blocks] int32: for every column behind the
+ *                 prompt's full blocks K blocks that are this request's alone,
+ *                 reserved when it was admitted (the prompt's last block, if
+ *                 not full, may be one of them)
+ *   finished      [B, K] uint8 or NULL: children that get no further token
+ *   tables_out    [B, K, max_blocks] int32
+ *   lens_out      [B, K] int32: lens with the next token counted
+ *   slots         [B, K] int64: the next token's slot, for the write; -1 for
+ *                 finished and unused children, whose length stays
+ * With n a child's length and c = n / block_size: columns before c are its
+ * parent's; column c is its parent's block if n is not a multiple of
+ * block_size and no child before it continues in that block and no other child
+ * holds it whole; else, children in order, owned[b, k, c] or, where that is in
+ * use in this column, the first of owned[b, :, c] that is not, with the
+ * n % block_size rows copied; columns behind c are owned[b, k].
+ *   num_pools     caches to copy in, 0 .. 256: K and V of every layer, quantised
+ *                 ones with their parameters
+ *   pools         HOST array of device pointers, each to num_blocks blocks
+ *   block_bytes   HOST array: bytes of a block of each
+ *   row_bytes     HOST array: bytes of one token where a block is its tokens'
+ *                 rows one after the other, or 0: the block is copied whole
+ *                 (quantisation parameters)
+ * A parent outside [-1, W) or a length outside [0, max_blocks * block_size]
+ * raises PKV_FLAG_BEAM, the child is then unused; a child without room for a
+ * token raises PKV_FLAG_CONTEXT_TOO_LONG (slot -1, length unchanged); a
+ * block outside [0, num_blocks) where one is written or copied raises
+ * PKV_FLAG_BLOCK_OUT_OF_RANGE, and no block left PKV_FLAG_OUT_OF_BLOCKS: in
+ * both cases the child's slot is -1, its length stays and nothing is copied
+ * for it.
+ * No written array overlaps another argument, nor pools one another.
+ * Supported: W, K <= 32, B <= 16384.  Errors: PKV_ERR_INVALID_ARG,
+ * PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.  B == 0 enqueues nothing.
+ */
+PKV_API pkv_status pkv_beam_reorder(int32_t *tables_out, int32_t *lens_out, int64_t *slots,
+                                    const int32_t *tables, const int32_t *lens,
+                                    const int32_t *parents, const int32_t *owned,
+                                    const uint8_t *finished, int B, int W, int K, int max_blocks,
+                                    int64_t num_blocks, int block_size, int num_pools,
+                                    void *const *pools, const int64_t *block_bytes,
+                                    const int64_t *row_bytes, int *err_flags, pkv_stream_t stream);
 
 /*
  * The layout experiment: vLLM's packed cache layout, which the interview

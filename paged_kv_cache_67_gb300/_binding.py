@@ -36,6 +36,8 @@ FLAG_STEP_INVALID = 0x200
 FLAG_OUT_OF_BLOCKS = 0x400
 FLAG_POSITION = 0x800
 FLAG_TOKENS_OVER = 0x1000
+FLAG_BEAM = 0x2000
+FLAG_LOGITS = 0x4000
 
 _lock = threading.Lock()
 _lib = None
@@ -105,6 +107,21 @@ def load_library():
         lib.pkv_chunk_workspace_size.restype = c_size
         lib.pkv_chunk_plan.argtypes = [c_int, i64] + [c_int] * 11 + [ctypes.POINTER(c_int)] * 2
         lib.pkv_chunk_plan.restype = c_int
+        lib.pkv_quant_write.argtypes = [vp] * 7 + [i64] * 4 + [c_int] * 5 + [vp, vp]
+        lib.pkv_quant_write.restype = c_int
+        lib.pkv_quant_read.argtypes = lib.pkv_quant_write.argtypes
+        lib.pkv_quant_read.restype = c_int
+        lib.pkv_quant_decode_attention.argtypes = [vp] * 8 + [c_int] * 6 + [i64, c_float, c_float] + [c_int] * 5 + [
+            vp, c_size, vp, vp]
+        lib.pkv_quant_decode_attention.restype = c_int
+        lib.pkv_quant_decode_workspace_size.argtypes = [c_int] * 8
+        lib.pkv_quant_decode_workspace_size.restype = c_size
+        lib.pkv_beam_select.argtypes = [vp] * 7 + [c_int] * 3 + [i64, i64, c_int, c_int, vp, c_size, vp, vp]
+        lib.pkv_beam_select.restype = c_int
+        lib.pkv_beam_select_workspace_size.argtypes = [c_int] * 3 + [i64]
+        lib.pkv_beam_select_workspace_size.restype = c_size
+        lib.pkv_beam_reorder.argtypes = [vp] * 8 + [c_int] * 4 + [i64, c_int, c_int] + [vp] * 5
+        lib.pkv_beam_reorder.restype = c_int
         P = ctypes.POINTER
         lib.pkv_bm_create.argtypes = [i64, c_int, c_int, P(vp)]
         lib.pkv_bm_create.restype = c_int
@@ -772,6 +789,296 @@ def prepare_chunk_attention(out, q, k_cache, v_cache, block_tables, cu_seqlens_q
                                 window, slopes, prefix_lens, kv_starts, max_q_len, max_context_len, partition_size,
                                 workspace, err_flags, stream)
     return PreparedCall(lib.pkv_chunk_attention, args, "pkv_chunk_attention", keep, dev)
+
+
+# ------------------------------------------------------------ quantised cache
+
+PKV_QUANT_INT8, PKV_QUANT_E4M3, PKV_QUANT_INT4 = 0, 1, 2
+_QUANT = {torch.int8: PKV_QUANT_INT8, torch.float8_e4m3fn: PKV_QUANT_E4M3, torch.uint8: PKV_QUANT_INT4}
+
+
+def _quant_cache(k_codes, v_codes, k_params, v_params):
+    """(num_blocks, block_size, KVH, D, format) of a quantised cache: codes
+    int8, float8_e4m3fn or (4 bits, two a byte) uint8."""
+    _require(k_codes.dim() == 4 and v_codes.shape == k_codes.shape and k_codes.dtype == v_codes.dtype
+             and k_codes.dtype in _QUANT,
+             "codes must be int8, float8_e4m3fn [nb, bs, KVH, D] or uint8 [nb, bs, KVH, D / 2]")
+    nb, bs, kvh, d = k_codes.shape
+    fmt = _QUANT[k_codes.dtype]
+    shape = (nb, kvh, bs) + ((2,) if fmt == PKV_QUANT_INT4 else ())
+    for t in (k_params, v_params):
+        _require(t.dtype == torch.float32 and tuple(t.shape) == shape,
+                 "params must be float32 [nb, KVH, bs] (4 bits: [nb, KVH, bs, 2])")
+    for t in (k_codes, v_codes, k_params, v_params):
+        _require(t.is_contiguous(), "codes and params must be contiguous")
+    return nb, bs, kvh, 2 * d if fmt == PKV_QUANT_INT4 else d, fmt
+
+
+def _quant_rows_args(dense, codes_and_params, slot_mapping, err_flags, stream, read):
+    nb, bs, kvh, d, fmt = _quant_cache(*codes_and_params)
+    k, v = dense
+    _require(k.dim() == 3 and v.shape == k.shape and tuple(k.shape[1:]) == (kvh, d), "rows must be [T, KVH, D]")
+    _require(k.dtype == v.dtype and k.dtype in _DT, "dtype mismatch")
+    T = k.shape[0]
+    for t in dense:
+        _require(t.stride(2) == 1 and t.stride(1) == d, "each token's heads must be contiguous")
+    _require(slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.shape == (T,),
+             "slot_mapping must be contiguous int64 [T]")
+    tensors = tuple(codes_and_params) + tuple(dense) + (slot_mapping,)
+    dev = k.device
+    _require(dev.type == "cuda" and all(t.device == dev for t in tensors),
+             "all tensors must be on the same CUDA device")
+    _flags_ok(err_flags, dev)
+    row = kvh * d
+    first = tuple(_ptr(t) for t in ((*dense, *codes_and_params) if read else (*codes_and_params, *dense)))
+    args = first + (_ptr(slot_mapping), T, k.stride(0) if T > 1 else row, v.stride(0) if T > 1 else row, nb, bs, kvh,
+                    d, fmt, _DT[k.dtype], _ptr(err_flags), _stream_handle(stream, dev))
+    return args, tensors + (err_flags,), dev
+
+
+def pkv_quant_write(k_codes, v_codes, k_params, v_params, k, v, slot_mapping, err_flags=None, stream=None) -> None:
+    """Quantise k and v [T, KVH, D] row by row into the paged cache at
+    slot_mapping [T] (negative = padding, skipped).  The codes' type names the
+    format: int8 and float8_e4m3fn [nb, bs, KVH, D] with float32 scales
+    [nb, KVH, bs], or uint8 [nb, bs, KVH, D / 2] (4 bits) with scales and zero
+    points [nb, KVH, bs, 2]."""
+    lib = load_library()
+    args, _, dev = _quant_rows_args((k, v), (k_codes, v_codes, k_params, v_params), slot_mapping, err_flags, stream,
+                                    False)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_quant_write(*args), "pkv_quant_write")
+
+
+def prepare_quant_write(k_codes, v_codes, k_params, v_params, k, v, slot_mapping, err_flags=None,
+                        stream=None) -> PreparedCall:
+    """pkv_quant_write, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _quant_rows_args((k, v), (k_codes, v_codes, k_params, v_params), slot_mapping, err_flags,
+                                       stream, False)
+    return PreparedCall(lib.pkv_quant_write, args, "pkv_quant_write", keep, dev)
+
+
+def pkv_quant_read(k_out, v_out, k_codes, v_codes, k_params, v_params, slot_mapping, err_flags=None, stream=None):
+    """The values of the cached rows at slot_mapping [T] into k_out and v_out
+    [T, KVH, D] (returned); rows of negative slots stay as they were."""
+    lib = load_library()
+    args, _, dev = _quant_rows_args((k_out, v_out), (k_codes, v_codes, k_params, v_params), slot_mapping, err_flags,
+                                    stream, True)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_quant_read(*args), "pkv_quant_read")
+    return k_out, v_out
+
+
+def prepare_quant_read(k_out, v_out, k_codes, v_codes, k_params, v_params, slot_mapping, err_flags=None,
+                       stream=None) -> PreparedCall:
+    """pkv_quant_read, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _quant_rows_args((k_out, v_out), (k_codes, v_codes, k_params, v_params), slot_mapping,
+                                       err_flags, stream, True)
+    return PreparedCall(lib.pkv_quant_read, args, "pkv_quant_read", keep, dev)
+
+
+def pkv_quant_decode_workspace_size(B, H, num_kv_heads, head_dim, block_size, max_blocks, max_context_len=0,
+                                    partition_size=0) -> int:
+    return int(load_library().pkv_quant_decode_workspace_size(B, H, num_kv_heads, head_dim, block_size, max_blocks,
+                                                              max_context_len, partition_size))
+
+
+class QuantDecodeWorkspace:
+    """A zero-filled device workspace sized for pkv_quant_decode_attention."""
+
+    def __init__(self, B, H, num_kv_heads, head_dim, block_size, max_blocks, max_context_len=0, partition_size=0,
+                 device="cuda"):
+        self.nbytes = pkv_quant_decode_workspace_size(B, H, num_kv_heads, head_dim, block_size, max_blocks,
+                                                      max_context_len, partition_size)
+        self.buffer = torch.zeros(max(self.nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _quant_decode_args(out, q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, scale, softcap,
+                       window, max_context_len, partition_size, workspace, err_flags, stream):
+    nb, bs, kvh, d, fmt = _quant_cache(k_codes, v_codes, k_params, v_params)
+    _require(q.dim() == 3 and out.shape == q.shape and q.shape[2] == d, "q and out must be [B, H, D]")
+    B, H, _ = q.shape
+    _require(q.dtype == out.dtype and q.dtype in _DT, "dtype mismatch")
+    _require(context_lens.dtype == torch.int32 and context_lens.shape == (B,), "context_lens must be int32 [B]")
+    _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == B,
+             "block_tables must be int32 [B, max_blocks]")
+    buf = workspace.buffer if isinstance(workspace, QuantDecodeWorkspace) else workspace
+    tensors = tuple(t for t in (out, q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, buf)
+                    if t is not None)
+    for t in tensors:
+        _require(t.is_contiguous(), "tensors must be contiguous")
+    dev = q.device
+    _require(dev.type == "cuda" and all(t.device == dev for t in tensors),
+             "all tensors must be on the same CUDA device")
+    _flags_ok(err_flags, dev)
+    args = (_ptr(out), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), _ptr(block_tables),
+            _ptr(context_lens), B, H, kvh, d, bs, block_tables.shape[1], nb, float(scale), float(softcap),
+            int(window), fmt, _DT[q.dtype], int(max_context_len), int(partition_size), _ptr(buf),
+            0 if buf is None else buf.numel() * buf.element_size(), _ptr(err_flags), _stream_handle(stream, dev))
+    return args, tensors + (err_flags,), dev
+
+
+def pkv_quant_decode_attention(out, q, k_codes, v_codes, k_params, v_params, block_tables, context_lens,
+                               scale: float, softcap: float = 0.0, window: int = 0, max_context_len: int = 0,
+                               partition_size: int = 0, workspace=None, err_flags=None, stream=None):
+    """Decode attention of q [B, H, D] over a quantised paged cache (see
+    pkv_quant_write) into ``out`` (returned), with capped scores (``softcap``)
+    or a sliding ``window``.  An empty context gives zeros."""
+    lib = load_library()
+    args, _, dev = _quant_decode_args(out, q, k_codes, v_codes, k_params, v_params, block_tables, context_lens,
+                                      scale, softcap, window, max_context_len, partition_size, workspace, err_flags,
+                                      stream)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_quant_decode_attention(*args), "pkv_quant_decode_attention")
+    return out
+
+
+def prepare_quant_decode_attention(out, q, k_codes, v_codes, k_params, v_params, block_tables, context_lens,
+                                   scale: float, softcap: float = 0.0, window: int = 0, max_context_len: int = 0,
+                                   partition_size: int = 0, workspace=None, err_flags=None,
+                                   stream=None) -> PreparedCall:
+    """pkv_quant_decode_attention, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _quant_decode_args(out, q, k_codes, v_codes, k_params, v_params, block_tables, context_lens,
+                                       scale, softcap, window, max_context_len, partition_size, workspace, err_flags,
+                                       stream)
+    return PreparedCall(lib.pkv_quant_decode_attention, args, "pkv_quant_decode_attention", keep, dev)
+
+
+# ---------------------------------------------------------------- beam search
+
+def pkv_beam_select_workspace_size(B, W, K, V) -> int:
+    return int(load_library().pkv_beam_select_workspace_size(B, W, K, V))
+
+
+class BeamSelectWorkspace:
+    """A zero-filled device workspace sized for pkv_beam_select."""
+
+    def __init__(self, B, W, K, V, device="cuda"):
+        self.nbytes = pkv_beam_select_workspace_size(B, W, K, V)
+        self.buffer = torch.zeros(max(self.nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _bytes_ok(t, shape, name):
+    _require(t is None or (t.dtype in (torch.uint8, torch.bool) and tuple(t.shape) == shape),
+             f"{name} must be uint8 or bool {list(shape)}")
+
+
+def _beam_select_args(scores_out, parents, tokens, finished_out, logits, scores, finished, end_token, workspace,
+                      err_flags, stream):
+    _require(logits.dim() == 3 and logits.dtype in _DT, "logits must be [B, W, V]")
+    B, W, V = logits.shape
+    K = parents.shape[-1]
+    stride = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
+    _require((V <= 1 or logits.stride(2) == 1) and (B <= 1 or logits.stride(0) == W * stride),
+             "logits rows must be contiguous and evenly spaced")
+    _require(scores.dtype == torch.float32 and scores.shape == (B, W), "scores must be float32 [B, W]")
+    _require(scores_out.dtype == torch.float32 and scores_out.shape == (B, K), "scores_out must be float32 [B, K]")
+    for t, name in ((parents, "parents"), (tokens, "tokens")):
+        _require(t.dtype == torch.int32 and t.shape == (B, K), f"{name} must be int32 [B, K]")
+    _bytes_ok(finished, (B, W), "finished")
+    _require(finished_out is not None, "finished_out is needed")
+    _bytes_ok(finished_out, (B, K), "finished_out")
+    buf = workspace.buffer if isinstance(workspace, BeamSelectWorkspace) else workspace
+    tensors = tuple(t for t in (scores_out, parents, tokens, finished_out, scores, finished, buf) if t is not None)
+    for t in tensors:
+        _require(t.is_contiguous(), "tensors must be contiguous")
+    dev = logits.device
+    _require(dev.type == "cuda" and all(t.device == dev for t in tensors),
+             "all tensors must be on the same CUDA device")
+    _flags_ok(err_flags, dev)
+    args = (_ptr(scores_out), _ptr(parents), _ptr(tokens), _ptr(finished_out), _ptr(logits), _ptr(scores),
+            _ptr(finished), B, W, K, V, stride, int(end_token), _DT[logits.dtype], _ptr(buf),
+            0 if buf is None else buf.numel() * buf.element_size(), _ptr(err_flags), _stream_handle(stream, dev))
+    return args, tensors + (logits, err_flags), dev
+
+
+def pkv_beam_select(scores_out, parents, tokens, finished_out, logits, scores, finished=None, end_token: int = -1,
+                    workspace=None, err_flags=None, stream=None) -> None:
+    """The K best continuations of each request over its beams and the
+    vocabulary: logits [B, W, V], the beams' scores [B, W] (-inf: not in use)
+    and which have ended (``finished`` [B, W]) in; scores_out, parents, tokens
+    and finished_out [B, K] out, best first."""
+    lib = load_library()
+    args, _, dev = _beam_select_args(scores_out, parents, tokens, finished_out, logits, scores, finished, end_token,
+                                     workspace, err_flags, stream)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_beam_select(*args), "pkv_beam_select")
+
+
+def prepare_beam_select(scores_out, parents, tokens, finished_out, logits, scores, finished=None,
+                        end_token: int = -1, workspace=None, err_flags=None, stream=None) -> PreparedCall:
+    """pkv_beam_select, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _beam_select_args(scores_out, parents, tokens, finished_out, logits, scores, finished,
+                                      end_token, workspace, err_flags, stream)
+    return PreparedCall(lib.pkv_beam_select, args, "pkv_beam_select", keep, dev)
+
+
+def _beam_reorder_args(tables_out, lens_out, slots, tables, lens, parents, owned, block_size, num_blocks, pools,
+                       block_pools, finished, err_flags, stream):
+    i32 = torch.int32
+    _require(tables.dim() == 3 and tables.dtype == i32, "tables must be int32 [B, W, max_blocks]")
+    B, W, MB = tables.shape
+    _require(parents.dim() == 2 and parents.dtype == i32 and parents.shape[0] == B, "parents must be int32 [B, K]")
+    K = parents.shape[1]
+    _require(lens.dtype == i32 and lens.shape == (B, W), "lens must be int32 [B, W]")
+    _require(lens_out.dtype == i32 and lens_out.shape == (B, K), "lens_out must be int32 [B, K]")
+    _require(slots.dtype == torch.int64 and slots.shape == (B, K), "slots must be int64 [B, K]")
+    for t, name in ((tables_out, "tables_out"), (owned, "owned")):
+        _require(t.dtype == i32 and t.shape == (B, K, MB), f"{name} must be int32 [B, K, max_blocks]")
+    _bytes_ok(finished, (B, K), "finished")
+    pools, block_pools = list(pools), list(block_pools)
+    every = pools + block_pools
+    if num_blocks is None:
+        _require(len(every) > 0, "num_blocks is needed where there are no pools")
+        num_blocks = every[0].shape[0]
+    for t in pools:
+        _require(t.dim() >= 2 and t.shape[0] == num_blocks and t.shape[1] == block_size,
+                 "pools must be [num_blocks, block_size, ...]")
+    for t in block_pools:
+        _require(t.dim() >= 1 and t.shape[0] == num_blocks, "block_pools must be [num_blocks, ...]")
+    tensors = tuple(t for t in (tables_out, lens_out, slots, tables, lens, parents, owned, finished) if t is not None)
+    for t in tensors + tuple(every):
+        _require(t.is_contiguous(), "tensors must be contiguous")
+    dev = tables.device
+    _require(dev.type == "cuda" and all(t.device == dev for t in tensors + tuple(every)),
+             "all tensors must be on the same CUDA device")
+    _flags_ok(err_flags, dev)
+    n = len(every)
+    block = [t.numel() // max(1, num_blocks) * t.element_size() for t in every]
+    rows = [b // block_size for b in block[:len(pools)]] + [0] * len(block_pools)
+    host = ((ctypes.c_void_p * max(1, n))(*[t.data_ptr() for t in every]),
+            (ctypes.c_int64 * max(1, n))(*block), (ctypes.c_int64 * max(1, n))(*rows))
+    args = tuple(_ptr(t) for t in (tables_out, lens_out, slots, tables, lens, parents, owned, finished)) + (
+        B, W, K, MB, int(num_blocks), int(block_size), n) + tuple(
+        ctypes.cast(h, ctypes.c_void_p) for h in host) + (_ptr(err_flags), _stream_handle(stream, dev))
+    return args, tensors + tuple(every) + (host, err_flags), dev
+
+
+def pkv_beam_reorder(tables_out, lens_out, slots, tables, lens, parents, owned, block_size: int, num_blocks=None,
+                     pools=(), block_pools=(), finished=None, err_flags=None, stream=None) -> None:
+    """Block tables [B, K, max_blocks], lengths and next slots of the children
+    that ``parents`` [B, K] chose from ``tables`` [B, W, max_blocks] and
+    ``lens`` [B, W], with the last blocks that two of them would share copied
+    into blocks of ``owned`` [B, K, max_blocks] in every cache of ``pools``
+    ([num_blocks, block_size, ...]: a token's rows in order) and
+    ``block_pools`` ([num_blocks, ...]: copied whole, quantisation parameters)."""
+    lib = load_library()
+    args, _, dev = _beam_reorder_args(tables_out, lens_out, slots, tables, lens, parents, owned, block_size,
+                                      num_blocks, pools, block_pools, finished, err_flags, stream)
+    with torch.cuda.device(dev):
+        _check(lib.pkv_beam_reorder(*args), "pkv_beam_reorder")
+
+
+def prepare_beam_reorder(tables_out, lens_out, slots, tables, lens, parents, owned, block_size: int, num_blocks=None,
+                         pools=(), block_pools=(), finished=None, err_flags=None, stream=None) -> PreparedCall:
+    """pkv_beam_reorder, checked and marshalled once (see PreparedCall)."""
+    lib = load_library()
+    args, keep, dev = _beam_reorder_args(tables_out, lens_out, slots, tables, lens, parents, owned, block_size,
+                                       num_blocks, pools, block_pools, finished, err_flags, stream)
+    return PreparedCall(lib.pkv_beam_reorder, args, "pkv_beam_reorder", keep, dev)
 
 
 PKV_ERR_OUT_OF_BLOCKS = 5

@@ -1,0 +1,483 @@
+// pkv_beam_select.cu -- one step of beam search: the K best of W beams x V
+// tokens by c_w + x_wv - log sum exp x_w.
+//
+// Within a beam the order is that of its logits, so a row can be cut into
+// pieces that each give their K largest logits and a share of the sum, in one
+// pass over the row.  A CTA holds its piece in registers:
+//   1. load; maximum m of the piece, sum of 2^((x - m) log2 e);
+//   2. a bound: in a warp the K-th largest of the lanes' maxima has K elements
+//      at or above it, so the largest such bound of the 8 warps has, too;
+//   3. the elements at or above the bound (K, and few more) go to shared memory
+//      as 64-bit keys -- the logit's bits in their order, then the lowest token --
+//      and each counts the keys above its own: its rank.
+// The CTA that finishes a request's last piece joins: a warp a beam merges the
+// pieces' sorted keys (lane = piece, K rounds of a warp-wide maximum) and adds
+// up the sums in 64 bits; one warp then merges the beams' lists by score in 64
+// bits (lane = beam).  Memory bounds the call: every logit is read once.
+//
+// Which token comes first must not hang on where a row starts in memory: beams
+// with equal logits have to tie.  So thread t of piece i takes the same
+// elements of every row, and rows that are not 16-byte aligned are read by
+// aligned granules, two for one, and shifted.
+#include <type_traits>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+constexpr int kBsThreads = 256;
+constexpr int kBsWarps = kBsThreads / 32;
+constexpr int kBsMost = 32;              // beams, continuations
+constexpr int kBsKeys = 512;             // keys of a piece that are ranked by counting
+constexpr int kBsParts = 256;            // pieces of a row
+constexpr int kBsSms = 152;              // of the one GPU this library is built for (speed alone)
+constexpr long long kBsMaxV = 1LL << 21;
+constexpr int kBsMaxB = 16384;
+
+struct BeamSelectArgs {
+  float *scores_out;
+  int32_t *parents, *tokens;
+  uint8_t *finished_out;
+  const char *logits;
+  const float *scores;
+  const uint8_t *finished;
+  int *err;
+  int *cnt;                              // [B] finished pieces
+  unsigned long long *keys;              // [B * W][parts][K]
+  double *sums;                          // [B * W][parts]
+  float *maxima;                         // [B * W][parts]; NaN: not a number among them
+  long long V, stride;
+  int W, K, parts, end;
+};
+
+// The bits of x in the order of its values (-0 as 0).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+// Larger: the larger logit, of equal ones the lower token.  0: none.
+__device__ __forceinline__ unsigned long long beam_key(float x, uint32_t v) {
+  return ((unsigned long long)ordered(x) << 32) | (0xffffffffu - v);
+}
+
+// Whether a beam's row is to be read.
+__device__ __forceinline__ bool beam_live(const BeamSelectArgs &a, long long row) {
+  if (a.finished && __ldg(a.finished + row)) return false;
+  const float c = __ldg(a.scores + row);
+  return c > -INFINITY && c < INFINITY;  // (NaN and +inf are flagged where the request is joined)
+}
+
+// 16 bytes of a row from byte `at` on (a multiple of 16, counted from the
+// row's start), whatever the row's alignment; 0 past its end.
+template <typename T>
+__device__ __forceinline__ uint4 row_granule(const char *row, long long at, long long bytes) {
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
+  if (off == 0 && at + 16 <= bytes) return __ldg(reinterpret_cast<const uint4 *>(row + at));
+  if (off != 0 && at >= 16 && at + 32 <= bytes) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(row + at - off);
+    const uint4 x = __ldg(p), y = __ldg(p + 1);
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    const uint32_t words = off >> 2;
+    if (words & 2)
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    if (words & 1)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    const uint32_t bits = (off & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+  }
+  // the row's ends, element by element
+  constexpr int kPer = 16 / sizeof(T);
+  union {
+    uint4 v;
+    uint16_t h[8];
+    uint32_t w[4];
+  } u;
+  u.v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const long long b = at + e * (long long)sizeof(T);
+    if (b >= bytes) continue;
+    if constexpr (sizeof(T) == 2)
+      u.h[e] = __ldg(reinterpret_cast<const unsigned short *>(row + b));
+    else
+      u.w[e] = __ldg(reinterpret_cast<const unsigned int *>(row + b));
+  }
+  return u.v;
+}
+
+template <typename T>
+__device__ __forceinline__ float granule_at(const uint4 &g, int e) {
+  const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+  const uint32_t h = e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(h << 16);
+  return __half2float(__ushort_as_half((unsigned short)h));
+}
+
+__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long y = __shfl_xor_sync(0xffffffffu, x, o);
+    x = y > x ? y : x;
+  }
+  return x;
+}
+
+// The request's K best from its pieces, by the whole CTA.
+__device__ void beam_join(const BeamSelectArgs &a, int b) {
+  __shared__ unsigned long long s_key[kBsMost][kBsMost];   // a beam's best, sorted
+  __shared__ double s_base[kBsMost];                       // c - log sum exp; finished beams: c
+  __shared__ int s_mode[kBsMost];                          // 0 no proposals, 1 its tokens, 2 itself
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.K, parts = a.parts;
+  for (int w = warp; w < a.W; w += kBsWarps) {
+    const long long row = (long long)b * a.W + w;
+    const float c = __ldg(a.scores + row);
+    const bool done = a.finished && __ldg(a.finished + row);
+    int mode = c > -INFINITY && c < INFINITY ? (done ? 2 : 1) : 0;
+    bool bad = !(c < INFINITY);
+    double base = c;
+    if (mode == 1) {
+      float m = -INFINITY;
+      bool nan = false;
+      for (int i = lane; i < parts; i += 32) {
+        const float x = __ldcg(a.maxima + row * parts + i);
+        nan = nan || !(x < INFINITY);
+        m = fmaxf(m, x);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      nan = __any_sync(0xffffffffu, nan);
+      double sum = 0.0;
+      if (m > -INFINITY)
+        for (int i = lane; i < parts; i += 32) {
+          const float x = __ldcg(a.maxima + row * parts + i);
+          if (x > -INFINITY) sum += __ldcg(a.sums + row * parts + i) * exp((double)x - (double)m);
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      bad = nan;
+      if (nan || m == -INFINITY) mode = 0;
+      base = (double)c - ((double)m + log(sum));
+    }
+    if (mode == 1) {
+      // lane = piece (32 apart): its next key not yet taken
+      const unsigned long long *keys = a.keys + row * parts * K;
+      unsigned long long head[kBsParts / 32];
+      uint32_t taken[kBsParts / 32];
+#pragma unroll
+      for (int j = 0; j < kBsParts / 32; ++j) {
+        const int i = lane + 32 * j;
+        taken[j] = 0;
+        head[j] = i < parts ? __ldcg(keys + (long long)i * K) : 0;
+      }
+      for (int k = 0; k < K; ++k) {
+        unsigned long long best = 0;
+#pragma unroll
+        for (int j = 0; j < kBsParts / 32; ++j) best = head[j] > best ? head[j] : best;
+        best = warp_max_u64(best);
+        if (lane == 0) s_key[w][k] = best;
+#pragma unroll
+        for (int j = 0; j < kBsParts / 32; ++j)
+          if (best != 0 && head[j] == best) {              // (keys differ: one lane has it)
+            ++taken[j];
+            head[j] = taken[j] < K ? __ldcg(keys + (long long)(lane + 32 * j) * K + taken[j]) : 0;
+          }
+      }
+    }
+    if (lane == 0) {
+      s_mode[w] = mode;
+      s_base[w] = base;
+      if (bad) raise_flag(a.err, PKV_FLAG_LOGITS);
+    }
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  // lane = beam: its best proposal not yet taken, -inf: none left
+  const int w = lane;
+  const int mode = w < a.W ? s_mode[w] : 0;
+  int at = 0;
+  auto head_score = [&]() {
+    if (mode == 2) return at == 0 ? s_base[w] : -INFINITY;
+    if (mode == 0 || at >= K || s_key[w][at] == 0) return (double)-INFINITY;
+    return s_base[w] + (double)from_ordered((uint32_t)(s_key[w][at] >> 32));
+  };
+  double head = head_score();
+  for (int k = 0; k < K; ++k) {
+    double best = head;
+    int from = lane;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double x = __shfl_xor_sync(0xffffffffu, best, o);
+      const int i = __shfl_xor_sync(0xffffffffu, from, o);
+      if (x > best || (x == best && i < from)) {
+        best = x;
+        from = i;
+      }
+    }
+    if (lane == from) {
+      const bool none = best == -INFINITY;
+      const int token = none ? -1 : mode == 2 ? a.end : (int)(0xffffffffu - (uint32_t)s_key[w][at]);
+      const long long out = (long long)b * K + k;
+      a.scores_out[out] = (float)best;
+      a.parents[out] = none ? -1 : w;
+      a.tokens[out] = token;
+      a.finished_out[out] = !none && (mode == 2 || token == a.end);
+      ++at;
+      head = head_score();
+    }
+    __syncwarp();
+  }
+}
+
+// GRANULES 16-byte granules a thread: a piece is kBsThreads * GRANULES of them.
+template <typename T, int GRANULES>
+__global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __grid_constant__ BeamSelectArgs a) {
+  constexpr int kPer = 16 / sizeof(T), E = GRANULES * kPer;
+  constexpr long long kPiece = (long long)kBsThreads * E;
+  __shared__ float s_f[kBsWarps];
+  __shared__ uint32_t s_u[kBsWarps];
+  __shared__ double s_d[kBsWarps];
+  __shared__ int s_n, s_last;
+  __shared__ unsigned long long s_keys[kBsKeys];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long row = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x - row * a.parts), b = (int)(row / a.W);
+  if (beam_live(a, row)) {
+    const char *base = a.logits + row * a.stride * (long long)sizeof(T);
+    const long long bytes = a.V * (long long)sizeof(T), first = part * kPiece;
+    uint4 g[GRANULES];
+#pragma unroll
+    for (int i = 0; i < GRANULES; ++i) {
+      const long long at = (first + (long long)(i * kBsThreads + tid) * kPer) * (long long)sizeof(T);
+      g[i] = at < bytes ? row_granule<T>(base, at, bytes) : make_uint4(0, 0, 0, 0);
+    }
+    auto token = [&](int i, int e) { return first + (long long)(i * kBsThreads + tid) * kPer + e; };
+    auto value = [&](int i, int e) { return token(i, e) < a.V ? granule_at<T>(g[i], e) : -INFINITY; };
+    if (tid == 0) s_n = 0;
+    // 1. maximum and sum
+    float m = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < GRANULES; ++i)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const float x = value(i, e);
+        nan = nan || !(x < INFINITY);                      // NaN, +inf
+        m = fmaxf(m, x);
+      }
+    const float mine = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // 2. the warp's bound: its lanes' maxima sorted downwards, the K-th
+    uint32_t u = ordered(mine);
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+      for (int o = size >> 1; o > 0; o >>= 1) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, u, o);
+        const bool up = ((lane & size) != 0) == ((lane & o) == 0);   // keep the smaller
+        u = up ? min(u, y) : max(u, y);
+      }
+    u = __shfl_sync(0xffffffffu, u, a.K - 1);
+    if (lane == 0) {
+      s_f[warp] = m;
+      s_u[warp] = u;
+    }
+    const bool any_nan = __syncthreads_or(nan);
+#pragma unroll
+    for (int k = 0; k < kBsWarps; ++k) {
+      m = fmaxf(m, s_f[k]);
+      u = max(u, s_u[k]);
+    }
+    float sum = 0.f;
+    if (m > -INFINITY)
+#pragma unroll
+      for (int i = 0; i < GRANULES; ++i)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) sum += fast_exp2((value(i, e) - m) * kLog2e);
+    double total = sum;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_d[warp] = total;
+    // 3. what is at or above the bound, -inf excepted
+    const float bound = from_ordered(u);
+    if (!any_nan && mine >= bound)
+#pragma unroll
+      for (int i = 0; i < GRANULES; ++i)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const float x = value(i, e);
+          if (x >= bound && x > -INFINITY) {
+            const int n = atomicAdd(&s_n, 1);
+            if (n < kBsKeys) s_keys[n] = beam_key(x, (uint32_t)token(i, e));
+          }
+        }
+    __syncthreads();
+    const int n = s_n;
+    const long long out = row * a.parts + part;
+    if (tid == 0) {
+      total = 0.0;
+      for (int k = 0; k < kBsWarps; ++k) total += s_d[k];
+      a.maxima[out] = any_nan ? __int_as_float(0x7fc00000) : m;
+      a.sums[out] = total;
+    }
+    unsigned long long *keys = a.keys + out * a.K;
+    if (n <= kBsKeys) {
+      for (int i = tid; i < n; i += kBsThreads) {
+        const unsigned long long key = s_keys[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += s_keys[j] > key;
+        if (rank < a.K) keys[rank] = key;
+      }
+      for (int i = n + tid; i < a.K; i += kBsThreads) keys[i] = 0;
+    } else {
+      // that many ties at the bound: one at a time, the largest key below the last
+      unsigned long long last = ~0ull;
+      for (int k = 0; k < a.K; ++k) {
+        unsigned long long best = 0;
+#pragma unroll
+        for (int i = 0; i < GRANULES; ++i)
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const float x = value(i, e);
+            const unsigned long long key = x > -INFINITY ? beam_key(x, (uint32_t)token(i, e)) : 0;
+            if (key < last && key > best) best = key;
+          }
+        best = warp_max_u64(best);
+        __syncthreads();
+        if (lane == 0) s_keys[warp] = best;
+        __syncthreads();
+        for (int j = 0; j < kBsWarps; ++j) best = s_keys[j] > best ? s_keys[j] : best;
+        if (tid == 0) keys[k] = best;
+        last = best;
+      }
+    }
+  }
+  // the request's last piece joins them
+  __syncthreads();
+  if (tid == 0) {
+    int prev;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                 : "=r"(prev)
+                 : "l"(reinterpret_cast<uint64_t>(a.cnt + b))
+                 : "memory");
+    s_last = prev == a.W * a.parts - 1;
+    if (s_last) a.cnt[b] = 0;                              // ready for the next call
+  }
+  __syncthreads();
+  if (s_last) beam_join(a, b);
+}
+
+struct BeamPlan {
+  int granules, parts;
+};
+// Pieces of 2 granules a thread where 8 would not give every SM two CTAs.
+static BeamPlan beam_plan(long long rows, long long V, int el) {
+  auto parts = [&](int granules) {
+    const long long piece = (long long)kBsThreads * granules * (16 / el);
+    return (V + piece - 1) / piece;
+  };
+  const int granules = rows * parts(8) >= 2 * kBsSms || parts(2) > kBsParts ? 8 : 2;
+  return {granules, (int)parts(granules)};
+}
+
+constexpr size_t kBsCntBytes = kBsMaxB * sizeof(int);
+static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+static size_t beam_ws_bytes(long long rows, int parts, int K) {
+  return kBsCntBytes + align256((size_t)rows * parts * K * sizeof(unsigned long long)) +
+         align256((size_t)rows * parts * sizeof(double)) + align256((size_t)rows * parts * sizeof(float));
+}
+static bool beam_sizes_ok(int B, int W, int K, int64_t V) { return B >= 0 && W > 0 && K > 0 && V > 0; }
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+PKV_API size_t pkv_beam_select_workspace_size(int B, int W, int K, int64_t V) {
+  if (!beam_sizes_ok(B, W, K, V) || W > kBsMost || K > kBsMost || V > kBsMaxV || B > kBsMaxB) return 0;
+  const long long rows = (long long)B * W;
+  const size_t a = beam_ws_bytes(rows, beam_plan(rows, V, 4).parts, K), b = beam_ws_bytes(rows, beam_plan(rows, V, 2).parts, K);
+  return a > b ? a : b;
+}
+
+PKV_API pkv_status pkv_beam_select(float *scores_out, int32_t *parents, int32_t *tokens, uint8_t *finished_out,
+                                   const void *logits, const float *scores, const uint8_t *finished, int B, int W,
+                                   int K, int64_t V, int64_t row_stride, int end_token, pkv_dtype dt, void *workspace,
+                                   size_t workspace_bytes, int *err_flags, pkv_stream_t stream) {
+  if (!beam_sizes_ok(B, W, K, V) || row_stride < V || end_token < -1 || end_token >= V ||
+      (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16))
+    return PKV_ERR_INVALID_ARG;
+  if (W > kBsMost || K > kBsMost || V > kBsMaxV || B > kBsMaxB) return PKV_ERR_UNSUPPORTED;
+  if (B == 0) return PKV_OK;
+  if (!scores_out || !parents || !tokens || !finished_out || !logits || !scores) return PKV_ERR_INVALID_ARG;
+  auto at = [](const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  const int el = dt == PKV_F32 ? 4 : 2;
+  if (!at(scores_out, 4) || !at(parents, 4) || !at(tokens, 4) || !at(scores, 4) || !at(err_flags, 4) || !at(logits, el))
+    return PKV_ERR_INVALID_ARG;
+  const long long rows = (long long)B * W;
+  const BeamPlan plan = beam_plan(rows, V, el);
+  const size_t need = beam_ws_bytes(rows, plan.parts, K);
+  if (!workspace || workspace_bytes < need || !at(workspace, 256)) return PKV_ERR_WORKSPACE;
+  const size_t outs = (size_t)B * K, ins = (size_t)rows;
+  const ArgRange written[] = {{scores_out, outs * 4}, {parents, outs * 4}, {tokens, outs * 4}, {finished_out, outs}, {workspace, need}};
+  const ArgRange read[] = {{scores, ins * 4}, {finished, ins}, {logits, (size_t)((rows - 1) * row_stride + V) * el}, {err_flags, 4}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      const bool same = K == W && ((i == 0 && j == 0 && scores_out == scores) || (i == 3 && j == 1 && finished_out == finished));
+      if (!same && overlap(written[i], read[j])) return PKV_ERR_INVALID_ARG;
+    }
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(written[i], written[j])) return PKV_ERR_INVALID_ARG;
+  }
+  if (rows * plan.parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  BeamSelectArgs a = {};
+  a.scores_out = scores_out;
+  a.parents = parents;
+  a.tokens = tokens;
+  a.finished_out = finished_out;
+  a.logits = static_cast<const char *>(logits);
+  a.scores = scores;
+  a.finished = finished;
+  a.err = err_flags;
+  char *ws = static_cast<char *>(workspace);
+  a.cnt = reinterpret_cast<int *>(ws);
+  ws += kBsCntBytes;
+  a.keys = reinterpret_cast<unsigned long long *>(ws);
+  ws += align256((size_t)rows * plan.parts * K * sizeof(unsigned long long));
+  a.sums = reinterpret_cast<double *>(ws);
+  ws += align256((size_t)rows * plan.parts * sizeof(double));
+  a.maxima = reinterpret_cast<float *>(ws);
+  a.V = V;
+  a.stride = row_stride;
+  a.W = W;
+  a.K = K;
+  a.parts = plan.parts;
+  a.end = end_token;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = (unsigned)(rows * plan.parts);
+  auto go = [&](auto type) {
+    using T = decltype(type);
+    if (plan.granules == 8)
+      pkv_beam_select_kernel<T, 8><<<grid, kBsThreads, 0, s>>>(a);
+    else
+      pkv_beam_select_kernel<T, 2><<<grid, kBsThreads, 0, s>>>(a);
+  };
+  if (dt == PKV_F32)
+    go(float());
+  else if (dt == PKV_BF16)
+    go(__nv_bfloat16());
+  else
+    go(__half());
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,335 @@
+// pkv_quant.cu -- new tokens quantised as they are written to a paged cache,
+// and cached rows read back as numbers.
+//
+// A row is one token's head_dim values of one KV head.  Its scale hangs on its
+// largest magnitude, so a row is held in registers between the two looks at
+// it: a group of L lanes (a power of two) takes the row of K and the row of V
+// of one (token, head), VEC elements a lane at a time, finds both extremes
+// with log2 L exchanges and writes the codes.  Every element is read once and
+// every code written once: memory bounds both kernels.
+#include "pkv_quant.cuh"
+
+namespace pkv {
+
+constexpr int kQuantThreads = 256;
+constexpr float kQuantTiny = 7.888609052210118e-31f;   // 2^-100
+
+struct QuantRowsArgs {
+  char *codes[2];          // k, v
+  float *params[2];
+  char *x[2];              // dense rows (written by the read kernel)
+  const int64_t *slots;
+  int *err;
+  long long T, stride[2], capacity;   // strides in elements
+  int bs, KVH, D, lanes, vecs;        // lanes of a group, vectors of a row
+};
+
+// 16 bytes, or (fewer) elements at their own alignment.
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC == 16 ? 16 : sizeof(T)) QuantVec {
+  T e[VEC];
+};
+template <int BYTES>
+struct __align__(BYTES) QuantBytes {
+  uint8_t b[BYTES];
+};
+
+template <int FMT, int VEC>
+struct QuantCodes {
+  static constexpr int kBytes = FMT == kInt4 ? VEC / 2 : VEC;
+  using Pack = QuantBytes<kBytes>;
+};
+
+// (token, head) of this lane's group; false past the last, for padding and for
+// slots past the pool.
+__device__ __forceinline__ bool quant_row(const QuantRowsArgs &a, long long &t, int &h, long long &slot, int &at) {
+  const int per_cta = kQuantThreads / a.lanes;
+  const long long row = (long long)blockIdx.x * per_cta + threadIdx.x / a.lanes;
+  at = threadIdx.x % a.lanes;
+  t = row / a.KVH;
+  h = (int)(row - t * a.KVH);
+  if (t >= a.T) return false;
+  slot = __ldg(a.slots + t);
+  if (slot < 0) return false;
+  if (slot >= a.capacity) {
+    if (h == 0 && at == 0) raise_flag(a.err, PKV_FLAG_SLOT_OUT_OF_RANGE);
+    return false;
+  }
+  return true;
+}
+
+template <typename T, int VEC, int NV, int FMT>
+__global__ void __launch_bounds__(kQuantThreads) pkv_quant_write_kernel(const __grid_constant__ QuantRowsArgs a) {
+  using V = QuantVec<T, VEC>;
+  using C = QuantCodes<FMT, VEC>;
+  long long t, slot;
+  int h, at;
+  const bool has = quant_row(a, t, h, slot, at);
+  V x[2][NV];
+  float lo[2], hi[2];
+  // both rows' loads before anything is looked at
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = at + i * a.lanes;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[s][i].e[e] = from_f32<T>(0.f);
+      if (has && v < a.vecs)
+        x[s][i] = *(reinterpret_cast<const V *>(reinterpret_cast<const T *>(a.x[s]) + t * a.stride[s] + (long long)h * a.D) + v);
+    }
+  bool finite[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    lo[s] = hi[s] = 0.f;
+    float sum = 0.f;                                   // 0 * x: NaN for what is not finite
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float f = to_f32<T>(x[s][i].e[e]);
+        lo[s] = fminf(lo[s], f);
+        hi[s] = fmaxf(hi[s], f);
+        sum = fmaf(f, 0.f, sum);
+      }
+    finite[s] = sum == 0.f;
+  }
+  for (int o = a.lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      lo[s] = fminf(lo[s], __shfl_xor_sync(0xffffffffu, lo[s], o));
+      hi[s] = fmaxf(hi[s], __shfl_xor_sync(0xffffffffu, hi[s], o));
+      finite[s] = __shfl_xor_sync(0xffffffffu, (int)finite[s], o) && finite[s];
+    }
+  }
+  if (!has) return;
+  constexpr float kTop = FMT == kInt8 ? 127.f : FMT == kE4m3 ? 448.f : 15.f;
+  const long long blk = slot / a.bs;
+  const int off = (int)(slot - blk * a.bs);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const float span = FMT == kInt4 ? hi[s] - lo[s] : fmaxf(hi[s], -lo[s]);
+    const bool ok = finite[s] && span <= 3.402823466e38f;
+    const bool fine = ok && span >= kQuantTiny;
+    const float inv = fine ? __fdiv_rn(kTop, span) : 0.f;
+    const float scale = fine ? __fdiv_rn(span, kTop) : ok ? 0.f : __int_as_float(0x7fc00000);
+    const int zero = FMT == kInt4 && fine ? rint_product(-lo[s], inv) : 0;
+    if (at == 0) {
+      float *p = a.params[s] + ((blk * a.KVH + h) * a.bs + off) * quant_params<FMT>();
+      if (FMT == kInt4)
+        p[0] = scale, p[1] = (float)zero;
+      else
+        p[0] = scale;
+    }
+    typename C::Pack *dst = reinterpret_cast<typename C::Pack *>(a.codes[s] + (slot * a.KVH + h) * quant_row_bytes<FMT>(a.D));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = at + i * a.lanes;
+      if (v >= a.vecs) continue;
+      typename C::Pack out;
+      float f[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        f[e] = to_f32<T>(x[s][i].e[e]);
+        if (!fine) f[e] = 0.f;                         // (an infinity times 0)
+      }
+      if constexpr (FMT == kInt8) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out.b[e] = (uint8_t)rint_product(f[e], inv);
+      } else if constexpr (FMT == kE4m3) {
+        if constexpr (VEC == 1) {
+          out.b[0] = (uint8_t)e4m3x2_from(f[0] * inv, 0.f);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) {
+            const uint32_t two = e4m3x2_from(f[e] * inv, f[e + 1] * inv);
+            out.b[e] = (uint8_t)two;
+            out.b[e + 1] = (uint8_t)(two >> 8);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          const int c0 = min(max(rint_product(f[e], inv) + zero, 0), 15);
+          const int c1 = min(max(rint_product(f[e + 1], inv) + zero, 0), 15);
+          out.b[e / 2] = (uint8_t)(c0 | (c1 << 4));
+        }
+      }
+      dst[v] = out;
+    }
+  }
+}
+
+template <typename T, int VEC, int NV, int FMT>
+__global__ void __launch_bounds__(kQuantThreads) pkv_quant_read_kernel(const __grid_constant__ QuantRowsArgs a) {
+  using V = QuantVec<T, VEC>;
+  using C = QuantCodes<FMT, VEC>;
+  long long t, slot;
+  int h, at;
+  if (!quant_row(a, t, h, slot, at)) return;
+  const long long blk = slot / a.bs;
+  const int off = (int)(slot - blk * a.bs);
+  typename C::Pack in[2][NV];
+  float scale[2], zero[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const float *p = a.params[s] + ((blk * a.KVH + h) * a.bs + off) * quant_params<FMT>();
+    scale[s] = __ldg(p);
+    zero[s] = FMT == kInt4 ? __ldg(p + 1) : 0.f;
+    const typename C::Pack *src =
+        reinterpret_cast<const typename C::Pack *>(a.codes[s] + (slot * a.KVH + h) * quant_row_bytes<FMT>(a.D));
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at + i * a.lanes < a.vecs) in[s][i] = src[at + i * a.lanes];
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    V *dst = reinterpret_cast<V *>(reinterpret_cast<T *>(a.x[s]) + t * a.stride[s] + (long long)h * a.D);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = at + i * a.lanes;
+      if (v >= a.vecs) continue;
+      V out;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float c;
+        if constexpr (FMT == kInt8)
+          c = (float)(int8_t)in[s][i].b[e];
+        else if constexpr (FMT == kE4m3)
+          c = half2_to_float2(e4m3x2_to_half2(in[s][i].b[e])).x;
+        else
+          c = (float)((in[s][i].b[e / 2] >> (e & 1 ? 4 : 0)) & 15) - zero[s];
+        out.e[e] = from_f32<T>(c * scale[s]);
+      }
+      dst[v] = out;
+    }
+  }
+}
+
+template <typename T, int VEC, int NV, int FMT>
+static pkv_status launch_rows(const QuantRowsArgs &a, bool read, cudaStream_t stream) {
+  const long long per_cta = kQuantThreads / a.lanes, blocks = (a.T * a.KVH + per_cta - 1) / per_cta;
+  if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  if (read)
+    pkv_quant_read_kernel<T, VEC, NV, FMT><<<(unsigned)blocks, kQuantThreads, 0, stream>>>(a);
+  else
+    pkv_quant_write_kernel<T, VEC, NV, FMT><<<(unsigned)blocks, kQuantThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <typename T, int VEC, int FMT>
+static pkv_status launch_rows_v(QuantRowsArgs &a, bool read, cudaStream_t stream) {
+  constexpr int kMost = 512 / (32 * VEC);              // vectors of a lane at head_dim 512
+  a.vecs = a.D / VEC;
+  for (a.lanes = 1; a.lanes < 32 && a.lanes < a.vecs;) a.lanes *= 2;
+  return a.vecs <= 32 ? launch_rows<T, VEC, 1, FMT>(a, read, stream) : launch_rows<T, VEC, kMost, FMT>(a, read, stream);
+}
+
+// 16-byte vectors of the dense rows where every row start allows them, else
+// one element (4 bits: two, a byte of codes) at a time.
+template <typename T, int FMT>
+static pkv_status launch_rows_t(QuantRowsArgs &a, bool read, cudaStream_t stream) {
+  constexpr int kVec = 16 / sizeof(T), kPack = FMT == kInt4 ? kVec / 2 : kVec;
+  bool wide = a.D % kVec == 0;
+  for (int s = 0; s < 2; ++s)
+    wide = wide && reinterpret_cast<uintptr_t>(a.x[s]) % 16 == 0 && a.stride[s] % kVec == 0 &&
+           reinterpret_cast<uintptr_t>(a.codes[s]) % kPack == 0;
+  if (wide) return launch_rows_v<T, kVec, FMT>(a, read, stream);
+  if constexpr (FMT == kInt4) {
+    return launch_rows_v<T, 2, FMT>(a, read, stream);
+  } else {
+    return launch_rows_v<T, 1, FMT>(a, read, stream);
+  }
+}
+
+template <typename T>
+static pkv_status launch_rows_f(QuantRowsArgs &a, pkv_quant_format fmt, bool read, cudaStream_t stream) {
+  switch (fmt) {
+    case PKV_QUANT_INT8: return launch_rows_t<T, kInt8>(a, read, stream);
+    case PKV_QUANT_E4M3: return launch_rows_t<T, kE4m3>(a, read, stream);
+    case PKV_QUANT_INT4: return launch_rows_t<T, kInt4>(a, read, stream);
+  }
+  return PKV_ERR_INVALID_ARG;
+}
+
+// Both calls: `x` is read (write) or written (read).
+static pkv_status quant_rows(void *const (&codes)[2], float *const (&params)[2], void *const (&x)[2],
+                             const int64_t *slots, int64_t T, const int64_t (&stride)[2], int64_t num_blocks, int bs,
+                             int KVH, int D, pkv_quant_format fmt, pkv_dtype dt, bool read, int *err,
+                             cudaStream_t stream) {
+  if ((fmt != PKV_QUANT_INT8 && fmt != PKV_QUANT_E4M3 && fmt != PKV_QUANT_INT4) ||
+      (dt != PKV_F32 && dt != PKV_BF16 && dt != PKV_F16))
+    return PKV_ERR_INVALID_ARG;
+  if (T < 0 || T > 0x7fffffffLL || num_blocks < 0 || num_blocks > 0x7fffffffLL || bs <= 0 || KVH <= 0 || KVH > 65535 ||
+      D <= 0 || (fmt == PKV_QUANT_INT4 && D % 2) || stride[0] < (int64_t)KVH * D || stride[1] < (int64_t)KVH * D)
+    return PKV_ERR_INVALID_ARG;
+  if (D > 512) return PKV_ERR_UNSUPPORTED;
+  if (T == 0) return PKV_OK;
+  const size_t el = dt == PKV_F32 ? 4 : 2;
+  if (!slots || reinterpret_cast<uintptr_t>(slots) % 8 || reinterpret_cast<uintptr_t>(err) % 4) return PKV_ERR_INVALID_ARG;
+  QuantRowsArgs a = {};
+  const int64_t rows = num_blocks * bs * KVH;
+  ArgRange r[7];
+  for (int s = 0; s < 2; ++s) {
+    if (!codes[s] || !params[s] || !x[s] || reinterpret_cast<uintptr_t>(x[s]) % el ||
+        reinterpret_cast<uintptr_t>(params[s]) % 4)
+      return PKV_ERR_INVALID_ARG;
+    r[s] = {codes[s], quant_codes_bytes(fmt, rows, D)};
+    r[2 + s] = {params[s], quant_params_bytes(fmt, rows)};
+    r[4 + s] = {x[s], (size_t)((T - 1) * stride[s] + (int64_t)KVH * D) * el};
+    a.codes[s] = static_cast<char *>(codes[s]);
+    a.params[s] = params[s];
+    a.x[s] = static_cast<char *>(x[s]);
+    a.stride[s] = stride[s];
+  }
+  r[6] = {slots, (size_t)T * sizeof(int64_t)};
+  // what is written overlaps nothing else (two dense inputs, and two caches
+  // that are only read, may)
+  for (int i = 0; i < 7; ++i)
+    for (int j = i + 1; j < 7; ++j) {
+      const bool wi = read ? i == 4 || i == 5 : i < 4, wj = read ? j == 4 || j == 5 : j < 4;
+      if ((wi || wj) && overlap(r[i], r[j])) return PKV_ERR_INVALID_ARG;
+    }
+  a.slots = slots;
+  a.err = err;
+  a.T = T;
+  a.capacity = num_blocks * bs;
+  a.bs = bs;
+  a.KVH = KVH;
+  a.D = D;
+  switch (dt) {
+    case PKV_F32: return launch_rows_f<float>(a, fmt, read, stream);
+    case PKV_BF16: return launch_rows_f<__nv_bfloat16>(a, fmt, read, stream);
+    case PKV_F16: return launch_rows_f<__half>(a, fmt, read, stream);
+  }
+  return PKV_ERR_INVALID_ARG;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+PKV_API pkv_status pkv_quant_write(void *k_codes, void *v_codes, float *k_params, float *v_params, const void *k,
+                                   const void *v, const int64_t *slot_mapping, int64_t num_tokens,
+                                   int64_t k_token_stride, int64_t v_token_stride, int64_t num_blocks, int block_size,
+                                   int num_kv_heads, int head_dim, pkv_quant_format fmt, pkv_dtype dt, int *err_flags,
+                                   pkv_stream_t stream) {
+  return quant_rows({k_codes, v_codes}, {k_params, v_params}, {const_cast<void *>(k), const_cast<void *>(v)},
+                    slot_mapping, num_tokens, {k_token_stride, v_token_stride}, num_blocks, block_size, num_kv_heads,
+                    head_dim, fmt, dt, false, err_flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+PKV_API pkv_status pkv_quant_read(void *k_out, void *v_out, const void *k_codes, const void *v_codes,
+                                  const float *k_params, const float *v_params, const int64_t *slot_mapping,
+                                  int64_t num_tokens, int64_t k_out_stride, int64_t v_out_stride, int64_t num_blocks,
+                                  int block_size, int num_kv_heads, int head_dim, pkv_quant_format fmt, pkv_dtype dt,
+                                  int *err_flags, pkv_stream_t stream) {
+  return quant_rows({const_cast<void *>(k_codes), const_cast<void *>(v_codes)},
+                    {const_cast<float *>(k_params), const_cast<float *>(v_params)}, {k_out, v_out}, slot_mapping,
+                    num_tokens, {k_out_stride, v_out_stride}, num_blocks, block_size, num_kv_heads, head_dim, fmt, dt,
+                    true, err_flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,10 @@
+// pkv_quant_decode_e4m3.cu -- the tensor-core decode's instances for e4m3 codes.
+#include "pkv_quant_decode_mma.cuh"
+
+namespace pkv {
+
+pkv_status launch_quant_mma_e4m3(const QuantDecodeArgs &a, int tiles, bool split, pkv_dtype dt, cudaStream_t stream) {
+  return launch_qm_f<kE4m3>(a, tiles, split, dt, stream);
+}
+
+}  // namespace pkv
