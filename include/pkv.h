@@ -574,15 +574,15 @@ PKV_API int pkv_chunk_plan(int B, int64_t total_q, int H, int num_kv_heads, int 
 /*
  * A cache held in 8 or 4 bits.  Each row (one token's head_dim values of one
  * KV head) is quantised by itself:
- *   PKV_QUANT_INT8  code = rint(x * fl(127 / A)),    value = fl(A / 127) * code
- *   PKV_QUANT_E4M3  code = e4m3(fl(x * fl(448 / A))), value = fl(A / 448) * code
- *   PKV_QUANT_INT4  code = clamp(rint(x * inv) + zero, 0, 15), value = scale * (code - zero)
- * with A the row's largest magnitude, fl() a rounding to float32, rint the
- * nearest whole number (halves to even) of the exact product; for INT4
- *   lo = min(x, 0), hi = max(x, 0), R = fl(hi - lo), scale = fl(R / 15),
- *   inv = fl(15 / R), zero = rint(-lo * inv).
- * A row with A (R) below 2^-100 is held as zeros (scale 0); one that is not
- * finite, or whose R is not, has scale NaN and codes 0, so that everything
+ *   PKV_QUANT_INT8  code = rint(x * inv),                       value = scale * code
+ *   PKV_QUANT_E4M3  code = e4m3(fl(x * inv)),                   value = scale * code
+ *   PKV_QUANT_INT4  code = clamp(rint(x * inv) + zero, 0, 15),  value = scale * (code - zero)
+ * with scale = fl(A * fl(1 / top)) and inv = fl(fl(1 / A) * top), top = 127,
+ * 448 or 15; fl() a rounding to float32, rint the nearest whole number (halves
+ * to even) of the exact product.  A is the row's largest magnitude; for INT4
+ * lo = min(x, 0), hi = max(x, 0), A = fl(hi - lo), zero = rint(-lo * inv).
+ * A row with A below 2^-100 is held as zeros (scale 0); one that is not
+ * finite, or whose A is not, has scale NaN and codes 0, so that everything
  * read from it is NaN.
  *   codes   [num_blocks, block_size, num_kv_heads, head_dim] bytes; INT4
  *           head_dim / 2 bytes a row, the even element in the low half
@@ -641,9 +641,8 @@ PKV_API pkv_status pkv_quant_read(void *k_out, void *v_out, const void *k_codes,
  *   out = softmax(x) . V over the visible keys j < n = context_lens[b] and, if
  *   window > 0, j >= n - window,
  * with K and V the values that the codes stand for; nothing is rounded to 16
- * bits on the way but, for bf16 and more than four query heads per KV head,
- * the weights (fp16: half a step, 2^-11 of each).  Scores, statistics and sums
- * are fp32.  An empty context gives zeros.
+ * bits on the way but, for bf16, the weights (fp16: half a step, 2^-11 of
+ * each).  Scores, statistics and sums are fp32.  An empty context gives zeros.
  *   block_tables, context_lens, max_context_len as in pkv_decode_attention
  *   (the same flags; a context over the table is clamped)
  *   partition_size  0 = automatic, else a positive multiple of 128: keys per

@@ -4,7 +4,8 @@
 // Within a beam the order is that of its logits, so a row can be cut into
 // pieces that each give their K largest logits and a share of the sum, in one
 // pass over the row.  A CTA holds its piece in registers:
-//   1. load; maximum m of the piece, sum of 2^((x - m) log2 e);
+//   1. load; maximum m of the piece, sum of 2^(x L - fl(m L)), L = log2 e: the
+//      rounding of m L is in the piece's unit, so the sum carries none of it;
 //   2. a bound: in a warp the K-th largest of the lanes' maxima has K elements
 //      at or above it, so the largest such bound of the 8 warps has, too;
 //   3. the elements at or above the bound (K, and few more) go to shared memory
@@ -31,6 +32,7 @@ constexpr int kBsWarps = kBsThreads / 32;
 constexpr int kBsMost = 32;              // beams, continuations
 constexpr int kBsKeys = 512;             // keys of a piece that are ranked by counting
 constexpr int kBsParts = 256;            // pieces of a row
+constexpr int kBsList = 128;             // keys of a beam's pieces that a warp merges in shared memory
 constexpr int kBsSms = 152;              // of the one GPU this library is built for (speed alone)
 constexpr long long kBsMaxV = 1LL << 21;
 constexpr int kBsMaxB = 16384;
@@ -71,8 +73,11 @@ __device__ __forceinline__ bool beam_live(const BeamSelectArgs &a, long long row
   return c > -INFINITY && c < INFINITY;  // (NaN and +inf are flagged where the request is joined)
 }
 
+template <typename T>
+constexpr uint32_t kMinusInf = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+
 // 16 bytes of a row from byte `at` on (a multiple of 16, counted from the
-// row's start), whatever the row's alignment; 0 past its end.
+// row's start), whatever the row's alignment; -inf past its end.
 template <typename T>
 __device__ __forceinline__ uint4 row_granule(const char *row, long long at, long long bytes) {
   const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
@@ -99,7 +104,7 @@ __device__ __forceinline__ uint4 row_granule(const char *row, long long at, long
     uint16_t h[8];
     uint32_t w[4];
   } u;
-  u.v = make_uint4(0, 0, 0, 0);
+  u.v = make_uint4(kMinusInf<T>, kMinusInf<T>, kMinusInf<T>, kMinusInf<T>);
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
     const long long b = at + e * (long long)sizeof(T);
@@ -121,6 +126,29 @@ __device__ __forceinline__ float granule_at(const uint4 &g, int e) {
   return __half2float(__ushort_as_half((unsigned short)h));
 }
 
+// The largest element of a granule; NaN if there is one.
+template <typename T>
+__device__ __forceinline__ float granule_max(const uint4 &g) {
+  if constexpr (sizeof(T) == 4) {
+    float r;
+    asm("{.reg .f32 a, b;\n\tmax.NaN.f32 a, %1, %2;\n\tmax.NaN.f32 b, %3, %4;\n\tmax.NaN.f32 %0, a, b;}"
+        : "=f"(r) : "f"(__uint_as_float(g.x)), "f"(__uint_as_float(g.y)), "f"(__uint_as_float(g.z)), "f"(__uint_as_float(g.w)));
+    return r;
+  } else if constexpr (std::is_same<T, __half>::value) {
+    uint32_t r;
+    asm("{.reg .b32 a, b;\n\tmax.NaN.f16x2 a, %1, %2;\n\tmax.NaN.f16x2 b, %3, %4;\n\tmax.NaN.f16x2 %0, a, b;}"
+        : "=r"(r) : "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w));
+    const __half2 h = *reinterpret_cast<const __half2 *>(&r);
+    return __half2float(__hmax_nan(__low2half(h), __high2half(h)));
+  } else {
+    uint32_t r;
+    asm("{.reg .b32 a, b;\n\tmax.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 b, %3, %4;\n\tmax.NaN.bf16x2 %0, a, b;}"
+        : "=r"(r) : "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w));
+    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&r);
+    return __bfloat162float(__hmax_nan(__low2bfloat16(h), __high2bfloat16(h)));
+  }
+}
+
 __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -130,8 +158,16 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long x)
   return x;
 }
 
+// The sums' unit is 2^(m L), L = log2 e as fp32 has it, the product as fp32
+// rounds it; from kBsFar on, where it would leave fp32, exact (neighbours there
+// are 2^103 apart).
+constexpr float kBsFar = 1e38f;
+__device__ __forceinline__ double beam_unit(float m) {
+  return fabsf(m) < kBsFar ? (double)(m * kLog2e) : (double)m * (double)kLog2e;
+}
+
 // The request's K best from its pieces, by the whole CTA.
-__device__ void beam_join(const BeamSelectArgs &a, int b) {
+__device__ __noinline__ void beam_join(const BeamSelectArgs &a, int b, unsigned long long (*s_list)[kBsList]) {
   __shared__ unsigned long long s_key[kBsMost][kBsMost];   // a beam's best, sorted
   __shared__ double s_base[kBsMost];                       // c - log sum exp; finished beams: c
   __shared__ int s_mode[kBsMost];                          // 0 no proposals, 1 its tokens, 2 itself
@@ -158,37 +194,58 @@ __device__ void beam_join(const BeamSelectArgs &a, int b) {
       if (m > -INFINITY)
         for (int i = lane; i < parts; i += 32) {
           const float x = __ldcg(a.maxima + row * parts + i);
-          if (x > -INFINITY) sum += __ldcg(a.sums + row * parts + i) * exp((double)x - (double)m);
+          if (x > -INFINITY) sum += __ldcg(a.sums + row * parts + i) * exp2(beam_unit(x) - beam_unit(m));
         }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       bad = nan;
       if (nan || m == -INFINITY) mode = 0;
-      base = (double)c - ((double)m + log(sum));
+      base = (double)c - (beam_unit(m) / (double)kLog2e + log(sum));
     }
     if (mode == 1) {
-      // lane = piece (32 apart): its next key not yet taken
+      // lane = piece (32 apart): its next key not yet taken.  Short lists come
+      // to shared memory first: a round then waits for no load from L2.
       const unsigned long long *keys = a.keys + row * parts * K;
-      unsigned long long head[kBsParts / 32];
-      uint32_t taken[kBsParts / 32];
-#pragma unroll
-      for (int j = 0; j < kBsParts / 32; ++j) {
-        const int i = lane + 32 * j;
-        taken[j] = 0;
-        head[j] = i < parts ? __ldcg(keys + (long long)i * K) : 0;
-      }
-      for (int k = 0; k < K; ++k) {
-        unsigned long long best = 0;
-#pragma unroll
-        for (int j = 0; j < kBsParts / 32; ++j) best = head[j] > best ? head[j] : best;
-        best = warp_max_u64(best);
-        if (lane == 0) s_key[w][k] = best;
-#pragma unroll
-        for (int j = 0; j < kBsParts / 32; ++j)
-          if (best != 0 && head[j] == best) {              // (keys differ: one lane has it)
-            ++taken[j];
-            head[j] = taken[j] < K ? __ldcg(keys + (long long)(lane + 32 * j) * K + taken[j]) : 0;
+      const bool near = parts * K <= kBsList;
+      if (near) {
+        __syncwarp();
+        for (int i = lane; i < parts * K; i += 32) s_list[warp][i] = __ldcg(keys + i);
+        __syncwarp();
+        if (parts <= 32) {
+          unsigned long long head = lane < parts ? s_list[warp][lane * K] : 0;
+          int taken = 0;
+          for (int k = 0; k < K; ++k) {
+            const unsigned long long best = warp_max_u64(head);
+            if (lane == 0) s_key[w][k] = best;
+            if (best != 0 && head == best) {             // (keys differ: one lane has it)
+              ++taken;
+              head = taken < K ? s_list[warp][lane * K + taken] : 0;
+            }
           }
+        }
+      }
+      if (!near || parts > 32) {
+        unsigned long long head[kBsParts / 32];
+        uint32_t taken[kBsParts / 32];
+#pragma unroll
+        for (int j = 0; j < kBsParts / 32; ++j) {
+          const int i = lane + 32 * j;
+          taken[j] = 0;
+          head[j] = i < parts ? __ldcg(keys + (long long)i * K) : 0;
+        }
+        for (int k = 0; k < K; ++k) {
+          unsigned long long best = 0;
+#pragma unroll
+          for (int j = 0; j < kBsParts / 32; ++j) best = head[j] > best ? head[j] : best;
+          best = warp_max_u64(best);
+          if (lane == 0) s_key[w][k] = best;
+#pragma unroll
+          for (int j = 0; j < kBsParts / 32; ++j)
+            if (best != 0 && head[j] == best) {
+              ++taken[j];
+              head[j] = taken[j] < K ? __ldcg(keys + (long long)(lane + 32 * j) * K + taken[j]) : 0;
+            }
+        }
       }
     }
     if (lane == 0) {
@@ -238,7 +295,7 @@ __device__ void beam_join(const BeamSelectArgs &a, int b) {
 
 // GRANULES 16-byte granules a thread: a piece is kBsThreads * GRANULES of them.
 template <typename T, int GRANULES>
-__global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __grid_constant__ BeamSelectArgs a) {
+__global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __grid_constant__ BeamSelectArgs a) {
   constexpr int kPer = 16 / sizeof(T), E = GRANULES * kPer;
   constexpr long long kPiece = (long long)kBsThreads * E;
   __shared__ float s_f[kBsWarps];
@@ -246,6 +303,7 @@ __global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __gri
   __shared__ double s_d[kBsWarps];
   __shared__ int s_n, s_last;
   __shared__ unsigned long long s_keys[kBsKeys];
+  __shared__ unsigned long long s_list[kBsWarps][kBsList];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long row = blockIdx.x / a.parts;
   const int part = (int)(blockIdx.x - row * a.parts), b = (int)(row / a.W);
@@ -256,22 +314,19 @@ __global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < GRANULES; ++i) {
       const long long at = (first + (long long)(i * kBsThreads + tid) * kPer) * (long long)sizeof(T);
-      g[i] = at < bytes ? row_granule<T>(base, at, bytes) : make_uint4(0, 0, 0, 0);
+      g[i] = row_granule<T>(base, at, bytes);
     }
-    auto token = [&](int i, int e) { return first + (long long)(i * kBsThreads + tid) * kPer + e; };
-    auto value = [&](int i, int e) { return token(i, e) < a.V ? granule_at<T>(g[i], e) : -INFINITY; };
+    auto token = [&](int i, int e) { return (uint32_t)first + (uint32_t)(i * kBsThreads + tid) * kPer + e; };
     if (tid == 0) s_n = 0;
-    // 1. maximum and sum
+    // 1. maximum (NaN where there is one) and sum
     float m = -INFINITY;
     bool nan = false;
 #pragma unroll
-    for (int i = 0; i < GRANULES; ++i)
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const float x = value(i, e);
-        nan = nan || !(x < INFINITY);                      // NaN, +inf
-        m = fmaxf(m, x);
-      }
+    for (int i = 0; i < GRANULES; ++i) {
+      const float x = granule_max<T>(g[i]);
+      nan = nan || !(x < INFINITY);
+      m = fmaxf(m, x);
+    }
     const float mine = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -282,8 +337,8 @@ __global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __gri
 #pragma unroll
       for (int o = size >> 1; o > 0; o >>= 1) {
         const uint32_t y = __shfl_xor_sync(0xffffffffu, u, o);
-        const bool up = ((lane & size) != 0) == ((lane & o) == 0);   // keep the smaller
-        u = up ? min(u, y) : max(u, y);
+        const bool down = ((lane & size) != 0) == ((lane & o) == 0);   // keep the smaller
+        u = down ? min(u, y) : max(u, y);
       }
     u = __shfl_sync(0xffffffffu, u, a.K - 1);
     if (lane == 0) {
@@ -296,29 +351,44 @@ __global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __gri
       m = fmaxf(m, s_f[k]);
       u = max(u, s_u[k]);
     }
+    // (a thread's sum in fp32, threads' sums in 64 bits)
     float sum = 0.f;
-    if (m > -INFINITY)
+    const float unit = m > -INFINITY ? m * kLog2e : 0.f;
+    if (fabsf(m) >= kBsFar && m > -INFINITY) {             // what is not m is far below it
 #pragma unroll
       for (int i = 0; i < GRANULES; ++i)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) sum += fast_exp2((value(i, e) - m) * kLog2e);
+        for (int e = 0; e < kPer; ++e) sum += granule_at<T>(g[i], e) == m ? 1.f : 0.f;
+    } else
+#pragma unroll
+    for (int i = 0; i < GRANULES; ++i) {
+      float part_sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) part_sum += fast_exp2(fmaf(granule_at<T>(g[i], e), kLog2e, -unit));
+      sum += part_sum;
+    }
     double total = sum;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) s_d[warp] = total;
     // 3. what is at or above the bound, -inf excepted
     const float bound = from_ordered(u);
-    if (!any_nan && mine >= bound)
+    if (!any_nan && mine >= bound && mine > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < GRANULES; ++i)
-#pragma unroll
+      for (int i = 0; i < GRANULES; ++i) {
+        if (!(granule_max<T>(g[i]) >= bound)) continue;
+#pragma unroll 1
         for (int e = 0; e < kPer; ++e) {
-          const float x = value(i, e);
+          const uint32_t word = sizeof(T) == 4 ? e : e >> 1;
+          const uint32_t bits = word < 2 ? (word == 0 ? g[i].x : g[i].y) : (word == 2 ? g[i].z : g[i].w);
+          const float x = granule_at<T>(make_uint4(bits, 0, 0, 0), sizeof(T) == 4 ? 0 : e & 1);
           if (x >= bound && x > -INFINITY) {
             const int n = atomicAdd(&s_n, 1);
-            if (n < kBsKeys) s_keys[n] = beam_key(x, (uint32_t)token(i, e));
+            if (n < kBsKeys) s_keys[n] = beam_key(x, token(i, e));
           }
         }
+      }
+    }
     __syncthreads();
     const int n = s_n;
     const long long out = row * a.parts + part;
@@ -340,16 +410,17 @@ __global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __gri
     } else {
       // that many ties at the bound: one at a time, the largest key below the last
       unsigned long long last = ~0ull;
+      // (read again: rare, and no reason to hold every element apart)
       for (int k = 0; k < a.K; ++k) {
         unsigned long long best = 0;
-#pragma unroll
-        for (int i = 0; i < GRANULES; ++i)
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            const float x = value(i, e);
-            const unsigned long long key = x > -INFINITY ? beam_key(x, (uint32_t)token(i, e)) : 0;
-            if (key < last && key > best) best = key;
-          }
+#pragma unroll 1
+        for (int i = 0; i < E; ++i) {
+          const long long v = first + (long long)i * kBsThreads + tid;
+          if (v >= a.V) break;
+          const float x = to_f32<T>(reinterpret_cast<const T *>(base)[v]);
+          const unsigned long long key = x > -INFINITY ? beam_key(x, (uint32_t)v) : 0;
+          if (key < last && key > best) best = key;
+        }
         best = warp_max_u64(best);
         __syncthreads();
         if (lane == 0) s_keys[warp] = best;
@@ -372,7 +443,7 @@ __global__ void __launch_bounds__(kBsThreads) pkv_beam_select_kernel(const __gri
     if (s_last) a.cnt[b] = 0;                              // ready for the next call
   }
   __syncthreads();
-  if (s_last) beam_join(a, b);
+  if (s_last) beam_join(a, b, s_list);
 }
 
 struct BeamPlan {

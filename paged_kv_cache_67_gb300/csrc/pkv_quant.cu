@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kQuantThreads) pkv_quant_write_kernel(const __
     const float span = FMT == kInt4 ? hi[s] - lo[s] : fmaxf(hi[s], -lo[s]);
     const bool ok = finite[s] && span <= 3.402823466e38f;
     const bool fine = ok && span >= kQuantTiny;
-    const float inv = fine ? __fdiv_rn(kTop, span) : 0.f;
-    const float scale = fine ? __fdiv_rn(span, kTop) : ok ? 0.f : __int_as_float(0x7fc00000);
+    const float inv = fine ? __fmul_rn(__frcp_rn(span), kTop) : 0.f;
+    const float scale = fine ? __fmul_rn(span, 1.f / kTop) : ok ? 0.f : __int_as_float(0x7fc00000);
     const int zero = FMT == kInt4 && fine ? rint_product(-lo[s], inv) : 0;
     if (at == 0) {
       float *p = a.params[s] + ((blk * a.KVH + h) * a.bs + off) * quant_params<FMT>();

@@ -284,11 +284,14 @@ PKV_API pkv_status pkv_quant_decode_attention(
   c.scale_log2 = scale * kLog2e;
   c.cap_ratio = softcap > 0.f ? scale / softcap : 0.f;
   c.cap_log2 = std::min(softcap * kLog2e, FLT_MAX);
+  c.scale_y = softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f;
   a.k = static_cast<const uint8_t *>(k_codes);
   a.v = static_cast<const uint8_t *>(v_codes);
   a.kp = k_params;
   a.vp = v_params;
   a.heads = plan.heads;
+  while ((1LL << a.bs_shift) < block_size) ++a.bs_shift;
+  a.bs_mul = (uint32_t)((((1ULL << a.bs_shift) - (uint64_t)block_size) << 32) / (uint64_t)block_size + 1);
   char *ws = static_cast<char *>(workspace);
   c.ws_cnt = reinterpret_cast<int *>(ws);
   ws += kChunkCnt * sizeof(int);

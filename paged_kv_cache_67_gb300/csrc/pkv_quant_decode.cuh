@@ -17,6 +17,8 @@ struct QuantDecodeArgs {
   const uint8_t *k, *v;            // codes
   const float *kp, *vp;            // parameters
   int heads;                       // query heads of a CTA
+  uint32_t bs_mul;                 // t / block_size = (umulhi(t, bs_mul) + t) >> bs_shift for t < 2^31
+  int bs_shift;
 };
 
 // A CTA's place in the grid and its keys [t0, t1); nparts 0: nothing to do.

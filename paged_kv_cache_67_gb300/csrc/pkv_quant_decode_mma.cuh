@@ -9,20 +9,20 @@
 // unpacked once for 8 heads:
 //   S^T[16 tokens x 8] = CK[16 x D] Q^T[D x 8],   O^T[D x 8] += CV^T[D x 16] W[16 x 8].
 // q is scaled by a power of two a row (its largest element to [2^14, 2^15)),
-// so that fp16 holds bf16's range; weights w_j = p_j sv_j are taken against
-// their own running maximum, 2^4 there, so that they use fp16's range too,
-// whatever the values' scales: m' = max (x_j + log2 sv_j).
+// so that fp16 holds bf16's range; the weights w_j = p_j sv_j by another, of the
+// largest value scale that the warp has met, so that w <= 2^15 whatever the
+// scales are.  What falls below fp16 there is under 2^-30 of the largest value.
 //
 // SPLIT: columns 0-3 hold four heads, columns 4-7 what fp16 leaves of them: a
 // query or a weight is hi + lo, good to 2^-23.  fp32 always, other types where
-// the KV head has four query heads or fewer (the columns are free then).  With
-// more heads a weight is one fp16 number: half a step, 2^-11, an eighth of what
-// bf16 rounds off the output; for fp16, where it would be as much as the
-// output's own, the rest of the weights takes another turn of the second product.
+// the KV head has four query heads or fewer (the columns are free then).  bf16
+// goes without: its queries are exact and the weights' half step, 2^-11, is an
+// eighth of what it rounds off the output.  fp16 with more heads, where it would
+// be as much as the output's own, has the rest of the weights in another turn of
+// the second product.
 //
-// A running maximum is raised only when some score passes it by 2^8: one vote
-// a tile of 32 tokens instead of six exchanges, and the weights stay within
-// fp16 (2^13 at most).
+// The running maximum is raised only when some score passes it by 2^8: one vote
+// a tile of 32 tokens instead of three exchanges a head.
 //
 // CTA = 4 warps; warp w takes tiles w, w + 4, ... of 32 tokens through a ring of
 // its own in shared memory, filled by 16-byte cp.async row by row (a row's place
@@ -53,7 +53,7 @@ struct QmShape {
   static constexpr int kRing = kStages * kStage * kQmWarps;
   static constexpr int kOut = kQmWarps * kCols * kOStride * 4;
   static constexpr int kMain = kRing > kOut ? kRing : kOut;
-  static constexpr int kSmem = kMain + 4 * (3 * kQmWarps * kCols + 3 * kCols + 4);
+  static constexpr int kSmem = kMain + 4 * (2 * kQmWarps * kCols + 2 * kCols + 4);
   static_assert(kMain >= 1024, "the join's weights fit");
 };
 
@@ -97,31 +97,20 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// Four codes of a K row (one word) as two pairs of halves in the row's order.
-// int8: a byte in the low bits of the half 1024 + u is u exactly.
-template <int FMT>
-__device__ __forceinline__ void k_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
+// Four codes of a word (one K row; of V's ldmatrix word, two columns of token
+// 2t and the same of token 2t + 1) as two pairs of halves.
+// int8: bytes (0, 2) and (1, 3): a byte with its top bit turned, code + 128, in
+// the low bits of the half 1024 is 1152 + code exactly: one and-xor, one subtract.
+// e4m3: K's bytes (0, 1) and (2, 3), V's as int8's.
+template <int FMT, bool V>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &p0, uint32_t &p1) {
   if constexpr (FMT == kInt8) {
-    w ^= 0x80808080u;                                   // code + 128
-    lo = hsub2_u(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);   // - (1024 + 128)
-    hi = hsub2_u(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
+    p0 = hsub2_u((w & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
+    p1 = hsub2_u(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
   } else {
-    lo = e4m3x2_to_half2((uint16_t)w);
-    hi = e4m3x2_to_half2((uint16_t)(w >> 16));
-  }
-}
-// ldmatrix's word of V: two columns of token 2t (low half), the same of token
-// 2t + 1; out: the first column's two tokens, the second's.
-template <int FMT>
-__device__ __forceinline__ void v_pairs(uint32_t w, uint32_t &c0, uint32_t &c1) {
-  if constexpr (FMT == kInt8) {
-    w ^= 0x80808080u;
-    c0 = hsub2_u(__byte_perm(w, 0x64646464u, 0x4240), 0x64806480u);
-    c1 = hsub2_u(__byte_perm(w, 0x64646464u, 0x4341), 0x64806480u);
-  } else {
-    w = __byte_perm(w, 0, 0x3120);
-    c0 = e4m3x2_to_half2((uint16_t)w);
-    c1 = e4m3x2_to_half2((uint16_t)(w >> 16));
+    if (V) w = __byte_perm(w, 0, 0x3120);
+    p0 = e4m3x2_to_half2((uint16_t)w);
+    p1 = e4m3x2_to_half2((uint16_t)(w >> 16));
   }
 }
 // Eight 4-bit codes of a word, less the zero points: pairs (nibbles i, i + 4).
@@ -136,13 +125,9 @@ __device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t z1, uint32_t z
   p[3] = hfma2_u((u & 0x00f000f0u) | 0x64006400u, kSixteenth, z16);
 }
 
-// A value's scale as 2^ex * m, m in [1, 2): exact, where a logarithm would cost
-// the weight its last bits.  0 (and what is below 2^-126) has m = 0, NaN and
-// infinity have themselves.
-__device__ __forceinline__ void split_scale(uint32_t bits, float &ex, float &m) {
-  const int e = (int)(bits >> 23);
-  ex = (float)(e - 127);
-  m = e == 0 ? 0.f : __uint_as_float(e >= 255 ? bits : (bits & 0x007fffffu) | 0x3f800000u);
+// t / bs for t < 2^31 by a multiplication (mul, shift from the host).
+__device__ __forceinline__ int div_by(int t, uint32_t mul, int shift) {
+  return (int)((__umulhi((uint32_t)t, mul) + (uint32_t)t) >> shift);
 }
 
 template <int D, int FMT, int NT, bool SPLIT>
@@ -152,17 +137,15 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
   using Sh = QmShape<D, FMT, NT>;
   constexpr int W = kQmWarps, S = Sh::kStages, kSteps = D / 16, kHeads = SPLIT ? 4 : 8 * NT;
   extern __shared__ __align__(16) uint8_t ring[];
-  float *s_wm = reinterpret_cast<float *>(ring + Sh::kMain);     // [W][cols] maxima, of weights, sums
-  float *s_wo = s_wm + W * Sh::kCols;
-  float *s_wl = s_wo + W * Sh::kCols;
+  float *s_wm = reinterpret_cast<float *>(ring + Sh::kMain);     // [W][cols] maxima, sums
+  float *s_wl = s_wm + W * Sh::kCols;
   float *s_m = s_wl + W * Sh::kCols;                             // [cols]
   float *s_l = s_m + Sh::kCols;
-  float *s_qs = s_l + Sh::kCols;                                 // [cols] 1 / the query's power of two
-  int *s_scratch = reinterpret_cast<int *>(s_qs + Sh::kCols);
+  int *s_scratch = reinterpret_cast<int *>(s_l + Sh::kCols);
   const ChunkArgs &c = a.c;
   const QuantPart p = quant_part(a);
   if (p.nparts == 0) return;
-  const bool rest = dt == PKV_F16;
+  const bool rest = SPLIT ? dt != PKV_BF16 : dt == PKV_F16;   // weights of two parts
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const int ntiles = p.t1 > p.t0 ? (p.t1 - p.t0 + kQmTok - 1) / kQmTok : 0;
   const int mine = ntiles > w ? (ntiles - w + W - 1) / W : 0;
@@ -172,42 +155,55 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
 
   // Tile i of this warp into stage i mod S.  Lane r looks up token r's block one
   // tile ahead, so that the table entry is there when it is needed; what is
-  // not visible is filled with zeros and not read.
+  // not visible is filled with zeros and not read.  (Rows of the cache are fewer
+  // than 2^32 - 1 here.)
+  constexpr bool kEven = 32 % Sh::kChunks == 0;          // a lane keeps to one chunk of the rows
+  const int32_t *table = c.tables + (size_t)p.b * c.max_blocks;
+  const uint8_t *k_at = a.k + lane % Sh::kChunks * 16, *v_at = a.v + lane % Sh::kChunks * 16;
+  const uint32_t st_even = ring_at + lane / Sh::kChunks * Sh::kStride + lane % Sh::kChunks * 16;
   int next_phys = 0, next_off = -1;
   auto look_up = [&](int i) {
     const int t = p.t0 + kQmTok * (w + W * i) + lane;
     next_off = -1;
     if (i < mine && t >= first && t < p.t1) {
-      const int lb = t / c.bs;
+      const int lb = div_by(t, a.bs_mul, a.bs_shift);
       next_off = t - lb * c.bs;
-      next_phys = __ldg(c.tables + (size_t)p.b * c.max_blocks + lb);
+      next_phys = __ldg(table + lb);
     }
   };
   auto issue = [&](int i) {
     if (i < mine) {
-      long long slot = -1;
-      if (next_off >= 0) {
-        if (next_phys < 0 || (long long)next_phys >= c.num_blocks)
-          raise_flag(c.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
-        else
-          slot = (long long)next_phys * c.bs + next_off;
+      bool in = next_off >= 0;
+      if (in && (next_phys < 0 || (long long)next_phys >= c.num_blocks)) {
+        raise_flag(c.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
+        in = false;
       }
-      const uint32_t st = ring_at + (i % S) * Sh::kStage;
-      const uint32_t row = slot < 0 ? 0xffffffffu : (uint32_t)(slot * c.KVH + p.kvh);   // (rows are fewer than 2^32 - 1)
-      long long at = 0;
-      if (slot >= 0) at = (((long long)next_phys * c.KVH + p.kvh) * c.bs + next_off) * quant_params<FMT>();
+      const uint32_t phys = (uint32_t)next_phys, off = (uint32_t)next_off;
+      const uint32_t row = in ? (phys * (uint32_t)c.bs + off) * (uint32_t)c.KVH + (uint32_t)p.kvh : 0xffffffffu;
+      const uint32_t num = in ? (phys * (uint32_t)c.KVH + (uint32_t)p.kvh) * (uint32_t)c.bs + off : 0u;
+      const uint32_t stage = (i % S) * Sh::kStage, st = ring_at + stage;
       const uint32_t pa = st + 2 * kQmTok * Sh::kStride + lane * Sh::kParams;
-      cp_async_small<Sh::kParams>(pa, a.kp + at, slot < 0 ? 0 : Sh::kParams);
-      cp_async_small<Sh::kParams>(pa + kQmTok * Sh::kParams, a.vp + at, slot < 0 ? 0 : Sh::kParams);
+      cp_async_small<Sh::kParams>(pa, a.kp + (size_t)num * quant_params<FMT>(), in ? Sh::kParams : 0);
+      cp_async_small<Sh::kParams>(pa + kQmTok * Sh::kParams, a.vp + (size_t)num * quant_params<FMT>(), in ? Sh::kParams : 0);
+      if (kEven && __all_sync(0xffffffffu, in)) {
 #pragma unroll
-      for (int j = 0; j < Sh::kChunks; ++j) {
-        const int idx = lane + 32 * j, r = idx / Sh::kChunks, ch = idx - r * Sh::kChunks;
-        const uint32_t from = __shfl_sync(0xffffffffu, row, r);
-        const bool in = from != 0xffffffffu;
-        const size_t off = in ? (size_t)from * Sh::kRow + ch * 16 : 0;
-        const uint32_t to = st + r * Sh::kStride + ch * 16;
-        cp_async16(to, a.k + off, in ? 16 : 0);
-        cp_async16(to + kQmTok * Sh::kStride, a.v + off, in ? 16 : 0);
+        for (int j = 0; j < Sh::kChunks; ++j) {
+          const uint32_t from = __shfl_sync(0xffffffffu, row, lane / Sh::kChunks + j * (32 / Sh::kChunks));
+          const uint32_t to = st_even + stage + j * (32 / Sh::kChunks) * Sh::kStride;
+          cp_async16(to, k_at + (size_t)from * Sh::kRow, 16);
+          cp_async16(to + kQmTok * Sh::kStride, v_at + (size_t)from * Sh::kRow, 16);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < Sh::kChunks; ++j) {
+          const int idx = lane + 32 * j, r = idx / Sh::kChunks, ch = idx - r * Sh::kChunks;
+          const uint32_t from = __shfl_sync(0xffffffffu, row, r);
+          const bool has = from != 0xffffffffu;
+          const size_t at = has ? (size_t)from * Sh::kRow + ch * 16 : 0;
+          const uint32_t to = st + r * Sh::kStride + ch * 16;
+          cp_async16(to, a.k + at, has ? 16 : 0);
+          cp_async16(to + kQmTok * Sh::kStride, a.v + at, has ? 16 : 0);
+        }
       }
       look_up(i + 1);
     }
@@ -225,6 +221,10 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
          : dt == PKV_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(c.q)[i])
                           : __half2float(reinterpret_cast<const __half *>(c.q)[i]);
   };
+  // scores in log2 units, or what their cap wants (see chunk_capped: its error
+  // does for 16-bit types; chunk_cap)
+  const int cap = !(c.cap_log2 > 0.f) ? kCapNone : dt != PKV_F32 && c.cap_log2 <= kCapShort ? kCapUsual : kCapLarge;
+  const float score_unit = cap == kCapNone ? c.scale_log2 : cap == kCapUsual ? c.scale_y : 1.f;
   uint32_t qf[NT][kSteps][2];
   float qs[NT][2];
 #pragma unroll
@@ -236,8 +236,10 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
     for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // the column of A's element (see k_pairs, nibble_pairs)
-        const int d = FMT == kInt4 ? (ks >> 1) * 32 + 8 * t4 + 2 * (ks & 1) + (e >> 1) + 4 * (e & 1) : ks * 16 + 4 * t4 + e;
+        // the column of A's element (see code_pairs, nibble_pairs)
+        const int d = FMT == kInt4   ? (ks >> 1) * 32 + 8 * t4 + 2 * (ks & 1) + (e >> 1) + 4 * (e & 1)
+                      : FMT == kInt8 ? ks * 16 + 4 * t4 + (e >> 1) + 2 * (e & 1)
+                                     : ks * 16 + 4 * t4 + e;
         v[ks][e] = has ? q_at(col_head, d) : 0.f;
         big = fmaxf(big, fabsf(v[ks][e]));
       }
@@ -258,17 +260,21 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
         qf[nt][ks][e] = half2_bits(x, y);
       }
     // this lane's score columns are 2 t4, 2 t4 + 1
-    qs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
-    qs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
+    qs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4) * score_unit;
+    qs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4) * score_unit;
   }
 
   float o[NT][kSteps][4] = {};
-  float m[NT][2], mo[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2];
+  // O's unit is 2^(ve - kUnit): ve the largest exponent of a value's scale so far
+  // (fp32's biased one; from 2^-97 on, NaN and infinity aside)
+  constexpr int kUnit = 127 + 6;
+  int ve = 30;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m[nt][e] = mo[nt][e] = -INFINITY;
+      m[nt][e] = -INFINITY;
       l[nt][e] = 0.f;
     }
 
@@ -280,7 +286,8 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
     const uint32_t kpb = vb + kQmTok * Sh::kStride, vpb = kpb + kQmTok * Sh::kParams;
     const int tile0 = p.t0 + kQmTok * (w + W * i);
     const bool whole = tile0 >= first && tile0 + kQmTok <= p.t1;
-    float x[2][NT][4], lsv[2][2], vm[2][2];
+    float x[2][NT][4], sv[2][2];
+    int ve_new = ve;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const int r0 = mt * 16 + g, r1 = r0 + 8;
@@ -307,17 +314,20 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
           uint32_t A[4];
-          k_pairs<FMT>(lds32(k0 + ks * 16), A[0], A[2]);
-          k_pairs<FMT>(lds32(k1 + ks * 16), A[1], A[3]);
+          code_pairs<FMT, false>(lds32(k0 + ks * 16), A[0], A[2]);
+          code_pairs<FMT, false>(lds32(k1 + ks * 16), A[1], A[3]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) MmaOp<__half>::run(s[nt], A, qf[nt][ks][0], qf[nt][ks][1]);
         }
       }
       const float sk0 = lds_f32(kpb + r0 * Sh::kParams), sk1 = lds_f32(kpb + r1 * Sh::kParams);
-      split_scale(lds32(vpb + r0 * Sh::kParams), lsv[mt][0], vm[mt][0]);
-      split_scale(lds32(vpb + r1 * Sh::kParams), lsv[mt][1], vm[mt][1]);
-      const bool vis0 = whole || (tile0 + r0 >= first && tile0 + r0 < p.t1);
-      const bool vis1 = whole || (tile0 + r1 >= first && tile0 + r1 < p.t1);
+      sv[mt][0] = lds_f32(vpb + r0 * Sh::kParams);
+      sv[mt][1] = lds_f32(vpb + r1 * Sh::kParams);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int ex = (__float_as_int(sv[mt][hf]) >> 23) & 255;
+        if (ex != 255) ve_new = max(ve_new, ex);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (SPLIT && dt == PKV_F32) {
@@ -325,71 +335,85 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
           for (int e = 0; e < 4; ++e) s[nt][e] += __shfl_xor_sync(0xffffffffu, s[nt][e], 2);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = quant_score(c, s[nt][e] * (qs[nt][e & 1] * (e < 2 ? sk0 : sk1)));
-          x[mt][nt][e] = (e < 2 ? vis0 : vis1) ? y : -INFINITY;
-        }
+        for (int e = 0; e < 4; ++e) x[mt][nt][e] = s[nt][e] * qs[nt][e & 1] * (e < 2 ? sk0 : sk1);
       }
     }
-    // raise the maxima where a score passes them by 2^8
-    bool over = false;
+    if (cap != kCapNone) {
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          over = over || x[mt][nt][e] > m[nt][e & 1] + 8.f || x[mt][nt][e] + lsv[mt][e >> 1] > mo[nt][e & 1] + 8.f;
+          for (int e = 0; e < 4; ++e)
+            x[mt][nt][e] = cap == kCapUsual ? chunk_capped(x[mt][nt][e], c.cap_log2) : chunk_cap(c, x[mt][nt][e]);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int t = tile0 + mt * 16 + hf * 8 + g;
+          if (t >= first && t < p.t1) continue;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) x[mt][nt][2 * hf] = x[mt][nt][2 * hf + 1] = -INFINITY;
+        }
+    }
+    // raise the maxima where a score passes them by 2^8, and O's unit where a
+    // value's scale passes it
+    bool over = ve_new > ve;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float m0 = m[nt][0] + 8.f, m1 = m[nt][1] + 8.f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+        over = over || x[mt][nt][0] > m0 || x[mt][nt][1] > m1 || x[mt][nt][2] > m0 || x[mt][nt][3] > m1;
+    }
     if (__any_sync(0xffffffffu, over)) {
+      ve_new = __reduce_max_sync(0xffffffffu, ve_new);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float a0 = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
-          float a1 = fmaxf(fmaxf(x[0][nt][e] + lsv[0][0], x[0][nt][e + 2] + lsv[0][1]),
-                           fmaxf(x[1][nt][e] + lsv[1][0], x[1][nt][e + 2] + lsv[1][1]));
+          float top = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
 #pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) {
-            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, sh));
-            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, sh));
-          }
-          a0 = fmaxf(a0, m[nt][e]);
-          a1 = fmaxf(a1, mo[nt][e]);
-          l[nt][e] *= fast_exp2(m[nt][e] - chunk_ref(a0));
-          const float f = fast_exp2(mo[nt][e] - chunk_ref(a1));
-          m[nt][e] = a0;
-          mo[nt][e] = a1;
+          for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+          top = fmaxf(top, m[nt][e]);
+          const float d = m[nt][e] - chunk_ref(top), f = fast_exp2(d + (float)(ve - ve_new));
+          l[nt][e] *= fast_exp2(d);
+          m[nt][e] = top;
 #pragma unroll
           for (int ks = 0; ks < kSteps; ++ks) {
             o[nt][ks][e] *= f;
             o[nt][ks][e + 2] *= f;
           }
         }
+      ve = ve_new;
     }
+    const float unit = __int_as_float((127 + kUnit - ve) << 23);    // 2^(kUnit - ve)
     // weights, as the product's B
     uint32_t wb[2][NT][2], wl[2][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float r0 = chunk_ref(m[nt][0]), r1 = chunk_ref(m[nt][1]);
-      const float u0 = chunk_ref(mo[nt][0]) - 4.f, u1 = chunk_ref(mo[nt][1]) - 4.f;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const float x0 = x[mt][nt][2 * hf], x1 = x[mt][nt][2 * hf + 1], lv = lsv[mt][hf];
-          l[nt][0] += fast_exp2(x0 - r0);
-          l[nt][1] += fast_exp2(x1 - r1);
-          const float w0 = fast_exp2(x0 + lv - u0) * vm[mt][hf], w1 = fast_exp2(x1 + lv - u1) * vm[mt][hf];
+          const float p0 = fast_exp2(x[mt][nt][2 * hf] - r0), p1 = fast_exp2(x[mt][nt][2 * hf + 1] - r1);
+          const float s1 = sv[mt][hf] * unit, w0 = p0 * s1, w1 = p1 * s1;
+          l[nt][0] += p0;
+          l[nt][1] += p1;
           __half2 h = __floats2half2_rn(w0, w1);
-          if (SPLIT) {
+          if (rest) {
             const float2 f = __half22float2(h);
-            if (t4 >= 2) h = __floats2half2_rn(w0 - f.x, w1 - f.y);
+            const __half2 lo = __floats2half2_rn(w0 - f.x, w1 - f.y);
+            if (SPLIT) {
+              if (t4 >= 2) h = lo;
+            } else {
+              wl[mt][nt][hf] = movm_trans(*reinterpret_cast<const uint32_t *>(&lo));
+            }
           }
           wb[mt][nt][hf] = movm_trans(*reinterpret_cast<uint32_t *>(&h));
-          if (!SPLIT && rest) {
-            const float2 f = __half22float2(h);
-            wl[mt][nt][hf] = movm_trans(half2_bits(w0 - f.x, w1 - f.y));
-          }
         }
     }
 #pragma unroll
@@ -434,8 +458,8 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
       } else {
         auto block = [&](int ch, uint32_t r0, uint32_t r1) {      // 16 columns of 16 tokens
           uint32_t A[4];
-          v_pairs<FMT>(r0, A[0], A[1]);
-          v_pairs<FMT>(r1, A[2], A[3]);
+          code_pairs<FMT, true>(r0, A[0], A[1]);
+          code_pairs<FMT, true>(r1, A[2], A[3]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             MmaOp<__half>::run(o[nt][ch], A, wb[mt][nt][0], wb[mt][nt][1]);
@@ -469,7 +493,6 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
       if (g == 0) {
         const int at = w * Sh::kCols + 8 * nt + 2 * t4 + e;
         s_wm[at] = m[nt][e];
-        s_wo[at] = mo[nt][e];
         s_wl[at] = l[nt][e];
       }
     }
@@ -483,12 +506,11 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
       float M = -INFINITY;
 #pragma unroll
       for (int k = 0; k < W; ++k) M = fmaxf(M, s_wm[k * Sh::kCols + col]);
-      // O's unit is 2^(mo - 4); the parts' states have 2^m
-      const float f = mo[nt][e] == -INFINITY ? 0.f : exp2f(mo[nt][e] - 4.f - chunk_ref(M));
+      const float f = exp2f(m[nt][e] - chunk_ref(M) + (float)(ve - kUnit));
       float *dst = s_o + (w * Sh::kCols + col) * Sh::kOStride;
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
-        // rows g and g + 8 of tile ks are columns of V (see v_pairs, nibble_pairs)
+        // rows g and g + 8 of tile ks are columns of V (see code_pairs, nibble_pairs)
         const int d = FMT == kInt4 ? (ks >> 1) * 32 + 4 * g + 2 * (ks & 1) : ks * 16 + 2 * g;
         *reinterpret_cast<float2 *>(dst + d) = make_float2(o[nt][ks][e] * f, o[nt][ks][e + 2] * f);
       }
@@ -512,7 +534,7 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
 #pragma unroll
     for (int k = 0; k < W; ++k) {
       sum += s_o[(k * Sh::kCols + col) * Sh::kOStride + d];
-      if (SPLIT) sum += s_o[(k * Sh::kCols + col + 4) * Sh::kOStride + d];
+      if (SPLIT && rest) sum += s_o[(k * Sh::kCols + col + 4) * Sh::kOStride + d];
     }
     s_o[r * Sh::kOStride + d] = sum;
   }

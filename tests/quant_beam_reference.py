@@ -38,7 +38,7 @@ def quantise(x, fmt):
             continue
         if span < TINY:
             continue
-        inv, scale[i] = f32(top / span), f32(span / top)
+        inv, scale[i] = f32(f32(f32(1) / span) * top), f32(span * f32(f32(1) / top))
         if fmt == "e4m3":
             y = (r * inv).astype(f32).astype(np.float64)
             # nearest value, halves to the even code

@@ -184,7 +184,7 @@ def test_reference_quantise_pins():
     x = torch.tensor([[1.0, -2.0, 0.5, 0.0], [0.0, 0.0, 0.0, 0.0], [math.inf, 1.0, 2.0, 3.0], [1e-40, 0, 0, 0]])
     c, s, _ = ref.quantise(x, "int8")
     assert c[0].tolist() == [64, -127, 32, 0]                              # 63.5 -> 64, 31.75 -> 32
-    assert s[0] == torch.tensor(2.0 / 127).float().double() and s[1] == 0 and s[3] == 0 and s[2].isnan()
+    assert s[0] == (torch.tensor(2.0) * torch.tensor(1 / 127.0)).double() and s[1] == 0 and s[3] == 0 and s[2].isnan()
     c, s, z = ref.quantise(torch.tensor([[-1.0, 2.0, 0.0, 0.5], [3.0, 1.0, 1.5, 0.2]]), "int4")
     assert z.tolist() == [5, 0] and c[0].tolist() == [0, 15, 5, 7] and c[1].tolist() == [15, 5, 8, 1]   # 2.5 -> 2, 7.5 -> 8
     g = torch.Generator().manual_seed(0)
