@@ -137,8 +137,11 @@ static pkv_status launch_simt_t(const QuantDecodeArgs &a, pkv_quant_format fmt, 
 }
 
 struct QuantPlan {
-  int heads, chunks;               // query heads of a CTA, head groups of a KV head
-  int P, max_parts, most_parts;    // keys of a part, parts of this call, of any call of these sizes
+  bool mma;                        // tensor cores
+  int heads, chunks;               // query heads of a unit (a CTA), head groups of a KV head
+  int P, max_parts;                // CUDA cores: keys of a part, parts
+  int grid, least, team;           // tensor cores: CTAs, tiles that a warp takes at least, warps on the same tokens
+  size_t bytes;                    // workspace
 };
 
 static bool quant_sizes_ok(int B, int H, int KVH, int D, int bs, int max_blocks, int max_n, int partition_size) {
@@ -160,40 +163,57 @@ static long long quant_parts_wanted(long long units, long long slots, long long 
   return std::max<long long>(1, std::min<long long>({2 * slots / units, kQdAutoParts, ceil_div(span, 128)}));
 }
 
-static QuantPlan quant_plan(int B, int H, int KVH, int heads, long long span, int partition_size) {
-  QuantPlan p;
-  p.heads = std::min(heads, H / KVH);
-  p.chunks = (int)ceil_div(H / KVH, p.heads);
-  const long long units = (long long)B * KVH * p.chunks;
+static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// CUDA cores: `cap` keys at most, `span` of them visible.
+static void simt_plan(int B, int H, int KVH, int D, long long span, int partition_size, QuantPlan *p) {
+  p->heads = std::min(kQdHeads, H / KVH);
+  p->chunks = (int)ceil_div(H / KVH, p->heads);
+  const long long units = (long long)B * KVH * p->chunks;
   long long P = partition_size;
   if (P == 0) P = std::max<long long>(128, ceil_div(ceil_div(span, quant_parts_wanted(units, 2 * kQdSms, span)), 128) * 128);
   P = std::max(P, ceil_div(ceil_div(span, kQdMaxParts), 128) * 128);
   // more units than the workspace counts: whole
   if (units > kChunkCnt - kChunkCntFirst) P = ceil_div(span, 128) * 128;
-  p.P = (int)std::min(P, ceil_div(span, 128) * 128);
-  // (parts are counted from the last multiple of 32 before the first key)
-  p.max_parts = units > kChunkCnt - kChunkCntFirst ? 1 : (int)ceil_div(span, p.P);
-  return p;
+  p->P = (int)std::min(P, ceil_div(span, 128) * 128);
+  p->max_parts = (int)ceil_div(span, p->P);
+}
+static size_t simt_bytes(int B, int H, int D, long long parts) {
+  const size_t rows = (size_t)B * H;
+  return kChunkCnt * sizeof(int) +
+         (parts > 1 ? 2 * align256(rows * parts * sizeof(float)) + align256(rows * parts * (size_t)D * sizeof(float)) : 0);
 }
 
-static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-static size_t quant_ws_bytes(int B, int H, int D, long long parts) {
-  size_t bytes = kChunkCnt * sizeof(int);
-  const size_t rows = (size_t)B * H;
-  if (parts > 1) bytes += 2 * align256(rows * parts * sizeof(float)) + align256(rows * parts * (size_t)D * sizeof(float));
-  return bytes;
+// Tensor cores: query heads of a unit are four where a head has two columns of
+// the product (fp32, or no more heads than that), else eight.
+static bool mma_split(pkv_dtype dt, int G) { return dt == PKV_F32 || G <= 4; }
+static bool mma_shape(pkv_quant_format fmt, int D) {
+  return D == 64 || D == 96 || D == 128 || D == 192 || D == 256 || (D == 80 && fmt != PKV_QUANT_INT4);
 }
+static long long mma_tiles(int B, long long span) { return B * (ceil_div(span, kQmTok) + 1); }
+static void mma_plan(int B, int H, int KVH, int D, long long span, int partition_size, pkv_quant_format fmt, bool split,
+                     QuantPlan *p) {
+  p->heads = split ? 4 : 8;
+  p->chunks = (int)ceil_div(H / KVH, p->heads);
+  p->least = std::max(1, partition_size / kQmTok);
+  const int params = fmt == PKV_QUANT_INT4 ? 8 : 4, row = fmt == PKV_QUANT_INT4 ? D / 2 : D;
+  // one CTA resident everywhere, but no more warps than tiles
+  const int units = KVH * p->chunks;
+  p->team = units % 8 == 0 ? 8 : units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
+  const long long tiles = ceil_div(mma_tiles(B, span), p->least) * units;
+  p->grid = (int)std::min<long long>((long long)kQdSms * qm_ctas(row, params), 2 * ceil_div(tiles, 2 * kQmWarps));
+  p->bytes = kChunkCnt * sizeof(int) + (size_t)2 * p->grid * kQmWarps * p->heads * (D + 2) * sizeof(float);
+}
+constexpr int kQdLevels = 3;     // of joining: 16^3 warps
+static_assert(kChunkCntFirst + kQdLevels * 3 * kQdSms * kQmWarps <= kChunkCnt && 3 * kQdSms * kQmWarps <= 16 * 16 * 16,
+              "the counters fit the workspace's");
 
 }  // namespace pkv
 namespace pkv {
 
-pkv_status launch_quant_mma_int8(const QuantDecodeArgs &a, int tiles, bool split, pkv_dtype dt, cudaStream_t stream);
-pkv_status launch_quant_mma_e4m3(const QuantDecodeArgs &a, int tiles, bool split, pkv_dtype dt, cudaStream_t stream);
-pkv_status launch_quant_mma_int4(const QuantDecodeArgs &a, int tiles, bool split, pkv_dtype dt, cudaStream_t stream);
-
-// Query heads of a CTA: four where a head is split in two halves (fp32, or no
-// more of them than that), else eight.
-static int quant_heads(pkv_dtype dt, int G, bool mma) { return !mma || dt == PKV_F32 || G <= 4 ? 4 : 8; }
+pkv_status launch_quant_mma_int8(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream);
+pkv_status launch_quant_mma_e4m3(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream);
+pkv_status launch_quant_mma_int4(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream);
 
 }  // namespace pkv
 
@@ -205,14 +225,19 @@ PKV_API size_t pkv_quant_decode_workspace_size(int B, int H, int num_kv_heads, i
                                                int max_blocks, int max_context_len, int partition_size) {
   if (!quant_sizes_ok(B, H, num_kv_heads, head_dim, block_size, max_blocks, max_context_len, partition_size)) return 0;
   const long long cap = quant_cap(block_size, max_blocks, max_context_len);
-  long long most = 1;
-  for (int heads = 4; heads <= 8; heads += 4) {
-    const long long units = (long long)B * num_kv_heads * ceil_div(H / num_kv_heads, std::min(heads, H / num_kv_heads));
-    // (a window's shorter span never has more parts than are wanted here)
-    most = std::max(most, partition_size ? std::min<long long>(kQdMaxParts, ceil_div(cap, partition_size))
-                                         : quant_parts_wanted(units, 2 * kQdSms, cap));
-  }
-  return quant_ws_bytes(B, H, head_dim, most);
+  const int G = H / num_kv_heads;
+  // (a window's shorter span never has more parts than are wanted here)
+  const long long units = (long long)B * num_kv_heads * ceil_div(G, std::min(kQdHeads, G));
+  size_t most = simt_bytes(B, H, head_dim, partition_size ? std::min<long long>(kQdMaxParts, ceil_div(cap, partition_size))
+                                                          : quant_parts_wanted(units, 2 * kQdSms, cap));
+  for (int f = PKV_QUANT_INT8; f <= PKV_QUANT_INT4; ++f)
+    for (int split = 0; split < 2; ++split) {
+      if (!mma_shape((pkv_quant_format)f, head_dim)) continue;
+      QuantPlan p;
+      mma_plan(B, H, num_kv_heads, head_dim, cap, partition_size, (pkv_quant_format)f, split, &p);
+      most = std::max(most, p.bytes);
+    }
+  return most;
 }
 
 PKV_API pkv_status pkv_quant_decode_attention(
@@ -237,16 +262,23 @@ PKV_API pkv_status pkv_quant_decode_attention(
       !at(context_lens, 4) || !at(err_flags, 4))
     return PKV_ERR_INVALID_ARG;
   const int64_t cache_rows = num_blocks * block_size * num_kv_heads;
-  const bool wide = head_dim == 64 || head_dim == 96 || head_dim == 128 || head_dim == 192 || head_dim == 256 ||
-                    (head_dim == 80 && fmt != PKV_QUANT_INT4);
-  const int pbytes = fmt == PKV_QUANT_INT4 ? 8 : 4;
-  const bool mma = wide && at(k_codes, 16) && at(v_codes, 16) && at(k_params, pbytes) && at(v_params, pbytes) &&
-                   cache_rows < 0xffffffffLL;
+  const int pbytes = fmt == PKV_QUANT_INT4 ? 8 : 4, G = H / num_kv_heads;
   const long long cap = quant_cap(block_size, max_blocks, max_context_len);
+  // (keys are walked from a multiple of 32 on)
   const long long span = window > 0 ? std::min(cap, (long long)window + 31) : cap;
-  const QuantPlan plan = quant_plan(B, H, num_kv_heads, quant_heads(dt, H / num_kv_heads, mma), span, partition_size);
-  if ((long long)plan.chunks * num_kv_heads * plan.max_parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  const size_t need = quant_ws_bytes(B, H, head_dim, plan.max_parts);
+  QuantPlan plan = {};
+  // tensor cores where 16-byte copies can read the rows, rows have 32-bit
+  // numbers and a KV head's tiles are counted in 32 bits
+  plan.mma = mma_shape(fmt, head_dim) && at(k_codes, 16) && at(v_codes, 16) && at(k_params, pbytes) &&
+             at(v_params, pbytes) && cache_rows < 0xffffffffLL && mma_tiles(B, span) <= 0x7fffffffLL;
+  if (plan.mma) {
+    mma_plan(B, H, num_kv_heads, head_dim, span, partition_size, fmt, mma_split(dt, G), &plan);
+  } else {
+    simt_plan(B, H, num_kv_heads, head_dim, span, partition_size, &plan);
+    plan.bytes = simt_bytes(B, H, head_dim, plan.max_parts);
+    if ((long long)plan.chunks * num_kv_heads * plan.max_parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  }
+  const size_t need = plan.bytes;
   if (!workspace || workspace_bytes < need || !at(workspace, 256)) return PKV_ERR_WORKSPACE;
   const size_t rows_bytes = (size_t)B * H * head_dim * el;
   const size_t codes = quant_codes_bytes(fmt, cache_rows, head_dim), params = quant_params_bytes(fmt, cache_rows);
@@ -290,12 +322,17 @@ PKV_API pkv_status pkv_quant_decode_attention(
   a.kp = k_params;
   a.vp = v_params;
   a.heads = plan.heads;
+  a.grid = plan.grid;
+  a.least = plan.least;
+  a.team = plan.team;
   while ((1LL << a.bs_shift) < block_size) ++a.bs_shift;
   a.bs_mul = (uint32_t)((((1ULL << a.bs_shift) - (uint64_t)block_size) << 32) / (uint64_t)block_size + 1);
   char *ws = static_cast<char *>(workspace);
   c.ws_cnt = reinterpret_cast<int *>(ws);
   ws += kChunkCnt * sizeof(int);
-  if (plan.max_parts > 1) {
+  if (plan.mma) {
+    a.states = reinterpret_cast<float *>(ws);
+  } else if (plan.max_parts > 1) {
     const size_t rows = (size_t)B * H;
     c.ws_m = reinterpret_cast<float *>(ws);
     ws += align256(rows * plan.max_parts * sizeof(float));
@@ -304,12 +341,12 @@ PKV_API pkv_status pkv_quant_decode_attention(
     c.ws_o = reinterpret_cast<float *>(ws);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (mma) {
-    const bool split = dt == PKV_F32 || c.G <= 4;
+  if (plan.mma) {
+    const bool split = mma_split(dt, G);
     switch (fmt) {
-      case PKV_QUANT_INT8: return launch_quant_mma_int8(a, 1, split, dt, s);
-      case PKV_QUANT_E4M3: return launch_quant_mma_e4m3(a, 1, split, dt, s);
-      case PKV_QUANT_INT4: return launch_quant_mma_int4(a, 1, split, dt, s);
+      case PKV_QUANT_INT8: return launch_quant_mma_int8(a, split, dt, s);
+      case PKV_QUANT_E4M3: return launch_quant_mma_e4m3(a, split, dt, s);
+      case PKV_QUANT_INT4: return launch_quant_mma_int4(a, split, dt, s);
     }
   }
   switch (dt) {

@@ -1,10 +1,8 @@
 // pkv_quant_decode.cuh -- what the decode kernels over a quantised cache share.
 //
-// One new token per sequence.  Rows are the query heads of a KV head, `heads`
-// of them a CTA (a.chunks head groups a KV head); a CTA takes a part of the
-// visible keys [lo, n), lo = max(0, n - window), parts counted from lo & ~31.
-// The parts' states (max, sum, weighted sum in log2 units) are joined as in
-// chunk attention.
+// One new token per sequence.  Rows are the query heads of a KV head, a few of
+// them a unit (a.chunks head groups a KV head).  The visible keys are
+// [lo, n), lo = max(0, n - window), walked from lo & ~31 on.
 #pragma once
 
 #include "pkv_chunk.cuh"
@@ -12,11 +10,29 @@
 
 namespace pkv {
 
+// Shape of the tensor-core kernel's ring: tokens and bytes of a tile, tiles
+// ahead, CTAs of kQmWarps warps that fit an SM's 228 KB (1 KB of it a CTA's
+// own; more than three would cost registers).
+constexpr int kQmTok = 32;
+constexpr int kQmWarps = 4;
+constexpr int kQmGroups = 32 * kQmWarps;   // groups of sequences whose first tiles a CTA keeps
+constexpr int kQmPre = 4 * (kQmGroups + 2 + kQmWarps);
+constexpr int qm_stage(int row, int params) { return kQmTok * 2 * (16 * ((row / 16) | 1) + params); }
+constexpr int qm_smem(int row, int params, int stages) { return kQmWarps * stages * qm_stage(row, params) + kQmPre; }
+constexpr int qm_fit(int row, int params, int stages) {
+  const int n = 228 * 1024 / (qm_smem(row, params, stages) + 1024);
+  return n > 3 ? 3 : n;
+}
+constexpr int qm_stages(int row, int params) { return qm_fit(row, params, 3) == 3 ? 3 : 2; }
+constexpr int qm_ctas(int row, int params) { return qm_fit(row, params, qm_stages(row, params)); }
+
 struct QuantDecodeArgs {
   ChunkArgs c;                     // q, out, tables, lens, sizes, score form, split, workspace
   const uint8_t *k, *v;            // codes
   const float *kp, *vp;            // parameters
-  int heads;                       // query heads of a CTA
+  int heads;                       // query heads of a unit
+  float *states;                   // tensor cores: two places a warp for states to be joined
+  int grid, least, team;           // its CTAs; tiles that a warp takes at least; warps that walk the same tokens
   uint32_t bs_mul;                 // t / block_size = (umulhi(t, bs_mul) + t) >> bs_shift for t < 2^31
   int bs_shift;
 };

@@ -3,8 +3,8 @@
 
 namespace pkv {
 
-pkv_status launch_quant_mma_int4(const QuantDecodeArgs &a, int tiles, bool split, pkv_dtype dt, cudaStream_t stream) {
-  return launch_qm_f<kInt4>(a, tiles, split, dt, stream);
+pkv_status launch_quant_mma_int4(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream) {
+  return launch_qm_f<kInt4>(a, split, dt, stream);
 }
 
 }  // namespace pkv

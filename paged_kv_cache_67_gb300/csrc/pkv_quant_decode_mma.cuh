@@ -24,37 +24,38 @@
 // The running maximum is raised only when some score passes it by 2^8: one vote
 // a tile of 32 tokens instead of three exchanges a head.
 //
-// CTA = 4 warps; warp w takes tiles w, w + 4, ... of 32 tokens through a ring of
-// its own in shared memory, filled by 16-byte cp.async row by row (a row's place
-// comes from the block table, so any block size will do), with no barrier
-// between the warps.  Rows are padded to an odd number of 16-byte chunks: the
-// 4-byte fragment loads of K and the transposing ldmatrix of V both touch every
-// bank once.
+// Work.  All tiles of all units -- a unit is a sequence's visible keys for one
+// head group of a KV head -- stand in one line, and every warp of a grid that
+// fills the GPU once takes an equal stretch of it: lengths may be as ragged as
+// they like.  Warps run by themselves, with no barrier: each has a ring in shared
+// memory, filled ahead (across the ends of units too) by 16-byte cp.async row by
+// row -- a row's place comes from the block table, so any block size will do.
+// A warp that has a whole unit writes its output.  The others leave the states
+// (max, sum, weighted sum) of the unit they began in and the one they end in, two
+// places a warp, and the last one done of up to 16 neighbours joins them, then of
+// up to 16 such groups, until the unit is one.
+//
+// Rows in the ring are padded to an odd number of 16-byte chunks: the 4-byte
+// fragment loads of K and the transposing ldmatrix of V both touch every bank once.
 #pragma once
 
 #include "pkv_quant_decode.cuh"
 
 namespace pkv {
 
-constexpr int kQmTok = 32;
-constexpr int kQmWarps = 4;
+constexpr int kQmFan = 16;                 // states joined at once
 
-template <int D, int FMT, int NT>
+template <int D, int FMT>
 struct QmShape {
   static constexpr int kRow = quant_row_bytes<FMT>(D);
   static constexpr int kChunks = kRow / 16;
   static constexpr int kStride = 16 * (kChunks | 1);                  // an odd number of chunks
   static constexpr int kParams = 4 * quant_params<FMT>();             // bytes a row
-  static constexpr int kStage = kQmTok * 2 * (kStride + kParams);
-  static constexpr int kCols = 8 * NT;
-  static constexpr int kOStride = D + 4;
-  // two CTAs an SM and more, whichever the registers allow
-  static constexpr int kStages = kStage * kQmWarps * 3 <= 110 * 1024 ? 3 : 2;
-  static constexpr int kRing = kStages * kStage * kQmWarps;
-  static constexpr int kOut = kQmWarps * kCols * kOStride * 4;
-  static constexpr int kMain = kRing > kOut ? kRing : kOut;
-  static constexpr int kSmem = kMain + 4 * (2 * kQmWarps * kCols + 2 * kCols + 4);
-  static_assert(kMain >= 1024, "the join's weights fit");
+  static constexpr int kStage = qm_stage(kRow, kParams);
+  static constexpr int kStages = qm_stages(kRow, kParams);
+  static constexpr int kRing = kStages * kStage;                      // a warp's
+  static constexpr int kSmem = qm_smem(kRow, kParams, kStages);
+  static constexpr int kCtas = qm_ctas(kRow, kParams);
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
@@ -97,6 +98,19 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// (w & m) ^ c and (w & m) | c in one instruction each (written out, or two
+// constants become two instructions).
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(m), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t m, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(m), "r"(c));
+  return r;
+}
+
 // Four codes of a word (one K row; of V's ldmatrix word, two columns of token
 // 2t and the same of token 2t + 1) as two pairs of halves.
 // int8: bytes (0, 2) and (1, 3): a byte with its top bit turned, code + 128, in
@@ -105,8 +119,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 template <int FMT, bool V>
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &p0, uint32_t &p1) {
   if constexpr (FMT == kInt8) {
-    p0 = hsub2_u((w & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
-    p1 = hsub2_u(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
+    p0 = hsub2_u(and_xor(w, 0x00ff00ffu, 0x64806480u), 0x64806480u);
+    p1 = hsub2_u(and_xor(w >> 8, 0x00ff00ffu, 0x64806480u), 0x64806480u);
   } else {
     if (V) w = __byte_perm(w, 0, 0x3120);
     p0 = e4m3x2_to_half2((uint16_t)w);
@@ -119,10 +133,10 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &p0, uint32_t &p
 __device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t z1, uint32_t z16, uint32_t (&p)[4]) {
   const uint32_t u = w >> 8;
   constexpr uint32_t kSixteenth = 0x2c002c00u;
-  p[0] = hsub2_u((w & 0x000f000fu) | 0x64006400u, z1);
-  p[1] = hfma2_u((w & 0x00f000f0u) | 0x64006400u, kSixteenth, z16);
-  p[2] = hsub2_u((u & 0x000f000fu) | 0x64006400u, z1);
-  p[3] = hfma2_u((u & 0x00f000f0u) | 0x64006400u, kSixteenth, z16);
+  p[0] = hsub2_u(and_or(w, 0x000f000fu, 0x64006400u), z1);
+  p[1] = hfma2_u(and_or(w, 0x00f000f0u, 0x64006400u), kSixteenth, z16);
+  p[2] = hsub2_u(and_or(u, 0x000f000fu, 0x64006400u), z1);
+  p[3] = hfma2_u(and_or(u, 0x00f000f0u, 0x64006400u), kSixteenth, z16);
 }
 
 // t / bs for t < 2^31 by a multiplication (mul, shift from the host).
@@ -130,45 +144,191 @@ __device__ __forceinline__ int div_by(int t, uint32_t mul, int shift) {
   return (int)((__umulhi((uint32_t)t, mul) + (uint32_t)t) >> shift);
 }
 
-template <int D, int FMT, int NT, bool SPLIT>
-__global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(const __grid_constant__ QuantDecodeArgs a,
-                                                                             const int dt) {
-  static_assert(NT == 1 || !SPLIT, "a split head's columns are in one tile");
-  using Sh = QmShape<D, FMT, NT>;
-  constexpr int W = kQmWarps, S = Sh::kStages, kSteps = D / 16, kHeads = SPLIT ? 4 : 8 * NT;
-  extern __shared__ __align__(16) uint8_t ring[];
-  float *s_wm = reinterpret_cast<float *>(ring + Sh::kMain);     // [W][cols] maxima, sums
-  float *s_wl = s_wm + W * Sh::kCols;
-  float *s_m = s_wl + W * Sh::kCols;                             // [cols]
-  float *s_l = s_m + Sh::kCols;
-  int *s_scratch = reinterpret_cast<int *>(s_l + Sh::kCols);
+// Four consecutive elements of a query, q 16-byte aligned or not.
+__device__ __forceinline__ float4 q_four(const void *q, size_t at, int dt, bool aligned) {
+  if (dt == PKV_F32) {
+    const float *p = reinterpret_cast<const float *>(q) + at;
+    return aligned ? __ldg(reinterpret_cast<const float4 *>(p)) : make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+  }
+  const unsigned short *p = reinterpret_cast<const unsigned short *>(q) + at;
+  uint2 w;
+  if (aligned)
+    w = __ldg(reinterpret_cast<const uint2 *>(p));
+  else
+    w = make_uint2(__ldg(p) | ((uint32_t)__ldg(p + 1) << 16), __ldg(p + 2) | ((uint32_t)__ldg(p + 3) << 16));
+  if (dt == PKV_BF16)
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  const float2 a = half2_to_float2(w.x), b = half2_to_float2(w.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Two (four) neighbouring elements of an output row.
+__device__ __forceinline__ void put_two(void *out, size_t at, int dt, bool aligned, float x, float y) {
+  if (dt == PKV_F32) {
+    float *p = reinterpret_cast<float *>(out) + at;
+    if (aligned) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); return; }
+    p[0] = x; p[1] = y;
+    return;
+  }
+  uint32_t w;
+  if (dt == PKV_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    w = *reinterpret_cast<const uint32_t *>(&v);
+  } else {
+    w = half2_bits(x, y);
+  }
+  unsigned short *p = reinterpret_cast<unsigned short *>(out) + at;
+  if (aligned) { *reinterpret_cast<uint32_t *>(p) = w; return; }
+  p[0] = (unsigned short)w; p[1] = (unsigned short)(w >> 16);
+}
+
+// A place in the line of tiles: tile `tile` of `tiles` of a team's unit `unit` of
+// sequence b, this warp's KV head.
+struct QmAt {
+  int b, unit, kvh, tile, tiles, first, n, base;
+};
+
+// Sequence b's visible keys and tiles of them.
+__device__ __forceinline__ void qm_keys(const ChunkArgs &c, int b, QmAt &s) {
+  int n = __ldg(c.lens + b);
+  n = min(max(n, 0), c.max_n);             // (max_n is at most the table's keys)
+  s.n = n;
+  s.first = c.window > 0 ? max(0, n - c.window) : 0;
+  s.base = s.first & ~(kQmTok - 1);
+  s.tiles = (n - s.base + kQmTok - 1) / kQmTok;
+}
+
+template <int D, int FMT, bool SPLIT>
+__global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
+    pkv_quant_decode_mma_kernel(const __grid_constant__ QuantDecodeArgs a, const int dt) {
+  using Sh = QmShape<D, FMT>;
+  constexpr int S = Sh::kStages, kSteps = D / 16, kHeads = SPLIT ? 4 : 8;
+  extern __shared__ __align__(16) uint8_t smem[];
+  int *s_first = reinterpret_cast<int *>(smem + kQmWarps * Sh::kRing);      // [groups + 1] tiles of one (KV head, head group)
+  int *s_warp = s_first + kQmGroups + 2;
   const ChunkArgs &c = a.c;
-  const QuantPart p = quant_part(a);
-  if (p.nparts == 0) return;
   const bool rest = SPLIT ? dt != PKV_BF16 : dt == PKV_F16;   // weights of two parts
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-  const int ntiles = p.t1 > p.t0 ? (p.t1 - p.t0 + kQmTok - 1) / kQmTok : 0;
-  const int mine = ntiles > w ? (ntiles - w + W - 1) / W : 0;
-  const int first = max(p.t0, p.lo);
-  uint8_t *my_ring = ring + (size_t)w * S * Sh::kStage;
-  const uint32_t ring_at = smem_u32(my_ring);
+  const bool q16 = reinterpret_cast<uintptr_t>(c.q) % 16 == 0, out8 = reinterpret_cast<uintptr_t>(c.out) % 8 == 0;
 
-  // Tile i of this warp into stage i mod S.  Lane r looks up token r's block one
-  // tile ahead, so that the table entry is there when it is needed; what is
-  // not visible is filled with zeros and not read.  (Rows of the cache are fewer
-  // than 2^32 - 1 here.)
+  // ---- the line: first tiles of kQmGroups groups of sequences
+  const int per = (c.B + kQmGroups - 1) / kQmGroups;
+  {
+    int sum = 0;
+    for (int b = threadIdx.x * per; b < min(c.B, (int)(threadIdx.x + 1) * per); ++b) {
+      QmAt s;
+      qm_keys(c, b, s);
+      sum += s.tiles;                       // (fewer than 2^31 in all: the host's check)
+      if (blockIdx.x == 0) {
+        const int n = __ldg(c.lens + b);
+        if (n < 0) raise_flag(c.err, PKV_FLAG_CONTEXT_NEGATIVE);
+        if ((long long)n > (long long)c.max_blocks * c.bs) raise_flag(c.err, PKV_FLAG_CONTEXT_TOO_LONG);
+        else if (n > c.max_n) raise_flag(c.err, PKV_FLAG_CONTEXT_OVER_HINT);
+      }
+    }
+    int scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += x;
+    }
+    if (lane == 31) s_warp[w] = scan;
+    __syncthreads();
+    for (int k = 0; k < w; ++k) scan += s_warp[k];
+    s_first[threadIdx.x + 1] = scan;
+    if (threadIdx.x == 0) s_first[0] = 0;
+    __syncthreads();
+  }
+  // sequences without a visible key
+  for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+    QmAt s;
+    qm_keys(c, b, s);
+    if (s.tiles == 0)
+      for (int i = threadIdx.x; i < c.H * D / 2; i += 32 * kQmWarps) put_two(c.out, (size_t)b * c.H * D + 2 * i, dt, out8, 0.f, 0.f);
+  }
+  // A team of `team` neighbouring warps (of one CTA, or two) walks the same
+  // tokens for neighbouring units, so that a token's rows, which lie together,
+  // are read together; the line is one of teams' units.
+  const int team = a.team, per_b = c.KVH * c.chunks / team;
+  const long long total = (long long)s_first[kQmGroups] * per_b;
+  const long long warps = (long long)gridDim.x * kQmWarps;
+  const long long teams = warps / team;
+  const long long share = max((total + teams - 1) / teams, (long long)a.least);
+  const int mate = team > kQmWarps ? (blockIdx.x % (team / kQmWarps)) * kQmWarps + w : w % team;
+  // neighbours in the line are on different SMs: short lines use them all
+  const int me = team > kQmWarps ? blockIdx.x / (team / kQmWarps) : w / team * gridDim.x + blockIdx.x;
+  const long long begin = me * share;
+  if (begin >= total || me >= teams) return;
+  const int mine = (int)min(share, total - begin);
+
+  QmAt cur;
+  long long unit0;                          // the current unit's first tile in the line
+  {
+    // the group by bisection, its sequence 32 at a time, then the unit
+    int lo = 0, hi = kQmGroups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)s_first[mid] * per_b <= begin) lo = mid; else hi = mid - 1;
+    }
+    long long at = (long long)s_first[lo] * per_b;
+    int b = lo * per;
+    for (;;) {
+      QmAt s;
+      s.tiles = 0;
+      if (b + lane < c.B) qm_keys(c, b + lane, s);
+      int scan = s.tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, at + (long long)scan * per_b > begin);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        at += (long long)(__shfl_sync(0xffffffffu, scan, k) - __shfl_sync(0xffffffffu, s.tiles, k)) * per_b;
+        b += k;
+        break;
+      }
+      at += (long long)__shfl_sync(0xffffffffu, scan, 31) * per_b;
+      b += 32;                              // (begin < total: some sequence has the tile)
+    }
+    qm_keys(c, b, cur);
+    cur.b = b;
+    const int off = (int)(begin - at), unit = off / cur.tiles;
+    cur.tile = off - unit * cur.tiles;
+    cur.unit = unit;
+    cur.kvh = (unit * team + mate) / c.chunks;
+    unit0 = begin - cur.tile;
+  }
+  // the next tile's place; whether it is another unit's
+  auto advance = [&](QmAt &s) {
+    if (++s.tile < s.tiles) return false;
+    s.tile = 0;
+    if (++s.unit == per_b) {
+      s.unit = 0;
+      do qm_keys(c, ++s.b, s); while (s.tiles == 0);   // (only called where a tile follows)
+    }
+    s.kvh = (s.unit * team + mate) / c.chunks;
+    return true;
+  };
+
+  // ---- the ring.  Tile i of this warp into stage i mod S.  Lane r looks up
+  // token r's block one tile ahead, so that the table entry is there when it is
+  // needed; what is not visible is filled with zeros and not read.  (Rows of the
+  // cache are fewer than 2^32 - 1 here.)
   constexpr bool kEven = 32 % Sh::kChunks == 0;          // a lane keeps to one chunk of the rows
-  const int32_t *table = c.tables + (size_t)p.b * c.max_blocks;
+  const uint32_t ring_at = smem_u32(smem + w * Sh::kRing);
   const uint8_t *k_at = a.k + lane % Sh::kChunks * 16, *v_at = a.v + lane % Sh::kChunks * 16;
   const uint32_t st_even = ring_at + lane / Sh::kChunks * Sh::kStride + lane % Sh::kChunks * 16;
+  QmAt ahead = cur;
   int next_phys = 0, next_off = -1;
-  auto look_up = [&](int i) {
-    const int t = p.t0 + kQmTok * (w + W * i) + lane;
+  auto look_up = [&](const QmAt &s) {
+    const int t = s.base + kQmTok * s.tile + lane;
     next_off = -1;
-    if (i < mine && t >= first && t < p.t1) {
+    if (t >= s.first && t < s.n) {
       const int lb = div_by(t, a.bs_mul, a.bs_shift);
       next_off = t - lb * c.bs;
-      next_phys = __ldg(table + lb);
+      next_phys = __ldg(c.tables + (size_t)s.b * c.max_blocks + lb);
     }
   };
   auto issue = [&](int i) {
@@ -178,9 +338,9 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
         raise_flag(c.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
         in = false;
       }
-      const uint32_t phys = (uint32_t)next_phys, off = (uint32_t)next_off;
-      const uint32_t row = in ? (phys * (uint32_t)c.bs + off) * (uint32_t)c.KVH + (uint32_t)p.kvh : 0xffffffffu;
-      const uint32_t num = in ? (phys * (uint32_t)c.KVH + (uint32_t)p.kvh) * (uint32_t)c.bs + off : 0u;
+      const uint32_t phys = (uint32_t)next_phys, off = (uint32_t)next_off, kvh = (uint32_t)ahead.kvh;
+      const uint32_t row = in ? (phys * (uint32_t)c.bs + off) * (uint32_t)c.KVH + kvh : 0xffffffffu;
+      const uint32_t num = in ? (phys * (uint32_t)c.KVH + kvh) * (uint32_t)c.bs + off : 0u;
       const uint32_t stage = (i % S) * Sh::kStage, st = ring_at + stage;
       const uint32_t pa = st + 2 * kQmTok * Sh::kStride + lane * Sh::kParams;
       cp_async_small<Sh::kParams>(pa, a.kp + (size_t)num * quant_params<FMT>(), in ? Sh::kParams : 0);
@@ -205,93 +365,219 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
           cp_async16(to + kQmTok * Sh::kStride, a.v + at, has ? 16 : 0);
         }
       }
-      look_up(i + 1);
+      if (i + 1 < mine) {
+        advance(ahead);
+        look_up(ahead);
+      }
     }
     cp_async_commit();
   };
-  look_up(0);
+  look_up(ahead);
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(i);
 
-  // The queries, scaled, as the product's B: column g of a tile is a head (or
-  // what fp16 left of head g - 4); warp-wide maximum of a row's elements.
-  auto q_at = [&](int h, int d) {
-    const size_t i = ((size_t)p.b * c.H + p.head0 + h) * D + d;
-    return dt == PKV_F32 ? reinterpret_cast<const float *>(c.q)[i]
-         : dt == PKV_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(c.q)[i])
-                          : __half2float(reinterpret_cast<const __half *>(c.q)[i]);
-  };
+  // ---- a unit's state
   // scores in log2 units, or what their cap wants (see chunk_capped: its error
   // does for 16-bit types; chunk_cap)
   const int cap = !(c.cap_log2 > 0.f) ? kCapNone : dt != PKV_F32 && c.cap_log2 <= kCapShort ? kCapUsual : kCapLarge;
   const float score_unit = cap == kCapNone ? c.scale_log2 : cap == kCapUsual ? c.scale_y : 1.f;
-  uint32_t qf[NT][kSteps][2];
-  float qs[NT][2];
+  uint32_t qf[kSteps][2];
+  float qs[2], o[kSteps][4], m[2], l[2];
+  // O's unit is 2^(ve - kUnit): ve the largest exponent of a value's scale so far
+  // (fp32's biased one; from 2^-97 on, NaN and infinity aside)
+  constexpr int kUnit = 127 + 6;
+  int ve;
+  // The queries, scaled, as the product's B: column g is a head (or what fp16
+  // left of head g - 4).
+  auto start = [&]() {
+    const int head = ((cur.unit * team + mate) - cur.kvh * c.chunks) * kHeads + (SPLIT ? g & 3 : g);
+    const bool has = head < c.G, low = SPLIT && g >= 4;
+    const size_t row = ((size_t)cur.b * c.H + cur.kvh * c.G + head) * D;
+    float4 v[kSteps];
+    float big = 0.f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int col_head = SPLIT ? g & 3 : 8 * nt + g;
-    const bool has = col_head < p.rows, low = SPLIT && g >= 4;
-    float v[kSteps][4], big = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // the column of A's element (see code_pairs, nibble_pairs)
-        const int d = FMT == kInt4   ? (ks >> 1) * 32 + 8 * t4 + 2 * (ks & 1) + (e >> 1) + 4 * (e & 1)
-                      : FMT == kInt8 ? ks * 16 + 4 * t4 + (e >> 1) + 2 * (e & 1)
-                                     : ks * 16 + 4 * t4 + e;
-        v[ks][e] = has ? q_at(col_head, d) : 0.f;
-        big = fmaxf(big, fabsf(v[ks][e]));
-      }
+    for (int ks = 0; ks < kSteps; ++ks) {
+      // int4: a lane's eight columns of 32 are those of two steps
+      const int d = FMT == kInt4 ? (ks >> 1) * 32 + 8 * t4 + 4 * (ks & 1) : ks * 16 + 4 * t4;
+      v[ks] = has ? q_four(c.q, row + d, dt, q16) : make_float4(0.f, 0.f, 0.f, 0.f);
+      big = fmaxf(fmaxf(big, fmaxf(fabsf(v[ks].x), fabsf(v[ks].y))), fmaxf(fabsf(v[ks].z), fabsf(v[ks].w)));
+    }
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
     // 2^(14 - floor(log2 big)), both ends within fp32's exponents
     const int ex = min(max((__float_as_int(big) >> 23) - 127, -100), 100);
     const float up = __int_as_float((14 - ex + 127) << 23), down = __int_as_float((ex - 14 + 127) << 23);
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = v[ks][2 * e] * up, y = v[ks][2 * e + 1] * up;
-        if (low) {
-          x = dt == PKV_F32 ? x - __half2float(__float2half_rn(x)) : x;
-          y = dt == PKV_F32 ? y - __half2float(__float2half_rn(y)) : y;
-        }
-        qf[nt][ks][e] = half2_bits(x, y);
+    auto part = [&](float x, float y) {
+      x *= up;
+      y *= up;
+      if (low && dt == PKV_F32) {
+        x -= __half2float(__float2half_rn(x));
+        y -= __half2float(__float2half_rn(y));
       }
-    // this lane's score columns are 2 t4, 2 t4 + 1
-    qs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4) * score_unit;
-    qs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4) * score_unit;
-  }
-
-  float o[NT][kSteps][4] = {};
-  float m[NT][2], l[NT][2];
-  // O's unit is 2^(ve - kUnit): ve the largest exponent of a value's scale so far
-  // (fp32's biased one; from 2^-97 on, NaN and infinity aside)
-  constexpr int kUnit = 127 + 6;
-  int ve = 30;
+      return half2_bits(x, y);
+    };
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int ks = 0; ks < kSteps; ++ks) {
+      if constexpr (FMT == kInt4) {          // nibble pairs (i, i + 4): step 0 i = 0, 1, step 1 i = 2, 3
+        if (ks & 1) continue;
+        const float4 &x = v[ks], &y = v[ks + 1];
+        qf[ks][0] = part(x.x, y.x);
+        qf[ks][1] = part(x.y, y.y);
+        qf[ks + 1][0] = part(x.z, y.z);
+        qf[ks + 1][1] = part(x.w, y.w);
+      } else if constexpr (FMT == kInt8) {
+        qf[ks][0] = part(v[ks].x, v[ks].z);
+        qf[ks][1] = part(v[ks].y, v[ks].w);
+      } else {
+        qf[ks][0] = part(v[ks].x, v[ks].y);
+        qf[ks][1] = part(v[ks].z, v[ks].w);
+      }
+    }
+    // this lane's score columns are 2 t4, 2 t4 + 1
+    qs[0] = __shfl_sync(0xffffffffu, down, 8 * t4) * score_unit;
+    qs[1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4) * score_unit;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+    ve = 30;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) o[ks][0] = o[ks][1] = o[ks][2] = o[ks][3] = 0.f;
+  };
+
+  // ---- the end of this warp's part of the unit
+  float *ws_m = a.states, *ws_l = ws_m + 2 * warps * kHeads, *ws_o = ws_l + 2 * warps * kHeads;
+  auto finish = [&]() {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m[nt][e] = -INFINITY;
-      l[nt][e] = 0.f;
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], sh);
     }
+    if (SPLIT && rest) {                     // a head's two columns
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[ks][e] += __shfl_xor_sync(0xffffffffu, o[ks][e], 2);
+    }
+    const int chunk = (cur.unit * team + mate) - cur.kvh * c.chunks, rows = min(kHeads, c.G - chunk * kHeads);
+    const size_t out_row = (size_t)cur.b * c.H + cur.kvh * c.G + chunk * kHeads;
+    const long long first = unit0 / share, last = (unit0 + cur.tiles - 1) / share;
+    const float unit = exp2f((float)(ve - kUnit));
+    // columns of V that tile ks's rows g and g + 8 are (see code_pairs, nibble_pairs)
+    auto column = [&](int ks) { return FMT == kInt4 ? (ks >> 1) * 32 + 4 * g + 2 * (ks & 1) : ks * 16 + 2 * g; };
+    if (first == last) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 2 * t4 + e;
+        if (col >= rows) continue;
+        const float inv = unit / l[e];
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+          put_two(c.out, (out_row + col) * D + column(ks), dt, out8, o[ks][e] * inv, o[ks][e + 2] * inv);
+      }
+      return;
+    }
+    // place of fragment f (team first + f): its own end, the others' beginning
+    auto place = [&](long long f) { return ((2 * (first + f) + (f == 0)) * team + mate) * kHeads; };
+    long long f = me - first;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = 2 * t4 + e;
+      if (col >= rows) continue;
+      const size_t at = place(f) + col;
+      if (g == 0) {
+        __stcg(ws_m + at, m[e]);
+        __stcg(ws_l + at, l[e]);
+      }
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+        __stcg(reinterpret_cast<float2 *>(ws_o + at * D + column(ks)), make_float2(o[ks][e] * unit, o[ks][e + 2] * unit));
+    }
+    long long count = last - first + 1, stride = 1;
+    for (int level = 0; count > 1; ++level) {
+      const long long group = f / kQmFan;
+      const int size = (int)min((long long)kQmFan, count - group * kQmFan);
+      const long long head = group * kQmFan * stride;       // the group's first fragment
+      count = (count + kQmFan - 1) / kQmFan;
+      if (size > 1) {
+        // (the counter of the group's first warp: no other group of two or more
+        // at this level begins there)
+        int *counter = c.ws_cnt + kChunkCntFirst + level * warps + (first + head) * team + mate;
+        int prev = 0;
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                       : "=r"(prev)
+                       : "l"(reinterpret_cast<uint64_t>(counter))
+                       : "memory");
+        prev = __shfl_sync(0xffffffffu, prev, 0);
+        if (prev != size - 1) return;
+        if (lane == 0) *counter = 0;         // ready for the next call
+        __syncwarp();
+        for (int h = 0; h < rows; ++h) {
+          const size_t from = lane < size ? place(head + lane * stride) + h : 0;
+          const float mh = lane < size ? __ldcg(ws_m + from) : -INFINITY;
+          float M = mh;
+#pragma unroll
+          for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+          const float wt = lane < size ? fast_exp2(mh - chunk_ref(M)) : 0.f;
+          float L = lane < size ? __ldcg(ws_l + from) * wt : 0.f;
+#pragma unroll
+          for (int sh = 16; sh > 0; sh >>= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
+          float4 acc[(D + 127) / 128];
+#pragma unroll
+          for (int k = 0; k < (D + 127) / 128; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int j = 0; j < size; ++j) {
+            const float x = __shfl_sync(0xffffffffu, wt, j);
+            const float4 *src = reinterpret_cast<const float4 *>(ws_o + (place(head + j * stride) + h) * D);
+#pragma unroll
+            for (int k = 0; k < (D + 127) / 128; ++k)
+              if (lane + 32 * k < D / 4) {
+                const float4 y = __ldcg(src + lane + 32 * k);
+                acc[k].x = fmaf(x, y.x, acc[k].x);
+                acc[k].y = fmaf(x, y.y, acc[k].y);
+                acc[k].z = fmaf(x, y.z, acc[k].z);
+                acc[k].w = fmaf(x, y.w, acc[k].w);
+              }
+          }
+          const size_t to = place(head) + h;
+          const float inv = 1.f / L;
+#pragma unroll
+          for (int k = 0; k < (D + 127) / 128; ++k) {
+            const int d = 4 * (lane + 32 * k);
+            if (d >= D) continue;
+            if (count == 1) {
+              put_two(c.out, (out_row + h) * D + d, dt, out8, acc[k].x * inv, acc[k].y * inv);
+              put_two(c.out, (out_row + h) * D + d + 2, dt, out8, acc[k].z * inv, acc[k].w * inv);
+            } else {
+              __stcg(reinterpret_cast<float4 *>(ws_o + to * D + d), acc[k]);
+            }
+          }
+          __syncwarp();                      // (every lane has read the group's first state)
+          if (count > 1 && lane == 0) {
+            __stcg(ws_m + to, M);
+            __stcg(ws_l + to, L);
+          }
+        }
+      }
+      f = group;
+      stride *= kQmFan;
+    }
+  };
 
+  start();
   for (int i = 0; i < mine; ++i) {
     cp_async_wait<S - 2>();
     __syncwarp();                                        // (and every lane is done with tile i - 1, whose stage is next)
     issue(i + S - 1);
     const uint32_t kb = ring_at + (i % S) * Sh::kStage, vb = kb + kQmTok * Sh::kStride;
     const uint32_t kpb = vb + kQmTok * Sh::kStride, vpb = kpb + kQmTok * Sh::kParams;
-    const int tile0 = p.t0 + kQmTok * (w + W * i);
-    const bool whole = tile0 >= first && tile0 + kQmTok <= p.t1;
-    float x[2][NT][4], sv[2][2];
+    const int tile0 = cur.base + kQmTok * cur.tile;
+    float x[2][4], sv[2][2];
     int ve_new = ve;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const int r0 = mt * 16 + g, r1 = r0 + 8;
-      float s[NT][4] = {};
+      float s[2][4] = {};                                // (two chains)
       const uint32_t k0 = kb + r0 * Sh::kStride + 4 * t4, k1 = k0 + 8 * Sh::kStride;
       if constexpr (FMT == kInt4) {
         const uint32_t z0 = half2_bits(lds_f32(kpb + r0 * 8 + 4), 0.f) & 0xffffu, z1 = half2_bits(lds_f32(kpb + r1 * 8 + 4), 0.f) & 0xffffu;
@@ -304,11 +590,8 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
           nibble_pairs(lds32(k0 + k2 * 16), a1, a16, f0);
           nibble_pairs(lds32(k1 + k2 * 16), b1, b16, f1);
           const uint32_t A[4] = {f0[0], f1[0], f0[1], f1[1]}, B[4] = {f0[2], f1[2], f0[3], f1[3]};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            MmaOp<__half>::run(s[nt], A, qf[nt][2 * k2][0], qf[nt][2 * k2][1]);
-            MmaOp<__half>::run(s[nt], B, qf[nt][2 * k2 + 1][0], qf[nt][2 * k2 + 1][1]);
-          }
+          MmaOp<__half>::run(s[0], A, qf[2 * k2][0], qf[2 * k2][1]);
+          MmaOp<__half>::run(s[1], B, qf[2 * k2 + 1][0], qf[2 * k2 + 1][1]);
         }
       } else {
 #pragma unroll
@@ -316,8 +599,7 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
           uint32_t A[4];
           code_pairs<FMT, false>(lds32(k0 + ks * 16), A[0], A[2]);
           code_pairs<FMT, false>(lds32(k1 + ks * 16), A[1], A[3]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) MmaOp<__half>::run(s[nt], A, qf[nt][ks][0], qf[nt][ks][1]);
+          MmaOp<__half>::run(s[ks & 1], A, qf[ks][0], qf[ks][1]);
         }
       }
       const float sk0 = lds_f32(kpb + r0 * Sh::kParams), sk1 = lds_f32(kpb + r1 * Sh::kParams);
@@ -329,99 +611,87 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
         if (ex != 255) ve_new = max(ve_new, ex);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (SPLIT && dt == PKV_F32) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] += __shfl_xor_sync(0xffffffffu, s[nt][e], 2);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[mt][nt][e] = s[nt][e] * qs[nt][e & 1] * (e < 2 ? sk0 : sk1);
+      for (int e = 0; e < 4; ++e) {
+        float y = s[0][e] + s[1][e];
+        if (SPLIT && dt == PKV_F32) y += __shfl_xor_sync(0xffffffffu, y, 2);
+        x[mt][e] = y * qs[e & 1] * (e < 2 ? sk0 : sk1);
       }
     }
     if (cap != kCapNone) {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[mt][nt][e] = cap == kCapUsual ? chunk_capped(x[mt][nt][e], c.cap_log2) : chunk_cap(c, x[mt][nt][e]);
+        for (int e = 0; e < 4; ++e)
+          x[mt][e] = cap == kCapUsual ? chunk_capped(x[mt][e], c.cap_log2) : chunk_cap(c, x[mt][e]);
     }
-    if (!whole) {
+    if (tile0 < cur.first || tile0 + kQmTok > cur.n) {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const int t = tile0 + mt * 16 + hf * 8 + g;
-          if (t >= first && t < p.t1) continue;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) x[mt][nt][2 * hf] = x[mt][nt][2 * hf + 1] = -INFINITY;
+          if (t >= cur.first && t < cur.n) continue;
+          x[mt][2 * hf] = x[mt][2 * hf + 1] = -INFINITY;
         }
     }
     // raise the maxima where a score passes them by 2^8, and O's unit where a
     // value's scale passes it
+    const float m0 = m[0] + 8.f, m1 = m[1] + 8.f;
     bool over = ve_new > ve;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float m0 = m[nt][0] + 8.f, m1 = m[nt][1] + 8.f;
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-        over = over || x[mt][nt][0] > m0 || x[mt][nt][1] > m1 || x[mt][nt][2] > m0 || x[mt][nt][3] > m1;
-    }
+    for (int mt = 0; mt < 2; ++mt) over = over || x[mt][0] > m0 || x[mt][1] > m1 || x[mt][2] > m0 || x[mt][3] > m1;
     if (__any_sync(0xffffffffu, over)) {
       ve_new = __reduce_max_sync(0xffffffffu, ve_new);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int e = 0; e < 2; ++e) {
+        float top = fmaxf(fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2]));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
+        for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+        top = fmaxf(top, m[e]);
+        const float d = m[e] - chunk_ref(top), f = fast_exp2(d + (float)(ve - ve_new));
+        l[e] *= fast_exp2(d);
+        m[e] = top;
 #pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
-          top = fmaxf(top, m[nt][e]);
-          const float d = m[nt][e] - chunk_ref(top), f = fast_exp2(d + (float)(ve - ve_new));
-          l[nt][e] *= fast_exp2(d);
-          m[nt][e] = top;
-#pragma unroll
-          for (int ks = 0; ks < kSteps; ++ks) {
-            o[nt][ks][e] *= f;
-            o[nt][ks][e + 2] *= f;
-          }
+        for (int ks = 0; ks < kSteps; ++ks) {
+          o[ks][e] *= f;
+          o[ks][e + 2] *= f;
         }
+      }
       ve = ve_new;
     }
     const float unit = __int_as_float((127 + kUnit - ve) << 23);    // 2^(kUnit - ve)
     // weights, as the product's B
-    uint32_t wb[2][NT][2], wl[2][NT][2];
+    uint32_t wb[2][2], wl[2][2];
+    const float r0 = chunk_ref(m[0]), r1 = chunk_ref(m[1]);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float r0 = chunk_ref(m[nt][0]), r1 = chunk_ref(m[nt][1]);
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float p0 = fast_exp2(x[mt][nt][2 * hf] - r0), p1 = fast_exp2(x[mt][nt][2 * hf + 1] - r1);
-          const float s1 = sv[mt][hf] * unit, w0 = p0 * s1, w1 = p1 * s1;
-          l[nt][0] += p0;
-          l[nt][1] += p1;
-          __half2 h = __floats2half2_rn(w0, w1);
-          if (rest) {
-            const float2 f = __half22float2(h);
-            const __half2 lo = __floats2half2_rn(w0 - f.x, w1 - f.y);
-            if (SPLIT) {
-              if (t4 >= 2) h = lo;
-            } else {
-              wl[mt][nt][hf] = movm_trans(*reinterpret_cast<const uint32_t *>(&lo));
-            }
+      for (int hf = 0; hf < 2; ++hf) {
+        const float p0 = fast_exp2(x[mt][2 * hf] - r0), p1 = fast_exp2(x[mt][2 * hf + 1] - r1);
+        const float s1 = sv[mt][hf] * unit, w0 = p0 * s1, w1 = p1 * s1;
+        l[0] += p0;
+        l[1] += p1;
+        __half2 h = __floats2half2_rn(w0, w1);
+        if (rest) {
+          const float2 f = __half22float2(h);
+          const __half2 lo = __floats2half2_rn(w0 - f.x, w1 - f.y);
+          if (SPLIT) {
+            if (t4 >= 2) h = lo;
+          } else {
+            wl[mt][hf] = movm_trans(*reinterpret_cast<const uint32_t *>(&lo));
           }
-          wb[mt][nt][hf] = movm_trans(*reinterpret_cast<uint32_t *>(&h));
         }
-    }
+        wb[mt][hf] = movm_trans(*reinterpret_cast<uint32_t *>(&h));
+      }
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const uint32_t va = vb + (mt * 16 + (lane & 15)) * Sh::kStride + (lane >> 4) * 16;
+      auto product = [&](int ks, const uint32_t (&A)[4]) {
+        MmaOp<__half>::run(o[ks], A, wb[mt][0], wb[mt][1]);
+        if (!SPLIT && rest) MmaOp<__half>::run(o[ks], A, wl[mt][0], wl[mt][1]);
+      };
+      uint32_t z1[2], z16[2];                // int4: tokens 2 t4, 2 t4 + 1 (and 8 behind them) of this half tile
       if constexpr (FMT == kInt4) {
-        // tokens 2 t4, 2 t4 + 1 (and 8 behind them) of this half tile
-        uint32_t z1[2], z16[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const uint32_t z = half2_bits(lds_f32(vpb + (mt * 16 + 8 * hf + 2 * t4) * 8 + 4),
@@ -429,153 +699,75 @@ __global__ void __launch_bounds__(32 * kQmWarps) pkv_quant_decode_mma_kernel(con
           z1[hf] = hfma2_u(z, 0x3c003c00u, 0x64006400u);
           z16[hf] = hfma2_u(z, 0xbc00bc00u, 0xd400d400u);
         }
-        auto block = [&](int ch, uint32_t r0, uint32_t r1) {      // 32 columns of 16 tokens
+      }
+      auto block = [&](int ch, uint32_t w0, uint32_t w1) {        // a chunk's columns of 16 tokens
+        if constexpr (FMT == kInt4) {
           uint32_t f0[4], f1[4];
-          nibble_pairs(r0, z1[0], z16[0], f0);
-          nibble_pairs(r1, z1[1], z16[1], f1);
+          nibble_pairs(w0, z1[0], z16[0], f0);
+          nibble_pairs(w1, z1[1], z16[1], f1);
 #pragma unroll
           for (int q2 = 0; q2 < 2; ++q2) {
             const uint32_t A[4] = {f0[2 * q2], f0[2 * q2 + 1], f1[2 * q2], f1[2 * q2 + 1]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              MmaOp<__half>::run(o[nt][2 * ch + q2], A, wb[mt][nt][0], wb[mt][nt][1]);
-              if (!SPLIT && rest) MmaOp<__half>::run(o[nt][2 * ch + q2], A, wl[mt][nt][0], wl[mt][nt][1]);
-            }
+            product(2 * ch + q2, A);
           }
-        };
-#pragma unroll
-        for (int ch = 0; ch + 1 < Sh::kChunks; ch += 2) {
-          uint32_t r0, r1, r2, r3;
-          ldsm_x4_trans(va + ch * 16, r0, r1, r2, r3);
-          block(ch, r0, r1);
-          block(ch + 1, r2, r3);
-        }
-        if constexpr (Sh::kChunks & 1) {
-          uint32_t r0, r1;
-          ldsm_x2_trans(vb + (mt * 16 + (lane & 15)) * Sh::kStride + (Sh::kChunks - 1) * 16, r0, r1);
-          block(Sh::kChunks - 1, r0, r1);
-        }
-      } else {
-        auto block = [&](int ch, uint32_t r0, uint32_t r1) {      // 16 columns of 16 tokens
+        } else {
           uint32_t A[4];
-          code_pairs<FMT, true>(r0, A[0], A[1]);
-          code_pairs<FMT, true>(r1, A[2], A[3]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            MmaOp<__half>::run(o[nt][ch], A, wb[mt][nt][0], wb[mt][nt][1]);
-            if (!SPLIT && rest) MmaOp<__half>::run(o[nt][ch], A, wl[mt][nt][0], wl[mt][nt][1]);
-          }
-        };
-#pragma unroll
-        for (int ch = 0; ch + 1 < Sh::kChunks; ch += 2) {
-          uint32_t r0, r1, r2, r3;
-          ldsm_x4_trans(va + ch * 16, r0, r1, r2, r3);
-          block(ch, r0, r1);
-          block(ch + 1, r2, r3);
+          code_pairs<FMT, true>(w0, A[0], A[1]);
+          code_pairs<FMT, true>(w1, A[2], A[3]);
+          product(ch, A);
         }
-        if constexpr (Sh::kChunks & 1) {
-          uint32_t r0, r1;
-          ldsm_x2_trans(vb + (mt * 16 + (lane & 15)) * Sh::kStride + (Sh::kChunks - 1) * 16, r0, r1);
-          block(Sh::kChunks - 1, r0, r1);
-        }
+      };
+#pragma unroll
+      for (int ch = 0; ch + 1 < Sh::kChunks; ch += 2) {
+        uint32_t w0, w1, w2, w3;
+        ldsm_x4_trans(va + ch * 16, w0, w1, w2, w3);
+        block(ch, w0, w1);
+        block(ch + 1, w2, w3);
       }
+      if constexpr (Sh::kChunks & 1) {
+        uint32_t w0, w1;
+        ldsm_x2_trans(vb + (mt * 16 + (lane & 15)) * Sh::kStride + (Sh::kChunks - 1) * 16, w0, w1);
+        block(Sh::kChunks - 1, w0, w1);
+      }
+    }
+    const bool ends = cur.tile + 1 == cur.tiles;
+    if (ends || i + 1 == mine) finish();
+    if (i + 1 < mine && advance(cur)) {
+      unit0 = begin + i + 1;
+      start();
     }
   }
   cp_async_wait<0>();
-
-  // Merge the warps.  Column sums over the lanes of a column first.
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], sh);
-      if (g == 0) {
-        const int at = w * Sh::kCols + 8 * nt + 2 * t4 + e;
-        s_wm[at] = m[nt][e];
-        s_wl[at] = l[nt][e];
-      }
-    }
-  __syncthreads();                                       // (every ring is free too)
-  float *s_o = reinterpret_cast<float *>(ring);          // [W][cols][kOStride]
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int col = 8 * nt + 2 * t4 + e;
-      float M = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < W; ++k) M = fmaxf(M, s_wm[k * Sh::kCols + col]);
-      const float f = exp2f(m[nt][e] - chunk_ref(M) + (float)(ve - kUnit));
-      float *dst = s_o + (w * Sh::kCols + col) * Sh::kOStride;
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) {
-        // rows g and g + 8 of tile ks are columns of V (see code_pairs, nibble_pairs)
-        const int d = FMT == kInt4 ? (ks >> 1) * 32 + 4 * g + 2 * (ks & 1) : ks * 16 + 2 * g;
-        *reinterpret_cast<float2 *>(dst + d) = make_float2(o[nt][ks][e] * f, o[nt][ks][e + 2] * f);
-      }
-    }
-  if (threadIdx.x < Sh::kCols) {
-    const int col = threadIdx.x;
-    float M = -INFINITY, L = 0.f;
-    for (int k = 0; k < W; ++k) M = fmaxf(M, s_wm[k * Sh::kCols + col]);
-    for (int k = 0; k < W; ++k) L += s_wl[k * Sh::kCols + col] * exp2f(s_wm[k * Sh::kCols + col] - chunk_ref(M));
-    if (col < kHeads) {
-      s_m[col] = M;
-      s_l[col] = L;
-    }
-  }
-  __syncthreads();
-  // sum the warps (and a head's two columns) into the head's first row, which
-  // only the thread that writes it reads
-  for (int i = threadIdx.x; i < kHeads * D; i += 32 * W) {
-    const int r = i / D, d = i - r * D, col = r;
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      sum += s_o[(k * Sh::kCols + col) * Sh::kOStride + d];
-      if (SPLIT && rest) sum += s_o[(k * Sh::kCols + col + 4) * Sh::kOStride + d];
-    }
-    s_o[r * Sh::kOStride + d] = sum;
-  }
-  __syncthreads();
-  constexpr int kRoom = Sh::kMain / 4;
-  if (dt == PKV_F32)
-    quant_finish<float>(c, p, s_m, s_l, s_o, Sh::kOStride, kRoom, s_scratch);
-  else if (dt == PKV_BF16)
-    quant_finish<__nv_bfloat16>(c, p, s_m, s_l, s_o, Sh::kOStride, kRoom, s_scratch);
-  else
-    quant_finish<__half>(c, p, s_m, s_l, s_o, Sh::kOStride, kRoom, s_scratch);
 }
 
-template <int D, int FMT, int NT, bool SPLIT>
+// Warps of the grid: it fills kQdSms SMs once.
+template <int D, int FMT, bool SPLIT>
 static pkv_status launch_qm(const QuantDecodeArgs &a, pkv_dtype dt, cudaStream_t stream) {
   static int configured[64];
-  auto kern = pkv_quant_decode_mma_kernel<D, FMT, NT, SPLIT>;
-  constexpr int kSmem = QmShape<D, FMT, NT>::kSmem;
+  auto kern = pkv_quant_decode_mma_kernel<D, FMT, SPLIT>;
+  constexpr int kSmem = QmShape<D, FMT>::kSmem;
   if (!allow_smem(kern, kSmem, configured)) return PKV_ERR_CUDA;
-  kern<<<dim3((unsigned)(a.c.chunks * a.c.KVH * a.c.max_parts), (unsigned)a.c.B), 32 * kQmWarps, kSmem, stream>>>(a, (int)dt);
+  kern<<<(unsigned)a.grid, 32 * kQmWarps, kSmem, stream>>>(a, (int)dt);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 template <int D, int FMT>
-static pkv_status launch_qm_d(const QuantDecodeArgs &a, int tiles, bool split, pkv_dtype dt, cudaStream_t stream) {
-  if (split) return launch_qm<D, FMT, 1, true>(a, dt, stream);
-  return launch_qm<D, FMT, 1, false>(a, dt, stream);
+static pkv_status launch_qm_d(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream) {
+  return split ? launch_qm<D, FMT, true>(a, dt, stream) : launch_qm<D, FMT, false>(a, dt, stream);
 }
 
 // Every head_dim of a format.
 template <int FMT>
-static pkv_status launch_qm_f(const QuantDecodeArgs &a, int tiles, bool split, pkv_dtype dt, cudaStream_t stream) {
+static pkv_status launch_qm_f(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream) {
   switch (a.c.D) {
-    case 64: return launch_qm_d<64, FMT>(a, tiles, split, dt, stream);
+    case 64: return launch_qm_d<64, FMT>(a, split, dt, stream);
     case 80:
-      if constexpr (FMT != kInt4) return launch_qm_d<80, FMT>(a, tiles, split, dt, stream);
+      if constexpr (FMT != kInt4) return launch_qm_d<80, FMT>(a, split, dt, stream);
       break;
-    case 96: return launch_qm_d<96, FMT>(a, tiles, split, dt, stream);
-    case 128: return launch_qm_d<128, FMT>(a, tiles, split, dt, stream);
-    case 192: return launch_qm_d<192, FMT>(a, tiles, split, dt, stream);
-    case 256: return launch_qm_d<256, FMT>(a, tiles, split, dt, stream);
+    case 96: return launch_qm_d<96, FMT>(a, split, dt, stream);
+    case 128: return launch_qm_d<128, FMT>(a, split, dt, stream);
+    case 192: return launch_qm_d<192, FMT>(a, split, dt, stream);
+    case 256: return launch_qm_d<256, FMT>(a, split, dt, stream);
   }
   return PKV_ERR_UNSUPPORTED;
 }
