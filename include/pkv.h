@@ -647,14 +647,16 @@ PKV_API pkv_status pkv_quant_read(void *k_out, void *v_out, const void *k_codes,
  *   (the same flags; a context over the table is clamped)
  *   partition_size  0 = automatic, else a positive multiple of 128: keys per
  *                 part of the split over the context (raised where it would
- *                 give more than 256 parts)
+ *                 give more than 256 parts); on the tensor cores the fewest
+ *                 keys that a warp takes of its stretch
  *   workspace     pkv_quant_decode_workspace_size(...) bytes, 256-byte
- *                 aligned, zero-filled before its first use; every call leaves
- *                 it ready for the next on the same stream.  Calls that may
- *                 overlap need workspaces of their own (two captured graphs
- *                 that share one must not replay at the same time).
- * Rows no query sees may hold anything; they are not read, nor are table
- * entries of blocks that hold only such rows.  A table entry outside
+ *                 aligned, zero-filled before its first use; every call that
+ *                 completes without PKV_FLAG_TIMEOUT leaves it ready for the
+ *                 next on the same stream.  Calls that may overlap need
+ *                 workspaces of their own (two captured graphs that share one
+ *                 must not replay at the same time).
+ * Rows no query sees may hold anything, NaN included; table entries of blocks
+ * that hold only such rows are not read.  A table entry outside
  * [0, num_blocks) raises PKV_FLAG_BLOCK_OUT_OF_RANGE, that sequence's output is
  * unspecified.  A visible row whose scale is NaN makes its KV head's outputs
  * NaN.  out and the workspace overlap no other argument.

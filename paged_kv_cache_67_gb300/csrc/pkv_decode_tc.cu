@@ -528,6 +528,22 @@ bool encode_chunk_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long lo
 // Tensor map of a [rows, H, D] 16-bit tensor (one row of H heads per token):
 // box of 64 elements x box_heads heads x box_rows rows, 128-byte swizzle; rows
 // past the end read as zero.
+bool encode_codes_map(CUtensorMap *map, const void *codes, long long num_blocks, int bs, int KVH, int row, int part) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[5] = {(cuuint64_t)part, (cuuint64_t)bs, (cuuint64_t)(row / part), (cuuint64_t)KVH, (cuuint64_t)num_blocks};
+  cuuint64_t strides[4] = {(cuuint64_t)KVH * row, (cuuint64_t)part, (cuuint64_t)row, (cuuint64_t)bs * KVH * row};
+  cuuint32_t box[5] = {(cuuint32_t)part, 16, (cuuint32_t)(row / part), 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUtensorMapSwizzle swizzle = part == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : part == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : part == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                  : CU_TENSOR_MAP_SWIZZLE_NONE;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(codes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_packed_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,
                        int box_heads, int box_rows) {
   EncodeTiledFn fn = encode_fn();

@@ -79,6 +79,11 @@ bool encode_cache_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long lo
 bool encode_chunk_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long long num_blocks,
                       int bs, int KVH, int D);
 
+// Rows of `row` bytes of a quantised [num_blocks, bs, KVH] cache, 16 tokens of a
+// KV head a box: `part` bytes of a row (swizzled over themselves where that is a
+// power of two) x 16 rows x row / part parts x 1 head x 1 block.
+bool encode_codes_map(CUtensorMap *map, const void *codes, long long num_blocks, int bs, int KVH, int row, int part);
+
 // Tensor map of a [rows, H, D] 16-bit tensor: box of 64 elements x 1 head x
 // box_rows rows, 128-byte swizzle, zero past the last row.
 bool encode_rows_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,

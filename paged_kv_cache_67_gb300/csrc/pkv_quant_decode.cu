@@ -322,6 +322,8 @@ PKV_API pkv_status pkv_quant_decode_attention(
   a.kp = k_params;
   a.vp = v_params;
   a.heads = plan.heads;
+  // whole chunks of 16 tokens, whose parameters are 16-byte rows of their own too
+  a.tma = block_size % 16 == 0 && at(k_params, 16) && at(v_params, 16);
   a.grid = plan.grid;
   a.least = plan.least;
   a.team = plan.team;

@@ -10,21 +10,23 @@
 
 namespace pkv {
 
-// Shape of the tensor-core kernel's ring: tokens and bytes of a tile, tiles
-// ahead, CTAs of kQmWarps warps that fit an SM's 228 KB (1 KB of it a CTA's
+// Shape of the tensor-core kernel's ring: tokens and bytes of a tile, tiles of
+// a warp, CTAs of kQmWarps warps that fit an SM's 228 KB (1 KB of it a CTA's
 // own; more than three would cost registers).
 constexpr int kQmTok = 32;
 constexpr int kQmWarps = 4;
 constexpr int kQmGroups = 32 * kQmWarps;   // groups of sequences whose first tiles a CTA keeps
-constexpr int kQmPre = 4 * (kQmGroups + 2 + kQmWarps);
-constexpr int qm_stage(int row, int params) { return kQmTok * 2 * (16 * ((row / 16) | 1) + params); }
-constexpr int qm_smem(int row, int params, int stages) { return kQmWarps * stages * qm_stage(row, params) + kQmPre; }
-constexpr int qm_fit(int row, int params, int stages) {
-  const int n = 228 * 1024 / (qm_smem(row, params, stages) + 1024);
+constexpr int kQmStages = 3;
+// (the ring begins at a multiple of 1 KB; barriers, first tiles, a scan's sums)
+constexpr int kQmPre = 1024 + 8 * kQmWarps * kQmStages + 4 * (kQmGroups + 2 + kQmWarps);
+constexpr int qm_smem(int row, int params) { return kQmWarps * kQmStages * kQmTok * 2 * (row + params) + kQmPre; }
+constexpr int qm_ctas(int row, int params) {
+  const int n = 228 * 1024 / (qm_smem(row, params) + 1024);
   return n > 3 ? 3 : n;
 }
-constexpr int qm_stages(int row, int params) { return qm_fit(row, params, 3) == 3 ? 3 : 2; }
-constexpr int qm_ctas(int row, int params) { return qm_fit(row, params, qm_stages(row, params)); }
+// Bytes of a row that lie together in the ring: a power of two is swizzled by
+// TMA over itself, others are conflict-free or nearly so as they are.
+constexpr int qm_box(int row) { return row % 128 == 0 ? 128 : row == 192 ? 64 : row; }
 
 struct QuantDecodeArgs {
   ChunkArgs c;                     // q, out, tables, lens, sizes, score form, split, workspace
@@ -32,6 +34,7 @@ struct QuantDecodeArgs {
   const float *kp, *vp;            // parameters
   int heads;                       // query heads of a unit
   float *states;                   // tensor cores: two places a warp for states to be joined
+  int tma;                         // blocks of whole 16-token chunks, read by TMA
   int grid, least, team;           // its CTAs; tiles that a warp takes at least; warps that walk the same tokens
   uint32_t bs_mul;                 // t / block_size = (umulhi(t, bs_mul) + t) >> bs_shift for t < 2^31
   int bs_shift;

@@ -28,16 +28,21 @@
 // head group of a KV head -- stand in one line, and every warp of a grid that
 // fills the GPU once takes an equal stretch of it: lengths may be as ragged as
 // they like.  Warps run by themselves, with no barrier: each has a ring in shared
-// memory, filled ahead (across the ends of units too) by 16-byte cp.async row by
-// row -- a row's place comes from the block table, so any block size will do.
+// memory, filled ahead (across the ends of units too).  Where blocks are whole
+// chunks of 16 tokens, TMA brings them, a box of K and one of V a chunk; any other
+// block size goes row by row, 16 bytes a cp.async, to the same places.  (All by
+// cp.async, a batch of 64 x 2304 keys took 79 us, and 88 with the arithmetic
+// left out.)
 // A warp that has a whole unit writes its output.  The others leave the states
 // (max, sum, weighted sum) of the unit they began in and the one they end in, two
 // places a warp, and the last one done of up to 16 neighbours joins them, then of
 // up to 16 such groups, until the unit is one.
 //
-// Rows in the ring are padded to an odd number of 16-byte chunks: the 4-byte
-// fragment loads of K and the transposing ldmatrix of V both touch every bank once.
+// Rows in the ring are swizzled as TMA does it: the 4-byte fragment loads of K
+// and the transposing ldmatrix of V both touch every bank once.
 #pragma once
+
+#include <string.h>
 
 #include "pkv_quant_decode.cuh"
 
@@ -49,14 +54,23 @@ template <int D, int FMT>
 struct QmShape {
   static constexpr int kRow = quant_row_bytes<FMT>(D);
   static constexpr int kChunks = kRow / 16;
-  static constexpr int kStride = 16 * (kChunks | 1);                  // an odd number of chunks
+  static constexpr int kBox = qm_box(kRow);                           // bytes of a row that lie together
+  static constexpr int kSwizzle = kBox == 128 ? 0x70 : kBox == 64 ? 0x30 : kBox == 32 ? 0x10 : 0;
   static constexpr int kParams = 4 * quant_params<FMT>();             // bytes a row
-  static constexpr int kStage = qm_stage(kRow, kParams);
-  static constexpr int kStages = qm_stages(kRow, kParams);
-  static constexpr int kRing = kStages * kStage;                      // a warp's
-  static constexpr int kSmem = qm_smem(kRow, kParams, kStages);
+  static constexpr int kHalf = 16 * kRow;                             // 16 tokens' rows of K or V
+  static constexpr int kCodes = 4 * kHalf;                            // of a tile: K, K, V, V
+  static constexpr int kStages = kQmStages;
+  static constexpr int kSmem = qm_smem(kRow, kParams);
   static constexpr int kCtas = qm_ctas(kRow, kParams);
+  static_assert(kCodes % 1024 == 0 && (kSwizzle == 0 || kHalf % (8 * kBox) == 0), "the swizzle's period");
 };
+// Where chunk ch of row r of a half lies in it.
+template <int ROW, int BOX, int MASK>
+__device__ __forceinline__ int qm_at(int r, int ch) {
+  constexpr int kPer = BOX / 16;
+  const int in = r * BOX + ch % kPer * 16;
+  return ch / kPer * (16 * BOX) + (in ^ ((in >> 3) & MASK));
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -65,10 +79,14 @@ template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrives on `bar` once this thread's cp.async so far are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -200,11 +218,15 @@ __device__ __forceinline__ void qm_keys(const ChunkArgs &c, int b, QmAt &s) {
 
 template <int D, int FMT, bool SPLIT>
 __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
-    pkv_quant_decode_mma_kernel(const __grid_constant__ QuantDecodeArgs a, const int dt) {
+    pkv_quant_decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                                const __grid_constant__ QuantDecodeArgs a, const int dt) {
   using Sh = QmShape<D, FMT>;
   constexpr int S = Sh::kStages, kSteps = D / 16, kHeads = SPLIT ? 4 : 8;
-  extern __shared__ __align__(16) uint8_t smem[];
-  int *s_first = reinterpret_cast<int *>(smem + kQmWarps * Sh::kRing);      // [groups + 1] tiles of one (KV head, head group)
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *codes_all = smem, *params_all = smem + kQmWarps * S * Sh::kCodes;
+  uint64_t *bars_all = reinterpret_cast<uint64_t *>(params_all + kQmWarps * S * 2 * kQmTok * Sh::kParams);
+  int *s_first = reinterpret_cast<int *>(bars_all + kQmWarps * S);           // [groups + 1] tiles of one (KV head, head group)
   int *s_warp = s_first + kQmGroups + 2;
   const ChunkArgs &c = a.c;
   const bool rest = SPLIT ? dt != PKV_BF16 : dt == PKV_F16;   // weights of two parts
@@ -312,69 +334,92 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
     return true;
   };
 
-  // ---- the ring.  Tile i of this warp into stage i mod S.  Lane r looks up
-  // token r's block one tile ahead, so that the table entry is there when it is
-  // needed; what is not visible is filled with zeros and not read.  (Rows of the
-  // cache are fewer than 2^32 - 1 here.)
-  constexpr bool kEven = 32 % Sh::kChunks == 0;          // a lane keeps to one chunk of the rows
-  const uint32_t ring_at = smem_u32(smem + w * Sh::kRing);
-  const uint8_t *k_at = a.k + lane % Sh::kChunks * 16, *v_at = a.v + lane % Sh::kChunks * 16;
-  const uint32_t st_even = ring_at + lane / Sh::kChunks * Sh::kStride + lane % Sh::kChunks * 16;
+  // ---- the ring.  Tile i of this warp into stage i mod S: K's and V's halves of
+  // 16 tokens, then their parameters.  Block table entries are looked up one tile
+  // ahead, so that they are there when they are needed.  What holds no visible
+  // key is not read.
+  uint64_t *bars = bars_all + w * S;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&bars[s], a.tma ? 1 : 32);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  uint8_t *codes = codes_all + w * S * Sh::kCodes, *params = params_all + w * S * 2 * kQmTok * Sh::kParams;
+  const uint32_t codes_at = smem_u32(codes), params_at = smem_u32(params);
+  const uint64_t policy = l2_evict_first_policy();
   QmAt ahead = cur;
   int next_phys = 0, next_off = -1;
+  // TMA: lane 0-7's copy is of half lane & 1, of K, V, K's parameters, V's;
+  // else lane r's rows are token r's.
   auto look_up = [&](const QmAt &s) {
-    const int t = s.base + kQmTok * s.tile + lane;
+    const int t = s.base + kQmTok * s.tile + (a.tma ? 16 * (lane & 1) : lane);
     next_off = -1;
-    if (t >= s.first && t < s.n) {
+    if (a.tma ? lane < 8 && t + 16 > s.first && t < s.n : t >= s.first && t < s.n) {
       const int lb = div_by(t, a.bs_mul, a.bs_shift);
       next_off = t - lb * c.bs;
       next_phys = __ldg(c.tables + (size_t)s.b * c.max_blocks + lb);
     }
   };
   auto issue = [&](int i) {
-    if (i < mine) {
-      bool in = next_off >= 0;
-      if (in && (next_phys < 0 || (long long)next_phys >= c.num_blocks)) {
-        raise_flag(c.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
-        in = false;
-      }
-      const uint32_t phys = (uint32_t)next_phys, off = (uint32_t)next_off, kvh = (uint32_t)ahead.kvh;
-      const uint32_t row = in ? (phys * (uint32_t)c.bs + off) * (uint32_t)c.KVH + kvh : 0xffffffffu;
-      const uint32_t num = in ? (phys * (uint32_t)c.KVH + kvh) * (uint32_t)c.bs + off : 0u;
-      const uint32_t stage = (i % S) * Sh::kStage, st = ring_at + stage;
-      const uint32_t pa = st + 2 * kQmTok * Sh::kStride + lane * Sh::kParams;
-      cp_async_small<Sh::kParams>(pa, a.kp + (size_t)num * quant_params<FMT>(), in ? Sh::kParams : 0);
-      cp_async_small<Sh::kParams>(pa + kQmTok * Sh::kParams, a.vp + (size_t)num * quant_params<FMT>(), in ? Sh::kParams : 0);
-      if (kEven && __all_sync(0xffffffffu, in)) {
-#pragma unroll
-        for (int j = 0; j < Sh::kChunks; ++j) {
-          const uint32_t from = __shfl_sync(0xffffffffu, row, lane / Sh::kChunks + j * (32 / Sh::kChunks));
-          const uint32_t to = st_even + stage + j * (32 / Sh::kChunks) * Sh::kStride;
-          cp_async16(to, k_at + (size_t)from * Sh::kRow, 16);
-          cp_async16(to + kQmTok * Sh::kStride, v_at + (size_t)from * Sh::kRow, 16);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < Sh::kChunks; ++j) {
-          const int idx = lane + 32 * j, r = idx / Sh::kChunks, ch = idx - r * Sh::kChunks;
-          const uint32_t from = __shfl_sync(0xffffffffu, row, r);
-          const bool has = from != 0xffffffffu;
-          const size_t at = has ? (size_t)from * Sh::kRow + ch * 16 : 0;
-          const uint32_t to = st + r * Sh::kStride + ch * 16;
-          cp_async16(to, a.k + at, has ? 16 : 0);
-          cp_async16(to + kQmTok * Sh::kStride, a.v + at, has ? 16 : 0);
-        }
-      }
-      if (i + 1 < mine) {
-        advance(ahead);
-        look_up(ahead);
-      }
+    if (i >= mine) return;
+    const int st = i % S;
+    bool in = next_off >= 0;
+    if (in && (next_phys < 0 || (long long)next_phys >= c.num_blocks)) {
+      raise_flag(c.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
+      in = false;
     }
-    cp_async_commit();
+    const uint32_t phys = (uint32_t)next_phys, off = (uint32_t)next_off, kvh = (uint32_t)ahead.kvh;
+    // (rows of the cache are fewer than 2^32 - 1 here)
+    const uint32_t num = (phys * (uint32_t)c.KVH + kvh) * (uint32_t)c.bs + off;
+    if (a.tma) {
+      const uint32_t asked = __ballot_sync(0xffffffffu, in);
+      if (lane == 0)
+        mbar_arrive_expect_tx(&bars[st], __popc(asked & 0x0fu) * Sh::kHalf + __popc(asked & 0xf0u) * 16 * Sh::kParams);
+      __syncwarp();
+      if (in) {
+        if (lane < 4)
+          tma_load_5d(codes + st * Sh::kCodes + ((lane >> 1) * 2 + (lane & 1)) * Sh::kHalf, lane < 2 ? &tmK : &tmV, &bars[st],
+                      0, (int)off, 0, (int)kvh, (int)phys, policy);
+        else
+          bulk_load(params_at + (st * 2 * kQmTok + (lane < 6 ? 0 : kQmTok) + 16 * (lane & 1)) * Sh::kParams,
+                    (lane < 6 ? a.kp : a.vp) + (size_t)num * quant_params<FMT>(), 16 * Sh::kParams, &bars[st]);
+      }
+    } else {
+      const uint32_t row = in ? (phys * (uint32_t)c.bs + off) * (uint32_t)c.KVH + kvh : 0xffffffffu;
+      if (in) {
+        const uint32_t to = params_at + (st * 2 * kQmTok + lane) * Sh::kParams;
+        cp_async_small<Sh::kParams>(to, a.kp + (size_t)num * quant_params<FMT>(), Sh::kParams);
+        cp_async_small<Sh::kParams>(to + kQmTok * Sh::kParams, a.vp + (size_t)num * quant_params<FMT>(), Sh::kParams);
+      }
+#pragma unroll
+      for (int j = 0; j < Sh::kChunks; ++j) {
+        const int idx = lane + 32 * j, r = idx / Sh::kChunks, ch = idx - r * Sh::kChunks;
+        const uint32_t from = __shfl_sync(0xffffffffu, row, r);
+        if (from != 0xffffffffu) {
+          const uint32_t to = codes_at + st * Sh::kCodes + (r >> 4) * Sh::kHalf + qm_at<Sh::kRow, Sh::kBox, Sh::kSwizzle>(r & 15, ch);
+          cp_async16(to, a.k + (size_t)from * Sh::kRow + ch * 16, 16);
+          cp_async16(to + 2 * Sh::kHalf, a.v + (size_t)from * Sh::kRow + ch * 16, 16);
+        }
+      }
+      cp_async_arrive(&bars[st]);
+    }
+    if (i + 1 < mine) {
+      advance(ahead);
+      look_up(ahead);
+    }
   };
   look_up(ahead);
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(i);
+  // this lane's places in a half: K's row g (and g + 8, half a box further) at
+  // chunk j of a box, V's row lane mod 16 at chunk j and, from lane 16 on, j + 1
+  constexpr int kPer = Sh::kBox / 16;
+  int k_place[kPer], v_place[(kPer + 1) / 2];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) k_place[j] = qm_at<Sh::kRow, Sh::kBox, Sh::kSwizzle>(g, j) + 4 * t4;
+#pragma unroll
+  for (int j = 0; j < (kPer + 1) / 2; ++j)
+    v_place[j] = qm_at<Sh::kRow, Sh::kBox, Sh::kSwizzle>(lane & 15, min(2 * j + (lane >> 4), kPer - 1));
 
   // ---- a unit's state
   // scores in log2 units, or what their cap wants (see chunk_capped: its error
@@ -512,50 +557,80 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
         if (prev != size - 1) return;
         if (lane == 0) *counter = 0;         // ready for the next call
         __syncwarp();
-        for (int h = 0; h < rows; ++h) {
-          const size_t from = lane < size ? place(head + lane * stride) + h : 0;
-          const float mh = lane < size ? __ldcg(ws_m + from) : -INFINITY;
-          float M = mh;
+        // all heads at once: a round trip to L2 for their maxima and sums, then
+        // one for every other source
+        constexpr int kVec = (D + 127) / 128;
+        const size_t from = place(head + min(lane, size - 1) * stride);
+        float wt[kHeads], M[kHeads], L[kHeads];
 #pragma unroll
-          for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-          const float wt = lane < size ? fast_exp2(mh - chunk_ref(M)) : 0.f;
-          float L = lane < size ? __ldcg(ws_l + from) * wt : 0.f;
+        for (int h = 0; h < kHeads; ++h) {
+          wt[h] = lane < size && h < rows ? __ldcg(ws_m + from + h) : -INFINITY;
+          L[h] = lane < size && h < rows ? __ldcg(ws_l + from + h) : 0.f;
+        }
 #pragma unroll
-          for (int sh = 16; sh > 0; sh >>= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
-          float4 acc[(D + 127) / 128];
+        for (int h = 0; h < kHeads; ++h) {
+          M[h] = wt[h];
 #pragma unroll
-          for (int k = 0; k < (D + 127) / 128; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int j = 0; j < size; ++j) {
-            const float x = __shfl_sync(0xffffffffu, wt, j);
-            const float4 *src = reinterpret_cast<const float4 *>(ws_o + (place(head + j * stride) + h) * D);
+          for (int sh = 16; sh > 0; sh >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], sh));
+          wt[h] = fast_exp2(wt[h] - chunk_ref(M[h]));
+          L[h] *= wt[h];
 #pragma unroll
-            for (int k = 0; k < (D + 127) / 128; ++k)
-              if (lane + 32 * k < D / 4) {
-                const float4 y = __ldcg(src + lane + 32 * k);
-                acc[k].x = fmaf(x, y.x, acc[k].x);
-                acc[k].y = fmaf(x, y.y, acc[k].y);
-                acc[k].z = fmaf(x, y.z, acc[k].z);
-                acc[k].w = fmaf(x, y.w, acc[k].w);
-              }
+          for (int sh = 16; sh > 0; sh >>= 1) L[h] += __shfl_xor_sync(0xffffffffu, L[h], sh);
+        }
+        float4 acc[kHeads][kVec];
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) acc[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kAhead = kHeads * kVec <= 8 ? 2 : 1;     // sources whose loads are in flight
+        for (int j0 = 0; j0 < size; j0 += kAhead) {
+          float4 y[kAhead][kHeads][kVec];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const float4 *src = reinterpret_cast<const float4 *>(ws_o + place(head + min(j0 + j, size - 1) * stride) * D);
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+              for (int k = 0; k < kVec; ++k)
+                y[j][h][k] = h < rows && lane + 32 * k < D / 4 ? __ldcg(src + h * (D / 4) + lane + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
-          const size_t to = place(head) + h;
-          const float inv = 1.f / L;
 #pragma unroll
-          for (int k = 0; k < (D + 127) / 128; ++k) {
-            const int d = 4 * (lane + 32 * k);
-            if (d >= D) continue;
-            if (count == 1) {
-              put_two(c.out, (out_row + h) * D + d, dt, out8, acc[k].x * inv, acc[k].y * inv);
-              put_two(c.out, (out_row + h) * D + d + 2, dt, out8, acc[k].z * inv, acc[k].w * inv);
-            } else {
-              __stcg(reinterpret_cast<float4 *>(ws_o + to * D + d), acc[k]);
+          for (int j = 0; j < kAhead; ++j) {
+            if (j0 + j >= size) break;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+              const float x = __shfl_sync(0xffffffffu, wt[h], j0 + j);
+#pragma unroll
+              for (int k = 0; k < kVec; ++k) {
+                acc[h][k].x = fmaf(x, y[j][h][k].x, acc[h][k].x);
+                acc[h][k].y = fmaf(x, y[j][h][k].y, acc[h][k].y);
+                acc[h][k].z = fmaf(x, y[j][h][k].z, acc[h][k].z);
+                acc[h][k].w = fmaf(x, y[j][h][k].w, acc[h][k].w);
+              }
             }
           }
-          __syncwarp();                      // (every lane has read the group's first state)
+        }
+        const size_t to = place(head);
+        __syncwarp();                        // (every lane has read the group's first state)
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+          if (h >= rows) break;
+          const float inv = 1.f / L[h];
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) {
+            const int d = 4 * (lane + 32 * k);
+            if (d >= D) continue;
+            const float4 &y = acc[h][k];
+            if (count == 1) {
+              put_two(c.out, (out_row + h) * D + d, dt, out8, y.x * inv, y.y * inv);
+              put_two(c.out, (out_row + h) * D + d + 2, dt, out8, y.z * inv, y.w * inv);
+            } else {
+              __stcg(reinterpret_cast<float4 *>(ws_o + (to + h) * D + d), y);
+            }
+          }
           if (count > 1 && lane == 0) {
-            __stcg(ws_m + to, M);
-            __stcg(ws_l + to, L);
+            __stcg(ws_m + to + h, M[h]);
+            __stcg(ws_l + to + h, L[h]);
           }
         }
       }
@@ -566,19 +641,44 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
 
   start();
   for (int i = 0; i < mine; ++i) {
-    cp_async_wait<S - 2>();
-    __syncwarp();                                        // (and every lane is done with tile i - 1, whose stage is next)
-    issue(i + S - 1);
-    const uint32_t kb = ring_at + (i % S) * Sh::kStage, vb = kb + kQmTok * Sh::kStride;
-    const uint32_t kpb = vb + kQmTok * Sh::kStride, vpb = kpb + kQmTok * Sh::kParams;
+    const int st = i % S;
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], (i / S) & 1))) {
+      // give up, once the copies that were asked for have landed (bounded)
+      if (lane == 0) raise_flag(c.err, PKV_FLAG_TIMEOUT);
+      for (int k = i + 1; k < min(mine, i + S - 1); ++k) mbar_wait_bounded(&bars[k % S], (k / S) & 1);
+      return;
+    }
+    const uint32_t kb = codes_at + st * Sh::kCodes, vb = kb + 2 * Sh::kHalf;
+    const uint32_t kpb = params_at + st * 2 * kQmTok * Sh::kParams, vpb = kpb + kQmTok * Sh::kParams;
     const int tile0 = cur.base + kQmTok * cur.tile;
+    const bool whole = tile0 >= cur.first && tile0 + kQmTok <= cur.n;
+    if (!whole) {
+      // values that no query sees, and their parameters, become 0: they may be anything
+      for (int j = lane; j < kQmTok * (Sh::kChunks + 1); j += 32) {
+        const int r = j / (Sh::kChunks + 1), ch = j - r * (Sh::kChunks + 1), t = tile0 + r;
+        if (t >= cur.first && t < cur.n) continue;
+        if (ch < Sh::kChunks) {
+          st_shared_v4(vb + (r >> 4) * Sh::kHalf + qm_at<Sh::kRow, Sh::kBox, Sh::kSwizzle>(r & 15, ch), make_uint4(0, 0, 0, 0));
+        } else {
+          float *to = reinterpret_cast<float *>(params + (st * 2 * kQmTok + kQmTok + r) * Sh::kParams);
+          for (int k = 0; k < quant_params<FMT>(); ++k) to[k] = 0.f;
+        }
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+    }
+    // every lane is done with tile i - 1, whose stage is next (the vote above)
+    issue(i + S - 1);
     float x[2][4], sv[2][2];
     int ve_new = ve;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const int r0 = mt * 16 + g, r1 = r0 + 8;
       float s[2][4] = {};                                // (two chains)
-      const uint32_t k0 = kb + r0 * Sh::kStride + 4 * t4, k1 = k0 + 8 * Sh::kStride;
+      const uint32_t kh = kb + mt * Sh::kHalf;
+      auto k_word = [&](int ch, int up) {                // chunk ch of row g (+ 8)
+        return lds32(kh + ch / kPer * (16 * Sh::kBox) + up * 8 * Sh::kBox + k_place[ch % kPer]);
+      };
       if constexpr (FMT == kInt4) {
         const uint32_t z0 = half2_bits(lds_f32(kpb + r0 * 8 + 4), 0.f) & 0xffffu, z1 = half2_bits(lds_f32(kpb + r1 * 8 + 4), 0.f) & 0xffffu;
         const uint32_t zz0 = z0 | (z0 << 16), zz1 = z1 | (z1 << 16);
@@ -587,8 +687,8 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
           uint32_t f0[4], f1[4];
-          nibble_pairs(lds32(k0 + k2 * 16), a1, a16, f0);
-          nibble_pairs(lds32(k1 + k2 * 16), b1, b16, f1);
+          nibble_pairs(k_word(k2, 0), a1, a16, f0);
+          nibble_pairs(k_word(k2, 1), b1, b16, f1);
           const uint32_t A[4] = {f0[0], f1[0], f0[1], f1[1]}, B[4] = {f0[2], f1[2], f0[3], f1[3]};
           MmaOp<__half>::run(s[0], A, qf[2 * k2][0], qf[2 * k2][1]);
           MmaOp<__half>::run(s[1], B, qf[2 * k2 + 1][0], qf[2 * k2 + 1][1]);
@@ -597,8 +697,8 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
           uint32_t A[4];
-          code_pairs<FMT, false>(lds32(k0 + ks * 16), A[0], A[2]);
-          code_pairs<FMT, false>(lds32(k1 + ks * 16), A[1], A[3]);
+          code_pairs<FMT, false>(k_word(ks, 0), A[0], A[2]);
+          code_pairs<FMT, false>(k_word(ks, 1), A[1], A[3]);
           MmaOp<__half>::run(s[ks & 1], A, qf[ks][0], qf[ks][1]);
         }
       }
@@ -624,7 +724,7 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
         for (int e = 0; e < 4; ++e)
           x[mt][e] = cap == kCapUsual ? chunk_capped(x[mt][e], c.cap_log2) : chunk_cap(c, x[mt][e]);
     }
-    if (tile0 < cur.first || tile0 + kQmTok > cur.n) {
+    if (!whole) {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -685,7 +785,7 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
       }
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t va = vb + (mt * 16 + (lane & 15)) * Sh::kStride + (lane >> 4) * 16;
+      const uint32_t vh = vb + mt * Sh::kHalf;
       auto product = [&](int ks, const uint32_t (&A)[4]) {
         MmaOp<__half>::run(o[ks], A, wb[mt][0], wb[mt][1]);
         if (!SPLIT && rest) MmaOp<__half>::run(o[ks], A, wl[mt][0], wl[mt][1]);
@@ -720,13 +820,13 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
 #pragma unroll
       for (int ch = 0; ch + 1 < Sh::kChunks; ch += 2) {
         uint32_t w0, w1, w2, w3;
-        ldsm_x4_trans(va + ch * 16, w0, w1, w2, w3);
+        ldsm_x4_trans(vh + ch / kPer * (16 * Sh::kBox) + v_place[ch % kPer / 2], w0, w1, w2, w3);
         block(ch, w0, w1);
         block(ch + 1, w2, w3);
       }
-      if constexpr (Sh::kChunks & 1) {
+      if constexpr (Sh::kChunks & 1) {               // (one box then; lanes below 16 give the rows)
         uint32_t w0, w1;
-        ldsm_x2_trans(vb + (mt * 16 + (lane & 15)) * Sh::kStride + (Sh::kChunks - 1) * 16, w0, w1);
+        ldsm_x2_trans(vh + v_place[kPer / 2], w0, w1);
         block(Sh::kChunks - 1, w0, w1);
       }
     }
@@ -737,17 +837,20 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
       start();
     }
   }
-  cp_async_wait<0>();
 }
 
-// Warps of the grid: it fills kQdSms SMs once.
 template <int D, int FMT, bool SPLIT>
 static pkv_status launch_qm(const QuantDecodeArgs &a, pkv_dtype dt, cudaStream_t stream) {
   static int configured[64];
+  using Sh = QmShape<D, FMT>;
   auto kern = pkv_quant_decode_mma_kernel<D, FMT, SPLIT>;
-  constexpr int kSmem = QmShape<D, FMT>::kSmem;
-  if (!allow_smem(kern, kSmem, configured)) return PKV_ERR_CUDA;
-  kern<<<(unsigned)a.grid, 32 * kQmWarps, kSmem, stream>>>(a, (int)dt);
+  if (!allow_smem(kern, Sh::kSmem, configured)) return PKV_ERR_CUDA;
+  CUtensorMap maps[2];
+  memset(maps, 0, sizeof maps);
+  if (a.tma && (!encode_codes_map(&maps[0], a.k, a.c.num_blocks, a.c.bs, a.c.KVH, Sh::kRow, Sh::kBox) ||
+                !encode_codes_map(&maps[1], a.v, a.c.num_blocks, a.c.bs, a.c.KVH, Sh::kRow, Sh::kBox)))
+    return PKV_ERR_CUDA;
+  kern<<<(unsigned)a.grid, 32 * kQmWarps, Sh::kSmem, stream>>>(maps[0], maps[1], a, (int)dt);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
