@@ -205,7 +205,7 @@ static void mma_plan(int B, int H, int KVH, int D, long long span, int partition
   p->bytes = kChunkCnt * sizeof(int) + (size_t)2 * p->grid * kQmWarps * p->heads * (D + 2) * sizeof(float);
 }
 constexpr int kQdLevels = 3;     // of joining: 16^3 warps
-static_assert(kChunkCntFirst + kQdLevels * 3 * kQdSms * kQmWarps <= kChunkCnt && 3 * kQdSms * kQmWarps <= 16 * 16 * 16,
+static_assert(kChunkCntFirst + kQdLevels * kQmMostCtas * kQdSms * kQmWarps <= kChunkCnt && kQmMostCtas * kQdSms * kQmWarps <= 16 * 16 * 16,
               "the counters fit the workspace's");
 
 }  // namespace pkv

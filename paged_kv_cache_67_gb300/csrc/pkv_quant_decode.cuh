@@ -14,15 +14,17 @@ namespace pkv {
 // a warp, CTAs of kQmWarps warps that fit an SM's 228 KB (1 KB of it a CTA's
 // own; more than three would cost registers).
 constexpr int kQmTok = 32;
+constexpr int kQmHalves = kQmTok / 16;
 constexpr int kQmWarps = 4;
 constexpr int kQmGroups = 32 * kQmWarps;   // groups of sequences whose first tiles a CTA keeps
 constexpr int kQmStages = 3;
+constexpr int kQmMostCtas = 3;
 // (the ring begins at a multiple of 1 KB; barriers, first tiles, a scan's sums)
 constexpr int kQmPre = 1024 + 8 * kQmWarps * kQmStages + 4 * (kQmGroups + 2 + kQmWarps);
 constexpr int qm_smem(int row, int params) { return kQmWarps * kQmStages * kQmTok * 2 * (row + params) + kQmPre; }
 constexpr int qm_ctas(int row, int params) {
   const int n = 228 * 1024 / (qm_smem(row, params) + 1024);
-  return n > 3 ? 3 : n;
+  return n > kQmMostCtas ? kQmMostCtas : n;
 }
 // Bytes of a row that lie together in the ring: a power of two is swizzled by
 // TMA over itself, others are conflict-free or nearly so as they are.

@@ -22,7 +22,7 @@
 // the second product.
 //
 // The running maximum is raised only when some score passes it by 2^8: one vote
-// a tile of 32 tokens instead of three exchanges a head.
+// a tile instead of three exchanges a head.
 //
 // Work.  All tiles of all units -- a unit is a sequence's visible keys for one
 // head group of a KV head -- stand in one line, and every warp of a grid that
@@ -58,11 +58,11 @@ struct QmShape {
   static constexpr int kSwizzle = kBox == 128 ? 0x70 : kBox == 64 ? 0x30 : kBox == 32 ? 0x10 : 0;
   static constexpr int kParams = 4 * quant_params<FMT>();             // bytes a row
   static constexpr int kHalf = 16 * kRow;                             // 16 tokens' rows of K or V
-  static constexpr int kCodes = 4 * kHalf;                            // of a tile: K, K, V, V
+  static constexpr int kCodes = 2 * kQmHalves * kHalf;                // of a tile: K's halves, V's
   static constexpr int kStages = kQmStages;
   static constexpr int kSmem = qm_smem(kRow, kParams);
   static constexpr int kCtas = qm_ctas(kRow, kParams);
-  static_assert(kCodes % 1024 == 0 && (kSwizzle == 0 || kHalf % (8 * kBox) == 0), "the swizzle's period");
+  static_assert(kHalf % 128 == 0 && (kSwizzle == 0 || kHalf % (8 * kBox) == 0), "the swizzle's period");
 };
 // Where chunk ch of row r of a half lies in it.
 template <int ROW, int BOX, int MASK>
@@ -348,57 +348,71 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
   const uint32_t codes_at = smem_u32(codes), params_at = smem_u32(params);
   const uint64_t policy = l2_evict_first_policy();
   QmAt ahead = cur;
-  int next_phys = 0, next_off = -1;
-  // TMA: lane 0-7's copy is of half lane & 1, of K, V, K's parameters, V's;
-  // else lane r's rows are token r's.
+  // TMA: every lane has the halves' entries, one lane asks for their copies; else
+  // lane r's rows are token r's.
+  int next_phys[kQmHalves], next_off[kQmHalves];
   auto look_up = [&](const QmAt &s) {
-    const int t = s.base + kQmTok * s.tile + (a.tma ? 16 * (lane & 1) : lane);
-    next_off = -1;
-    if (a.tma ? lane < 8 && t + 16 > s.first && t < s.n : t >= s.first && t < s.n) {
-      const int lb = div_by(t, a.bs_mul, a.bs_shift);
-      next_off = t - lb * c.bs;
-      next_phys = __ldg(c.tables + (size_t)s.b * c.max_blocks + lb);
+#pragma unroll
+    for (int h = 0; h < kQmHalves; ++h) {
+      const int t = s.base + kQmTok * s.tile + (a.tma ? 16 * h : lane);
+      next_off[h] = -1;
+      if (a.tma ? t + 16 > s.first && t < s.n : h == 0 && lane < kQmTok && t >= s.first && t < s.n) {
+        const int lb = div_by(t, a.bs_mul, a.bs_shift);
+        next_off[h] = t - lb * c.bs;
+        next_phys[h] = __ldg(c.tables + (size_t)s.b * c.max_blocks + lb);
+      }
     }
   };
   auto issue = [&](int i) {
     if (i >= mine) return;
     const int st = i % S;
-    bool in = next_off >= 0;
-    if (in && (next_phys < 0 || (long long)next_phys >= c.num_blocks)) {
-      raise_flag(c.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
-      in = false;
-    }
-    const uint32_t phys = (uint32_t)next_phys, off = (uint32_t)next_off, kvh = (uint32_t)ahead.kvh;
-    // (rows of the cache are fewer than 2^32 - 1 here)
-    const uint32_t num = (phys * (uint32_t)c.KVH + kvh) * (uint32_t)c.bs + off;
-    if (a.tma) {
-      const uint32_t asked = __ballot_sync(0xffffffffu, in);
-      if (lane == 0)
-        mbar_arrive_expect_tx(&bars[st], __popc(asked & 0x0fu) * Sh::kHalf + __popc(asked & 0xf0u) * 16 * Sh::kParams);
-      __syncwarp();
-      if (in) {
-        if (lane < 4)
-          tma_load_5d(codes + st * Sh::kCodes + ((lane >> 1) * 2 + (lane & 1)) * Sh::kHalf, lane < 2 ? &tmK : &tmV, &bars[st],
-                      0, (int)off, 0, (int)kvh, (int)phys, policy);
-        else
-          bulk_load(params_at + (st * 2 * kQmTok + (lane < 6 ? 0 : kQmTok) + 16 * (lane & 1)) * Sh::kParams,
-                    (lane < 6 ? a.kp : a.vp) + (size_t)num * quant_params<FMT>(), 16 * Sh::kParams, &bars[st]);
+    bool in[kQmHalves];
+#pragma unroll
+    for (int h = 0; h < kQmHalves; ++h) {
+      in[h] = next_off[h] >= 0;
+      if (in[h] && (uint32_t)next_phys[h] >= (uint32_t)c.num_blocks) {   // (num_blocks is below 2^31)
+        raise_flag(c.err, PKV_FLAG_BLOCK_OUT_OF_RANGE);
+        in[h] = false;
       }
+    }
+    const uint32_t kvh = (uint32_t)ahead.kvh;
+    // (rows of the cache are fewer than 2^32 - 1 here)
+    auto number = [&](int h) { return ((uint32_t)next_phys[h] * (uint32_t)c.KVH + kvh) * (uint32_t)c.bs + (uint32_t)next_off[h]; };
+    if (a.tma) {
+      if (lane == 0) {
+        int halves = 0;
+#pragma unroll
+        for (int h = 0; h < kQmHalves; ++h) halves += in[h];
+        mbar_arrive_expect_tx(&bars[st], halves * 2 * (Sh::kHalf + 16 * Sh::kParams));
+#pragma unroll
+        for (int h = 0; h < kQmHalves; ++h) {
+          if (!in[h]) continue;
+          uint8_t *to = codes + st * Sh::kCodes + h * Sh::kHalf;
+          tma_load_5d(to, &tmK, &bars[st], 0, next_off[h], 0, (int)kvh, next_phys[h], policy);
+          tma_load_5d(to + kQmHalves * Sh::kHalf, &tmV, &bars[st], 0, next_off[h], 0, (int)kvh, next_phys[h], policy);
+          const uint32_t at = params_at + (st * 2 * kQmTok + 16 * h) * Sh::kParams;
+          const size_t num = (size_t)number(h) * quant_params<FMT>();
+          bulk_load(at, a.kp + num, 16 * Sh::kParams, &bars[st]);
+          bulk_load(at + kQmTok * Sh::kParams, a.vp + num, 16 * Sh::kParams, &bars[st]);
+        }
+      }
+      __syncwarp();
     } else {
-      const uint32_t row = in ? (phys * (uint32_t)c.bs + off) * (uint32_t)c.KVH + kvh : 0xffffffffu;
-      if (in) {
+      const uint32_t row = in[0] ? ((uint32_t)next_phys[0] * (uint32_t)c.bs + (uint32_t)next_off[0]) * (uint32_t)c.KVH + kvh : 0xffffffffu;
+      if (in[0]) {
         const uint32_t to = params_at + (st * 2 * kQmTok + lane) * Sh::kParams;
-        cp_async_small<Sh::kParams>(to, a.kp + (size_t)num * quant_params<FMT>(), Sh::kParams);
-        cp_async_small<Sh::kParams>(to + kQmTok * Sh::kParams, a.vp + (size_t)num * quant_params<FMT>(), Sh::kParams);
+        const size_t num = (size_t)number(0) * quant_params<FMT>();
+        cp_async_small<Sh::kParams>(to, a.kp + num, Sh::kParams);
+        cp_async_small<Sh::kParams>(to + kQmTok * Sh::kParams, a.vp + num, Sh::kParams);
       }
 #pragma unroll
-      for (int j = 0; j < Sh::kChunks; ++j) {
+      for (int j = 0; j < (kQmTok * Sh::kChunks + 31) / 32; ++j) {
         const int idx = lane + 32 * j, r = idx / Sh::kChunks, ch = idx - r * Sh::kChunks;
-        const uint32_t from = __shfl_sync(0xffffffffu, row, r);
-        if (from != 0xffffffffu) {
+        const uint32_t from = __shfl_sync(0xffffffffu, row, r & 31);
+        if (r < kQmTok && from != 0xffffffffu) {
           const uint32_t to = codes_at + st * Sh::kCodes + (r >> 4) * Sh::kHalf + qm_at<Sh::kRow, Sh::kBox, Sh::kSwizzle>(r & 15, ch);
           cp_async16(to, a.k + (size_t)from * Sh::kRow + ch * 16, 16);
-          cp_async16(to + 2 * Sh::kHalf, a.v + (size_t)from * Sh::kRow + ch * 16, 16);
+          cp_async16(to + kQmHalves * Sh::kHalf, a.v + (size_t)from * Sh::kRow + ch * 16, 16);
         }
       }
       cp_async_arrive(&bars[st]);
@@ -648,7 +662,7 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
       for (int k = i + 1; k < min(mine, i + S - 1); ++k) mbar_wait_bounded(&bars[k % S], (k / S) & 1);
       return;
     }
-    const uint32_t kb = codes_at + st * Sh::kCodes, vb = kb + 2 * Sh::kHalf;
+    const uint32_t kb = codes_at + st * Sh::kCodes, vb = kb + kQmHalves * Sh::kHalf;
     const uint32_t kpb = params_at + st * 2 * kQmTok * Sh::kParams, vpb = kpb + kQmTok * Sh::kParams;
     const int tile0 = cur.base + kQmTok * cur.tile;
     const bool whole = tile0 >= cur.first && tile0 + kQmTok <= cur.n;
@@ -669,10 +683,10 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
     }
     // every lane is done with tile i - 1, whose stage is next (the vote above)
     issue(i + S - 1);
-    float x[2][4], sv[2][2];
+    float x[kQmHalves][4], sv[kQmHalves][2];
     int ve_new = ve;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
+    for (int mt = 0; mt < kQmHalves; ++mt) {
       const int r0 = mt * 16 + g, r1 = r0 + 8;
       float s[2][4] = {};                                // (two chains)
       const uint32_t kh = kb + mt * Sh::kHalf;
@@ -719,14 +733,14 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
     }
     if (cap != kCapNone) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < kQmHalves; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           x[mt][e] = cap == kCapUsual ? chunk_capped(x[mt][e], c.cap_log2) : chunk_cap(c, x[mt][e]);
     }
     if (!whole) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < kQmHalves; ++mt)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const int t = tile0 + mt * 16 + hf * 8 + g;
@@ -739,12 +753,14 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
     const float m0 = m[0] + 8.f, m1 = m[1] + 8.f;
     bool over = ve_new > ve;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) over = over || x[mt][0] > m0 || x[mt][1] > m1 || x[mt][2] > m0 || x[mt][3] > m1;
+    for (int mt = 0; mt < kQmHalves; ++mt) over = over || x[mt][0] > m0 || x[mt][1] > m1 || x[mt][2] > m0 || x[mt][3] > m1;
     if (__any_sync(0xffffffffu, over)) {
       ve_new = __reduce_max_sync(0xffffffffu, ve_new);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float top = fmaxf(fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2]));
+        float top = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < kQmHalves; ++mt) top = fmaxf(top, fmaxf(x[mt][e], x[mt][e + 2]));
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
         top = fmaxf(top, m[e]);
@@ -761,10 +777,10 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
     }
     const float unit = __int_as_float((127 + kUnit - ve) << 23);    // 2^(kUnit - ve)
     // weights, as the product's B
-    uint32_t wb[2][2], wl[2][2];
+    uint32_t wb[kQmHalves][2], wl[kQmHalves][2];
     const float r0 = chunk_ref(m[0]), r1 = chunk_ref(m[1]);
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < kQmHalves; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const float p0 = fast_exp2(x[mt][2 * hf] - r0), p1 = fast_exp2(x[mt][2 * hf + 1] - r1);
@@ -784,7 +800,7 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
         wb[mt][hf] = movm_trans(*reinterpret_cast<uint32_t *>(&h));
       }
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
+    for (int mt = 0; mt < kQmHalves; ++mt) {
       const uint32_t vh = vb + mt * Sh::kHalf;
       auto product = [&](int ks, const uint32_t (&A)[4]) {
         MmaOp<__half>::run(o[ks], A, wb[mt][0], wb[mt][1]);
