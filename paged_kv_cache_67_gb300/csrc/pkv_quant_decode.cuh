@@ -10,22 +10,25 @@
 
 namespace pkv {
 
-// Shape of the tensor-core kernel's ring: tokens and bytes of a tile, tiles of
-// a warp, CTAs of kQmWarps warps that fit an SM's 228 KB (1 KB of it a CTA's
-// own; more than three would cost registers).
+// Shape of the tensor-core kernel: tokens of a tile, pairs of warps of a CTA, and
+// its rings: as many tiles as let two CTAs share an SM's 228 KB (1 KB of it a
+// CTA's own), at least two and at most six; rows too wide for that have one CTA.
 constexpr int kQmTok = 32;
 constexpr int kQmHalves = kQmTok / 16;
 constexpr int kQmWarps = 4;
+constexpr int kQmThreads = 2 * 32 * kQmWarps;
 constexpr int kQmGroups = 32 * kQmWarps;   // groups of sequences whose first tiles a CTA keeps
-constexpr int kQmStages = 3;
-constexpr int kQmMostCtas = 3;
-// (the ring begins at a multiple of 1 KB; barriers, first tiles, a scan's sums)
-constexpr int kQmPre = 1024 + 8 * kQmWarps * kQmStages + 4 * (kQmGroups + 2 + kQmWarps);
-constexpr int qm_smem(int row, int params) { return kQmWarps * kQmStages * kQmTok * 2 * (row + params) + kQmPre; }
-constexpr int qm_ctas(int row, int params) {
-  const int n = 228 * 1024 / (qm_smem(row, params) + 1024);
-  return n > kQmMostCtas ? kQmMostCtas : n;
+constexpr int kQmMostCtas = 2;
+constexpr int kQmMostStages = 6;
+// (the rings begin at a multiple of 1 KB; barriers, first tiles, a scan's sums)
+constexpr int kQmPre = 1024 + 16 * kQmWarps * kQmMostStages + 4 * (kQmGroups + 2 + kQmWarps);
+constexpr int qm_tile(int row, int params) { return kQmWarps * kQmTok * 2 * (row + params); }
+constexpr int qm_ctas(int row, int params) { return 2 * qm_tile(row, params) + kQmPre <= 113 * 1024 ? 2 : 1; }
+constexpr int qm_stages(int row, int params) {
+  const int n = ((qm_ctas(row, params) == 2 ? 113 : 227) * 1024 - kQmPre) / qm_tile(row, params);
+  return n > kQmMostStages ? kQmMostStages : n;
 }
+constexpr int qm_smem(int row, int params) { return qm_stages(row, params) * qm_tile(row, params) + kQmPre; }
 // Bytes of a row that lie together in the ring: a power of two is swizzled by
 // TMA over itself, others are conflict-free or nearly so as they are.
 constexpr int qm_box(int row) { return row % 128 == 0 ? 128 : row == 192 ? 64 : row; }

@@ -27,8 +27,9 @@
 // Work.  All tiles of all units -- a unit is a sequence's visible keys for one
 // head group of a KV head -- stand in one line, and every warp of a grid that
 // fills the GPU once takes an equal stretch of it: lengths may be as ragged as
-// they like.  Warps run by themselves, with no barrier: each has a ring in shared
-// memory, filled ahead (across the ends of units too).  Where blocks are whole
+// they like.  Warps run by themselves, with no barrier over the CTA: each has a
+// ring in shared memory and a second warp that fills it (across the ends of units
+// too): asking for a tile takes as long as computing on it, some 1300 cycles.  Where blocks are whole
 // chunks of 16 tokens, TMA brings them, a box of K and one of V a chunk; any other
 // block size goes row by row, 16 bytes a cp.async, to the same places.  (All by
 // cp.async, a batch of 64 x 2304 keys took 79 us, and 88 with the arithmetic
@@ -59,7 +60,7 @@ struct QmShape {
   static constexpr int kParams = 4 * quant_params<FMT>();             // bytes a row
   static constexpr int kHalf = 16 * kRow;                             // 16 tokens' rows of K or V
   static constexpr int kCodes = 2 * kQmHalves * kHalf;                // of a tile: K's halves, V's
-  static constexpr int kStages = kQmStages;
+  static constexpr int kStages = qm_stages(kRow, kParams);
   static constexpr int kSmem = qm_smem(kRow, kParams);
   static constexpr int kCtas = qm_ctas(kRow, kParams);
   static_assert(kHalf % 128 == 0 && (kSwizzle == 0 || kHalf % (8 * kBox) == 0), "the swizzle's period");
@@ -217,7 +218,7 @@ __device__ __forceinline__ void qm_keys(const ChunkArgs &c, int b, QmAt &s) {
 }
 
 template <int D, int FMT, bool SPLIT>
-__global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
+__global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
     pkv_quant_decode_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                                 const __grid_constant__ QuantDecodeArgs a, const int dt) {
   using Sh = QmShape<D, FMT>;
@@ -226,18 +227,19 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *codes_all = smem, *params_all = smem + kQmWarps * S * Sh::kCodes;
   uint64_t *bars_all = reinterpret_cast<uint64_t *>(params_all + kQmWarps * S * 2 * kQmTok * Sh::kParams);
-  int *s_first = reinterpret_cast<int *>(bars_all + kQmWarps * S);           // [groups + 1] tiles of one (KV head, head group)
+  int *s_first = reinterpret_cast<int *>(bars_all + 2 * kQmWarps * S);       // [groups + 1] tiles of one (KV head, head group)
   int *s_warp = s_first + kQmGroups + 2;
   const ChunkArgs &c = a.c;
   const bool rest = SPLIT ? dt != PKV_BF16 : dt == PKV_F16;   // weights of two parts
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+  const bool producer = threadIdx.x >= 32 * kQmWarps;         // warp w + 4 fills warp w's ring
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % kQmWarps, g = lane >> 2, t4 = lane & 3;
   const bool q16 = reinterpret_cast<uintptr_t>(c.q) % 16 == 0, out8 = reinterpret_cast<uintptr_t>(c.out) % 8 == 0;
 
   // ---- the line: first tiles of kQmGroups groups of sequences
   const int per = (c.B + kQmGroups - 1) / kQmGroups;
   {
     int sum = 0;
-    for (int b = threadIdx.x * per; b < min(c.B, (int)(threadIdx.x + 1) * per); ++b) {
+    for (int b = threadIdx.x * per; !producer && b < min(c.B, (int)(threadIdx.x + 1) * per); ++b) {
       QmAt s;
       qm_keys(c, b, s);
       sum += s.tiles;                       // (fewer than 2^31 in all: the host's check)
@@ -254,11 +256,20 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
       const int x = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += x;
     }
-    if (lane == 31) s_warp[w] = scan;
+    if (!producer && lane == 31) s_warp[w] = scan;
+    if (threadIdx.x == 0) {
+      s_first[0] = 0;
+      for (int k = 0; k < kQmWarps * S; ++k) {
+        mbar_init(&bars_all[k], a.tma ? 33 : 32);         // full: the copies' lanes (and the one that asks for boxes)
+        mbar_init(&bars_all[kQmWarps * S + k], 1);        // free again
+      }
+      fence_mbar_init();
+    }
     __syncthreads();
-    for (int k = 0; k < w; ++k) scan += s_warp[k];
-    s_first[threadIdx.x + 1] = scan;
-    if (threadIdx.x == 0) s_first[0] = 0;
+    if (!producer) {
+      for (int k = 0; k < w; ++k) scan += s_warp[k];
+      s_first[threadIdx.x + 1] = scan;
+    }
     __syncthreads();
   }
   // sequences without a visible key
@@ -266,7 +277,7 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
     QmAt s;
     qm_keys(c, b, s);
     if (s.tiles == 0)
-      for (int i = threadIdx.x; i < c.H * D / 2; i += 32 * kQmWarps) put_two(c.out, (size_t)b * c.H * D + 2 * i, dt, out8, 0.f, 0.f);
+      for (int i = threadIdx.x; i < c.H * D / 2; i += kQmThreads) put_two(c.out, (size_t)b * c.H * D + 2 * i, dt, out8, 0.f, 0.f);
   }
   // A team of `team` neighbouring warps (of one CTA, or two) walks the same
   // tokens for neighbouring units, so that a token's rows, which lie together,
@@ -280,12 +291,11 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
   // neighbours in the line are on different SMs: short lines use them all
   const int me = team > kQmWarps ? blockIdx.x / (team / kQmWarps) : w / team * gridDim.x + blockIdx.x;
   const long long begin = me * share;
-  if (begin >= total || me >= teams) return;
-  const int mine = (int)min(share, total - begin);
+  const int mine = begin < total && me < teams ? (int)min(share, total - begin) : 0;
 
-  QmAt cur;
-  long long unit0;                          // the current unit's first tile in the line
-  {
+  QmAt cur = {};
+  long long unit0 = 0;                      // the current unit's first tile in the line
+  if (mine > 0) {
     // the group by bisection, its sequence 32 at a time, then the unit
     int lo = 0, hi = kQmGroups - 1;
     while (lo < hi) {
@@ -338,12 +348,7 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
   // 16 tokens, then their parameters.  Block table entries are looked up one tile
   // ahead, so that they are there when they are needed.  What holds no visible
   // key is not read.
-  uint64_t *bars = bars_all + w * S;
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&bars[s], a.tma ? 1 : 32);
-    fence_mbar_init();
-  }
-  __syncwarp();
+  uint64_t *bars = bars_all + w * S, *free_bars = bars_all + (kQmWarps + w) * S;
   uint8_t *codes = codes_all + w * S * Sh::kCodes, *params = params_all + w * S * 2 * kQmTok * Sh::kParams;
   const uint32_t codes_at = smem_u32(codes), params_at = smem_u32(params);
   const uint64_t policy = l2_evict_first_policy();
@@ -378,32 +383,35 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
     const uint32_t kvh = (uint32_t)ahead.kvh;
     // (rows of the cache are fewer than 2^32 - 1 here)
     auto number = [&](int h) { return ((uint32_t)next_phys[h] * (uint32_t)c.KVH + kvh) * (uint32_t)c.bs + (uint32_t)next_off[h]; };
+    const uint32_t params_to = params_at + (st * 2 * kQmTok + lane) * Sh::kParams;
     if (a.tma) {
       if (lane == 0) {
         int halves = 0;
 #pragma unroll
         for (int h = 0; h < kQmHalves; ++h) halves += in[h];
-        mbar_arrive_expect_tx(&bars[st], halves * 2 * (Sh::kHalf + 16 * Sh::kParams));
+        mbar_arrive_expect_tx(&bars[st], halves * 2 * Sh::kHalf);
 #pragma unroll
         for (int h = 0; h < kQmHalves; ++h) {
           if (!in[h]) continue;
           uint8_t *to = codes + st * Sh::kCodes + h * Sh::kHalf;
           tma_load_5d(to, &tmK, &bars[st], 0, next_off[h], 0, (int)kvh, next_phys[h], policy);
           tma_load_5d(to + kQmHalves * Sh::kHalf, &tmV, &bars[st], 0, next_off[h], 0, (int)kvh, next_phys[h], policy);
-          const uint32_t at = params_at + (st * 2 * kQmTok + 16 * h) * Sh::kParams;
-          const size_t num = (size_t)number(h) * quant_params<FMT>();
-          bulk_load(at, a.kp + num, 16 * Sh::kParams, &bars[st]);
-          bulk_load(at + kQmTok * Sh::kParams, a.vp + num, 16 * Sh::kParams, &bars[st]);
         }
       }
       __syncwarp();
+      // lane r token r's parameters
+      const int h = lane / 16;
+      if (h == 0 ? in[0] : in[kQmHalves - 1]) {
+        const size_t num = (size_t)(h == 0 ? number(0) : number(kQmHalves - 1)) + (lane & 15);
+        cp_async_small<Sh::kParams>(params_to, a.kp + num * quant_params<FMT>(), Sh::kParams);
+        cp_async_small<Sh::kParams>(params_to + kQmTok * Sh::kParams, a.vp + num * quant_params<FMT>(), Sh::kParams);
+      }
     } else {
       const uint32_t row = in[0] ? ((uint32_t)next_phys[0] * (uint32_t)c.bs + (uint32_t)next_off[0]) * (uint32_t)c.KVH + kvh : 0xffffffffu;
       if (in[0]) {
-        const uint32_t to = params_at + (st * 2 * kQmTok + lane) * Sh::kParams;
         const size_t num = (size_t)number(0) * quant_params<FMT>();
-        cp_async_small<Sh::kParams>(to, a.kp + num, Sh::kParams);
-        cp_async_small<Sh::kParams>(to + kQmTok * Sh::kParams, a.vp + num, Sh::kParams);
+        cp_async_small<Sh::kParams>(params_to, a.kp + num, Sh::kParams);
+        cp_async_small<Sh::kParams>(params_to + kQmTok * Sh::kParams, a.vp + num, Sh::kParams);
       }
 #pragma unroll
       for (int j = 0; j < (kQmTok * Sh::kChunks + 31) / 32; ++j) {
@@ -415,16 +423,32 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
           cp_async16(to + kQmHalves * Sh::kHalf, a.v + (size_t)from * Sh::kRow + ch * 16, 16);
         }
       }
-      cp_async_arrive(&bars[st]);
     }
+    cp_async_arrive(&bars[st]);
     if (i + 1 < mine) {
       advance(ahead);
       look_up(ahead);
     }
   };
-  look_up(ahead);
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i);
+  // Two CTAs an SM are launched with 128 registers a thread: the warps that fill
+  // the rings leave some of theirs to those that compute.  (Every warp comes here.)
+  if (producer) {
+    if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(48));
+    if (mine == 0) return;
+    look_up(ahead);
+    for (int i = 0; i < mine; ++i) {
+      if (i >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(&free_bars[i % S], (i / S - 1) & 1))) {
+        // give up, once the copies that were asked for have landed (bounded)
+        if (lane == 0) raise_flag(c.err, PKV_FLAG_TIMEOUT);
+        for (int k = max(0, i - S); k < i; ++k) mbar_wait_bounded(&bars[k % S], (k / S) & 1);
+        return;
+      }
+      issue(i);
+    }
+    return;
+  }
+  if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(200));
+  if (mine == 0) return;
   // this lane's places in a half: K's row g (and g + 8, half a box further) at
   // chunk j of a box, V's row lane mod 16 at chunk j and, from lane 16 on, j + 1
   constexpr int kPer = Sh::kBox / 16;
@@ -657,9 +681,7 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
   for (int i = 0; i < mine; ++i) {
     const int st = i % S;
     if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], (i / S) & 1))) {
-      // give up, once the copies that were asked for have landed (bounded)
-      if (lane == 0) raise_flag(c.err, PKV_FLAG_TIMEOUT);
-      for (int k = i + 1; k < min(mine, i + S - 1); ++k) mbar_wait_bounded(&bars[k % S], (k / S) & 1);
+      if (lane == 0) raise_flag(c.err, PKV_FLAG_TIMEOUT);   // (the warp that fills the ring gives up too)
       return;
     }
     const uint32_t kb = codes_at + st * Sh::kCodes, vb = kb + kQmHalves * Sh::kHalf;
@@ -681,8 +703,6 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
       fence_proxy_async_shared();
       __syncwarp();
     }
-    // every lane is done with tile i - 1, whose stage is next (the vote above)
-    issue(i + S - 1);
     float x[kQmHalves][4], sv[kQmHalves][2];
     int ve_new = ve;
 #pragma unroll
@@ -846,6 +866,8 @@ __global__ void __launch_bounds__(32 * kQmWarps, QmShape<D, FMT>::kCtas)
         block(Sh::kChunks - 1, w0, w1);
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&free_bars[st]);
     const bool ends = cur.tile + 1 == cur.tiles;
     if (ends || i + 1 == mine) finish();
     if (i + 1 < mine && advance(cur)) {
@@ -866,7 +888,7 @@ static pkv_status launch_qm(const QuantDecodeArgs &a, pkv_dtype dt, cudaStream_t
   if (a.tma && (!encode_codes_map(&maps[0], a.k, a.c.num_blocks, a.c.bs, a.c.KVH, Sh::kRow, Sh::kBox) ||
                 !encode_codes_map(&maps[1], a.v, a.c.num_blocks, a.c.bs, a.c.KVH, Sh::kRow, Sh::kBox)))
     return PKV_ERR_CUDA;
-  kern<<<(unsigned)a.grid, 32 * kQmWarps, Sh::kSmem, stream>>>(maps[0], maps[1], a, (int)dt);
+  kern<<<(unsigned)a.grid, kQmThreads, Sh::kSmem, stream>>>(maps[0], maps[1], a, (int)dt);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
