@@ -149,6 +149,15 @@ __device__ __forceinline__ float granule_max(const uint4 &g) {
   }
 }
 
+// (h, l) += (bh, bl), the sum's rounding kept in l: the order of a and b does not
+// matter, and 64-bit additions, of which this GPU does few, stay out of the way.
+__device__ __forceinline__ void add_pair(float &h, float &l, float bh, float bl) {
+  const float s = __fadd_rn(h, bh), t = __fadd_rn(s, -h);
+  const float e = __fadd_rn(__fadd_rn(h, -__fadd_rn(s, -t)), __fadd_rn(bh, -t));
+  h = s;
+  l = __fadd_rn(__fadd_rn(l, bl), e);
+}
+
 __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -300,7 +309,7 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
   constexpr long long kPiece = (long long)kBsThreads * E;
   __shared__ float s_f[kBsWarps];
   __shared__ uint32_t s_u[kBsWarps];
-  __shared__ double s_d[kBsWarps];
+  __shared__ float2 s_d[kBsWarps];
   __shared__ int s_n, s_last;
   __shared__ unsigned long long s_keys[kBsKeys];
   __shared__ unsigned long long s_list[kBsWarps][kBsList];
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
       m = fmaxf(m, s_f[k]);
       u = max(u, s_u[k]);
     }
-    // (a thread's sum in fp32, threads' sums in 64 bits)
+    // (a thread's sum in fp32, threads' sums in pairs of floats)
     float sum = 0.f;
     const float unit = m > -INFINITY ? m * kLog2e : 0.f;
     if (fabsf(m) >= kBsFar && m > -INFINITY) {             // what is not m is far below it
@@ -367,10 +376,10 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
       for (int e = 0; e < kPer; ++e) part_sum += fast_exp2(fmaf(granule_at<T>(g[i], e), kLog2e, -unit));
       sum += part_sum;
     }
-    double total = sum;
+    float low = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) s_d[warp] = total;
+    for (int o = 16; o > 0; o >>= 1) add_pair(sum, low, __shfl_xor_sync(0xffffffffu, sum, o), __shfl_xor_sync(0xffffffffu, low, o));
+    if (lane == 0) s_d[warp] = make_float2(sum, low);
     // 3. what is at or above the bound, -inf excepted
     const float bound = from_ordered(u);
     if (!any_nan && mine >= bound && mine > -INFINITY) {
@@ -392,11 +401,14 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
     __syncthreads();
     const int n = s_n;
     const long long out = row * a.parts + part;
-    if (tid == 0) {
-      total = 0.0;
-      for (int k = 0; k < kBsWarps; ++k) total += s_d[k];
-      a.maxima[out] = any_nan ? __int_as_float(0x7fc00000) : m;
-      a.sums[out] = total;
+    if (warp == kBsWarps - 1) {
+      float2 v = lane < kBsWarps ? s_d[lane] : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int o = kBsWarps / 2; o > 0; o >>= 1) add_pair(v.x, v.y, __shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+      if (lane == 0) {
+        a.maxima[out] = any_nan ? __int_as_float(0x7fc00000) : m;
+        a.sums[out] = (double)v.x + (double)v.y;
+      }
     }
     unsigned long long *keys = a.keys + out * a.K;
     if (n <= kBsKeys) {

@@ -14,6 +14,32 @@ namespace pkv {
 constexpr int kQuantThreads = 256;
 constexpr float kQuantTiny = 7.888609052210118e-31f;   // 2^-100
 
+// t / d for t < 2^31 by a multiplication: a division costs as much as a row's
+// arithmetic.
+struct QuantDiv {
+  uint32_t mul;
+  int shift;
+};
+static QuantDiv quant_div(uint32_t d) {
+  QuantDiv r = {0, 0};
+  while ((1ULL << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)((((1ULL << r.shift) - (uint64_t)d) << 32) / d + 1);
+  return r;
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t t, const QuantDiv &d) { return (__umulhi(t, d.mul) + t) >> d.shift; }
+
+// The larger (smaller) of two; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 struct QuantRowsArgs {
   char *codes[2];          // k, v
   float *params[2];
@@ -22,6 +48,8 @@ struct QuantRowsArgs {
   int *err;
   long long T, stride[2], capacity;   // strides in elements
   int bs, KVH, D, lanes, vecs;        // lanes of a group, vectors of a row
+  QuantDiv by_kvh, by_bs;             // (rows of a launch are fewer than 2^31)
+  int small;                          // slots are, too
 };
 
 // 16 bytes, or (fewer) elements at their own alignment.
@@ -43,11 +71,12 @@ struct QuantCodes {
 // (token, head) of this lane's group; false past the last, for padding and for
 // slots past the pool.
 __device__ __forceinline__ bool quant_row(const QuantRowsArgs &a, long long &t, int &h, long long &slot, int &at) {
-  const int per_cta = kQuantThreads / a.lanes;
-  const long long row = (long long)blockIdx.x * per_cta + threadIdx.x / a.lanes;
-  at = threadIdx.x % a.lanes;
-  t = row / a.KVH;
-  h = (int)(row - t * a.KVH);
+  const uint32_t lane = threadIdx.x & 31, group = lane / a.lanes;     // (a.lanes: a power of two)
+  at = (int)(lane - group * a.lanes);
+  const uint32_t row = (blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5)) * (32 / a.lanes) + group;
+  const uint32_t token = div_by(row, a.by_kvh);
+  t = token;
+  h = (int)(row - token * a.KVH);
   if (t >= a.T) return false;
   slot = __ldg(a.slots + t);
   if (slot < 0) return false;
@@ -78,38 +107,39 @@ __global__ void __launch_bounds__(kQuantThreads) pkv_quant_write_kernel(const __
       if (has && v < a.vecs)
         x[s][i] = *(reinterpret_cast<const V *>(reinterpret_cast<const T *>(a.x[s]) + t * a.stride[s] + (long long)h * a.D) + v);
     }
-  bool finite[2];
+  // lo, hi: the row's ends, 0 among them (int8, e4m3: hi its largest magnitude);
+  // NaN where it holds one
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     lo[s] = hi[s] = 0.f;
-    float sum = 0.f;                                   // 0 * x: NaN for what is not finite
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float f = to_f32<T>(x[s][i].e[e]);
-        lo[s] = fminf(lo[s], f);
-        hi[s] = fmaxf(hi[s], f);
-        sum = fmaf(f, 0.f, sum);
+        if constexpr (FMT == kInt4) {
+          lo[s] = min_nan(lo[s], f);
+          hi[s] = max_nan(hi[s], f);
+        } else {
+          hi[s] = max_nan(hi[s], fabsf(f));
+        }
       }
-    finite[s] = sum == 0.f;
   }
   for (int o = a.lanes >> 1; o > 0; o >>= 1) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      lo[s] = fminf(lo[s], __shfl_xor_sync(0xffffffffu, lo[s], o));
-      hi[s] = fmaxf(hi[s], __shfl_xor_sync(0xffffffffu, hi[s], o));
-      finite[s] = __shfl_xor_sync(0xffffffffu, (int)finite[s], o) && finite[s];
+      if constexpr (FMT == kInt4) lo[s] = min_nan(lo[s], __shfl_xor_sync(0xffffffffu, lo[s], o));
+      hi[s] = max_nan(hi[s], __shfl_xor_sync(0xffffffffu, hi[s], o));
     }
   }
   if (!has) return;
   constexpr float kTop = FMT == kInt8 ? 127.f : FMT == kE4m3 ? 448.f : 15.f;
-  const long long blk = slot / a.bs;
+  const long long blk = a.small ? (long long)div_by((uint32_t)slot, a.by_bs) : slot / a.bs;
   const int off = (int)(slot - blk * a.bs);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const float span = FMT == kInt4 ? hi[s] - lo[s] : fmaxf(hi[s], -lo[s]);
-    const bool ok = finite[s] && span <= 3.402823466e38f;
+    const float span = FMT == kInt4 ? hi[s] - lo[s] : hi[s];
+    const bool ok = span <= 3.402823466e38f;               // (neither NaN nor infinite)
     const bool fine = ok && span >= kQuantTiny;
     const float inv = fine ? __fmul_rn(__frcp_rn(span), kTop) : 0.f;
     const float scale = fine ? __fmul_rn(span, 1.f / kTop) : ok ? 0.f : __int_as_float(0x7fc00000);
@@ -167,7 +197,7 @@ __global__ void __launch_bounds__(kQuantThreads) pkv_quant_read_kernel(const __g
   long long t, slot;
   int h, at;
   if (!quant_row(a, t, h, slot, at)) return;
-  const long long blk = slot / a.bs;
+  const long long blk = a.small ? (long long)div_by((uint32_t)slot, a.by_bs) : slot / a.bs;
   const int off = (int)(slot - blk * a.bs);
   typename C::Pack in[2][NV];
   float scale[2], zero[2];
@@ -208,13 +238,21 @@ __global__ void __launch_bounds__(kQuantThreads) pkv_quant_read_kernel(const __g
 
 template <typename T, int VEC, int NV, int FMT>
 static pkv_status launch_rows(const QuantRowsArgs &a, bool read, cudaStream_t stream) {
-  const long long per_cta = kQuantThreads / a.lanes, blocks = (a.T * a.KVH + per_cta - 1) / per_cta;
-  if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  if (read)
-    pkv_quant_read_kernel<T, VEC, NV, FMT><<<(unsigned)blocks, kQuantThreads, 0, stream>>>(a);
-  else
-    pkv_quant_write_kernel<T, VEC, NV, FMT><<<(unsigned)blocks, kQuantThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  // fewer than 2^31 rows a launch
+  const long long most = 0x40000000LL / a.KVH;
+  for (long long t0 = 0; t0 < a.T; t0 += most) {
+    QuantRowsArgs b = a;
+    b.T = a.T - t0 < most ? a.T - t0 : most;
+    b.slots += t0;
+    for (int s = 0; s < 2; ++s) b.x[s] += t0 * a.stride[s] * (long long)sizeof(T);
+    const long long per_cta = kQuantThreads / a.lanes, blocks = (b.T * a.KVH + per_cta - 1) / per_cta;
+    if (read)
+      pkv_quant_read_kernel<T, VEC, NV, FMT><<<(unsigned)blocks, kQuantThreads, 0, stream>>>(b);
+    else
+      pkv_quant_write_kernel<T, VEC, NV, FMT><<<(unsigned)blocks, kQuantThreads, 0, stream>>>(b);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
 }
 
 template <typename T, int VEC, int FMT>
@@ -295,6 +333,9 @@ static pkv_status quant_rows(void *const (&codes)[2], float *const (&params)[2],
   a.T = T;
   a.capacity = num_blocks * bs;
   a.bs = bs;
+  a.by_kvh = quant_div((uint32_t)KVH);
+  a.by_bs = quant_div((uint32_t)bs);
+  a.small = a.capacity <= 0x7fffffffLL;
   a.KVH = KVH;
   a.D = D;
   switch (dt) {
