@@ -6,11 +6,14 @@
 // pass over the row.  A CTA holds its piece in registers:
 //   1. load; maximum m of the piece, sum of 2^(x L - fl(m L)), L = log2 e: the
 //      rounding of m L is in the piece's unit, so the sum carries none of it;
-//   2. a bound: in a warp the K-th largest of the lanes' maxima has K elements
-//      at or above it, so the largest such bound of the 8 warps has, too;
-//   3. the elements at or above the bound (K, and few more) go to shared memory
+//   2. a bound: the K-th largest of the 256 threads' maxima has K elements at or
+//      above it.  Each warp takes its K largest maxima off, one warp-wide maximum
+//      at a time, then all do so with the eight warps' lists;
+//   3. the elements at or above the bound (K, and a few more) go to shared memory
 //      as 64-bit keys -- the logit's bits in their order, then the lowest token --
 //      and each counts the keys above its own: its rank.
+//      (With the largest of the warps' own bounds some 50 elements came through:
+//      64 x 8 beams x 128256 tokens took 113 us.)
 // The CTA that finishes a request's last piece joins: a warp a beam merges the
 // pieces' sorted keys (lane = piece, K rounds of a warp-wide maximum) and adds
 // up the sums in 64 bits; one warp then merges the beams' lists by score in 64
@@ -76,27 +79,30 @@ __device__ __forceinline__ bool beam_live(const BeamSelectArgs &a, long long row
 template <typename T>
 constexpr uint32_t kMinusInf = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
 
+// 16 bytes from p on, `off` behind an aligned place (off > 0: two aligned loads).
+__device__ __forceinline__ uint4 shifted_granule(const char *from, uint32_t off) {
+  const uint4 *p = reinterpret_cast<const uint4 *>(from - off);
+  const uint4 x = __ldg(p), y = __ldg(p + 1);
+  uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  const uint32_t words = off >> 2;
+  if (words & 2)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (words & 1)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  const uint32_t bits = (off & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 // 16 bytes of a row from byte `at` on (a multiple of 16, counted from the
 // row's start), whatever the row's alignment; -inf past its end.
 template <typename T>
 __device__ __forceinline__ uint4 row_granule(const char *row, long long at, long long bytes) {
   const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
   if (off == 0 && at + 16 <= bytes) return __ldg(reinterpret_cast<const uint4 *>(row + at));
-  if (off != 0 && at >= 16 && at + 32 <= bytes) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(row + at - off);
-    const uint4 x = __ldg(p), y = __ldg(p + 1);
-    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    const uint32_t words = off >> 2;
-    if (words & 2)
-#pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    if (words & 1)
-#pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    const uint32_t bits = (off & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-  }
+  if (off != 0 && at >= 16 && at + 32 <= bytes) return shifted_granule(row + at, off);
   // the row's ends, element by element
   constexpr int kPer = 16 / sizeof(T);
   union {
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
   constexpr int kPer = 16 / sizeof(T), E = GRANULES * kPer;
   constexpr long long kPiece = (long long)kBsThreads * E;
   __shared__ float s_f[kBsWarps];
-  __shared__ uint32_t s_u[kBsWarps];
+  __shared__ uint32_t s_top[kBsWarps * kBsMost];
   __shared__ float2 s_d[kBsWarps];
   __shared__ int s_n, s_last;
   __shared__ unsigned long long s_keys[kBsKeys];
@@ -320,10 +326,23 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
     const char *base = a.logits + row * a.stride * (long long)sizeof(T);
     const long long bytes = a.V * (long long)sizeof(T), first = part * kPiece;
     uint4 g[GRANULES];
+    // inside the row every granule is a load, or two and a shift
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(base) & 15);
+    const bool inside = (first + kPiece) * (long long)sizeof(T) + 16 <= bytes;
+    if (off == 0 && inside) {
 #pragma unroll
-    for (int i = 0; i < GRANULES; ++i) {
-      const long long at = (first + (long long)(i * kBsThreads + tid) * kPer) * (long long)sizeof(T);
-      g[i] = row_granule<T>(base, at, bytes);
+      for (int i = 0; i < GRANULES; ++i)
+        g[i] = __ldg(reinterpret_cast<const uint4 *>(base + first * (long long)sizeof(T)) + i * kBsThreads + tid);
+    } else if (part > 0 && inside) {
+#pragma unroll
+      for (int i = 0; i < GRANULES; ++i)
+        g[i] = shifted_granule(base + (first + (long long)(i * kBsThreads + tid) * kPer) * (long long)sizeof(T), off);
+    } else {
+#pragma unroll
+      for (int i = 0; i < GRANULES; ++i) {
+        const long long at = (first + (long long)(i * kBsThreads + tid) * kPer) * (long long)sizeof(T);
+        g[i] = row_granule<T>(base, at, bytes);
+      }
     }
     auto token = [&](int i, int e) { return (uint32_t)first + (uint32_t)(i * kBsThreads + tid) * kPer + e; };
     if (tid == 0) s_n = 0;
@@ -339,27 +358,42 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
     const float mine = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // 2. the warp's bound: its lanes' maxima sorted downwards, the K-th
+    // 2. the warp's K largest of its lanes' maxima, largest first
     uint32_t u = ordered(mine);
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-      for (int o = size >> 1; o > 0; o >>= 1) {
-        const uint32_t y = __shfl_xor_sync(0xffffffffu, u, o);
-        const bool down = ((lane & size) != 0) == ((lane & o) == 0);   // keep the smaller
-        u = down ? min(u, y) : max(u, y);
+    for (int k = 0; k < a.K; ++k) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, u);
+      const int from = __ffs(__ballot_sync(0xffffffffu, u == best)) - 1;
+      if (lane == from) {
+        s_top[warp * a.K + k] = best;
+        u = 0;                                             // (below every number's)
       }
-    u = __shfl_sync(0xffffffffu, u, a.K - 1);
-    if (lane == 0) {
-      s_f[warp] = m;
-      s_u[warp] = u;
     }
+    if (lane == 0) s_f[warp] = m;
     const bool any_nan = __syncthreads_or(nan);
 #pragma unroll
-    for (int k = 0; k < kBsWarps; ++k) {
-      m = fmaxf(m, s_f[k]);
-      u = max(u, s_u[k]);
+    for (int k = 0; k < kBsWarps; ++k) m = fmaxf(m, s_f[k]);
+    // ... and the K-th of the 8 K: the bound
+    uint32_t held[kBsMost / 4];
+#pragma unroll
+    for (int j = 0; j < kBsMost / 4; ++j) held[j] = lane + 32 * j < kBsWarps * a.K ? s_top[lane + 32 * j] : 0;
+    for (int k = 0; k < a.K; ++k) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < kBsMost / 4; ++j)
+        if (4 * j < a.K) top = max(top, held[j]);
+      u = __reduce_max_sync(0xffffffffu, top);
+      const int from = __ffs(__ballot_sync(0xffffffffu, top == u)) - 1;
+      if (lane == from) {
+        bool gone = false;
+#pragma unroll
+        for (int j = 0; j < kBsMost / 4; ++j)
+          if (4 * j < a.K && !gone && held[j] == u) {
+            held[j] = 0;
+            gone = true;
+          }
+      }
     }
+    u = max(u, ordered(-INFINITY));                        // (threads past the row's end have nothing)
     // (a thread's sum in fp32, threads' sums in pairs of floats)
     float sum = 0.f;
     const float unit = m > -INFINITY ? m * kLog2e : 0.f;
@@ -386,15 +420,19 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
 #pragma unroll
       for (int i = 0; i < GRANULES; ++i) {
         if (!(granule_max<T>(g[i]) >= bound)) continue;
-#pragma unroll 1
+        uint32_t hits = 0;
+#pragma unroll
         for (int e = 0; e < kPer; ++e) {
-          const uint32_t word = sizeof(T) == 4 ? e : e >> 1;
+          const float x = granule_at<T>(g[i], e);
+          hits |= x >= bound && x > -INFINITY ? 1u << e : 0u;
+        }
+        while (hits) {
+          const int e = __ffs(hits) - 1, word = sizeof(T) == 4 ? e : e >> 1;
+          hits &= hits - 1;
           const uint32_t bits = word < 2 ? (word == 0 ? g[i].x : g[i].y) : (word == 2 ? g[i].z : g[i].w);
-          const float x = granule_at<T>(make_uint4(bits, 0, 0, 0), sizeof(T) == 4 ? 0 : e & 1);
-          if (x >= bound && x > -INFINITY) {
-            const int n = atomicAdd(&s_n, 1);
-            if (n < kBsKeys) s_keys[n] = beam_key(x, token(i, e));
-          }
+          const float x = granule_at<T>(make_uint4(bits, bits, 0, 0), sizeof(T) == 4 ? 0 : e & 1);
+          const int n = atomicAdd(&s_n, 1);
+          if (n < kBsKeys) s_keys[n] = beam_key(x, token(i, e));
         }
       }
     }
