@@ -308,9 +308,10 @@ __device__ __noinline__ void beam_join(const BeamSelectArgs &a, int b, unsigned 
   }
 }
 
-// GRANULES 16-byte granules a thread: a piece is kBsThreads * GRANULES of them.
-template <typename T, int GRANULES>
-__global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __grid_constant__ BeamSelectArgs a) {
+// GRANULES 16-byte granules a thread: a piece is kBsThreads * GRANULES of them;
+// HELD: the warps' lists' entries that a lane holds, 4 HELD >= K.
+template <typename T, int GRANULES, int HELD>
+__global__ void __launch_bounds__(kBsThreads, 4) pkv_beam_select_kernel(const __grid_constant__ BeamSelectArgs a) {
   constexpr int kPer = 16 / sizeof(T), E = GRANULES * kPer;
   constexpr long long kPiece = (long long)kBsThreads * E;
   __shared__ float s_f[kBsWarps];
@@ -373,21 +374,20 @@ __global__ void __launch_bounds__(kBsThreads, 3) pkv_beam_select_kernel(const __
 #pragma unroll
     for (int k = 0; k < kBsWarps; ++k) m = fmaxf(m, s_f[k]);
     // ... and the K-th of the 8 K: the bound
-    uint32_t held[kBsMost / 4];
+    uint32_t held[HELD];
 #pragma unroll
-    for (int j = 0; j < kBsMost / 4; ++j) held[j] = lane + 32 * j < kBsWarps * a.K ? s_top[lane + 32 * j] : 0;
+    for (int j = 0; j < HELD; ++j) held[j] = lane + 32 * j < kBsWarps * a.K ? s_top[lane + 32 * j] : 0;
     for (int k = 0; k < a.K; ++k) {
       uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < kBsMost / 4; ++j)
-        if (4 * j < a.K) top = max(top, held[j]);
+      for (int j = 0; j < HELD; ++j) top = max(top, held[j]);
       u = __reduce_max_sync(0xffffffffu, top);
       const int from = __ffs(__ballot_sync(0xffffffffu, top == u)) - 1;
       if (lane == from) {
         bool gone = false;
 #pragma unroll
-        for (int j = 0; j < kBsMost / 4; ++j)
-          if (4 * j < a.K && !gone && held[j] == u) {
+        for (int j = 0; j < HELD; ++j)
+          if (!gone && held[j] == u) {
             held[j] = 0;
             gone = true;
           }
@@ -587,10 +587,18 @@ PKV_API pkv_status pkv_beam_select(float *scores_out, int32_t *parents, int32_t 
   const unsigned grid = (unsigned)(rows * plan.parts);
   auto go = [&](auto type) {
     using T = decltype(type);
-    if (plan.granules == 8)
-      pkv_beam_select_kernel<T, 8><<<grid, kBsThreads, 0, s>>>(a);
+    auto held = [&](auto n) {
+      if (plan.granules == 8)
+        pkv_beam_select_kernel<T, 8, decltype(n)::value><<<grid, kBsThreads, 0, s>>>(a);
+      else
+        pkv_beam_select_kernel<T, 2, decltype(n)::value><<<grid, kBsThreads, 0, s>>>(a);
+    };
+    if (K <= 4)
+      held(std::integral_constant<int, 1>());
+    else if (K <= 8)
+      held(std::integral_constant<int, 2>());
     else
-      pkv_beam_select_kernel<T, 2><<<grid, kBsThreads, 0, s>>>(a);
+      held(std::integral_constant<int, kBsMost / 4>());
   };
   if (dt == PKV_F32)
     go(float());
