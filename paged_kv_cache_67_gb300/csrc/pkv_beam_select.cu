@@ -155,15 +155,6 @@ __device__ __forceinline__ float granule_max(const uint4 &g) {
   }
 }
 
-// (h, l) += (bh, bl), the sum's rounding kept in l: the order of a and b does not
-// matter, and 64-bit additions, of which this GPU does few, stay out of the way.
-__device__ __forceinline__ void add_pair(float &h, float &l, float bh, float bl) {
-  const float s = __fadd_rn(h, bh), t = __fadd_rn(s, -h);
-  const float e = __fadd_rn(__fadd_rn(h, -__fadd_rn(s, -t)), __fadd_rn(bh, -t));
-  h = s;
-  l = __fadd_rn(__fadd_rn(l, bl), e);
-}
-
 __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -316,7 +307,7 @@ __global__ void __launch_bounds__(kBsThreads, 4) pkv_beam_select_kernel(const __
   constexpr long long kPiece = (long long)kBsThreads * E;
   __shared__ float s_f[kBsWarps];
   __shared__ uint32_t s_top[kBsWarps * kBsMost];
-  __shared__ float2 s_d[kBsWarps];
+  __shared__ unsigned long long s_d[kBsWarps];
   __shared__ int s_n, s_last;
   __shared__ unsigned long long s_keys[kBsKeys];
   __shared__ unsigned long long s_list[kBsWarps][kBsList];
@@ -394,7 +385,7 @@ __global__ void __launch_bounds__(kBsThreads, 4) pkv_beam_select_kernel(const __
       }
     }
     u = max(u, ordered(-INFINITY));                        // (threads past the row's end have nothing)
-    // (a thread's sum in fp32, threads' sums in pairs of floats)
+    // (a thread's sum in fp32, threads' sums in whole numbers)
     float sum = 0.f;
     const float unit = m > -INFINITY ? m * kLog2e : 0.f;
     if (fabsf(m) >= kBsFar && m > -INFINITY) {             // what is not m is far below it
@@ -410,10 +401,12 @@ __global__ void __launch_bounds__(kBsThreads, 4) pkv_beam_select_kernel(const __
       for (int e = 0; e < kPer; ++e) part_sum += fast_exp2(fmaf(granule_at<T>(g[i], e), kLog2e, -unit));
       sum += part_sum;
     }
-    float low = 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) add_pair(sum, low, __shfl_xor_sync(0xffffffffu, sum, o), __shfl_xor_sync(0xffffffffu, low, o));
-    if (lane == 0) s_d[warp] = make_float2(sum, low);
+    // a thread's sum is at most 64: whole units of 2^-20 and of 2^-40 add up
+    // exactly, in any order, and stay out of the way of the few FP64 units
+    const float whole = floorf(sum * 0x1p20f);
+    const uint32_t units = __reduce_add_sync(0xffffffffu, (uint32_t)whole);
+    const uint32_t parts = __reduce_add_sync(0xffffffffu, (uint32_t)((sum * 0x1p20f - whole) * 0x1p20f));
+    if (lane == 0) s_d[warp] = ((unsigned long long)units << 20) + parts;
     // 3. what is at or above the bound, -inf excepted
     const float bound = from_ordered(u);
     if (!any_nan && mine >= bound && mine > -INFINITY) {
@@ -439,14 +432,12 @@ __global__ void __launch_bounds__(kBsThreads, 4) pkv_beam_select_kernel(const __
     __syncthreads();
     const int n = s_n;
     const long long out = row * a.parts + part;
-    if (warp == kBsWarps - 1) {
-      float2 v = lane < kBsWarps ? s_d[lane] : make_float2(0.f, 0.f);
+    if (tid == kBsThreads - 1) {
+      unsigned long long total = 0;
 #pragma unroll
-      for (int o = kBsWarps / 2; o > 0; o >>= 1) add_pair(v.x, v.y, __shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
-      if (lane == 0) {
-        a.maxima[out] = any_nan ? __int_as_float(0x7fc00000) : m;
-        a.sums[out] = (double)v.x + (double)v.y;
-      }
+      for (int k = 0; k < kBsWarps; ++k) total += s_d[k];
+      a.maxima[out] = any_nan ? __int_as_float(0x7fc00000) : m;
+      a.sums[out] = (double)total * 0x1p-40;
     }
     unsigned long long *keys = a.keys + out * a.K;
     if (n <= kBsKeys) {

@@ -257,12 +257,10 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
       if (lane >= o) scan += x;
     }
     if (!producer && lane == 31) s_warp[w] = scan;
-    if (threadIdx.x == 0) {
-      s_first[0] = 0;
-      for (int k = 0; k < kQmWarps * S; ++k) {
-        mbar_init(&bars_all[k], a.tma ? 33 : 32);         // full: the copies' lanes (and the one that asks for boxes)
-        mbar_init(&bars_all[kQmWarps * S + k], 1);        // free again
-      }
+    if (threadIdx.x == 0) s_first[0] = 0;
+    if (threadIdx.x < 2 * kQmWarps * S) {
+      // full: the copies' lanes (and the one that asks for boxes); then free again
+      mbar_init(&bars_all[threadIdx.x], threadIdx.x >= kQmWarps * S ? 1 : a.tma ? 33 : 32);
       fence_mbar_init();
     }
     __syncthreads();
@@ -271,13 +269,6 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
       s_first[threadIdx.x + 1] = scan;
     }
     __syncthreads();
-  }
-  // sequences without a visible key
-  for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
-    QmAt s;
-    qm_keys(c, b, s);
-    if (s.tiles == 0)
-      for (int i = threadIdx.x; i < c.H * D / 2; i += kQmThreads) put_two(c.out, (size_t)b * c.H * D + 2 * i, dt, out8, 0.f, 0.f);
   }
   // A team of `team` neighbouring warps (of one CTA, or two) walks the same
   // tokens for neighbouring units, so that a token's rows, which lie together,
@@ -434,8 +425,7 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
   // the rings leave some of theirs to those that compute.  (Every warp comes here.)
   if (producer) {
     if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(48));
-    if (mine == 0) return;
-    look_up(ahead);
+    if (mine > 0) look_up(ahead);
     for (int i = 0; i < mine; ++i) {
       if (i >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(&free_bars[i % S], (i / S - 1) & 1))) {
         // give up, once the copies that were asked for have landed (bounded)
@@ -444,6 +434,14 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
         return;
       }
       issue(i);
+    }
+    // sequences without a visible key
+    for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+      QmAt s;
+      qm_keys(c, b, s);
+      if (s.tiles == 0)
+        for (int i = threadIdx.x - 32 * kQmWarps; i < c.H * D / 2; i += 32 * kQmWarps)
+          put_two(c.out, (size_t)b * c.H * D + 2 * i, dt, out8, 0.f, 0.f);
     }
     return;
   }
