@@ -80,6 +80,28 @@ template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
+// As mbar_wait_bounded; the warp sleeps up to a millisecond at a time: looking
+// again and again took a third of this kernel's instructions from the warps that
+// compute.
+__device__ __forceinline__ bool mbar_sleep_bounded(uint64_t *bar, uint32_t parity) {
+  auto done = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return true;
+  const unsigned long long t0 = global_timer_ns();
+  while (!done()) {
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return true;
+}
 // Arrives on `bar` once this thread's cp.async so far are done.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -427,10 +449,10 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
     if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(48));
     if (mine > 0) look_up(ahead);
     for (int i = 0; i < mine; ++i) {
-      if (i >= S && !__all_sync(0xffffffffu, mbar_wait_bounded(&free_bars[i % S], (i / S - 1) & 1))) {
+      if (i >= S && !__all_sync(0xffffffffu, mbar_sleep_bounded(&free_bars[i % S], (i / S - 1) & 1))) {
         // give up, once the copies that were asked for have landed (bounded)
         if (lane == 0) raise_flag(c.err, PKV_FLAG_TIMEOUT);
-        for (int k = max(0, i - S); k < i; ++k) mbar_wait_bounded(&bars[k % S], (k / S) & 1);
+        for (int k = max(0, i - S); k < i; ++k) mbar_sleep_bounded(&bars[k % S], (k / S) & 1);
         return;
       }
       issue(i);
@@ -593,80 +615,84 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
         if (prev != size - 1) return;
         if (lane == 0) *counter = 0;         // ready for the next call
         __syncwarp();
-        // all heads at once: a round trip to L2 for their maxima and sums, then
-        // one for every other source
-        constexpr int kVec = (D + 127) / 128;
-        const size_t from = place(head + min(lane, size - 1) * stride);
-        float wt[kHeads], M[kHeads], L[kHeads];
+        // as many heads at once as registers take: a round trip to L2 for their
+        // maxima and sums, then one for every other source
+        constexpr int kVec = (D + 127) / 128, kGroup = kHeads * kVec <= 8 ? kHeads : 4, kAhead = 2;
+        const size_t to = place(head);
+#pragma unroll 1
+        for (int h0 = 0; h0 < rows; h0 += kGroup) {
+          const size_t from = place(head + min(lane, size - 1) * stride) + h0;
+          float wt[kGroup], M[kGroup], L[kGroup];
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          wt[h] = lane < size && h < rows ? __ldcg(ws_m + from + h) : -INFINITY;
-          L[h] = lane < size && h < rows ? __ldcg(ws_l + from + h) : 0.f;
-        }
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          M[h] = wt[h];
-#pragma unroll
-          for (int sh = 16; sh > 0; sh >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], sh));
-          wt[h] = fast_exp2(wt[h] - chunk_ref(M[h]));
-          L[h] *= wt[h];
-#pragma unroll
-          for (int sh = 16; sh > 0; sh >>= 1) L[h] += __shfl_xor_sync(0xffffffffu, L[h], sh);
-        }
-        float4 acc[kHeads][kVec];
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-          for (int k = 0; k < kVec; ++k) acc[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kAhead = kHeads * kVec <= 8 ? 2 : 1;     // sources whose loads are in flight
-        for (int j0 = 0; j0 < size; j0 += kAhead) {
-          float4 y[kAhead][kHeads][kVec];
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const float4 *src = reinterpret_cast<const float4 *>(ws_o + place(head + min(j0 + j, size - 1) * stride) * D);
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-              for (int k = 0; k < kVec; ++k)
-                y[j][h][k] = h < rows && lane + 32 * k < D / 4 ? __ldcg(src + h * (D / 4) + lane + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int h = 0; h < kGroup; ++h) {
+            wt[h] = lane < size && h0 + h < rows ? __ldcg(ws_m + from + h) : -INFINITY;
+            L[h] = lane < size && h0 + h < rows ? __ldcg(ws_l + from + h) : 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            if (j0 + j >= size) break;
+          for (int h = 0; h < kGroup; ++h) {
+            M[h] = wt[h];
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-              const float x = __shfl_sync(0xffffffffu, wt[h], j0 + j);
+            for (int sh = 16; sh > 0; sh >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], sh));
+            wt[h] = fast_exp2(wt[h] - chunk_ref(M[h]));
+            L[h] *= wt[h];
 #pragma unroll
-              for (int k = 0; k < kVec; ++k) {
-                acc[h][k].x = fmaf(x, y[j][h][k].x, acc[h][k].x);
-                acc[h][k].y = fmaf(x, y[j][h][k].y, acc[h][k].y);
-                acc[h][k].z = fmaf(x, y[j][h][k].z, acc[h][k].z);
-                acc[h][k].w = fmaf(x, y[j][h][k].w, acc[h][k].w);
+            for (int sh = 16; sh > 0; sh >>= 1) L[h] += __shfl_xor_sync(0xffffffffu, L[h], sh);
+          }
+          float4 acc[kGroup][kVec];
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h)
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) acc[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int j0 = 0; j0 < size; j0 += kAhead) {
+            float4 y[kAhead][kGroup][kVec];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+              const float4 *src = reinterpret_cast<const float4 *>(ws_o + (place(head + min(j0 + j, size - 1) * stride) + h0) * D);
+#pragma unroll
+              for (int h = 0; h < kGroup; ++h)
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                  y[j][h][k] = h0 + h < rows && lane + 32 * k < D / 4 ? __ldcg(src + h * (D / 4) + lane + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+              const bool has = j0 + j < size;
+#pragma unroll
+              for (int h = 0; h < kGroup; ++h) {
+                float x = __shfl_sync(0xffffffffu, wt[h], j0 + j);
+                if (!has) continue;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                  acc[h][k].x = fmaf(x, y[j][h][k].x, acc[h][k].x);
+                  acc[h][k].y = fmaf(x, y[j][h][k].y, acc[h][k].y);
+                  acc[h][k].z = fmaf(x, y[j][h][k].z, acc[h][k].z);
+                  acc[h][k].w = fmaf(x, y[j][h][k].w, acc[h][k].w);
+                }
               }
             }
           }
-        }
-        const size_t to = place(head);
-        __syncwarp();                        // (every lane has read the group's first state)
+          __syncwarp();                      // (every lane has read the group's first state)
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          if (h >= rows) break;
-          const float inv = 1.f / L[h];
+          for (int h = 0; h < kGroup; ++h) {
+            if (h0 + h >= rows) break;
+            const float inv = 1.f / L[h];
 #pragma unroll
-          for (int k = 0; k < kVec; ++k) {
-            const int d = 4 * (lane + 32 * k);
-            if (d >= D) continue;
-            const float4 &y = acc[h][k];
-            if (count == 1) {
-              put_two(c.out, (out_row + h) * D + d, dt, out8, y.x * inv, y.y * inv);
-              put_two(c.out, (out_row + h) * D + d + 2, dt, out8, y.z * inv, y.w * inv);
-            } else {
-              __stcg(reinterpret_cast<float4 *>(ws_o + (to + h) * D + d), y);
+            for (int k = 0; k < kVec; ++k) {
+              const int d = 4 * (lane + 32 * k);
+              if (d >= D) continue;
+              const float4 &y = acc[h][k];
+              if (count == 1) {
+                put_two(c.out, (out_row + h0 + h) * D + d, dt, out8, y.x * inv, y.y * inv);
+                put_two(c.out, (out_row + h0 + h) * D + d + 2, dt, out8, y.z * inv, y.w * inv);
+              } else {
+                __stcg(reinterpret_cast<float4 *>(ws_o + (to + h0 + h) * D + d), y);
+              }
             }
-          }
-          if (count > 1 && lane == 0) {
-            __stcg(ws_m + to + h, M[h]);
-            __stcg(ws_l + to + h, L[h]);
+            if (count > 1 && lane == 0) {
+              __stcg(ws_m + to + h0 + h, M[h]);
+              __stcg(ws_l + to + h0 + h, L[h]);
+            }
           }
         }
       }
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
   start();
   for (int i = 0; i < mine; ++i) {
     const int st = i % S;
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], (i / S) & 1))) {
+    if (!__all_sync(0xffffffffu, mbar_sleep_bounded(&bars[st], (i / S) & 1))) {
       if (lane == 0) raise_flag(c.err, PKV_FLAG_TIMEOUT);   // (the warp that fills the ring gives up too)
       return;
     }
