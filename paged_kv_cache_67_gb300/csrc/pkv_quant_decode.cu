@@ -204,8 +204,9 @@ static void mma_plan(int B, int H, int KVH, int D, long long span, int partition
   p->grid = (int)std::min<long long>((long long)kQdSms * qm_ctas(row, params), 2 * ceil_div(tiles, 2 * kQmWarps));
   p->bytes = kChunkCnt * sizeof(int) + (size_t)2 * p->grid * kQmWarps * p->heads * (D + 2) * sizeof(float);
 }
-constexpr int kQdLevels = 3;     // of joining: 16^3 warps
-static_assert(kChunkCntFirst + kQdLevels * kQmMostCtas * kQdSms * kQmWarps <= kChunkCnt && kQmMostCtas * kQdSms * kQmWarps <= 16 * 16 * 16,
+constexpr long long kQdMostWarps = (long long)kQmMostCtas * kQdSms * kQmWarps;
+constexpr long long power(long long base, int n) { return n == 0 ? 1 : base * power(base, n - 1); }
+static_assert(kChunkCntFirst + kQmLevels * kQdMostWarps <= kChunkCnt && kQdMostWarps <= power(kQmFan, kQmLevels),
               "the counters fit the workspace's");
 
 }  // namespace pkv

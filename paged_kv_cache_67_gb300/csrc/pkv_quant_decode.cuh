@@ -19,6 +19,8 @@ constexpr int kQmWarps = 4;
 constexpr int kQmThreads = 2 * 32 * kQmWarps;
 constexpr int kQmGroups = 32 * kQmWarps;   // groups of sequences whose first tiles a CTA keeps
 constexpr int kQmMostCtas = 2;
+constexpr int kQmFan = 16;                 // states joined at once
+constexpr int kQmLevels = 3;               // joins one after the other: kQmFan^kQmLevels warps
 constexpr int kQmMostStages = 6;
 // (the rings begin at a multiple of 1 KB; barriers, first tiles, a scan's sums)
 constexpr int kQmPre = 1024 + 16 * kQmWarps * kQmMostStages + 4 * (kQmGroups + 2 + kQmWarps);

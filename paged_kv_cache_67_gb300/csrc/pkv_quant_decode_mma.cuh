@@ -49,7 +49,6 @@
 
 namespace pkv {
 
-constexpr int kQmFan = 16;                 // states joined at once
 
 template <int D, int FMT>
 struct QmShape {
@@ -185,22 +184,44 @@ __device__ __forceinline__ int div_by(int t, uint32_t mul, int shift) {
   return (int)((__umulhi((uint32_t)t, mul) + (uint32_t)t) >> shift);
 }
 
-// Four consecutive elements of a query, q 16-byte aligned or not.
-__device__ __forceinline__ float4 q_four(const void *q, size_t at, int dt, bool aligned) {
+// N times four consecutive elements of a query row, place(i) the first of the
+// i-th: every load is on its way before the first is looked at.
+template <int N, typename Place>
+__device__ __forceinline__ void q_fours(const void *q, int dt, bool aligned, const Place &place, float4 (&v)[N]) {
   if (dt == PKV_F32) {
-    const float *p = reinterpret_cast<const float *>(q) + at;
-    return aligned ? __ldg(reinterpret_cast<const float4 *>(p)) : make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+    const float *p = reinterpret_cast<const float *>(q);
+    if (aligned) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __ldg(reinterpret_cast<const float4 *>(p + place(i)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = make_float4(__ldg(p + place(i)), __ldg(p + place(i) + 1), __ldg(p + place(i) + 2), __ldg(p + place(i) + 3));
+    }
+    return;
   }
-  const unsigned short *p = reinterpret_cast<const unsigned short *>(q) + at;
-  uint2 w;
-  if (aligned)
-    w = __ldg(reinterpret_cast<const uint2 *>(p));
-  else
-    w = make_uint2(__ldg(p) | ((uint32_t)__ldg(p + 1) << 16), __ldg(p + 2) | ((uint32_t)__ldg(p + 3) << 16));
-  if (dt == PKV_BF16)
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-  const float2 a = half2_to_float2(w.x), b = half2_to_float2(w.y);
-  return make_float4(a.x, a.y, b.x, b.y);
+  const unsigned short *p = reinterpret_cast<const unsigned short *>(q);
+  uint2 w[N];
+  if (aligned) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint2 *>(p + place(i)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      w[i] = make_uint2(__ldg(p + place(i)) | ((uint32_t)__ldg(p + place(i) + 1) << 16),
+                        __ldg(p + place(i) + 2) | ((uint32_t)__ldg(p + place(i) + 3) << 16));
+  }
+  if (dt == PKV_BF16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = make_float4(__uint_as_float(w[i].x << 16), __uint_as_float(w[i].x & 0xffff0000u), __uint_as_float(w[i].y << 16),
+                         __uint_as_float(w[i].y & 0xffff0000u));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 a = half2_to_float2(w[i].x), b = half2_to_float2(w[i].y);
+      v[i] = make_float4(a.x, a.y, b.x, b.y);
+    }
+  }
 }
 
 // Two (four) neighbouring elements of an output row.
@@ -495,14 +516,17 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
   auto start = [&]() {
     const int head = ((cur.unit * team + mate) - cur.kvh * c.chunks) * kHeads + (SPLIT ? g & 3 : g);
     const bool has = head < c.G, low = SPLIT && g >= 4;
-    const size_t row = ((size_t)cur.b * c.H + cur.kvh * c.G + head) * D;
+    // (columns past the last head have a head's row, times 0)
+    const size_t row = ((size_t)cur.b * c.H + cur.kvh * c.G + (has ? head : 0)) * D;
     float4 v[kSteps];
+    // int4: a lane's eight columns of 32 are those of two steps
+    q_fours<kSteps>(c.q, dt, q16, [&](int ks) {
+      return row + (FMT == kInt4 ? (ks >> 1) * 32 + 8 * t4 + 4 * (ks & 1) : ks * 16 + 4 * t4);
+    }, v);
     float big = 0.f;
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) {
-      // int4: a lane's eight columns of 32 are those of two steps
-      const int d = FMT == kInt4 ? (ks >> 1) * 32 + 8 * t4 + 4 * (ks & 1) : ks * 16 + 4 * t4;
-      v[ks] = has ? q_four(c.q, row + d, dt, q16) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!has) v[ks] = make_float4(0.f, 0.f, 0.f, 0.f);
       big = fmaxf(fmaxf(big, fmaxf(fabsf(v[ks].x), fabsf(v[ks].y))), fmaxf(fabsf(v[ks].z), fabsf(v[ks].w)));
     }
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
