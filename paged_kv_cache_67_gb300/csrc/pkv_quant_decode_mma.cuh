@@ -244,6 +244,31 @@ __device__ __forceinline__ void put_two(void *out, size_t at, int dt, bool align
   p[0] = (unsigned short)w; p[1] = (unsigned short)(w >> 16);
 }
 
+// N pairs of neighbouring elements of an output row that begins at element `at`:
+// the i-th at column(i).  (The type is looked at once, not for every pair.)
+template <int N, typename Column, typename Pair>
+__device__ __forceinline__ void put_pairs(void *out, size_t at, int dt, bool aligned, const Column &column, const Pair &pair) {
+  if (aligned && dt == PKV_BF16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 v = pair(i);
+      *reinterpret_cast<__nv_bfloat162 *>(reinterpret_cast<__nv_bfloat16 *>(out) + at + column(i)) = __floats2bfloat162_rn(v.x, v.y);
+    }
+  } else if (aligned && dt == PKV_F16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 v = pair(i);
+      *reinterpret_cast<__half2 *>(reinterpret_cast<__half *>(out) + at + column(i)) = __floats2half2_rn(v.x, v.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 v = pair(i);
+      put_two(out, at + column(i), dt, aligned, v.x, v.y);
+    }
+  }
+}
+
 // A place in the line of tiles: tile `tile` of `tiles` of a team's unit `unit` of
 // sequence b, this warp's KV head.
 struct QmAt {
@@ -596,9 +621,7 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
         const int col = 2 * t4 + e;
         if (col >= rows) continue;
         const float inv = unit / l[e];
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks)
-          put_two(c.out, (out_row + col) * D + column(ks), dt, out8, o[ks][e] * inv, o[ks][e + 2] * inv);
+        put_pairs<kSteps>(c.out, (out_row + col) * D, dt, out8, column, [&](int ks) { return make_float2(o[ks][e] * inv, o[ks][e + 2] * inv); });
       }
       return;
     }
@@ -706,12 +729,11 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
               const int d = 4 * (lane + 32 * k);
               if (d >= D) continue;
               const float4 &y = acc[h][k];
-              if (count == 1) {
-                put_two(c.out, (out_row + h0 + h) * D + d, dt, out8, y.x * inv, y.y * inv);
-                put_two(c.out, (out_row + h0 + h) * D + d + 2, dt, out8, y.z * inv, y.w * inv);
-              } else {
+              if (count > 1)
                 __stcg(reinterpret_cast<float4 *>(ws_o + (to + h0 + h) * D + d), y);
-              }
+              else
+                put_pairs<2>(c.out, (out_row + h0 + h) * D + d, dt, out8, [](int i) { return 2 * i; },
+                             [&](int i) { return i == 0 ? make_float2(y.x * inv, y.y * inv) : make_float2(y.z * inv, y.w * inv); });
             }
             if (count > 1 && lane == 0) {
               __stcg(ws_m + to + h0 + h, M[h]);
@@ -738,15 +760,14 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
     const bool whole = tile0 >= cur.first && tile0 + kQmTok <= cur.n;
     if (!whole) {
       // values that no query sees, and their parameters, become 0: they may be anything
-      for (int j = lane; j < kQmTok * (Sh::kChunks + 1); j += 32) {
-        const int r = j / (Sh::kChunks + 1), ch = j - r * (Sh::kChunks + 1), t = tile0 + r;
-        if (t >= cur.first && t < cur.n) continue;
-        if (ch < Sh::kChunks) {
-          st_shared_v4(vb + (r >> 4) * Sh::kHalf + qm_at<Sh::kRow, Sh::kBox, Sh::kSwizzle>(r & 15, ch), make_uint4(0, 0, 0, 0));
-        } else {
-          float *to = reinterpret_cast<float *>(params + (st * 2 * kQmTok + kQmTok + r) * Sh::kParams);
-          for (int k = 0; k < quant_params<FMT>(); ++k) to[k] = 0.f;
-        }
+      const int t = tile0 + lane;
+      if (lane < kQmTok && !(t >= cur.first && t < cur.n)) {
+#pragma unroll
+        for (int ch = 0; ch < Sh::kChunks; ++ch)
+          st_shared_v4(vb + (lane >> 4) * Sh::kHalf + qm_at<Sh::kRow, Sh::kBox, Sh::kSwizzle>(lane & 15, ch), make_uint4(0, 0, 0, 0));
+        float *to = reinterpret_cast<float *>(params + (st * 2 * kQmTok + kQmTok + lane) * Sh::kParams);
+#pragma unroll
+        for (int k = 0; k < quant_params<FMT>(); ++k) to[k] = 0.f;
       }
       fence_proxy_async_shared();
       __syncwarp();
