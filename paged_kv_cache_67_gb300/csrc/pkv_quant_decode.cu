@@ -309,7 +309,7 @@ PKV_API pkv_status pkv_quant_decode_attention(
   c.bs = block_size;
   c.max_blocks = max_blocks;
   c.max_q = 1;
-  c.max_n = (int)cap;
+  c.max_n = (int)std::min<long long>(cap, (long long)max_blocks * block_size);   // (0 for a table without columns)
   c.window = window;
   c.P = plan.P;
   c.max_parts = plan.max_parts;
@@ -324,7 +324,7 @@ PKV_API pkv_status pkv_quant_decode_attention(
   a.vp = v_params;
   a.heads = plan.heads;
   // whole chunks of 16 tokens, whose parameters are 16-byte rows of their own too
-  a.tma = block_size % 16 == 0 && at(k_params, 16) && at(v_params, 16);
+  a.tma = block_size % 16 == 0 && at(k_params, 16) && at(v_params, 16) && num_blocks > 0;
   a.grid = plan.grid;
   a.least = plan.least;
   a.team = plan.team;

@@ -17,6 +17,7 @@ constexpr int kQmTok = 32;
 constexpr int kQmHalves = kQmTok / 16;
 constexpr int kQmWarps = 4;
 constexpr int kQmThreads = 2 * 32 * kQmWarps;
+constexpr int kQmRegsCompute = 200, kQmRegsFill = 48;   // of two CTAs an SM: 128 a thread in all
 constexpr int kQmGroups = 32 * kQmWarps;   // groups of sequences whose first tiles a CTA keeps
 constexpr int kQmMostCtas = 2;
 constexpr int kQmFan = 16;                 // states joined at once

@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
   // Two CTAs an SM are launched with 128 registers a thread: the warps that fill
   // the rings leave some of theirs to those that compute.  (Every warp comes here.)
   if (producer) {
-    if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(48));
+    if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQmRegsFill));
     if (mine > 0) look_up(ahead);
     for (int i = 0; i < mine; ++i) {
       if (i >= S && !__all_sync(0xffffffffu, mbar_sleep_bounded(&free_bars[i % S], (i / S - 1) & 1))) {
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
     }
     return;
   }
-  if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(200));
+  if constexpr (Sh::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQmRegsCompute));
   if (mine == 0) return;
   // this lane's places in a half: K's row g (and g + 8, half a box further) at
   // chunk j of a box, V's row lane mod 16 at chunk j and, from lane 16 on, j + 1
@@ -952,6 +952,19 @@ static pkv_status launch_qm(const QuantDecodeArgs &a, pkv_dtype dt, cudaStream_t
   using Sh = QmShape<D, FMT>;
   auto kern = pkv_quant_decode_mma_kernel<D, FMT, SPLIT>;
   if (!allow_smem(kern, Sh::kSmem, configured)) return PKV_ERR_CUDA;
+  if constexpr (Sh::kCtas == 2) {
+    // the two shares of registers come out of what a CTA is launched with; a build
+    // that gave it fewer would wait for them
+    static int regs;
+    int n = __atomic_load_n(&regs, __ATOMIC_RELAXED);
+    if (n == 0) {
+      cudaFuncAttributes attr;
+      if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return PKV_ERR_CUDA;
+      n = attr.numRegs;
+      __atomic_store_n(&regs, n, __ATOMIC_RELAXED);
+    }
+    if (n * kQmThreads < (kQmRegsCompute + kQmRegsFill) * (kQmThreads / 2)) return PKV_ERR_UNSUPPORTED;
+  }
   CUtensorMap maps[2];
   memset(maps, 0, sizeof maps);
   if (a.tma && (!encode_codes_map(&maps[0], a.k, a.c.num_blocks, a.c.bs, a.c.KVH, Sh::kRow, Sh::kBox) ||

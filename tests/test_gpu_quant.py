@@ -332,6 +332,28 @@ def test_decode_flags(fmt, D):
     assert torch.equal(out[1:], good[1:])
 
 
+@pytest.mark.parametrize("D", [128, 40])
+def test_decode_table_without_columns(D):
+    """A table of no columns holds no context: lengths are flagged, rows are
+    zeros, and the entry that is not there is not read."""
+    import ctypes
+    lib = pkv.load_library()
+    case = Case([40, 0], 4, 2, D, 16, "int8", torch.bfloat16)
+    q, kc, vc, kp, vp, tables, lens = case.on(DEV)
+    tables.fill_(0x7fffffff)
+    out = torch.full_like(q, math.nan)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+    f, p = ctypes.c_float, lambda t: ctypes.c_void_p(t.data_ptr())
+    for max_n in (0, 5):
+        out.fill_(math.nan)
+        assert lib.pkv_quant_decode_attention(p(out), p(q), p(kc), p(vc), p(kp), p(vp), p(tables), p(lens), 2, 4, 2, D, 16, 0,
+                                              case.nb, f(0.1), f(0.0), 0, 0, 1, max_n, 0, p(ws), ws.numel(), p(err), None) == 0
+        torch.cuda.synchronize()
+        assert int(err) == pkv.FLAG_CONTEXT_TOO_LONG
+        assert torch.equal(out, torch.zeros_like(out))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_decode_long_split(fmt):
     """One long context over many parts, and repeated bit for bit."""
