@@ -640,9 +640,10 @@ PKV_API pkv_status pkv_quant_read(void *k_out, void *v_out, const void *k_codes,
  *   x_j = scale * q . K_j,  x_j = softcap * tanh(x_j / softcap) if softcap > 0,
  *   out = softmax(x) . V over the visible keys j < n = context_lens[b] and, if
  *   window > 0, j >= n - window,
- * with K and V the values that the codes stand for; nothing is rounded to 16
- * bits on the way but, for bf16, the weights (fp16: half a step, 2^-11 of
- * each).  Scores, statistics and sums are fp32.  An empty context gives zeros.
+ * with K and V the values that the codes stand for.  Scores, statistics and
+ * sums are fp32; queries and weights enter the products as two fp16 numbers
+ * each (good to 2^-22; what a key adds is held to 2^-30 of the largest value
+ * scale among the visible keys).  An empty context gives zeros.
  *   block_tables, context_lens, max_context_len as in pkv_decode_attention
  *   (the same flags; a context over the table is clamped)
  *   partition_size  0 = automatic, else a positive multiple of 128: keys per

@@ -14,12 +14,13 @@
 // scales are.  What falls below fp16 there is under 2^-30 of the largest value.
 //
 // SPLIT: columns 0-3 hold four heads, columns 4-7 what fp16 leaves of them: a
-// query or a weight is hi + lo, good to 2^-23.  fp32 always, other types where
-// the KV head has four query heads or fewer (the columns are free then).  bf16
-// goes without: its queries are exact and the weights' half step, 2^-11, is an
-// eighth of what it rounds off the output.  fp16 with more heads, where it would
-// be as much as the output's own, has the rest of the weights in another turn of
-// the second product.
+// query or a weight is hi + lo, good to 2^-22.  fp32 always, other types where
+// the KV head has four query heads or fewer (the columns are free then).  16-bit
+// types with more heads, whose queries are exact in one column, have the rest of
+// the weights in another turn of the second product.  (Weights of one fp16
+// number, 2^-11 each, would move bf16 outputs by a step in places: the second
+// turn takes 64 x 512-4096 keys of 8 heads of 128, int8, 64 query heads, from
+// 76.2 to 77.2 us.)
 //
 // The running maximum is raised only when some score passes it by 2^8: one vote
 // a tile instead of three exchanges a head.
@@ -302,7 +303,6 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
   int *s_first = reinterpret_cast<int *>(bars_all + 2 * kQmWarps * S);       // [groups + 1] tiles of one (KV head, head group)
   int *s_warp = s_first + kQmGroups + 2;
   const ChunkArgs &c = a.c;
-  const bool rest = SPLIT ? dt != PKV_BF16 : dt == PKV_F16;   // weights of two parts
   const bool producer = threadIdx.x >= 32 * kQmWarps;         // warp w + 4 fills warp w's ring
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % kQmWarps, g = lane >> 2, t4 = lane & 3;
   const bool q16 = reinterpret_cast<uintptr_t>(c.q) % 16 == 0, out8 = reinterpret_cast<uintptr_t>(c.out) % 8 == 0;
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
 #pragma unroll
       for (int sh = 4; sh < 32; sh <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], sh);
     }
-    if (SPLIT && rest) {                     // a head's two columns
+    if (SPLIT) {                             // a head's two columns
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
@@ -881,14 +881,12 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
         l[0] += p0;
         l[1] += p1;
         __half2 h = __floats2half2_rn(w0, w1);
-        if (rest) {
-          const float2 f = __half22float2(h);
-          const __half2 lo = __floats2half2_rn(w0 - f.x, w1 - f.y);
-          if (SPLIT) {
-            if (t4 >= 2) h = lo;
-          } else {
-            wl[mt][hf] = movm_trans(*reinterpret_cast<const uint32_t *>(&lo));
-          }
+        const float2 f = __half22float2(h);
+        const __half2 lo = __floats2half2_rn(w0 - f.x, w1 - f.y);
+        if (SPLIT) {
+          if (t4 >= 2) h = lo;
+        } else {
+          wl[mt][hf] = movm_trans(*reinterpret_cast<const uint32_t *>(&lo));
         }
         wb[mt][hf] = movm_trans(*reinterpret_cast<uint32_t *>(&h));
       }
@@ -897,7 +895,7 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
       const uint32_t vh = vb + mt * Sh::kHalf;
       auto product = [&](int ks, const uint32_t (&A)[4]) {
         MmaOp<__half>::run(o[ks], A, wb[mt][0], wb[mt][1]);
-        if (!SPLIT && rest) MmaOp<__half>::run(o[ks], A, wl[mt][0], wl[mt][1]);
+        if (!SPLIT) MmaOp<__half>::run(o[ks], A, wl[mt][0], wl[mt][1]);
       };
       uint32_t z1[2], z16[2];                // int4: tokens 2 t4, 2 t4 + 1 (and 8 behind them) of this half tile
       if constexpr (FMT == kInt4) {

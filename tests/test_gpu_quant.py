@@ -457,3 +457,33 @@ def test_prefill_over_read_back(fmt):
         m = n - ql + i + 1
         want = ref.decode(q[i].cpu(), k[:m], v[:m], 0.088)
         assert (out[i].cpu().double() - want).abs().max() <= (2.0 ** -7 + 2.0 ** -18) * float(v[:m].abs().max())
+
+
+def off_by(case, b, h, scale):
+    """What the 32-bit arithmetic of a score, its weight and the sums may be off
+    by, of the largest |v| (see the head; the weights' two parts: 2^-22)."""
+    G, n = case.H // case.KVH, case.lens[b]
+    k = case.k[b][:, h // G].abs()
+    A = abs(scale) * float((k @ case.q[b, h].double().abs()).max()) * 1.4427
+    x = A * (2.0 ** -22 + case.D / 16 * 2.0 ** -23 + 2.0 ** -21)
+    return 2 * (x * 0.6932 + 2.0 ** -21) + 2.0 ** -22 + 2.0 ** -23 * (n / 32 + 8)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,KVH,D", [(4, 4, 64), (8, 2, 128), (4, 1, 256), (8, 1, 128), (16, 2, 96)])
+def test_decode_weights_keep_their_bits(fmt, dtype, H, KVH, D):
+    """Weights are not rounded to 16 bits.  Few keys of nearly equal weight and
+    values of both signs: outputs near 0, whose own rounding is small, show what
+    a weight lost.  Each is off by its own half step and the 32-bit form's."""
+    case = Case([2, 3, 5, 37, 64], H, KVH, D, 16, fmt, dtype, seed=50 + D, qscale=0.1)
+    scale = 1 / math.sqrt(D)
+    out = case.run(scale)
+    for b in range(len(case.lens)):
+        want = ref.decode(case.q[b], case.k[b], case.v[b], scale)
+        for h in range(H):
+            top = float(case.v[b][:, h // (H // KVH)].abs().max())
+            # (an output below fp16's normal numbers: half of 2^-24)
+            room = HALF[dtype] * want[h].abs() + 1.01 * off_by(case, b, h, scale) * top + 2.0 ** -25
+            off = (out[b, h].double() - want[h]).abs()
+            assert (off <= room).all(), (b, h, float((off - room).max()))
