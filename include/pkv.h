@@ -696,7 +696,9 @@ PKV_API size_t pkv_quant_decode_workspace_size(int B, int H, int num_kv_heads, i
  *   where finished[b, w] is not 0, itself: end_token with the score c.
  * Taken are the K best by score; of equal ones the lowest beam, then the lowest
  * token.  The order is that of the scores in 64 bits (a beam's own proposals
- * go by their logits), the sum behind the logarithm is accurate to some 1e-7.
+ * go by their logits), the sum behind the logarithm is accurate to some 1e-7
+ * for finite logits of any size: they enter as differences from the row's
+ * largest.
  *   scores_out    [B, K] float32; -inf where fewer than K were proposed
  *   parents       [B, K] int32: the beam that each one continues, -1 there
  *   tokens        [B, K] int32: the token it adds, -1 there

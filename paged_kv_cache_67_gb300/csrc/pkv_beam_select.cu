@@ -5,7 +5,9 @@
 // pieces that each give their K largest logits and a share of the sum, in one
 // pass over the row.  A CTA holds its piece in registers:
 //   1. load; maximum m of the piece, sum of 2^(x L - fl(m L)), L = log2 e: the
-//      rounding of m L is in the piece's unit, so the sum carries none of it;
+//      rounding of m L is in the piece's unit, so the sum carries none of it.
+//      Where that rounding is no longer small (|m| >= 2^15: it grows with m, and
+//      2^ of it with that) sums of 2^((x - m) L), whose difference carries none;
 //   2. a bound: the K-th largest of the 256 threads' maxima has K elements at or
 //      above it.  Each warp takes its K largest maxima off, one warp-wide maximum
 //      at a time, then all do so with the eight warps' lists;
@@ -20,7 +22,7 @@
 // The CTA that finishes a request's last piece joins: a warp a beam merges the
 // pieces' sorted keys (lane = piece, K rounds of a warp-wide maximum) and adds
 // up the sums in 64 bits; one warp then merges the beams' lists by score in 64
-// bits (lane = beam).  Memory bounds the call: every logit is read once.
+// bits (lane = beam).  Every logit is read once.
 //
 // Which token comes first must not hang on where a row starts in memory: beams
 // with equal logits have to tie.  So thread t of piece i takes the same
@@ -168,9 +170,8 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long x)
 }
 
 // The sums' unit is 2^(m L), L = log2 e as fp32 has it, the product as fp32
-// rounds it; from kBsFar on, where it would leave fp32, exact (neighbours there
-// are 2^103 apart).
-constexpr float kBsFar = 1e38f;
+// rounds it (by 2^-9 at most: a term is below 1.002); from kBsFar on, exact.
+constexpr float kBsFar = 32768.f;
 __device__ __forceinline__ double beam_unit(float m) {
   return fabsf(m) < kBsFar ? (double)(m * kLog2e) : (double)m * (double)kLog2e;
 }
@@ -178,7 +179,8 @@ __device__ __forceinline__ double beam_unit(float m) {
 // The request's K best from its pieces, by the whole CTA.
 __device__ __noinline__ void beam_join(const BeamSelectArgs &a, int b, unsigned long long (*s_list)[kBsList]) {
   __shared__ unsigned long long s_key[kBsMost][kBsMost];   // a beam's best, sorted
-  __shared__ double s_base[kBsMost];                       // c - log sum exp; finished beams: c
+  __shared__ double s_base[kBsMost];                       // c - log sum exp(x - m); finished beams: c
+  __shared__ float s_top[kBsMost];                         // m, the largest logit
   __shared__ int s_mode[kBsMost];                          // 0 no proposals, 1 its tokens, 2 itself
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.K, parts = a.parts;
   for (int w = warp; w < a.W; w += kBsWarps) {
@@ -188,8 +190,8 @@ __device__ __noinline__ void beam_join(const BeamSelectArgs &a, int b, unsigned 
     int mode = c > -INFINITY && c < INFINITY ? (done ? 2 : 1) : 0;
     bool bad = !(c < INFINITY);
     double base = c;
+    float m = -INFINITY;
     if (mode == 1) {
-      float m = -INFINITY;
       bool nan = false;
       for (int i = lane; i < parts; i += 32) {
         const float x = __ldcg(a.maxima + row * parts + i);
@@ -209,7 +211,7 @@ __device__ __noinline__ void beam_join(const BeamSelectArgs &a, int b, unsigned 
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       bad = nan;
       if (nan || m == -INFINITY) mode = 0;
-      base = (double)c - (beam_unit(m) / (double)kLog2e + log(sum));
+      base = (double)c - ((beam_unit(m) - (double)m * (double)kLog2e) / (double)kLog2e + log(sum));
     }
     if (mode == 1) {
       // lane = piece (32 apart): its next key not yet taken.  Short lists come
@@ -260,19 +262,21 @@ __device__ __noinline__ void beam_join(const BeamSelectArgs &a, int b, unsigned 
     if (lane == 0) {
       s_mode[w] = mode;
       s_base[w] = base;
+      s_top[w] = m;
       if (bad) raise_flag(a.err, PKV_FLAG_LOGITS);
     }
   }
   __syncthreads();
   if (warp != 0) return;
-  // lane = beam: its best proposal not yet taken, -inf: none left
+  // lane = beam: its best proposal not yet taken, -inf: none left.  (A score goes
+  // by the difference from the largest logit: of any size, they cancel exactly.)
   const int w = lane;
   const int mode = w < a.W ? s_mode[w] : 0;
   int at = 0;
   auto head_score = [&]() {
     if (mode == 2) return at == 0 ? s_base[w] : -INFINITY;
     if (mode == 0 || at >= K || s_key[w][at] == 0) return (double)-INFINITY;
-    return s_base[w] + (double)from_ordered((uint32_t)(s_key[w][at] >> 32));
+    return s_base[w] + ((double)from_ordered((uint32_t)(s_key[w][at] >> 32)) - (double)s_top[w]);
   };
   double head = head_score();
   for (int k = 0; k < K; ++k) {
@@ -391,21 +395,21 @@ __global__ void __launch_bounds__(kBsThreads, 4) pkv_beam_select_kernel(const __
     // (a thread's sum in fp32, threads' sums in whole numbers)
     float sum = 0.f;
     const float unit = m > -INFINITY ? m * kLog2e : 0.f;
-    if (fabsf(m) >= kBsFar && m > -INFINITY) {             // what is not m is far below it
+    auto add_up = [&](auto term) {
 #pragma unroll
-      for (int i = 0; i < GRANULES; ++i)
+      for (int i = 0; i < GRANULES; ++i) {
+        float part_sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) sum += granule_at<T>(g[i], e) == m ? 1.f : 0.f;
-    } else
-#pragma unroll
-    for (int i = 0; i < GRANULES; ++i) {
-      float part_sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) part_sum += fast_exp2(fmaf(granule_at<T>(g[i], e), kLog2e, -unit));
-      sum += part_sum;
-    }
-    // a thread's sum is at most 64: whole units of 2^-20 and of 2^-40 add up
-    // exactly, in any order, and stay out of the way of the few FP64 units
+        for (int e = 0; e < kPer; ++e) part_sum += fast_exp2(term(granule_at<T>(g[i], e)));
+        sum += part_sum;
+      }
+    };
+    if (fabsf(m) >= kBsFar && m > -INFINITY)
+      add_up([&](float x) { return (x - m) * kLog2e; });
+    else
+      add_up([&](float x) { return fmaf(x, kLog2e, -unit); });
+    // a thread's sum is at most 64 and a little: whole units of 2^-20 and of 2^-40
+    // add up exactly, in any order, and stay out of the way of the few FP64 units
     const float whole = floorf(sum * 0x1p20f);
     const uint32_t units = __reduce_add_sync(0xffffffffu, (uint32_t)whole);
     const uint32_t parts = __reduce_add_sync(0xffffffffu, (uint32_t)((sum * 0x1p20f - whole) * 0x1p20f));

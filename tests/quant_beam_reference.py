@@ -117,8 +117,9 @@ def beam_select(logits, scores, finished, K, end):
                 continue
             keep = np.nonzero(x > -math.inf)[0]
             m = x.max()
-            base = c - (m + math.log(np.exp(x - m).sum()))
-            s.append(base + x[keep]), w_.append(np.full(len(keep), w)), v_.append(keep)
+            # (differences from the largest first: added to a logit of 1e38, c would be lost)
+            base = c - math.log(np.exp(x - m).sum())
+            s.append(base + (x[keep] - m)), w_.append(np.full(len(keep), w)), v_.append(keep)
         if not s:
             continue
         s, w_, v_ = np.concatenate(s), np.concatenate(w_), np.concatenate(v_)

@@ -332,3 +332,59 @@ def test_reorder_flags():
     # a request that has no block left
     t, n, s, f, same = go(tables, [5, 5, 5], [0, 0, 0], [[1, 2, 3]] * 3)
     assert f == pkv.FLAG_OUT_OF_BLOCKS and same and n == [6, 5, 5] and s == [9, -1, -1] and t[1] == [1, 2, 3]
+
+
+def from_largest(logits, scores, K):
+    """The selection from differences to each row's largest logit, in 64 bits:
+    exact for logits of any size.  Every beam in use, none ended."""
+    B, W, V = logits.shape
+    x = logits.double()
+    d = x - x.amax(2, keepdim=True)
+    s = (scores.double()[..., None] + (d - d.exp().sum(2, keepdim=True).log())).flatten(1)
+    # best first, of equal ones the lowest (beam, token)
+    best, at = s.sort(dim=1, descending=True, stable=True)
+    return best[:, :K], (at[:, :K] // V).to(I32), (at[:, :K] % V).to(I32)
+
+
+def check_from_largest(x, c, K, apart=None):
+    got = select(x, c, None, K)
+    s, p, t = from_largest(x, c, K)
+    if apart:
+        s1, p1, _ = from_largest(x, c, K + 1)
+        gap = (s1[:, :-1] - s1[:, 1:])[p1[:, :-1] != p1[:, 1:]]
+        assert (gap > apart).all(), "beams too near"
+    assert torch.equal(got[1], p) and torch.equal(got[2], t), (got[1], p, got[2], t)
+    assert ((got[0].double() - s).abs() <= (s.abs() + 20) * 2.0 ** -22).all(), (got[0], s)
+
+
+LEVELS = [(torch.float32, v) for v in (-6e4, -7e4, -3e8, -1e9, -1e10, -1e12, -1e30, -3.4e38, 1e6, 3e9, 5e9, 1e20, 3.4e38)] + [
+    (torch.bfloat16, v) for v in (-1e9, -1e10, -1e12, -1e30, -3.38e38, 3e9, 1e20, 3.38e38)] + [(torch.float16, v) for v in (-65504.0, -3e4, 65504.0)]
+
+
+@pytest.mark.parametrize("dtype,level", LEVELS)
+@pytest.mark.parametrize("V", [50, 5000, 40001])
+def test_select_rows_at_one_level(dtype, level, V):
+    """A row that is masked throughout with a finite number is an even
+    distribution, whatever the number: beside live beams, and alone; and live
+    rows whose masked tokens have that number."""
+    x = logits_of(3, 4, V, dtype, V + 1)
+    c = torch.tensor([[-0.5, -1.0, -1.75, -2.5]]).expand(3, 4).contiguous()
+    x[0, 0] = x[0, 2] = level
+    x[1] = level
+    if level < 0:
+        x[2, :, 20:] = level                                   # (whole pieces among them)
+        x[2, 1, :30] = level                                   # a live beam among masked ones, and a dead one
+    check_from_largest(x, c, 6, apart=1e-5)
+
+
+@pytest.mark.parametrize("offset", [3e4, 6.4e4, 6.6e4, 1e5, 1e6, 2e7])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_select_far_logits(offset, sign):
+    """Logits far from 0 that differ by little: a row is what it is without the offset."""
+    B, W, V = 2, 3, 9001
+    unit = 2.0 ** (math.floor(math.log2(offset)) - 23)
+    g = torch.Generator().manual_seed(int(offset))
+    d = (torch.randn(B, W, V, generator=g).double() * 3 / unit).round() * unit
+    x = (sign * math.floor(offset / unit) * unit + d).float()
+    assert torch.equal(x.double() - sign * math.floor(offset / unit) * unit, d) or offset > 1e6
+    check_from_largest(x, torch.tensor([[-1.0, -1.3, -1.7], [-2.0, -0.1, -0.6]]), 8, apart=1e-6)
