@@ -560,8 +560,9 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
     }
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    // 2^(14 - floor(log2 big)), both ends within fp32's exponents
-    const int ex = min(max((__float_as_int(big) >> 23) - 127, -100), 100);
+    // 2^(14 - floor(log2 big)), both ways a normal number; no more than the type's
+    // largest (an infinity stays one), no less than 2^-100
+    const int ex = min(max((__float_as_int(big) >> 23) - 127, -100), 127);
     const float up = __int_as_float((14 - ex + 127) << 23), down = __int_as_float((ex - 14 + 127) << 23);
     auto part = [&](float x, float y) {
       x *= up;

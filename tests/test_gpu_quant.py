@@ -487,3 +487,19 @@ def test_decode_weights_keep_their_bits(fmt, dtype, H, KVH, D):
             room = HALF[dtype] * want[h].abs() + 1.01 * off_by(case, b, h, scale) * top + 2.0 ** -25
             off = (out[b, h].double() - want[h]).abs()
             assert (off <= room).all(), (b, h, float((off - room).max()))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H,KVH", [(8, 2), (8, 1)])
+def test_decode_large_queries(fmt, dtype, H, KVH):
+    """Queries up to the end of their type's range, with a scale to match: a
+    score is what it is for ordinary ones."""
+    case = Case([400, 33], H, KVH, 128, 16, fmt, dtype, seed=60, qscale=0.05)
+    q = case.q.clone()
+    for power in (99, 101, 110, 124):
+        case.q = (q.double() * 2.0 ** power).to(dtype)
+        case.check(case.run(0.5 * 2.0 ** -power), 0.5 * 2.0 ** -power)
+    case.q = torch.zeros_like(q)
+    case.q[..., 5] = torch.finfo(dtype).max
+    case.check(case.run(2.0 ** -126), 2.0 ** -126)
