@@ -822,7 +822,9 @@ __global__ void __launch_bounds__(kQmThreads, QmShape<D, FMT>::kCtas)
       for (int e = 0; e < 4; ++e) {
         float y = s[0][e] + s[1][e];
         if (SPLIT && dt == PKV_F32) y += __shfl_xor_sync(0xffffffffu, y, 2);
-        x[mt][e] = y * qs[e & 1] * (e < 2 ? sk0 : sk1);
+        // (scales first: the codes' product with a large query may pass fp32 where
+        // the score does not)
+        x[mt][e] = y * (qs[e & 1] * (e < 2 ? sk0 : sk1));
       }
     }
     if (cap != kCapNone) {

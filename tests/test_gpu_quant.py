@@ -503,3 +503,17 @@ def test_decode_large_queries(fmt, dtype, H, KVH):
     case.q = torch.zeros_like(q)
     case.q[..., 5] = torch.finfo(dtype).max
     case.check(case.run(2.0 ** -126), 2.0 ** -126)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("H,KVH", [(8, 2), (8, 1)])
+def test_decode_large_queries_of_small_keys(fmt, H, KVH):
+    """A query of 2^120 and keys of 2^-100: the score is in range (one key: its
+    value comes out), though the query times the codes is not."""
+    case = Case([1], H, KVH, 128, 16, fmt, torch.float32, seed=61)
+    case.q = case.q * 2.0 ** 120
+    p = case.cache[2][..., 0] if fmt == "int4" else case.cache[2]
+    p *= 2.0 ** -100
+    out = case.run(1.0)
+    want = case.v[0][0].repeat_interleave(H // KVH, 0)
+    assert (out[0].double() - want).abs().max() <= 2.0 ** -20 * want.abs().max()
