@@ -727,8 +727,8 @@ PKV_API pkv_status pkv_beam_select(float *scores_out, int32_t *parents, int32_t 
                                    void *workspace, size_t workspace_bytes, int *err_flags,
                                    pkv_stream_t stream);
 
-/* Bytes of workspace pkv_beam_select needs for these sizes, for every dtype
- * (host only); 0 for invalid sizes. */
+/* Bytes of workspace pkv_beam_select needs for these sizes and for smaller B,
+ * W, K and V, for every dtype (host only); 0 for invalid sizes. */
 PKV_API size_t pkv_beam_select_workspace_size(int B, int W, int K, int64_t V);
 
 /*

@@ -28,6 +28,7 @@
 // with equal logits have to tie.  So thread t of piece i takes the same
 // elements of every row, and rows that are not 16-byte aligned are read by
 // aligned granules, two for one, and shifted.
+#include <algorithm>
 #include <type_traits>
 
 #include "pkv_device.cuh"
@@ -497,21 +498,30 @@ __global__ void __launch_bounds__(kBsThreads, 4) pkv_beam_select_kernel(const __
 struct BeamPlan {
   int granules, parts;
 };
+// Pieces of a row, `granules` a thread.
+static long long beam_parts(int granules, long long V, int el) {
+  const long long piece = (long long)kBsThreads * granules * (16 / el);
+  return (V + piece - 1) / piece;
+}
 // Pieces of 2 granules a thread where 8 would not give every SM two CTAs.
 static BeamPlan beam_plan(long long rows, long long V, int el) {
-  auto parts = [&](int granules) {
-    const long long piece = (long long)kBsThreads * granules * (16 / el);
-    return (V + piece - 1) / piece;
-  };
-  const int granules = rows * parts(8) >= 2 * kBsSms || parts(2) > kBsParts ? 8 : 2;
-  return {granules, (int)parts(granules)};
+  const bool large = rows * beam_parts(8, V, el) >= 2 * kBsSms || beam_parts(2, V, el) > kBsParts;
+  const int granules = large ? 8 : 2;
+  return {granules, (int)beam_parts(granules, V, el)};
+}
+// The most pieces that a call of these or any smaller sizes has: fewer rows are
+// cut into small pieces again, four of them for a large one at most, of which
+// there are fewer than two an SM then.
+static long long beam_most_pieces(long long rows, long long V) {
+  const long long small = rows * std::min<long long>(beam_parts(2, V, 4), kBsParts);
+  return std::max(rows * beam_parts(8, V, 4), std::min<long long>(small, 4 * (2 * kBsSms - 1)));
 }
 
 constexpr size_t kBsCntBytes = kBsMaxB * sizeof(int);
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-static size_t beam_ws_bytes(long long rows, int parts, int K) {
-  return kBsCntBytes + align256((size_t)rows * parts * K * sizeof(unsigned long long)) +
-         align256((size_t)rows * parts * sizeof(double)) + align256((size_t)rows * parts * sizeof(float));
+static size_t beam_ws_bytes(long long pieces, int K) {
+  return kBsCntBytes + align256((size_t)pieces * K * sizeof(unsigned long long)) +
+         align256((size_t)pieces * sizeof(double)) + align256((size_t)pieces * sizeof(float));
 }
 static bool beam_sizes_ok(int B, int W, int K, int64_t V) { return B >= 0 && W > 0 && K > 0 && V > 0; }
 
@@ -523,9 +533,7 @@ extern "C" {
 
 PKV_API size_t pkv_beam_select_workspace_size(int B, int W, int K, int64_t V) {
   if (!beam_sizes_ok(B, W, K, V) || W > kBsMost || K > kBsMost || V > kBsMaxV || B > kBsMaxB) return 0;
-  const long long rows = (long long)B * W;
-  const size_t a = beam_ws_bytes(rows, beam_plan(rows, V, 4).parts, K), b = beam_ws_bytes(rows, beam_plan(rows, V, 2).parts, K);
-  return a > b ? a : b;
+  return beam_ws_bytes(beam_most_pieces((long long)B * W, V), K);
 }
 
 PKV_API pkv_status pkv_beam_select(float *scores_out, int32_t *parents, int32_t *tokens, uint8_t *finished_out,
@@ -544,7 +552,7 @@ PKV_API pkv_status pkv_beam_select(float *scores_out, int32_t *parents, int32_t 
     return PKV_ERR_INVALID_ARG;
   const long long rows = (long long)B * W;
   const BeamPlan plan = beam_plan(rows, V, el);
-  const size_t need = beam_ws_bytes(rows, plan.parts, K);
+  const size_t need = beam_ws_bytes(rows * plan.parts, K);
   if (!workspace || workspace_bytes < need || !at(workspace, 256)) return PKV_ERR_WORKSPACE;
   const size_t outs = (size_t)B * K, ins = (size_t)rows;
   const ArgRange written[] = {{scores_out, outs * 4}, {parents, outs * 4}, {tokens, outs * 4}, {finished_out, outs}, {workspace, need}};

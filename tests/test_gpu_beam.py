@@ -388,3 +388,10 @@ def test_select_far_logits(offset, sign):
     x = (sign * math.floor(offset / unit) * unit + d).float()
     assert torch.equal(x.double() - sign * math.floor(offset / unit) * unit, d) or offset > 1e6
     check_from_largest(x, torch.tensor([[-1.0, -1.3, -1.7], [-2.0, -0.1, -0.6]]), 8, apart=1e-6)
+
+
+def test_select_workspace_of_a_larger_batch():
+    """Requests finish: ten, then four, one, with the first's workspace."""
+    ws = pkv.BeamSelectWorkspace(10, 4, 4, 128256)
+    for B in (10, 4, 1, 10):
+        check_select(logits_of(B, 4, 128256, torch.float32, B), scores_of(B, 4, B), None, 4, ws=ws)

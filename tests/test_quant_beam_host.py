@@ -204,3 +204,22 @@ def test_reference_beam_pins():
     # one prompt of 3 tokens in blocks of 2 (block 9, then 4 half full), two children of it
     t, n, s, c = ref.beam_reorder([[9, 4, 0]], [3], [0, 0, -1], [[9, 4, 6], [9, 5, 7], [9, 8, 3]], None, 2)
     assert t == [[9, 4, 6], [9, 5, 7], [9, 8, 3]] and n == [4, 4, 0] and s == [9, 11, -1] and c == [(4, 5, 1)]
+
+
+def test_beam_select_workspace_of_the_largest_serves_all(pkv):
+    """A workspace for B, W, K, V serves every smaller one: a loop's requests finish."""
+    lib, size = pkv.load_library(), pkv.pkv_beam_select_workspace_size
+    if torch.cuda.is_available():
+        return                                                             # (the calls below have no memory behind them)
+    for B, W, K, V in ((10, 4, 4, 128256), (64, 8, 8, 128256), (16, 4, 4, 32000), (300, 2, 32, 50257), (16384, 1, 1, 50),
+                       (3, 32, 32, 1 << 21), (40, 16, 8, 300001)):
+        need = size(B, W, K, V)
+        for b in sorted({1, 2, 3, B // 2 or 1, B - 1 or 1, B, *range(1, min(B, 40))}):
+            for w in sorted({1, W // 2 or 1, W}):
+                for k in sorted({1, K}):
+                    for v in sorted({1, 2048, 2049, V // 3 + 1, V - 1 or 1, V}):
+                        if v > V or b > B:
+                            continue
+                        assert size(b, w, k, v) <= need, (B, W, K, V, b, w, k, v)
+                        for dt in (0, 1, 2):
+                            assert _select(lib, B=b, W=w, K=k, V=v, dt=dt, end=-1, wsb=need) == CUDA, (B, W, K, V, b, w, k, v, dt)
