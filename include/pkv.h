@@ -679,8 +679,9 @@ PKV_API pkv_status pkv_quant_decode_attention(
 
 /*
  * pkv_quant_decode_workspace_size -- bytes of workspace
- * pkv_quant_decode_attention needs for these sizes, for every format, dtype
- * and window (host only).  Returns 0 for invalid sizes.
+ * pkv_quant_decode_attention needs for these sizes and for a smaller batch or
+ * context length, for every format, dtype and window (host only).  Returns 0
+ * for invalid sizes.
  */
 PKV_API size_t pkv_quant_decode_workspace_size(int B, int H, int num_kv_heads, int head_dim,
                                                int block_size, int max_blocks, int max_context_len,

@@ -178,10 +178,27 @@ static void simt_plan(int B, int H, int KVH, int D, long long span, int partitio
   p->P = (int)std::min(P, ceil_div(span, 128) * 128);
   p->max_parts = (int)ceil_div(span, p->P);
 }
-static size_t simt_bytes(int B, int H, int D, long long parts) {
-  const size_t rows = (size_t)B * H;
+// `rows`: (query row, part) pairs of a call in parts.
+static size_t simt_bytes(size_t rows, int D) {
   return kChunkCnt * sizeof(int) +
-         (parts > 1 ? 2 * align256(rows * parts * sizeof(float)) + align256(rows * parts * (size_t)D * sizeof(float)) : 0);
+         (rows ? 2 * align256(rows * sizeof(float)) + align256(rows * (size_t)D * sizeof(float)) : 0);
+}
+// The most (unit, part) pairs, in more parts than one, of a call of as many units
+// and keys or fewer: a smaller batch is split further (see quant_parts_wanted).
+static long long simt_most_pairs(long long units, long long span, int partition_size) {
+  if (partition_size) {
+    const long long parts = std::min<long long>(kQdMaxParts, ceil_div(span, partition_size));
+    return parts > 1 ? units * parts : 0;
+  }
+  const long long slots = 2 * kQdSms;
+  long long most = 0;
+  const long long few = std::min(units, slots - 1);
+  if (span > 128) most = std::min(2 * slots, few * std::min<long long>(kQdAutoParts, ceil_div(span, 128)));
+  if (units >= slots && span >= 2 * 1024) {
+    const long long many = std::min(units, 4 * slots - 1);
+    most = std::max(most, std::min(4 * slots + many, many * (span / 1024)));
+  }
+  return most;
 }
 
 // Tensor cores: query heads of a unit are four where a head has two columns of
@@ -227,10 +244,10 @@ PKV_API size_t pkv_quant_decode_workspace_size(int B, int H, int num_kv_heads, i
   if (!quant_sizes_ok(B, H, num_kv_heads, head_dim, block_size, max_blocks, max_context_len, partition_size)) return 0;
   const long long cap = quant_cap(block_size, max_blocks, max_context_len);
   const int G = H / num_kv_heads;
-  // (a window's shorter span never has more parts than are wanted here)
-  const long long units = (long long)B * num_kv_heads * ceil_div(G, std::min(kQdHeads, G));
-  size_t most = simt_bytes(B, H, head_dim, partition_size ? std::min<long long>(kQdMaxParts, ceil_div(cap, partition_size))
-                                                          : quant_parts_wanted(units, 2 * kQdSms, cap));
+  const int chunks = (int)ceil_div(G, std::min(kQdHeads, G));
+  const long long pairs = simt_most_pairs((long long)B * num_kv_heads * chunks, cap, partition_size);
+  // (G rows a KV head over its units)
+  size_t most = simt_bytes((size_t)ceil_div(pairs * G, chunks), head_dim);
   for (int f = PKV_QUANT_INT8; f <= PKV_QUANT_INT4; ++f)
     for (int split = 0; split < 2; ++split) {
       if (!mma_shape((pkv_quant_format)f, head_dim)) continue;
@@ -276,7 +293,7 @@ PKV_API pkv_status pkv_quant_decode_attention(
     mma_plan(B, H, num_kv_heads, head_dim, span, partition_size, fmt, mma_split(dt, G), &plan);
   } else {
     simt_plan(B, H, num_kv_heads, head_dim, span, partition_size, &plan);
-    plan.bytes = simt_bytes(B, H, head_dim, plan.max_parts);
+    plan.bytes = simt_bytes(plan.max_parts > 1 ? (size_t)B * H * plan.max_parts : 0, head_dim);
     if ((long long)plan.chunks * num_kv_heads * plan.max_parts > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   }
   const size_t need = plan.bytes;

@@ -223,3 +223,22 @@ def test_beam_select_workspace_of_the_largest_serves_all(pkv):
                         assert size(b, w, k, v) <= need, (B, W, K, V, b, w, k, v)
                         for dt in (0, 1, 2):
                             assert _select(lib, B=b, W=w, K=k, V=v, dt=dt, end=-1, wsb=need) == CUDA, (B, W, K, V, b, w, k, v, dt)
+
+
+def test_quant_decode_workspace_of_the_largest_serves_all(pkv):
+    """A workspace for a batch and a context length serves smaller ones, on the
+    tensor cores and on the CUDA cores (head_dim 40; unaligned codes)."""
+    lib, size = pkv.load_library(), pkv.pkv_quant_decode_workspace_size
+    if torch.cuda.is_available():
+        return
+    for B, H, KVH, D, bs, mb, P in ((400, 4, 1, 40, 16, 20, 0), (200, 8, 2, 40, 16, 128, 0), (64, 32, 8, 64, 16, 256, 0),
+                                    (2000, 6, 1, 72, 16, 300, 0), (300, 16, 1, 256, 32, 256, 0), (40, 5, 1, 40, 1, 5000, 256),
+                                    (20000, 4, 4, 40, 16, 30, 128)):
+        need = size(B, H, KVH, D, bs, mb, 0, P)
+        for b in sorted({1, 2, B // 7 or 1, B // 2 or 1, B - 1, B, *range(1, min(B, 80)), *(x for x in range(290, 320) if x <= B)}):
+            for n in (0, 1, 130, mb * bs // 3 + 1, mb * bs):
+                assert size(b, H, KVH, D, bs, mb, n, P) <= need, (B, b, n)
+                for odd in (0, 1):
+                    for dt in (0, 1):
+                        assert _decode(lib, B=b, H=H, KVH=KVH, D=D, bs=bs, mb=mb, maxn=n, P=P, dt=dt, nb=8, k_codes=at(2) + odd,
+                                       wsb=need) == CUDA, (B, b, n, odd, dt)
