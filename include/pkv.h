@@ -624,7 +624,7 @@ PKV_API pkv_status pkv_quant_write(void *k_codes, void *v_codes, float *k_params
  * negative slot leaves its rows as they were, one past the pool does too and
  * raises PKV_FLAG_SLOT_OUT_OF_RANGE.  The same slot may come more than once.
  * Sizes, alignment and errors as in pkv_quant_write; k_out and v_out overlap
- * no other argument.
+ * no other argument (rows side by side in one buffer, of one stride, do not).
  */
 PKV_API pkv_status pkv_quant_read(void *k_out, void *v_out, const void *k_codes,
                                   const void *v_codes, const float *k_params,

@@ -517,3 +517,25 @@ def test_decode_large_queries_of_small_keys(fmt, H, KVH):
     out = case.run(1.0)
     want = case.v[0][0].repeat_interleave(H // KVH, 0)
     assert (out[0].double() - want).abs().max() <= 2.0 ** -20 * want.abs().max()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pad", [0, 5])
+def test_read_into_one_buffer(fmt, dtype, pad):
+    """K and V read back side by side, as one projection's output has them (the
+    layout that the write takes)."""
+    kvh, d, bs, nb, T = 2, 64, 16, 4, 40
+    x = rows_like(T, kvh, d, dtype, 3).to(DEV)
+    slots = torch.randperm(nb * bs, generator=torch.Generator().manual_seed(4))[:T].to(DEV)
+    cache = [t.to(DEV) for t in empty_cache(nb, bs, kvh, d, fmt)]
+    pkv.pkv_quant_write(*cache, x[:, 0], x[:, 1], slots)
+    apart = [torch.zeros(T, kvh, d, dtype=dtype, device=DEV) for _ in range(2)]
+    pkv.pkv_quant_read(*apart, *cache, slots)
+    for first in (0, 1):
+        buf = torch.full((T, 2 * kvh * d + pad), 7.0, dtype=dtype, device=DEV)
+        halves = [buf[:, i * kvh * d:(i + 1) * kvh * d].view(T, kvh, d) for i in (first, 1 - first)]
+        pkv.pkv_quant_read(*halves, *cache, slots)
+        for got, want in zip(halves, apart):
+            assert torch.equal(got, want)
+        assert (buf[:, 2 * kvh * d:] == 7).all()

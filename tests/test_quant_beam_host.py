@@ -242,3 +242,18 @@ def test_quant_decode_workspace_of_the_largest_serves_all(pkv):
                     for dt in (0, 1):
                         assert _decode(lib, B=b, H=H, KVH=KVH, D=D, bs=bs, mb=mb, maxn=n, P=P, dt=dt, nb=8, k_codes=at(2) + odd,
                                        wsb=need) == CUDA, (B, b, n, odd, dt)
+
+
+def test_quant_read_side_by_side(pkv):
+    """Rows of K and V in one buffer are not an overlap, rows that meet are."""
+    lib = pkv.load_library()
+    row, far = 2 * 64 * 2, 1 << 30                                         # bytes of a token's row (bf16)
+    call = lambda shift, stride=256, other=None, T=5: _rows(lib, True, k=at(4) + far, v=at(4) + far + shift, T=T, ks=stride,
+                                                            vs=other or stride)
+    for bad in (call(0), call(row - 2), call(-row + 2), call(2 * row - 2), call(2 * row + 2), call(8 * row + 2), call(4, 300), call(row, 256, 300),
+                call(row, 129), call(-8 * row - row + 2), call(0, T=1), call(row - 2, T=1)):
+        assert bad == INVALID
+    if not torch.cuda.is_available():
+        for fine in (call(row), call(-row), call(row, 257), call(-row, 300), call(3 * row), call(row + 40, 300), call(9 * row + row),
+                     call(row, 256, 300, T=1), call(100 * row, 256, 300)):
+            assert fine == CUDA
