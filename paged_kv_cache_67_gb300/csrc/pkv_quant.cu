@@ -340,7 +340,7 @@ static pkv_status quant_rows(void *const (&codes)[2], float *const (&params)[2],
   if (!slots || reinterpret_cast<uintptr_t>(slots) % 8 || reinterpret_cast<uintptr_t>(err) % 4) return PKV_ERR_INVALID_ARG;
   QuantRowsArgs a = {};
   const int64_t rows = num_blocks * bs * KVH;
-  ArgRange r[7];
+  ArgRange r[8];
   for (int s = 0; s < 2; ++s) {
     if (!codes[s] || !params[s] || !x[s] || reinterpret_cast<uintptr_t>(x[s]) % el ||
         reinterpret_cast<uintptr_t>(params[s]) % 4)
@@ -354,10 +354,11 @@ static pkv_status quant_rows(void *const (&codes)[2], float *const (&params)[2],
     a.stride[s] = stride[s];
   }
   r[6] = {slots, (size_t)T * sizeof(int64_t)};
+  r[7] = {err, sizeof(int)};
   // what is written overlaps nothing else (two dense inputs, and two caches
   // that are only read, may)
-  for (int i = 0; i < 7; ++i)
-    for (int j = i + 1; j < 7; ++j) {
+  for (int i = 0; i < 8; ++i)
+    for (int j = i + 1; j < 8; ++j) {
       const bool wi = read ? i == 4 || i == 5 : i < 4, wj = read ? j == 4 || j == 5 : j < 4;
       if (i == 4 && j == 5 && stride[0] == stride[1] && rows_apart(x[0], x[1], T, (size_t)KVH * D * el, (size_t)stride[0] * el)) continue;
       if ((wi || wj) && overlap(r[i], r[j])) return PKV_ERR_INVALID_ARG;

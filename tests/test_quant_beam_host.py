@@ -257,3 +257,14 @@ def test_quant_read_side_by_side(pkv):
         for fine in (call(row), call(-row), call(row, 257), call(-row, 300), call(3 * row), call(row + 40, 300), call(9 * row + row),
                      call(row, 256, 300, T=1), call(100 * row, 256, 300)):
             assert fine == CUDA
+
+
+@pytest.mark.parametrize("read", [False, True])
+def test_quant_rows_flags_apart(pkv, read):
+    """The flags are an argument that what is written overlaps as little as the others."""
+    lib = pkv.load_library()
+    for i in (4, 5) if read else (0, 1, 2, 3):
+        assert _rows(lib, read, err=at(i) + 8) == INVALID, i
+    if not torch.cuda.is_available():
+        for i in (0, 1, 2, 3) if read else (4, 5):
+            assert _rows(lib, read, err=at(i) + (1 << 30)) == CUDA, i
