@@ -539,3 +539,59 @@ def test_read_into_one_buffer(fmt, dtype, pad):
         for got, want in zip(halves, apart):
             assert torch.equal(got, want)
         assert (buf[:, 2 * kvh * d:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,KVH,D,bs", [(32, 8, 64, 16), (16, 16, 64, 32), (64, 8, 64, 16), (8, 8, 128, 24), (24, 8, 96, 16)])
+def test_decode_eight_heads_at_once(fmt, dtype, H, KVH, D, bs):
+    """Eight KV heads (or head groups) a token: warps of two CTAs walk the same
+    tokens.  Ragged lengths, empty sequences, splits and joins, windows."""
+    case = Case([0, 1, 700, 31, 32, 0, 33, 257, 2100, 0], H, KVH, D, bs, fmt, dtype, seed=70 + H + D)
+    scale = 1 / math.sqrt(D)
+    out = case.run(scale)
+    case.check(out, scale)
+    assert torch.equal(out, case.run(scale))
+    case.check(case.run(scale, P=128), scale)
+    case.check(case.run(scale, 20.0, 100), scale, 20.0, 100)
+    case.check(case.run(scale, window=33, P=1 << 20), scale, window=33)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_decode_more_units_than_counters(shift):
+    """The CUDA cores: (sequence, KV head) units past the workspace's counters
+    are not split, whatever partition is asked for.  A head size of 40, and one
+    of 64 whose codes begin at an odd byte."""
+    B, KVH, D, bs = 16400, 4, 64 if shift else 40, 16
+    g = torch.Generator().manual_seed(1)
+    codes = [torch.randint(-127, 128, (8, bs, KVH, D), generator=g, dtype=torch.int8) for _ in range(2)]
+    params = [torch.rand(8, KVH, bs, generator=g) * 0.02 for _ in range(2)]
+    tables = torch.randint(0, 8, (B, 19), generator=g, dtype=torch.int32)
+    lens = torch.randint(0, 301, (B,), generator=g, dtype=torch.int32)
+    q = torch.randn(B, KVH, D, generator=g).to(torch.bfloat16)
+    dev = []
+    for t in codes:
+        buf = torch.zeros(t.numel() + shift, dtype=torch.int8, device=DEV)[shift:]
+        dev.append(buf.view(t.shape).copy_(t.to(DEV)))
+    dev += [t.to(DEV) for t in params]
+    out = torch.full_like(q, math.nan, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = pkv.QuantDecodeWorkspace(B, KVH, KVH, D, bs, 19, 0, 128)
+    for _ in range(2):
+        pkv.pkv_quant_decode_attention(out, q.to(DEV), *dev, tables.to(DEV), lens.to(DEV), 0.05, partition_size=128,
+                                       workspace=ws, err_flags=err)
+    out = out.cpu()
+    assert int(err) == 0 and torch.isfinite(out).all()
+    for b in [*range(0, B, 211), *range(B - 30, B)]:           # (the last are past the counters)
+        n = int(lens[b])
+        k, v = (ref.values(c[tables[b].long()].flatten(0, 1)[:n], p[tables[b].long()].transpose(1, 2).flatten(0, 1)[:n], "int8")
+                for c, p in zip(codes, params))
+        want = ref.decode(q[b], k, v, 0.05)
+        if n == 0:
+            assert torch.equal(out[b].double(), want)
+            continue
+        # a score's sum of D products and 5 steps of a warp's, its weight's, the sums' over n keys
+        A = 0.05 * float((k.abs() * q[b].double().abs()).sum(-1).max()) * 1.4427
+        tol = 2 * (A * (D / 32 + 8) * 2.0 ** -23 * 0.6932 + 2.0 ** -21) + 2.0 ** -23 * (n / 8 + 16)
+        room = HALF[torch.bfloat16] * want.abs() + 1.01 * tol * v.abs().amax((0, 2))[:, None]
+        assert ((out[b].double() - want).abs() <= room).all()
