@@ -589,7 +589,7 @@ PKV_API int pkv_chunk_plan(int B, int64_t total_q, int H, int num_kv_heads, int 
  *   params  float32 [num_blocks, num_kv_heads, block_size]: scale; INT4
  *           [num_blocks, num_kv_heads, block_size, 2]: scale, zero.  A head's
  *           numbers of one block lie together, as the decode reads them.
- * Scales must not be negative.
+ * Scales must not be negative; zero points are whole numbers from 0 to 15.
  */
 typedef enum pkv_quant_format {
   PKV_QUANT_INT8 = 0,
@@ -643,7 +643,9 @@ PKV_API pkv_status pkv_quant_read(void *k_out, void *v_out, const void *k_codes,
  * with K and V the values that the codes stand for.  Scores, statistics and
  * sums are fp32; queries and weights enter the products as two fp16 numbers
  * each (good to 2^-22; what a key adds is held to 2^-30 of the largest value
- * scale among the visible keys).  An empty context gives zeros.
+ * scale among the visible keys).  The division comes after the sums, whose
+ * weights are at most 2^8: values above 2^120 / n may leave fp32 on the way.
+ * An empty context gives zeros.
  *   block_tables, context_lens, max_context_len as in pkv_decode_attention
  *   (the same flags; a context over the table is clamped)
  *   partition_size  0 = automatic, else a positive multiple of 128: keys per

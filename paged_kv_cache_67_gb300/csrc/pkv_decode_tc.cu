@@ -525,9 +525,10 @@ bool encode_chunk_map(CUtensorMap *map, const void *cache, pkv_dtype dt, long lo
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tensor map of a [rows, H, D] 16-bit tensor (one row of H heads per token):
-// box of 64 elements x box_heads heads x box_rows rows, 128-byte swizzle; rows
-// past the end read as zero.
+// Tensor map of a [num_blocks, bs, KVH] cache of `row` bytes a row seen as 5-D,
+// innermost first: `part` bytes of a row, row in the block, part of the row,
+// head, block; box of all parts x 16 rows x 1 head x 1 block, swizzled over
+// `part` bytes where those are a power of two.
 bool encode_codes_map(CUtensorMap *map, const void *codes, long long num_blocks, int bs, int KVH, int row, int part) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
@@ -544,6 +545,9 @@ bool encode_codes_map(CUtensorMap *map, const void *codes, long long num_blocks,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map of a [rows, H, D] 16-bit tensor (one row of H heads per token):
+// box of 64 elements x box_heads heads x box_rows rows, 128-byte swizzle; rows
+// past the end read as zero.
 bool encode_packed_map(CUtensorMap *map, const void *base, pkv_dtype dt, long long rows, int H, int D,
                        int box_heads, int box_rows) {
   EncodeTiledFn fn = encode_fn();

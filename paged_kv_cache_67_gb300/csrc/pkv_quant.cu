@@ -145,6 +145,9 @@ __global__ void __launch_bounds__(kQuantThreads) pkv_quant_write_kernel(const __
     const float span = FMT == kInt4 ? hi[s] - lo[s] : hi[s];
     const bool ok = span <= 3.402823466e38f;               // (neither NaN nor infinite)
     const bool fine = ok && span >= kQuantTiny;
+    // (reciprocals, as pkv.h defines them: 2^-23 off where quotients would be 2^-24,
+    // next to a code's half step of 2^-9 and more; quotients took 16384 tokens to int8
+    // from 26.8 to 28.7 us, to e4m3 from 27.6 to 28.8)
     const float inv = fine ? __fmul_rn(__frcp_rn(span), kTop) : 0.f;
     const float scale = fine ? __fmul_rn(span, 1.f / kTop) : ok ? 0.f : __int_as_float(0x7fc00000);
     const int zero = FMT == kInt4 && fine ? rint_product(-lo[s], inv) : 0;

@@ -226,9 +226,6 @@ constexpr long long power(long long base, int n) { return n == 0 ? 1 : base * po
 static_assert(kChunkCntFirst + kQmLevels * kQdMostWarps <= kChunkCnt && kQdMostWarps <= power(kQmFan, kQmLevels),
               "the counters fit the workspace's");
 
-}  // namespace pkv
-namespace pkv {
-
 pkv_status launch_quant_mma_int8(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream);
 pkv_status launch_quant_mma_e4m3(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream);
 pkv_status launch_quant_mma_int4(const QuantDecodeArgs &a, bool split, pkv_dtype dt, cudaStream_t stream);

@@ -54,7 +54,6 @@
 
 namespace pkv {
 
-
 template <int D, int FMT>
 struct QmShape {
   static constexpr int kRow = quant_row_bytes<FMT>(D);
@@ -110,11 +109,6 @@ __device__ __forceinline__ bool mbar_sleep_bounded(uint64_t *bar, uint32_t parit
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -158,6 +152,8 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t m, uint32_t c) {
 
 // Four codes of a word (one K row; of V's ldmatrix word, two columns of token
 // 2t and the same of token 2t + 1) as two pairs of halves.
+// (Whole numbers become halves by their bits, as is usual: or-ed into the low
+// bits of 1024, whose unit in fp16 is 1.)
 // int8: bytes (0, 2) and (1, 3): a byte with its top bit turned, code + 128, in
 // the low bits of the half 1024 is 1152 + code exactly: one and-xor, one subtract.
 // e4m3: K's bytes (0, 1) and (2, 3), V's as int8's.
