@@ -16,8 +16,8 @@
 //      and each counts the keys above its own: its rank.
 //      (With the largest of the warps' own bounds some 50 elements came through:
 //      64 x 8 beams x 128256 tokens took 113 us.)
-// 64 x 8 beams x 128256 bf16: 66 us (116 MB), bound by instructions and the
-// barriers between the passes (two issued a cycle); 4 x 32000 fp32: 14 us, latency.
+// 64 x 8 beams x 128256 bf16: 67 us (116 MB), bound by instructions and the
+// barriers between the passes (two issued a cycle); 4 x 32000 fp32: 15 us, latency.
 //
 // The CTA that finishes a request's last piece joins: a warp a beam merges the
 // pieces' sorted keys (lane = piece, K rounds of a warp-wide maximum) and adds

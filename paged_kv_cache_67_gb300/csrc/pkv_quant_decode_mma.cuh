@@ -40,9 +40,12 @@
 // places a warp, and the last one done of up to 16 neighbours joins them, then of
 // up to 16 such groups, until the unit is one.
 //
-// Measured: 64 x 512-4096 keys of 8 heads of 128, int8, 32 query heads: 61.7 us,
-// 5.1 TB/s; 8 x 16-32k keys, e4m3, capped: 79 us, 5.2 TB/s.  What bounds it: a
-// tile is a chain of some 1600 cycles in each of an SM's eight computing warps.
+// Measured: 64 x 512-4096 keys of 8 heads of 128, int8, 32 query heads: 60-61.7 us,
+// 5.1 TB/s (4 bits 56 us, 3.0 TB/s); 8 x 16-32k keys, e4m3, capped: 75-77 us,
+// 5.3 TB/s.  What bounds it: a tile is a chain of some 1600 cycles in each of an
+// SM's eight computing warps.  One KV head of 16 heads of 256, 4 bits, 128 x 1-8192
+// keys: 56 us, where the 16-bit cache's kernel takes 35 (two units unpack every
+// key, and start and end for every short sequence).
 //
 // Rows in the ring are swizzled as TMA does it: the 4-byte fragment loads of K
 // and the transposing ldmatrix of V both touch every bank once.
